@@ -5,13 +5,16 @@
  * sums wrapping at 2^32, and the primitives built on them: segmented scan and
  * reduce over head-flagged segments, stream compaction (flags -> inclusive
  * offsets -> gathered indices -> count) and a stable LSD radix-sort
- * permutation of U32 keys.
+ * permutation of U32 keys; and, for programs that decode with a language
+ * model, token sampling and the operations of a paged cache, exact integer
+ * arithmetic like the rest.
  *
  * Conventions for every entry point below:
  *   - Pointers named as device pointers must point to memory the current
  *     CUDA device can access (cudaMalloc, torch tensors, managed memory),
- *     aligned to 4 bytes. 16-byte alignment is not required. Only the
- *     *_host scans take host pointers, and say so.
+ *     aligned to 4 bytes (logits: to their element; a pool's pages: not at
+ *     all). 16-byte alignment is not required. Only the *_host scans take
+ *     host pointers, and say so.
  *   - Every call is asynchronous on `stream` (NULL = the legacy default
  *     stream). Results, totals and counts stay in device memory (the
  *     *_host scans write theirs to host memory).
@@ -79,6 +82,15 @@ typedef struct CUstream_st *u32scan_stream_t;
 #define U32SCAN_OP_SCAN64 6    /* scan_u64_op */
 #define U32SCAN_OP_SCAN_HOST 7 /* scan_exclusive_u32_host, scan_inclusive_u32_host */
 #define U32SCAN_OP_REDUCE 8    /* reduce_u32_op (the same size for every n) */
+#define U32SCAN_OP_PAGES 9     /* pages_fork, pages_free, pages_compact: n = pages + rows */
+
+/* Element types of logits (sample_tokens). */
+#define U32SCAN_F32 0
+#define U32SCAN_F16 1
+#define U32SCAN_BF16 2
+
+/* The largest vocabulary of sample_tokens (its weights' sums stay below 2^53). */
+#define U32SCAN_MAX_VOCAB (1u << 22)
 
 /* Bytes of device workspace an operation needs for n elements (a multiple
  * of 256, at least 256). Returns 0 for an unknown op. Pure host function. */
@@ -598,6 +610,145 @@ int u32scan_test_noalloc_set_epoch(unsigned int epoch, u32scan_stream_t stream);
  */
 int u32scan_fill_splitmix_u32(uint32_t *out, size_t n, uint32_t seed, uint32_t stream, size_t start,
                               u32scan_stream_t cuda_stream);
+
+/*
+ * The next token of every row of logits, drawn with given random words (no
+ * counterpart on the pages: a use of their prefix sums and selections, for
+ * programs that decode with a language model).
+ *
+ * With l a row's logits (NaN counts as -inf), m the largest, T its
+ * temperature:
+ *   weight  q[i] = floor(2^31 * 2^-y), y = (m - l[i]) * (log2(e) / T), every
+ *           f32 operation rounded alone (exp2 by the degree-5 polynomial in
+ *           csrc/sample.cu); 0 from y = 32 on and for l[i] = -inf. T that is
+ *           not above 0 (or NaN): the least i with l[i] = m is the token.
+ *   min-p   with min_p > 0: q[i] below ceil(min(min_p, 1) * 2^31) becomes 0.
+ *   order   l descending, then i ascending (-0 equals +0).
+ *   top-k   with top_k > 0: q becomes 0 past the first top_k in that order.
+ *   top-p   with 0 < top_p < 1: with S = sum of q, the shortest prefix in
+ *           that order whose sum reaches ceil(top_p * S) (a double product)
+ *           is kept, the rest becomes 0.
+ *   draw    with S' = sum of what is left: r = floor(random * S' / 2^32); the
+ *           token is the first i, in index order, at which the running sum
+ *           of q exceeds r.
+ * All sums are u64, so the result is the same on every machine and for every
+ * launch shape.
+ *   logits      device, rows of `vocab` elements of `type` (U32SCAN_F32, _F16,
+ *               _BF16), row b at logits + b * row_stride elements (a stride
+ *               below vocab, 0 among them, is fine: rows are only read).
+ *               Aligned to its element; nothing more is needed.
+ *   temperature, top_k, top_p, min_p  device, one value a row, or NULL: 1, and
+ *               no filter. Values outside the ranges above switch a filter
+ *               off.
+ *   random      device, uint32_t[rows], uniform words (for instance from
+ *               u32scan_fill_splitmix_u32).
+ *   tokens      device, int32_t[rows]: the token; -1 for a row in which no
+ *               logit is above -inf (or vocab = 0).
+ *   probs       device, float[rows] or NULL: q[token] / S' rounded from
+ *               double; 1 where T is not above 0, 0 where the token is -1.
+ * No workspace. Errors: EINVAL (unknown type, null logits with vocab > 0,
+ * null random or tokens with rows > 0, misaligned pointers, vocab above
+ * U32SCAN_MAX_VOCAB, rows >= 2^31, row_stride >= 2^32), ECUDA.
+ */
+int sample_tokens(const void *logits, int type, size_t rows, size_t vocab, size_t row_stride,
+                  const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                  const uint32_t *random, int32_t *tokens, float *probs, u32scan_stream_t stream);
+
+/*
+ * A paged cache (no counterpart on the pages: their prefix sums, compaction
+ * and runs layout, applied to a cache's pages). `pages` pages of
+ * `page_bytes` bytes lie `page_stride` bytes apart in every one of
+ * `n_planes` planes (say, a layer's keys). `planes` is a DEVICE array of the
+ * planes' device addresses; this struct itself is read on the host during
+ * the call. Any alignment works; 16 bytes of address, size and stride copy
+ * fastest.
+ *
+ * Beside the pool a program holds
+ *   table  device, int32_t rows of `width` page numbers, row s at table +
+ *          s * table_stride; the first ceil(lens[s] / page_tokens) of a row
+ *          are in use;
+ *   lens   device, int32_t[rows]: each row's length in tokens;
+ *   refs   device, int32_t[pages]: how many entries in use hold a page; a
+ *          page with refs = 0 is free.
+ * The operations below keep them so. Page numbers outside [0, pages) are
+ * skipped wherever they occur; if refs disagree with the table the results
+ * are unspecified, but every access stays inside the arrays.
+ */
+typedef struct {
+    const uint64_t *planes;
+    size_t n_planes, pages, page_bytes, page_stride;
+} u32scan_page_pool;
+
+/*
+ * Copies page src[i] to page dst[i] in every plane, i < n. Pairs with a
+ * number outside [0, pages) (say -1), or with src[i] = dst[i], are skipped.
+ * A page must not be a destination twice, or a destination and another
+ * pair's source: such pages' bytes are unspecified afterwards.
+ *   src, dst  device, int32_t[n];  n below 2^31.
+ *   count     device, one int32_t or NULL: only the first min(n, max(count,
+ *             0)) pairs are copied (so the number can come from a kernel).
+ * No workspace. Errors: EINVAL (null pool, planes, src or dst, misaligned
+ * pointers (planes: 8 bytes), sizes out of range, page_stride below
+ * page_bytes), ECUDA.
+ */
+int pages_copy(const u32scan_page_pool *pool, const int32_t *src, const int32_t *dst, size_t n,
+               const int32_t *count, u32scan_stream_t stream);
+
+/*
+ * Forks rows and gives rows their next pages, in one step over all rows.
+ *   parent  device, int32_t[rows] or NULL: with parent[s] >= 0 the empty row
+ *           s becomes a copy of row parent[s] as it was before the call: it
+ *           shares the parent's full pages (their refs + 1) and gets a fresh
+ *           page with the contents of a partly filled last one.
+ *   grow    device, int32_t[rows] or NULL (0): tokens by which every row
+ *           (children too) then gets longer; it takes the fresh pages those
+ *           need.
+ * Fresh pages are the free ones in ascending order, dealt in row order: row
+ * s needs need[s], and is served when need[s] = 0 or need[0] + .. + need[s]
+ * is at most the number of free pages; a row that is not served stays as it
+ * was. Fresh pages get refs = 1.
+ *   pool    host struct or NULL: the pages' bytes; with NULL (or no planes)
+ *           no bytes are copied.
+ *   status  device, int32_t[rows]: the fresh pages row s took, or -1 when its
+ *           arguments are refused (a child that is not empty, or whose
+ *           parent is not a row or is a child itself in this call; a
+ *           negative length or growth; more than `width` pages or 2^31 - 1
+ *           tokens), or -2 when pages ran out. Rows with -1 need nothing.
+ *   free_pages device, one int32_t or NULL: free pages left.
+ *   ws, ws_bytes  u32scan_workspace_bytes(U32SCAN_OP_PAGES, pages + rows).
+ * The arrays must not overlap. Errors: EINVAL (null or misaligned pointers,
+ * rows, width, pages, table_stride or page_tokens at or above 2^31,
+ * page_tokens = 0, table_stride below width, a pool of other size),
+ * EWORKSPACE, ECUDA.
+ */
+int pages_fork(int32_t *table, size_t table_stride, size_t rows, size_t width, int32_t *lens, int32_t *refs,
+               size_t pages, size_t page_tokens, const int32_t *parent, const int32_t *grow,
+               const u32scan_page_pool *pool, int32_t *status, int32_t *free_pages, void *ws, size_t ws_bytes,
+               u32scan_stream_t stream);
+
+/*
+ * Releases every row s with release[s] != 0: lowers refs of its entries,
+ * sets them to -1 and its length to 0.
+ *   freed  device, one int32_t or NULL: pages whose refs fell to 0.
+ * Other arguments and errors as pages_fork.
+ */
+int pages_free(int32_t *table, size_t table_stride, size_t rows, size_t width, int32_t *lens, int32_t *refs,
+               size_t pages, size_t page_tokens, const int32_t *release, int32_t *freed, void *ws, size_t ws_bytes,
+               u32scan_stream_t stream);
+
+/*
+ * Packs the live pages (refs != 0) into the first L pages, L their number:
+ * the k-th live page at or above L moves into the k-th free page below L,
+ * the others stay. Table entries in use and refs follow; pages from L on are
+ * then free. With pool NULL only the numbers change.
+ *   live   device, one int32_t or NULL: L.
+ *   remap  device, int32_t[pages] or NULL: each live page's new number, -1
+ *          for a free page (for page numbers held elsewhere).
+ * Other arguments and errors as pages_fork.
+ */
+int pages_compact(const u32scan_page_pool *pool, int32_t *table, size_t table_stride, size_t rows, size_t width,
+                  const int32_t *lens, int32_t *refs, size_t pages, size_t page_tokens, int32_t *live,
+                  int32_t *remap, void *ws, size_t ws_bytes, u32scan_stream_t stream);
 
 #ifdef __cplusplus
 }

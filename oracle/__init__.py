@@ -41,13 +41,26 @@ def build(force: bool = False) -> pathlib.Path:
         tmp = _SO.with_suffix(f".so.tmp{os.getpid()}")
         subprocess.check_call(
             ["gcc", "-O2", "-std=c11", "-Wall", "-Wextra", "-shared", "-fPIC",
-             "-o", str(tmp), str(_SRC)])
+             "-o", str(tmp), str(_SRC), "-lm"])
         os.replace(tmp, _SO)
     return _SO
 
 
 def _configure(lib):
     """Declare the C signatures on a loaded oracle library."""
+    f32, i32, u8p = ctypes.c_float, ctypes.c_int32, ctypes.POINTER(ctypes.c_uint8)
+    table = [_i32p, _u64, _u64, _i32p, _i32p, _u64, _u64]  # table, rows, width, lens, refs, pages, page_tokens
+    lib.oracle_sample_token.argtypes = [ctypes.POINTER(f32), _u64, f32, i32, f32, f32, ctypes.c_uint32,
+                                        ctypes.POINTER(f32)]
+    lib.oracle_sample_token.restype = i32
+    lib.oracle_pages_copy.argtypes = [u8p, _u64, _u64, _u64, _i32p, _i32p, _u64]
+    lib.oracle_pages_copy.restype = None
+    lib.oracle_pages_fork.argtypes = [*table, _i32p, _i32p, u8p, _u64, _u64, _i32p]
+    lib.oracle_pages_fork.restype = i32
+    lib.oracle_pages_free.argtypes = [*table, _i32p]
+    lib.oracle_pages_free.restype = i32
+    lib.oracle_pages_compact.argtypes = [*table, u8p, _u64, _u64, _i32p]
+    lib.oracle_pages_compact.restype = i32
     lib.oracle_scan_exclusive_u32.argtypes = [_u32p, _u64]
     lib.oracle_scan_exclusive_u32.restype = ctypes.c_uint32
     lib.oracle_scan_inclusive_u32.argtypes = [_u32p, _u64]
@@ -244,3 +257,80 @@ def scan_op_u64(a, op: str, inclusive: bool):
     total = _load().oracle_scan_op_u64(SCAN_OPS[op], int(bool(inclusive)),
                                        out.ctypes.data_as(ctypes.POINTER(ctypes.c_uint64)), out.size)
     return out, int(total)
+
+
+def sample_tokens(logits, random, temperature=None, top_k=None, top_p=None, min_p=None):
+    """(tokens, probs) of float32 logits [rows, vocab] under per-row
+    temperature, top_k, top_p and min_p (None: 1 and no filter), drawn with
+    the uint32 words `random`."""
+    x = np.ascontiguousarray(np.asarray(logits, dtype=np.float32))
+    rows, n = x.shape
+    words = np.asarray(random).astype(np.uint32)
+
+    def values(v, none):
+        return np.full(rows, none) if v is None else np.asarray(v)
+
+    t, k, p, a = values(temperature, 1.0), values(top_k, 0), values(top_p, 1.0), values(min_p, 0.0)
+    tokens, probs = np.empty(rows, dtype=np.int32), np.empty(rows, dtype=np.float32)
+    prob = ctypes.c_float()
+    for b in range(rows):
+        row = np.ascontiguousarray(x[b])
+        tokens[b] = _load().oracle_sample_token(row.ctypes.data_as(ctypes.POINTER(ctypes.c_float)), n, float(t[b]),
+                                                int(k[b]), float(p[b]), float(a[b]), int(words[b]),
+                                                ctypes.byref(prob))
+        probs[b] = prob.value
+    return tokens, probs
+
+
+def _cache(table, lens, refs):
+    return _i32(table).copy(), _i32(lens).copy(), _i32(refs).copy()
+
+
+def _bytes(pool, pages):
+    """(copy as [planes, pages, page_bytes] bytes, pointer, planes, page_bytes) of a pool, or of none."""
+    if pool is None:
+        return None, None, 0, 0
+    p = np.ascontiguousarray(np.asarray(pool, dtype=np.uint8)).copy()
+    if p.ndim != 3 or p.shape[1] != pages:
+        raise ValueError("pool must be [planes, pages, page_bytes]")
+    return p, p.ctypes.data_as(ctypes.POINTER(ctypes.c_uint8)), p.shape[0], p.shape[2]
+
+
+def pages_copy(pool, src, dst):
+    """The pool [planes, pages, page_bytes] after copying page src[i] to dst[i]."""
+    p, ptr, planes, page_bytes = _bytes(pool, np.asarray(pool).shape[1])
+    s, d = _i32(src), _i32(dst)
+    _load().oracle_pages_copy(ptr, planes, p.shape[1], page_bytes, _p(s, _i32p), _p(d, _i32p), s.size)
+    return p
+
+
+def pages_fork(table, lens, refs, page_tokens, parent=None, grow=None, pool=None):
+    """(table, lens, refs, status, free pages left, pool) after the fork."""
+    t, l, r = _cache(table, lens, refs)
+    p, ptr, planes, page_bytes = _bytes(pool, r.size)
+    par = None if parent is None else _i32(parent)
+    g = None if grow is None else _i32(grow)
+    status = np.empty(l.size, dtype=np.int32)
+    left = _load().oracle_pages_fork(_p(t, _i32p), t.shape[0], t.shape[1], _p(l, _i32p), _p(r, _i32p), r.size,
+                                     page_tokens, None if par is None else _p(par, _i32p),
+                                     None if g is None else _p(g, _i32p), ptr, planes, page_bytes, _p(status, _i32p))
+    return t, l, r, status, int(left), p
+
+
+def pages_free(table, lens, refs, page_tokens, release):
+    """(table, lens, refs, pages that became free) after the release."""
+    t, l, r = _cache(table, lens, refs)
+    rel = _i32(release)
+    freed = _load().oracle_pages_free(_p(t, _i32p), t.shape[0], t.shape[1], _p(l, _i32p), _p(r, _i32p), r.size,
+                                      page_tokens, _p(rel, _i32p))
+    return t, l, r, int(freed)
+
+
+def pages_compact(table, lens, refs, page_tokens, pool=None):
+    """(table, refs, live, remap, pool) after packing the live pages."""
+    t, l, r = _cache(table, lens, refs)
+    p, ptr, planes, page_bytes = _bytes(pool, r.size)
+    remap = np.empty(r.size, dtype=np.int32)
+    live = _load().oracle_pages_compact(_p(t, _i32p), t.shape[0], t.shape[1], _p(l, _i32p), _p(r, _i32p), r.size,
+                                        page_tokens, ptr, planes, page_bytes, _p(remap, _i32p))
+    return t, r, int(live), remap, p

@@ -33,7 +33,11 @@
  * slots with -1; sort keys are unsigned 32-bit and all 32 bits are sorted;
  * run counts are unsigned 32-bit; owner(e, ends) is the owner whose run
  * holds entry e, -1 for the one slot of a layout with no entries.
+ *
+ * The token sampler and the paged cache's operations at the end have no
+ * page behind them: they follow their definitions in include/u32scan.h.
  */
+#include <math.h>
 #include <stdint.h>
 #include <stdlib.h>
 #include <string.h>
@@ -460,4 +464,196 @@ uint64_t oracle_scan_op_u64(int op, int inclusive, uint64_t *a, uint64_t n)
         }
     }
     return s;
+}
+
+/*
+ * The next token of one row (logits already as float). The definition: f32
+ * weights' exponents operation by operation, integer weights and sums, a
+ * full sort for the filters' order, one walk in index order for the draw.
+ * Compiled without contraction (ISO mode), so every operation rounds alone.
+ */
+typedef struct {
+    float l;
+    uint32_t i;
+} oracle_logit;
+
+static int oracle_logit_order(const void *pa, const void *pb)
+{
+    const oracle_logit *a = pa, *b = pb;
+    if (a->l != b->l) return a->l > b->l ? -1 : 1;
+    return a->i < b->i ? -1 : a->i > b->i;
+}
+
+static uint64_t oracle_token_weight(float m, float l, float scale)
+{
+    if (l == -INFINITY) return 0;
+    float y = 0.0f;
+    if (l != m) {
+        const float d = m - l;
+        y = d * scale;
+    }
+    if (!(y < 32.0f)) return 0;
+    const float n = nearbyintf(y), f = y - n;
+    static const float c[6] = {1.0f, -0x1.62e42ap-1f, 0x1.ebf9bcp-3f, -0x1.c6b752p-5f, 0x1.3cea88p-7f,
+                               -0x1.5bba14p-10f};
+    float p = c[5];
+    for (int k = 4; k >= 0; --k) {
+        const float t = p * f;
+        p = t + c[k];
+    }
+    return (uint64_t)ldexp((double)p, 31 - (int)n);
+}
+
+int32_t oracle_sample_token(const float *logits, uint64_t n, float temperature, int32_t top_k, float top_p,
+                            float min_p, uint32_t word, float *prob)
+{
+    float m = -INFINITY;
+    for (uint64_t i = 0; i < n; ++i)
+        if (logits[i] > m) m = logits[i];
+    *prob = 0.0f;
+    if (m == -INFINITY) return -1;
+    if (!(temperature > 0.0f)) {
+        uint64_t i = 0;
+        while (!(logits[i] == m)) ++i;
+        *prob = 1.0f;
+        return (int32_t)i;
+    }
+    const float scale = 0x1.715476p+0f / temperature;
+    oracle_logit *row = malloc(n * sizeof *row);
+    uint64_t *q = calloc(n, sizeof *q);
+    for (uint64_t i = 0; i < n; ++i) {
+        row[i].l = logits[i] == logits[i] ? logits[i] : -INFINITY;
+        row[i].i = (uint32_t)i;
+        q[i] = oracle_token_weight(m, row[i].l, scale);
+        if (min_p > 0.0f && (double)q[i] < ceil((double)(min_p < 1.0f ? min_p : 1.0f) * 2147483648.0)) q[i] = 0;
+    }
+    qsort(row, n, sizeof *row, oracle_logit_order);
+    if (top_k > 0)
+        for (uint64_t j = (uint64_t)top_k; j < n; ++j) q[row[j].i] = 0;
+    uint64_t total = 0;
+    for (uint64_t i = 0; i < n; ++i) total += q[i];
+    if (top_p > 0.0f && top_p < 1.0f) {
+        const uint64_t want = (uint64_t)ceil((double)top_p * (double)total);
+        uint64_t sum = 0;
+        for (uint64_t j = 0; j < n; ++j) {
+            if (sum >= want) q[row[j].i] = 0;
+            sum += q[row[j].i];
+        }
+        total = sum;
+    }
+    /* floor(word * total / 2^32) without 128 bits: total < 2^54 */
+    const uint64_t hi = (uint64_t)word * (total >> 32), lo = ((uint64_t)word * (total & 0xffffffffu)) >> 32;
+    const uint64_t r = hi + lo;
+    uint64_t sum = 0, i = 0;
+    while (sum + q[i] <= r) sum += q[i++];
+    *prob = (float)((double)q[i] / (double)total);
+    free(q);
+    free(row);
+    return (int32_t)i;
+}
+
+/*
+ * A paged cache, row after row. pool: planes x pages x page_bytes bytes, or
+ * NULL. Page numbers outside [0, pages) are passed over.
+ */
+static void oracle_copy_page(uint8_t *pool, uint64_t planes, uint64_t pages, uint64_t page_bytes, int64_t src,
+                             int64_t dst)
+{
+    if (!pool || src < 0 || dst < 0 || src == dst || (uint64_t)src >= pages || (uint64_t)dst >= pages) return;
+    for (uint64_t k = 0; k < planes; ++k)
+        memcpy(pool + (k * pages + dst) * page_bytes, pool + (k * pages + src) * page_bytes, page_bytes);
+}
+
+void oracle_pages_copy(uint8_t *pool, uint64_t planes, uint64_t pages, uint64_t page_bytes, const int32_t *src,
+                       const int32_t *dst, uint64_t n)
+{
+    for (uint64_t i = 0; i < n; ++i) oracle_copy_page(pool, planes, pages, page_bytes, src[i], dst[i]);
+}
+
+int32_t oracle_pages_fork(int32_t *table, uint64_t rows, uint64_t width, int32_t *lens, int32_t *refs, uint64_t pages,
+                          uint64_t page_tokens, const int32_t *parent, const int32_t *grow, uint8_t *pool,
+                          uint64_t planes, uint64_t page_bytes, int32_t *status)
+{
+    int32_t *before = malloc((rows + 1) * sizeof *before);
+    int32_t *was = malloc((rows * width + 1) * sizeof *was);
+    uint8_t *is_free = malloc(pages + 1);
+    uint64_t n_free = 0, asked = 0, taken = 0, next = 0;
+    memcpy(before, lens, rows * sizeof *before);
+    memcpy(was, table, rows * width * sizeof *was);
+    for (uint64_t p = 0; p < pages; ++p) n_free += is_free[p] = refs[p] == 0;
+    for (uint64_t s = 0; s < rows; ++s) {
+        const int child = parent && parent[s] >= 0;
+        const int64_t g = grow ? grow[s] : 0;
+        status[s] = -1;
+        if (child && ((uint64_t)parent[s] >= rows || before[s] != 0 || parent[parent[s]] >= 0)) continue;
+        const int64_t old = before[child ? parent[s] : (int64_t)s];
+        if (old < 0 || g < 0 || old + g > 0x7fffffff) continue;
+        const uint64_t held = child ? old / page_tokens : (old + page_tokens - 1) / page_tokens;
+        const uint64_t all = (old + g + page_tokens - 1) / page_tokens;
+        if (all > width) continue;
+        const uint64_t need = all - held;
+        asked += need;
+        status[s] = -2;
+        if (need > 0 && asked > n_free) continue;
+        status[s] = (int32_t)need;
+        if (child)
+            for (uint64_t j = 0; j < held; ++j) {
+                const int32_t e = table[s * width + j] = was[parent[s] * width + j];
+                if (e >= 0 && (uint64_t)e < pages) refs[e] += 1;
+            }
+        for (uint64_t j = 0; j < need; ++j) {
+            while (!is_free[next]) ++next;
+            table[s * width + held + j] = (int32_t)next;
+            refs[next++] = 1;
+        }
+        if (child && old % page_tokens != 0)
+            oracle_copy_page(pool, planes, pages, page_bytes, was[parent[s] * width + held], table[s * width + held]);
+        lens[s] = (int32_t)(old + g);
+        taken += need;
+    }
+    free(before);
+    free(was);
+    free(is_free);
+    return (int32_t)(n_free - taken);
+}
+
+int32_t oracle_pages_free(int32_t *table, uint64_t rows, uint64_t width, int32_t *lens, int32_t *refs, uint64_t pages,
+                          uint64_t page_tokens, const int32_t *release)
+{
+    int32_t freed = 0;
+    for (uint64_t s = 0; s < rows; ++s) {
+        if (release[s] == 0) continue;
+        for (uint64_t j = 0; j < width && lens[s] > 0 && j * page_tokens < (uint64_t)lens[s]; ++j) {
+            const int32_t e = table[s * width + j];
+            table[s * width + j] = -1;
+            if (e >= 0 && (uint64_t)e < pages && --refs[e] == 0) ++freed;
+        }
+        lens[s] = 0;
+    }
+    return freed;
+}
+
+int32_t oracle_pages_compact(int32_t *table, uint64_t rows, uint64_t width, const int32_t *lens, int32_t *refs,
+                             uint64_t pages, uint64_t page_tokens, uint8_t *pool, uint64_t planes,
+                             uint64_t page_bytes, int32_t *remap)
+{
+    uint64_t live = 0, hole = 0;
+    for (uint64_t p = 0; p < pages; ++p) {
+        remap[p] = refs[p] != 0 ? (int32_t)p : -1;
+        live += refs[p] != 0;
+    }
+    for (uint64_t p = live; p < pages; ++p) {
+        if (refs[p] == 0) continue;
+        while (refs[hole] != 0) ++hole;
+        oracle_copy_page(pool, planes, pages, page_bytes, (int64_t)p, (int64_t)hole);
+        refs[hole] = refs[p];
+        refs[p] = 0;
+        remap[p] = (int32_t)hole;
+    }
+    for (uint64_t s = 0; s < rows; ++s)
+        for (uint64_t j = 0; j < width && lens[s] > 0 && j * page_tokens < (uint64_t)lens[s]; ++j) {
+            const int32_t e = table[s * width + j];
+            if (e >= 0 && (uint64_t)e < pages && remap[e] >= 0) table[s * width + j] = remap[e];
+        }
+    return (int32_t)live;
 }

@@ -31,6 +31,12 @@ _API = {
     "radix_sort_u32",
     "runs_layout_u32",
     "runs_owner_u32",
+    "sample_tokens",
+    "PagePool",
+    "pages_copy",
+    "pages_fork",
+    "pages_free",
+    "pages_compact",
     "check",
 }
 

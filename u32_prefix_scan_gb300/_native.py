@@ -27,10 +27,25 @@ OP_RUNS = 5
 OP_SCAN64 = 6
 OP_SCAN_HOST = 7
 OP_REDUCE = 8
+OP_PAGES = 9
+
+F32, F16, BF16 = 0, 1, 2
+MAX_VOCAB = 1 << 22
 
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _int = ctypes.c_int
+
+
+
+class PagePoolStruct(ctypes.Structure):
+    """u32scan_page_pool."""
+
+    _fields_ = [("planes", _vp), ("n_planes", _sz), ("pages", _sz), ("page_bytes", _sz), ("page_stride", _sz)]
+
+
+_pool = ctypes.POINTER(PagePoolStruct)
+_table = [_vp, _sz, _sz, _sz, _vp, _vp, _sz, _sz]  # table, stride, rows, width, lens, refs, pages, page_tokens
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -65,6 +80,11 @@ SIGNATURES = {
     "radix_sort_u32": (_int, [_vp, _sz, _vp, _vp, _vp, _sz, _vp]),
     "runs_layout_u32": (_int, [_vp, _sz, _vp, _vp, _sz, _vp, _sz, _vp]),
     "runs_owner_u32": (_int, [_vp, _sz, _vp, _sz, _vp]),
+    "sample_tokens": (_int, [_vp, _int, _sz, _sz, _sz, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "pages_copy": (_int, [_pool, _vp, _vp, _sz, _vp, _vp]),
+    "pages_fork": (_int, [*_table, _vp, _vp, _pool, _vp, _vp, _vp, _sz, _vp]),
+    "pages_free": (_int, [*_table, _vp, _vp, _vp, _sz, _vp]),
+    "pages_compact": (_int, [_pool, *_table, _vp, _vp, _vp, _sz, _vp]),
     "u32scan_test_scan_skip_publish": (_int, [_vp, _sz, _vp, _vp, _sz, ctypes.c_uint, ctypes.c_ulonglong, _vp]),
     "u32scan_test_segscan_skip_publish": (_int, [_vp, _vp, _sz, _vp, _sz, _vp, _vp, _sz, ctypes.c_uint,
                                                   ctypes.c_ulonglong, _vp]),

@@ -11,6 +11,7 @@ the same; wrapping u32 addition and two's-complement int32 addition agree).
 
 from __future__ import annotations
 
+import functools
 import threading
 
 import torch
@@ -42,15 +43,27 @@ __all__ = [
     "radix_sort_u32",
     "runs_layout_u32",
     "runs_owner_u32",
+    "sample_tokens",
+    "PagePool",
+    "pages_copy",
+    "pages_fork",
+    "pages_free",
+    "pages_compact",
     "check",
 ]
 
 _U32_DTYPES = (torch.int32, getattr(torch, "uint32", torch.int32))
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
+
+
 def _stream_handle(stream) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is not None:
+        return int(stream.cuda_stream)
+    if _raw_stream is None:
+        return int(torch.cuda.current_stream().cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _require_cuda(t: torch.Tensor, name: str, dtypes=_U32_DTYPES) -> None:
@@ -77,25 +90,29 @@ class Workspace:
 
     def __init__(self, nbytes: int, device: torch.device):
         self.buf = torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-
-    @property
-    def ptr(self) -> int:
-        return self.buf.data_ptr()
-
-    @property
-    def nbytes(self) -> int:
-        return self.buf.numel()
+        self.ptr = self.buf.data_ptr()
+        self.nbytes = self.buf.numel()
 
     @classmethod
     def get(cls, op: int, n: int, device: torch.device, stream_handle: int) -> "Workspace":
-        need = _native.lib().u32scan_workspace_bytes(op, n)
+        need = _workspace_bytes(op, n)
         key = (device.index, stream_handle)
         with cls._lock:
             ws = cls._cache.get(key)
             if ws is None or ws.nbytes < need:
                 ws = cls(max(need, 2 * ws.nbytes if ws else need), device)
+                current = torch.cuda.current_stream(device)
+                if stream_handle != current.cuda_stream:  # filled on the current stream, used on the caller's
+                    other = torch.cuda.ExternalStream(stream_handle, device)
+                    other.wait_stream(current)
+                    ws.buf.record_stream(other)
                 cls._cache[key] = ws
         return ws
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(op: int, n: int) -> int:
+    return _native.lib().u32scan_workspace_bytes(op, n)
 
 
 def _ws(op: int, n: int, device, stream_handle: int, workspace) -> Workspace:
@@ -576,6 +593,233 @@ def runs_owner_u32(ends: torch.Tensor, owner: torch.Tensor | None = None, capaci
     sh = _stream_handle(stream)
     _native.check(_native.lib().runs_owner_u32(ends.data_ptr(), n, owner.data_ptr(), cap, sh), "runs_owner_u32")
     return owner
+
+
+_LOGIT_TYPES = {torch.float32: _native.F32, torch.float16: _native.F16, torch.bfloat16: _native.BF16}
+
+
+def _arg(t, name: str, dtype, numel: int, dev: int) -> int:
+    """The device pointer of a contiguous tensor of at least numel elements
+    on CUDA device `dev`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} must hold at least {numel} elements")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _optional(t, name: str, dtype, numel: int, dev: int) -> int | None:
+    return None if t is None else _arg(t, name, dtype, numel, dev)
+
+
+def sample_tokens(logits: torch.Tensor, random: torch.Tensor, *, temperature: torch.Tensor | None = None,
+                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                  min_p: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                  probs: torch.Tensor | None = None, stream=None):
+    """The next token of every row of logits [rows, vocab] (float32, float16
+    or bfloat16; rows may be strided, elements of a row are adjacent), drawn
+    with the u32 words random [rows]. temperature, top_p, min_p (float32) and
+    top_k (int32) hold one value a row; None is temperature 1 and no filter.
+    Returns (tokens, probs): int32 tokens, -1 where every logit is -inf or
+    NaN, and the chosen tokens' probabilities after the filters. The result
+    is exact: integer weights, sums and draw, as include/u32scan.h states
+    them."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor (this library has no CPU path)")
+    kind = _LOGIT_TYPES.get(logits.dtype)
+    if kind is None:
+        raise TypeError(f"logits must have dtype in {tuple(_LOGIT_TYPES)}, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must have two dimensions, [rows, vocab]")
+    rows, vocab = logits.shape
+    row_stride, step = logits.stride()
+    if step != 1 and vocab > 1 and rows > 0:
+        raise ValueError("the elements of a row of logits must be adjacent")
+    dev = logits.get_device()
+    if tokens is None:
+        tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+    if probs is None:
+        probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+    f32, i32 = torch.float32, torch.int32
+    words = _arg(random, "random", i32 if random.dtype is i32 else _U32_DTYPES[1], rows, dev)
+    _native.check(_native.lib().sample_tokens(
+        logits.data_ptr(), kind, rows, vocab, row_stride, _optional(temperature, "temperature", f32, rows, dev),
+        _optional(top_k, "top_k", i32, rows, dev), _optional(top_p, "top_p", f32, rows, dev),
+        _optional(min_p, "min_p", f32, rows, dev), words, _arg(tokens, "tokens", i32, rows, dev),
+        _arg(probs, "probs", f32, rows, dev), _stream_handle(stream)), "sample_tokens")
+    return tokens, probs
+
+
+class PagePool:
+    """The planes of a paged cache, for the pages_* calls.
+
+    tensors: one CUDA tensor a plane, [pages, ...] (say, each layer's keys
+    and each layer's values), all of one shape, dtype and strides, with a
+    page's elements adjacent; or, with planes_first, one tensor [planes,
+    pages, ...]. The pool keeps the tensors alive and their addresses in
+    device memory; make it once per cache.
+    """
+
+    def __init__(self, tensors, *, planes_first: bool = False):
+        if isinstance(tensors, torch.Tensor):
+            if planes_first and tensors.dim() < 2:
+                raise ValueError("a tensor with its planes first must have at least two dimensions")
+            tensors = list(tensors.unbind(0)) if planes_first else [tensors]
+        tensors = list(tensors)
+        if not tensors:
+            raise ValueError("a pool needs at least one plane")
+        first = tensors[0]
+        for t in tensors:
+            if not isinstance(t, torch.Tensor):
+                raise TypeError("a pool's planes must be torch tensors")
+            if t.device.type != "cuda":
+                raise ValueError("a pool's planes must be CUDA tensors (this library has no CPU path)")
+            if (t.dim() < 1 or t.shape != first.shape or t.stride() != first.stride() or t.dtype != first.dtype
+                    or t.device != first.device):
+                raise ValueError("a pool's planes must agree in shape, strides, dtype and device")
+        item = first.element_size()
+        self.pages = first.shape[0]
+        self.page_bytes = item
+        for d in first.shape[1:]:
+            self.page_bytes *= d
+        if self.pages > 0 and not first[0].is_contiguous():
+            raise ValueError("a page's elements must be adjacent")
+        self.page_stride = first.stride(0) * item if self.pages > 1 else self.page_bytes
+        if self.page_stride < self.page_bytes:
+            raise ValueError("a pool's pages must not overlap")
+        self.tensors = tensors
+        self.device = first.device
+        self._planes = torch.tensor([t.data_ptr() for t in tensors], dtype=torch.int64, device=self.device)
+        torch.cuda.current_stream(self.device).synchronize()  # the addresses may be read on any stream
+        self.struct = _native.PagePoolStruct(self._planes.data_ptr(), len(tensors), self.pages, self.page_bytes,
+                                             self.page_stride)
+
+
+def _pool_struct(pool, dev: int):
+    if not isinstance(pool, PagePool):
+        raise TypeError("pool must be a PagePool")
+    if pool.device.index != dev:
+        raise ValueError(f"pool must be on cuda:{dev}")
+    return pool.struct
+
+
+def pages_copy(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, count: torch.Tensor | None = None, *,
+               stream=None) -> None:
+    """Copies page src[i] to page dst[i] in every plane of the pool (int32
+    tensors; pairs with a number outside the pool are skipped; no page may
+    be a destination twice, or both a destination and another pair's
+    source). count, a one-element int32 tensor, limits the pairs on the
+    device."""
+    struct, i32 = _pool_struct(pool, pool.device.index if isinstance(pool, PagePool) else -1), torch.int32
+    dev, n = pool.device.index, src.numel()
+    if dst.numel() != n:
+        raise ValueError("src and dst differ in length")
+    _native.check(_native.lib().pages_copy(struct, _arg(src, "src", i32, n, dev), _arg(dst, "dst", i32, n, dev), n,
+                                           _optional(count, "count", i32, 1, dev), _stream_handle(stream)),
+                  "pages_copy")
+
+
+def _cache_args(table, lens, refs, page_tokens):
+    """The checked leading arguments of the calls on a paged cache, and their
+    device."""
+    if not isinstance(table, torch.Tensor):
+        raise TypeError("table must be a torch.Tensor")
+    if not table.is_cuda:
+        raise ValueError("table must be a CUDA tensor (this library has no CPU path)")
+    if table.dtype is not torch.int32:
+        raise TypeError(f"table must have dtype torch.int32, got {table.dtype}")
+    if table.dim() != 2:
+        raise ValueError("table must have two dimensions, [rows, width]")
+    rows, width = table.shape
+    stride, step = table.stride()
+    if rows == 0:
+        stride = width
+    elif step != 1 and width > 1:
+        raise ValueError("the entries of a row of table must be adjacent")
+    elif rows == 1:
+        stride = width
+    elif stride < width:
+        raise ValueError("the rows of table must not overlap")
+    dev = table.get_device()
+    lens_ptr, refs_ptr = _arg(lens, "lens", torch.int32, rows, dev), _arg(refs, "refs", torch.int32, 0, dev)
+    if lens.numel() != rows:
+        raise ValueError("lens must hold one length for every row of table")
+    return (table.data_ptr(), stride, rows, width, lens_ptr, refs_ptr, refs.numel(), page_tokens), dev
+
+
+def _one_out(out, name: str, like: torch.Tensor, dev: int) -> tuple[torch.Tensor, int]:
+    if out is None:
+        out = torch.empty(1, dtype=torch.int32, device=like.device)
+    return out, _arg(out, name, torch.int32, 1, dev)
+
+
+def pages_fork(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_tokens: int, *,
+               parent: torch.Tensor | None = None, grow: torch.Tensor | None = None, pool: PagePool | None = None,
+               status: torch.Tensor | None = None, free_pages: torch.Tensor | None = None, stream=None,
+               workspace: Workspace | None = None):
+    """Forks rows and gives rows their next pages, in place. Empty rows s
+    with parent[s] >= 0 become copies of that row (full pages shared, a
+    partly filled last one copied in the pool); then every row grows by
+    grow[s] tokens. Fresh pages are the free ones (refs = 0) in ascending
+    order, dealt in row order. Returns (status, free_pages): per row the
+    fresh pages taken, -1 (refused) or -2 (out of pages; the row is left as
+    it was), and the number of free pages left."""
+    args, dev = _cache_args(table, lens, refs, page_tokens)
+    rows, i32 = args[2], torch.int32
+    if status is None:
+        status = torch.empty(rows, dtype=i32, device=table.device)
+    free_pages, free_ptr = _one_out(free_pages, "free_pages", table, dev)
+    sh = _stream_handle(stream)
+    ws = _ws(_native.OP_PAGES, args[6] + rows, table.device, sh, workspace)
+    _native.check(_native.lib().pages_fork(
+        *args, _optional(parent, "parent", i32, rows, dev), _optional(grow, "grow", i32, rows, dev),
+        None if pool is None else _pool_struct(pool, dev), _arg(status, "status", i32, rows, dev), free_ptr, ws.ptr,
+        ws.nbytes, sh), "pages_fork")
+    return status, free_pages
+
+
+def pages_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_tokens: int, release: torch.Tensor,
+               *, freed: torch.Tensor | None = None, stream=None, workspace: Workspace | None = None) -> torch.Tensor:
+    """Releases, in place, every row s with release[s] != 0 (int32): its
+    pages' refs fall by one, its entries become -1, its length 0. Returns the
+    number of pages that became free (one-element device tensor)."""
+    args, dev = _cache_args(table, lens, refs, page_tokens)
+    freed, freed_ptr = _one_out(freed, "freed", table, dev)
+    sh = _stream_handle(stream)
+    ws = _ws(_native.OP_PAGES, args[6] + args[2], table.device, sh, workspace)
+    _native.check(_native.lib().pages_free(*args, _arg(release, "release", torch.int32, args[2], dev), freed_ptr,
+                                           ws.ptr, ws.nbytes, sh), "pages_free")
+    return freed
+
+
+def pages_compact(pool: PagePool | None, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                  page_tokens: int, *, live: torch.Tensor | None = None, remap: torch.Tensor | None = None,
+                  stream=None, workspace: Workspace | None = None):
+    """Packs the live pages (refs != 0) into the first ones, in place: those
+    past the number L of live pages move, in order, into the free pages
+    below L; table and refs follow. Returns (live, remap): L, and each live
+    page's new number (-1 for free ones)."""
+    args, dev = _cache_args(table, lens, refs, page_tokens)
+    pages = args[6]
+    live, live_ptr = _one_out(live, "live", table, dev)
+    if remap is None:
+        remap = torch.empty(pages, dtype=torch.int32, device=table.device)
+    sh = _stream_handle(stream)
+    ws = _ws(_native.OP_PAGES, pages + args[2], table.device, sh, workspace)
+    _native.check(_native.lib().pages_compact(
+        None if pool is None else _pool_struct(pool, dev), *args, live_ptr,
+        _arg(remap, "remap", torch.int32, pages, dev), ws.ptr, ws.nbytes, sh), "pages_compact")
+    return live, remap
 
 
 def check(stream=None, workspace: Workspace | None = None, device=None) -> int:

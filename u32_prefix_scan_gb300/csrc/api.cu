@@ -48,6 +48,8 @@ extern "C" size_t u32scan_workspace_bytes(int op, size_t n) {
         return scan_host_workspace_bytes(n);
     case U32SCAN_OP_REDUCE:
         return reduce_workspace_bytes();
+    case U32SCAN_OP_PAGES:
+        return pages_workspace_bytes(n);
     default:
         return 0;
     }

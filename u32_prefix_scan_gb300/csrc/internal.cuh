@@ -475,6 +475,7 @@ size_t radix_workspace_bytes(unsigned long long n);
 size_t compact_values_workspace_bytes(unsigned long long n);
 size_t scan64_workspace_bytes(unsigned long long n);
 size_t reduce_workspace_bytes();
+size_t pages_workspace_bytes(unsigned long long n);
 
 // In-library launches of the add-scan: one chunk of a longer array after a
 // device carry-in (the host-buffer pipeline), and the inclusive scan with
