@@ -27,9 +27,10 @@
 //           512 thread maxima is a bound below which no kept token lies;
 //           the few logits at or above it are gathered into one block, which
 //           ranks them.
-//   top-p   a histogram of y (32 bins an octave) bounds each prefix sum from
-//           both sides; only the bins in which the sum may cross are
-//           gathered and sorted (or everything above, if that is little).
+//   top-p   a histogram of the weights by y (32 bins an octave) gives the bin
+//           in which the prefix sum crosses; that bin's logits are gathered
+//           and sorted (or all above it too, if they are few: then the
+//           gathering block makes the draw as well).
 //   else    (huge k, long ties, infinite logits) radix selection on the
 //           logits' bits, 8 a level, on counts or sums of weights.
 // A filter ends at a key `tau` and at how many of the logits equal to it stay
@@ -48,7 +49,8 @@ typedef unsigned long long u64;
 constexpr int kSThreads = 512;
 constexpr int kSWarps = kSThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kList = 2048;   // logits gathered into one block
+constexpr int kLocal = 1024;  // logits a block may put forward
+constexpr int kList = 2048;   // and all blocks of a row together
 constexpr int kRanked = 256;  // of them, ranked by counting rather than by sorting
 constexpr int kBins = 1024;   // histogram of y: 32 bins an octave, 31 octaves
 constexpr float kLog2e = 0x1.715476p+0f;
@@ -72,18 +74,31 @@ struct SampleArgs {
 // written again while a slow block still reads it.
 enum Slot { kSlotMax, kSlotFirst, kSlotSecond, kSlotThird, kSlotAbove, kSlotDraw, kSlots };
 
+// Sums of u32 by bin, exact in 64 bits at one native shared-memory atomic an
+// addition: the carries out of the low words are counted in the high ones.
+template <int N>
+struct SumBins {
+    uint32_t low[N], high[N];
+    __device__ __forceinline__ void add(uint32_t bin, uint32_t v) {
+        const uint32_t old = atomicAdd(&low[bin], v);
+        if (old + v < v) atomicAdd(&high[bin], 1u);
+    }
+    __device__ __forceinline__ void clear() {
+        for (int b = threadIdx.x; b < N; b += kSThreads) low[b] = high[b] = 0u;
+    }
+};
+
 struct alignas(16) SampleShared {
-    u64 list[kList];    // this block's gathered logits: (~key, index), ascending = in order
+    u64 list[kLocal];   // this block's: (~key, index), ascending = in order
     u64 gather[kList];  // the cluster's, in the block of rank 0
     union {
-        uint32_t bins[kBins];
-        u64 digits[2][256];
+        SumBins<kBins> bins;
+        SumBins<256> digits[2];
     };
     u64 slots[kSlots][kMaxCluster][2];
     u64 warp_a[kSWarps], warp_b[kSWarps], warp_c[kSWarps];
     u64 cast[4];
     uint32_t n_list;
-    uint32_t bin_lo, bin_hi, before_lo, through_hi;
 };
 
 // ---------------------------------------------------------------------------
@@ -275,6 +290,11 @@ __device__ __forceinline__ uint32_t at_rank(const void *p, uint32_t rank) {
 __device__ __forceinline__ void st_cluster(uint32_t addr, u64 a, u64 b) {
     asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(addr), "l"(a), "l"(b) : "memory");
 }
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
 __device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
     u64 v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
@@ -407,15 +427,16 @@ struct Cut {
 // The key at which the running total over keys in descending order, of counts
 // or of weights (MASS) of the keys from floor_key on, first reaches `target`
 // (1 <= target <= the whole total), and what is missing above it (>= 1).
-// `level` numbers the levels of a row's selections (their two buffers swap).
+// `level` numbers the levels of a row's selections (their two buffers swap:
+// a slow block may still read the last level's).
 template <bool MASS, typename T>
 __device__ __noinline__ void radix_select(SampleShared &sh, const Slice<T> &sl, const RowRule &rule,
                                           uint32_t floor_key, u64 target, int &level, uint32_t *tau, u64 *missing) {
     const int lane = threadIdx.x & 31;
     uint32_t prefix = 0, mask = 0;
     for (int shift = 24; shift >= 0; shift -= 8, ++level) {
-        u64 *hist = sh.digits[level & 1];
-        if (threadIdx.x < 256) hist[threadIdx.x] = 0;
+        SumBins<256> &hist = sh.digits[level & 1];
+        hist.clear();
         __syncthreads();
         sl.each(lane, [&](const uint4 &r, unsigned int) {
             float x[Vec<T>::N];
@@ -425,8 +446,8 @@ __device__ __noinline__ void radix_select(SampleShared &sh, const Slice<T> &sl, 
                 if (x[e] != x[e]) x[e] = -INFINITY;
                 const uint32_t k = key_of(x[e]);
                 if ((k & mask) != prefix || k < floor_key) continue;
-                const u64 w = MASS ? (u64)token_weight(x[e], rule) : 1ull;
-                if (w) atomicAdd(&hist[(k >> shift) & 255u], w);
+                const uint32_t w = MASS ? token_weight(x[e], rule) : 1u;
+                if (w) hist.add((k >> shift) & 255u, w);
             }
         });
         cluster_arrive();
@@ -434,7 +455,9 @@ __device__ __noinline__ void radix_select(SampleShared &sh, const Slice<T> &sl, 
         // the digits in descending order: thread t has digit 255 - t
         u64 mine = 0;
         if (threadIdx.x < 256)
-            for (uint32_t c = 0; c < cluster_size(); ++c) mine += ld_cluster_u64(at_rank(hist + 255 - threadIdx.x, c));
+            for (uint32_t c = 0; c < cluster_size(); ++c)
+                mine += (u64)ld_cluster(at_rank(&hist.low[255 - threadIdx.x], c)) +
+                        ((u64)ld_cluster(at_rank(&hist.high[255 - threadIdx.x], c)) << 32);
         const u64 before = block_before(mine, sh.warp_a);
         if (before < target && target <= before + mine) {
             sh.cast[0] = 255u - threadIdx.x;
@@ -578,14 +601,25 @@ __device__ __forceinline__ void collect(SampleShared &sh, const Slice<T> &sl, fl
         for (int e = 0; e < Vec<T>::N; ++e)
             if (x[e] >= thr && x[e] > -INFINITY && keep(x[e])) {
                 const uint32_t at = atomicAdd(&sh.n_list, 1u);
-                if (at < kList) sh.list[at] = (u64)~key_of(x[e]) << 32 | sl.index(v, e);
+                if (at < kLocal) sh.list[at] = (u64)~key_of(x[e]) << 32 | sl.index(v, e);
             }
     });
     __syncthreads();
 }
 
-// All blocks' lists, one after another in rank 0's gather (called there, after
-// an exchange of their lengths as `slot`'s first word).
+// The length of all blocks' lists, after an exchange of their lengths as
+// `slot`'s first word; over kList when one of them or all do not fit.
+__device__ __forceinline__ uint32_t gathered(const SampleShared &sh, Slot slot) {
+    uint32_t n = 0;
+    for (uint32_t c = 0; c < cluster_size(); ++c) {
+        const uint32_t one = (uint32_t)sh.slots[slot][c][0];
+        n += one <= kLocal ? one : kList + 1;
+    }
+    return n;
+}
+
+// All blocks' lists, one after another in rank 0's gather (called there, when
+// they fit).
 __device__ __forceinline__ void pull(SampleShared &sh, Slot slot) {
     uint32_t at = 0;
     for (uint32_t c = 0; c < cluster_size(); ++c) {
@@ -763,9 +797,9 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     const uint32_t warp_key = __reduce_max_sync(0xffffffffu, thread_key);
     if (lane == 0) sh.warp_a[warp] = warp_key;
     const uint32_t share = (k + blocks - 1) / blocks;
-    const bool bounded = k > 0 && (sl.n <= kList || share <= kSThreads / 2);
+    const bool bounded = k > 0 && (sl.n <= kLocal || share <= kSThreads / 2);
     uint32_t bound = 0;
-    if (bounded && sl.n > kList) {
+    if (bounded && sl.n > kLocal) {
         // the largest 16-bit prefix that at least `share` thread maxima reach
         for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
             if (__syncthreads_count(thread_key >= (bound | bit)) >= (int)share) bound |= bit;
@@ -822,8 +856,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     if (finite && bounded) {
         collect(sh, sl, bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY, [](float) { return true; });
         exchange(sh, kSlotFirst, sh.n_list, 0);
-        uint32_t n = 0;
-        for (uint32_t c = 0; c < blocks; ++c) n += (uint32_t)sh.slots[kSlotFirst][c][0];
+        const uint32_t n = gathered(sh, kSlotFirst);
         if (n <= kList) {
             if (rank == 0) pull(sh, kSlotFirst);
             cluster_arrive();
@@ -836,7 +869,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         // cut_y the row holds less than (1 - p) of the largest weight
         const float cut_y = cut_p ? fminf(31.0f, log2f((float)sl.n / (1.0f - p)) + 0.1f) : 0.0f;
         if (cut_p) {
-            for (int b = threadIdx.x; b < kBins; b += kSThreads) sh.bins[b] = 0;
+            sh.bins.clear();
             __syncthreads();
         }
         const u64 m2 = pack2(rule.m, rule.m), scale2 = pack2(rule.scale, rule.scale);
@@ -851,8 +884,9 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
                 weigh2(x[e], x[e + 1], m2, scale2, y, q);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    mass += q[i] >= rule.qmin ? q[i] : 0u;
-                    if (y[i] < cut_y) atomicAdd(&sh.bins[bin_of(y[i])], 1u);
+                    const uint32_t w = q[i] >= rule.qmin ? q[i] : 0u;
+                    mass += w;
+                    if (y[i] < cut_y && w) sh.bins.add(bin_of(y[i]), w);
                 }
             }
         });
@@ -870,72 +904,47 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         u64 total = 0;
         for (uint32_t c = 0; c < blocks; ++c) total += sh.slots[kSlotFirst][c][0];
         const u64 want = top_p_target(p, total);
-        // bounds of the running sum at every bin, two bins a thread
-        const uint32_t b0 = 2 * threadIdx.x;
-        uint32_t count[2] = {0, 0};
+        // the bin in which the running sum reaches `want`, two bins a thread
+        u64 bin_mass[2] = {0, 0};
         for (uint32_t c = 0; c < blocks; ++c) {
-            const u64 two = ld_cluster_u64(at_rank(sh.bins + b0, c));
-            count[0] += (uint32_t)two;
-            count[1] += (uint32_t)(two >> 32);
+            const u64 low = ld_cluster_u64(at_rank(&sh.bins.low[2 * threadIdx.x], c));
+            const u64 high = ld_cluster_u64(at_rank(&sh.bins.high[2 * threadIdx.x], c));
+            bin_mass[0] += (low & 0xffffffffull) | high << 32;
+            bin_mass[1] += low >> 32 | (high >> 32) << 32;
         }
-        u64 most[2], least[2];
+        // at most so many logits with a weight lie in a bin: none weighs less than its far end,
+        // less more than the recipe's error
+        u64 at_most[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float near = ((float)(b0 + i) - 0.5f) * (1.0f / 32.0f), far = near + 1.0f / 32.0f;
-            // weights of the bin's ends, widened by more than the recipe's error
-            const uint32_t hi = exp2_weight(fmaxf(near, 0.0f)), lo = exp2_weight(far);
-            const u64 up = (u64)hi + (hi >> 16) + 2;
-            const uint32_t slack = (lo >> 16) + 2;
-            uint32_t down = lo > slack ? lo - slack : 0u;
-            if (down < rule.qmin) down = 0u;  // min-p may have taken some
-            most[i] = count[i] * up;
-            least[i] = (u64)count[i] * down;
+            const uint32_t far = exp2_weight(((float)(2 * threadIdx.x + i) + 0.5f) * (1.0f / 32.0f));
+            const uint32_t slack = (far >> 16) + 2;
+            const uint32_t least = max(far > slack ? far - slack : 0u, max(rule.qmin, 1u));
+            at_most[i] = (u64)((float)bin_mass[i] / (float)least * 1.001f) + (bin_mass[i] ? 1u : 0u);
         }
-        if (threadIdx.x == 0) {
-            sh.bin_hi = kBins - 1;
-            sh.bin_lo = kBins - 1;
-            sh.before_lo = 0;
-        }
-        const u64 most_before = block_before(most[0] + most[1], sh.warp_a);
-        const u64 least_before = block_before(least[0] + least[1], sh.warp_b);
-        const uint32_t before = (uint32_t)block_before(count[0] + count[1], sh.warp_c);
-        if (threadIdx.x == kSThreads - 1) sh.through_hi = before + count[0] + count[1];
-        __syncthreads();
-        if (most_before < want && want <= most_before + most[0] + most[1]) {
-            const bool second = want > most_before + most[0];
-            sh.bin_lo = b0 + second;
-            sh.before_lo = before + (second ? count[0] : 0u);
-        }
-        if (least_before < want && want <= least_before + least[0] + least[1]) {
-            const bool second = want > least_before + least[0];
-            sh.bin_hi = b0 + second;
-            sh.through_hi = before + count[0] + (second ? count[1] : 0u);
+        const u64 before = block_before(bin_mass[0] + bin_mass[1], sh.warp_a);
+        const u64 count_before = block_before(at_most[0] + at_most[1], sh.warp_b);
+        if (before < want && want <= before + bin_mass[0] + bin_mass[1]) {
+            const bool second = want > before + bin_mass[0];
+            sh.cast[0] = 2 * threadIdx.x + second;
+            sh.cast[1] = before + (second ? bin_mass[0] : 0ull);
+            sh.cast[2] = count_before + at_most[0] + (second ? at_most[1] : 0ull);
         }
         __syncthreads();
-        const uint32_t lo = sh.bin_lo, hi = sh.bin_hi, n_hi = sh.through_hi, n_lo = sh.before_lo;
-        // every logit in a bin up to hi is at or above this one
-        const float thr = __fsub_rd(rule.m, __fdiv_ru(((float)hi + 1.0f) * (1.0f / 32.0f), rule.scale));
-        if (n_hi <= kList || n_hi - n_lo <= kList) {
-            const bool all = n_hi <= kList;
-            u64 above = 0;  // weights in the bins below lo
-            collect(sh, sl, thr, [&](float x) {
-                const float y = __fmul_rn(__fsub_rn(rule.m, x), rule.scale);
-                if (!(y < cut_y)) return false;
-                const uint32_t b = bin_of(y);
-                if (!all && b < lo) {
-                    above += token_weight(x, rule);
-                    return false;
-                }
-                return b <= hi;
-            });
-            if (!all) above = block_total(above, sh.warp_c);
-            exchange(sh, kSlotSecond, sh.n_list, above);
-            uint32_t n = 0;
-            above = 0;
-            for (uint32_t c = 0; c < blocks; ++c) {
-                n += (uint32_t)sh.slots[kSlotSecond][c][0];
-                above += sh.slots[kSlotSecond][c][1];
-            }
+        const uint32_t bin = (uint32_t)sh.cast[0];
+        const u64 above = sh.cast[1];
+        const bool all = sh.cast[2] <= kList;
+        // every logit in a bin up to this one is at or above
+        const float thr = __fsub_rd(rule.m, __fdiv_ru(((float)bin + 1.0f) * (1.0f / 32.0f), rule.scale));
+        collect(sh, sl, thr, [&](float x) {
+            const float y = __fmul_rn(__fsub_rn(rule.m, x), rule.scale);
+            if (!(y < cut_y) || token_weight(x, rule) == 0u) return false;
+            const uint32_t b = bin_of(y);
+            return all ? b <= bin : b == bin;
+        });
+        exchange(sh, kSlotSecond, sh.n_list, 0);
+        const uint32_t n = gathered(sh, kSlotSecond);
+        if (n <= kList) {
             if (rank == 0) pull(sh, kSlotSecond);
             if (all) {
                 cluster_arrive();
@@ -983,9 +992,6 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
             draw(sh, sl, rule, cut, q_tau, left, kept, tied, a, row);
             return;
         }
-        __syncthreads();
-        cluster_arrive();  // the bins' words hold digits next
-        cluster_wait();
     }
     sample_by_selection(sh, sl, rule, k, p, a, row);
 }
