@@ -23,18 +23,18 @@
 // One cluster of blocks takes a row: each block reads its slice once from
 // HBM and keeps it in shared memory (what does not fit is read again, from
 // L2), so the passes after the maximum touch no HBM. No row is sorted:
-//   top-k   the bound pass: the ceil(k / blocks)-th largest of each block's
-//           512 thread maxima is a bound below which no kept token lies;
-//           the few logits at or above it are gathered into one block, which
-//           ranks them.
+//   top-k   the ceil(k / blocks)-th largest of the maxima of groups of each
+//           block's threads is a bound below which no kept token lies; the
+//           few logits at or above it are gathered into one block, which
+//           makes the draw.
 //   top-p   a histogram of the weights by y (32 bins an octave) gives the bin
 //           in which the prefix sum crosses; that bin's logits are gathered
-//           and sorted (or all above it too, if they are few: then the
-//           gathering block makes the draw as well).
+//           (or all above it too, if they are few: then the gathering block
+//           makes the draw as well).
 //   else    (huge k, long ties, infinite logits) radix selection on the
 //           logits' bits, 8 a level, on counts or sums of weights.
-// A filter ends at a key `tau` and at how many of the logits equal to it stay
-// (those with the lowest indices).
+// A filter ends at an item, (~key, index) as one u64: what stands at or
+// before it in order stays, so ties need no count of their own.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -51,7 +51,7 @@ constexpr int kSWarps = kSThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kLocal = 1024;  // logits a block may put forward
 constexpr int kList = 2048;   // and all blocks of a row together
-constexpr int kRanked = 256;  // of them, ranked by counting rather than by sorting
+constexpr int kRanked = 256;  // up to here items are ranked by counting, past it selected by histograms
 constexpr int kBins = 1024;   // histogram of y: 32 bins an octave, 31 octaves
 constexpr float kLog2e = 0x1.715476p+0f;
 constexpr uint32_t kKeyOfMinusInf = 0x007fffffu;
@@ -72,7 +72,8 @@ struct SampleArgs {
 
 // Exchanges between a cluster's blocks: one slot each, so that none is
 // written again while a slow block still reads it.
-enum Slot { kSlotMax, kSlotFirst, kSlotSecond, kSlotThird, kSlotAbove, kSlotDraw, kSlots };
+enum Slot { kSlotMax, kSlotFirst, kSlotSecond, kSlotThird, kSlotSum, kSlotTies, kSlotTieAt, kSlotTies2, kSlotTieAt2, kSlotDraw,
+            kSlots };
 
 // Sums of u32 by bin, exact in 64 bits at one native shared-memory atomic an
 // addition: the carries out of the low words are counted in the high ones.
@@ -94,6 +95,11 @@ struct alignas(16) SampleShared {
     union {
         SumBins<kBins> bins;
         SumBins<256> digits[2];
+        struct {
+            SumBins<kSThreads> sums;
+            uint32_t counts[kSThreads];
+        } picks;
+        uint32_t group_max[kSThreads];
     };
     u64 slots[kSlots][kMaxCluster][2];
     u64 warp_a[kSWarps], warp_b[kSWarps], warp_c[kSWarps];
@@ -177,10 +183,16 @@ struct Vec<__half> {
 // floor(2^31 * 2^-y) for 0 <= y < 100 (0 from y = 31 on): 2^-n exactly, times
 // 2^-f on [-1/2, 1/2] by a degree-5 polynomial with constant term 1 (a minimax
 // fit in relative error, 1.9e-7 in f32). Every operation is rounded alone (no
-// contraction).
-constexpr float kC1 = -0x1.62e42ap-1f, kC2 = 0x1.ebf9bcp-3f, kC3 = -0x1.c6b752p-5f, kC4 = 0x1.3cea88p-7f,
-                kC5 = -0x1.5bba14p-10f;
+// contraction); the coefficients carry the factor 2^31, which changes no
+// rounding, and 2^-n is taken off the exponent's bits.
+constexpr float kC0 = 0x1p31f, kC1 = -0x1.62e42ap30f, kC2 = 0x1.ebf9bcp28f, kC3 = -0x1.c6b752p26f,
+                kC4 = 0x1.3cea88p24f, kC5 = -0x1.5bba14p21f;
 constexpr float kRound = 0x1.8p23f;  // adding and taking it away rounds to an integer, ties to even
+
+// p * 2^-n, n in the low bits of t = n + kRound (whose bits << 23 are n << 23).
+__device__ __forceinline__ uint32_t scaled_floor(float p, float t) {
+    return __float2uint_rz(__uint_as_float(__float_as_uint(p) - (__float_as_uint(t) << 23)));
+}
 
 __device__ __forceinline__ uint32_t exp2_weight(float y) {
     const float t = __fadd_rn(y, kRound);
@@ -189,9 +201,8 @@ __device__ __forceinline__ uint32_t exp2_weight(float y) {
     p = __fadd_rn(__fmul_rn(p, f), kC3);
     p = __fadd_rn(__fmul_rn(p, f), kC2);
     p = __fadd_rn(__fmul_rn(p, f), kC1);
-    p = __fadd_rn(__fmul_rn(p, f), 1.0f);
-    // times 2^(31 - n), exact; n is in t's low bits, and 0x4b400000 << 23 = 0
-    return __float2uint_rz(__fmul_rn(p, __uint_as_float((158u << 23) - (__float_as_uint(t) << 23))));
+    p = __fadd_rn(__fmul_rn(p, f), kC0);
+    return scaled_floor(p, t);
 }
 
 struct RowRule {
@@ -251,14 +262,12 @@ __device__ __forceinline__ void weigh2(float x0, float x1, u64 m2, u64 scale2, f
     p2 = add2(mul2(p2, f2), pack2(kC3, kC3));
     p2 = add2(mul2(p2, f2), pack2(kC2, kC2));
     p2 = add2(mul2(p2, f2), pack2(kC1, kC1));
-    p2 = add2(mul2(p2, f2), pack2(1.0f, 1.0f));
-    float t[2], w[2];
+    p2 = add2(mul2(p2, f2), pack2(kC0, kC0));
+    float t[2], p[2];
     unpack2(t2, t[0], t[1]);
-    unpack2(mul2(p2, pack2(__uint_as_float((158u << 23) - (__float_as_uint(t[0]) << 23)),
-                           __uint_as_float((158u << 23) - (__float_as_uint(t[1]) << 23)))),
-            w[0], w[1]);
-    q[0] = __float2uint_rz(w[0]);
-    q[1] = __float2uint_rz(w[1]);
+    unpack2(p2, p[0], p[1]);
+    q[0] = scaled_floor(p[0], t[0]);
+    q[1] = scaled_floor(p[1], t[1]);
 }
 
 // The histogram's bin of a distance: the nearest of the bins' centres, so
@@ -346,20 +355,79 @@ __device__ __forceinline__ u64 block_before(u64 v, u64 *s_warp) {
     return base + inc - v;
 }
 
-// Ascending sort of the first `size` (a power of two) words by the block.
-__device__ __forceinline__ void block_sort(u64 *a, unsigned int size) {
-    for (unsigned int k = 2; k <= size; k <<= 1)
-        for (unsigned int j = k >> 1; j > 0; j >>= 1) {
-            for (unsigned int c = threadIdx.x; c < size / 2; c += kSThreads) {
-                const unsigned int i = 2 * c - (c & (j - 1)), o = i + j;  // c-th pair at distance j
-                const u64 x = a[i], y = a[o];
-                if ((x > y) == ((i & k) == 0)) {
-                    a[i] = y;
-                    a[o] = x;
-                }
-            }
-            __syncthreads();
+__device__ __forceinline__ u64 warp_min(u64 v) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, d));
+    return v;
+}
+
+constexpr int kOwn = kList / kSThreads;  // gathered items a thread holds
+
+// Over the block's items with a weight (those at distinct places): the place
+// at which the running sum of weights, in ascending order of place, reaches
+// `target` (1 <= target <= the sum of all), and the sum before it. Histograms
+// of the places still in question, 512 bins a turn, the next turn within the
+// bin that holds the crossing, until that is one item.
+__device__ __noinline__ u64 block_select(SampleShared &sh, const u64 (&place)[kOwn], const uint32_t (&weight)[kOwn],
+                                         u64 target, u64 *before_it) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 lo = ~0ull, hi = ~0ull;  // hi: complemented, so that both are minima
+#pragma unroll
+    for (int c = 0; c < kOwn; ++c)
+        if (weight[c]) {
+            lo = min(lo, place[c]);
+            hi = min(hi, ~place[c]);
         }
+    lo = warp_min(lo);
+    hi = warp_min(hi);
+    __syncthreads();
+    if (lane == 0) {
+        sh.warp_a[warp] = lo;
+        sh.warp_b[warp] = hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSWarps; ++w) {
+        lo = min(lo, sh.warp_a[w]);
+        hi = min(hi, sh.warp_b[w]);
+    }
+    int shift = 64 - __clzll((~hi - lo) | 511ull) - 9;
+    u64 base = 0;
+    while (true) {
+        sh.picks.sums.clear();
+        sh.picks.counts[threadIdx.x] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < kOwn; ++c) {
+            const u64 bin = (place[c] - lo) >> shift;  // places below lo wrap to large bins
+            if (weight[c] && bin < kSThreads) {
+                sh.picks.sums.add((uint32_t)bin, weight[c]);
+                atomicAdd(&sh.picks.counts[bin], 1u);
+            }
+        }
+        __syncthreads();
+        const u64 mine = (u64)sh.picks.sums.high[threadIdx.x] << 32 | sh.picks.sums.low[threadIdx.x];
+        const u64 before = base + block_before(mine, sh.warp_a);
+        if (before < target && target <= before + mine) {
+            sh.cast[0] = threadIdx.x;
+            sh.cast[1] = before;
+            sh.cast[2] = sh.picks.counts[threadIdx.x];
+        }
+        __syncthreads();
+        const u64 bin = sh.cast[0], left = sh.cast[2];
+        base = sh.cast[1];
+        if (left == 1 || shift == 0) {
+#pragma unroll
+            for (int c = 0; c < kOwn; ++c)
+                if (weight[c] && (place[c] - lo) >> shift == bin) sh.cast[3] = place[c];
+            __syncthreads();
+            *before_it = base;
+            return sh.cast[3];
+        }
+        lo += bin << shift;
+        shift = shift > 9 ? shift - 9 : 0;
+        __syncthreads();  // cast is written again
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -415,37 +483,237 @@ struct Slice {
     }
 
     __device__ __forceinline__ uint32_t index(unsigned int v, int e) const { return v * V::N + e - pad; }
+
+    // The share of the warp `by` warps on in this block.
+    __device__ __forceinline__ Slice of_warp(int by) const {
+        Slice s = *this;
+        s.v0 += by * (int)per_warp;
+        s.stage += by * 32 * (int)staged_iters;
+        return s;
+    }
 };
 
-// Where a filter ends: keys above tau stay, and the first `ties` (by index)
-// of those equal to it.
-struct Cut {
-    uint32_t tau;
-    u64 ties;
-};
+// A logit's place in the filters' order, ascending.
+__device__ __forceinline__ u64 item_of(uint32_t key, uint32_t index) { return (u64)~key << 32 | index; }
+__device__ __forceinline__ uint32_t item_weight(u64 item, const RowRule &rule) {
+    return token_weight(key_logit(~(uint32_t)(item >> 32)), rule);
+}
+constexpr u64 kKeepAll = ~0ull;
 
-// The key at which the running total over keys in descending order, of counts
-// or of weights (MASS) of the keys from floor_key on, first reaches `target`
+__device__ __forceinline__ void write_token(const SampleArgs &a, u64 row, uint32_t index, u64 q, u64 total) {
+    a.tokens[row] = (int32_t)index;
+    if (a.probs) a.probs[row] = (float)((double)q / (double)total);
+}
+
+__device__ __forceinline__ u64 draw_of(uint32_t word, u64 total) { return __umul64hi((u64)word << 32, total); }
+
+__device__ __forceinline__ u64 top_p_target(float p, u64 total) {
+    return (u64)ceil(__dmul_rn((double)p, (double)total));
+}
+
+// The sum of what the blocks put into a slot's first word.
+__device__ __forceinline__ u64 slot_total(const SampleShared &sh, Slot slot) {
+    u64 t = 0;
+    for (uint32_t c = 0; c < cluster_size(); ++c) t += sh.slots[slot][c][0];
+    return t;
+}
+
+// The draw among the items up to `last`, in index order; mass: what this
+// warp's vectors keep. The block that holds the draw walks the one warp's
+// share that does, a turn of 32 vectors a warp.
+template <typename T>
+__device__ __forceinline__ void draw(SampleShared &sh, const Slice<T> &own, const RowRule &rule, u64 last, u64 total,
+                                     u64 mass, const SampleArgs &a, u64 row) {
+    constexpr int N = Vec<T>::N;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const u64 r = draw_of(a.random[row], total);
+    __syncthreads();
+    if (lane == 0) sh.warp_a[warp] = mass;
+    __syncthreads();
+    u64 block_mass = 0;
+#pragma unroll
+    for (int w = 0; w < kSWarps; ++w) block_mass += sh.warp_a[w];
+    exchange(sh, kSlotDraw, block_mass, 0);
+    u64 before = 0;
+    for (uint32_t c = 0; c < cluster_rank(); ++c) before += sh.slots[kSlotDraw][c][0];
+    if (r < before || r - before >= block_mass) return;
+    int w = 0;
+    while (r - before >= sh.warp_a[w]) before += sh.warp_a[w++];
+    const Slice<T> sl = own.of_warp(w - warp);
+    for (unsigned int j0 = 0, it0 = 0; j0 < sl.per_warp; j0 += 32 * kSWarps, it0 += kSWarps) {
+        const unsigned int it = it0 + warp, j = 32 * it + lane;
+        float x[N];
+        uint32_t q[N];
+        u64 sum = 0;
+        const bool in = j < sl.per_warp && sl.v0 + j < sl.nv;
+        if (in) Vec<T>::unpack(it < sl.staged_iters ? sl.stage[32 * it] : sl.load(sl.v0 + j), x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            q[e] = 0;
+            if (in && x[e] > -INFINITY && item_of(key_of(x[e]), sl.index(sl.v0 + j, e)) <= last)
+                q[e] = token_weight(x[e], rule);
+            sum += q[e];
+        }
+        u64 inc = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const u64 o = __shfl_up_sync(0xffffffffu, inc, d);
+            if (lane >= d) inc += o;
+        }
+        __syncthreads();
+        if (lane == 31) sh.warp_b[warp] = inc;
+        __syncthreads();
+        u64 turn = before, at = before;
+#pragma unroll
+        for (int o = 0; o < kSWarps; ++o) {
+            if (o == warp) at = turn;
+            turn += sh.warp_b[o];
+        }
+        at += inc - sum;
+        if (at <= r && r - at < sum) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                if (at <= r && r - at < q[e]) write_token(a, row, sl.index(sl.v0 + j, e), q[e], total);
+                at += q[e];
+            }
+        }
+        if (r < turn) return;
+        before = turn;
+    }
+}
+
+// Puts an item into this block's list.
+__device__ __forceinline__ void put(SampleShared &sh, u64 item) {
+    const uint32_t at = atomicAdd(&sh.n_list, 1u);
+    if (at < kLocal) sh.list[at] = item;
+}
+
+// The length of all blocks' lists, after an exchange of their lengths as
+// `slot`'s first word; over kList when one of them or all do not fit.
+__device__ __forceinline__ uint32_t gathered(const SampleShared &sh, Slot slot) {
+    uint32_t n = 0;
+    for (uint32_t c = 0; c < cluster_size(); ++c) {
+        const uint32_t one = (uint32_t)sh.slots[slot][c][0];
+        n += one <= kLocal ? one : kList + 1;
+    }
+    return n;
+}
+
+// All blocks' n items, one list after another, in rank 0's gather (called
+// there, when they fit): every thread finds its items' blocks by itself, so
+// that all of them are on their way at once.
+__device__ __forceinline__ void pull(SampleShared &sh, Slot slot, uint32_t n) {
+    for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
+        uint32_t c = 0, at = i;
+        while (at >= (uint32_t)sh.slots[slot][c][0]) at -= (uint32_t)sh.slots[slot][c++][0];
+        sh.gather[i] = ld_cluster_u64(at_rank(sh.list + at, c));
+    }
+    __syncthreads();
+}
+
+// The token among the n gathered items, which hold all that the filters keep:
+// the first k of them in order, and of those the top-p prefix (0 < p < 1),
+// measured against `total` if that is not 0, else against their own sum.
+__device__ __noinline__ void finish_list(SampleShared &sh, uint32_t n, uint32_t k, float p, u64 total,
+                                         const RowRule &rule, const SampleArgs &a, u64 row) {
+    const bool cut_p = p > 0.0f && p < 1.0f;
+    const uint32_t word = a.random[row];
+    if (n <= kRanked) {
+        // `team` threads an item count what stands before it
+        uint32_t team = 2;
+        while (team < 16 && 2 * team * n <= kSThreads) team *= 2;
+        const uint32_t i = threadIdx.x / team, part = threadIdx.x % team;
+        u64 *weight = sh.list;  // pulled: free
+        const u64 item = i < n ? sh.gather[i] : ~0ull;
+        const u64 q = i < n ? item_weight(item, rule) : 0u;
+        if (part == 0) weight[i] = q;
+        __syncthreads();
+        uint32_t rank = 0;
+        u64 before = 0;
+#pragma unroll 4
+        for (uint32_t j = part; j < n; j += team) {
+            const bool first = sh.gather[j] < item;
+            rank += first;
+            before += first ? weight[j] : 0ull;
+        }
+        for (uint32_t d = 1; d < team; d *= 2) {
+            rank += __shfl_xor_sync(0xffffffffu, rank, d);
+            before += __shfl_xor_sync(0xffffffffu, before, d);
+        }
+        u64 kept = i < n && rank < k ? q : 0ull;
+        if (total == 0) total = block_total(part == 0 ? kept : 0ull, sh.warp_a);
+        if (cut_p) {
+            if (before >= top_p_target(p, total)) kept = 0;
+            total = block_total(part == 0 ? kept : 0ull, sh.warp_b);
+        }
+        __syncthreads();
+        if (part == 0) weight[i] = kept;
+        __syncthreads();
+        u64 at = 0;
+#pragma unroll 4
+        for (uint32_t j = part; j < n; j += team) at += (uint32_t)sh.gather[j] < (uint32_t)item ? weight[j] : 0ull;
+        for (uint32_t d = 1; d < team; d *= 2) at += __shfl_xor_sync(0xffffffffu, at, d);
+        const u64 r = draw_of(word, total);
+        if (part == 0 && at <= r && r < at + kept) write_token(a, row, (uint32_t)item, kept, total);
+        return;
+    }
+    u64 item[kOwn], before;
+    uint32_t q[kOwn], one[kOwn];
+#pragma unroll
+    for (int c = 0; c < kOwn; ++c) {
+        const uint32_t i = threadIdx.x + c * kSThreads;
+        one[c] = i < n;
+        item[c] = i < n ? sh.gather[i] : ~0ull;
+        q[c] = i < n ? item_weight(item[c], rule) : 0u;
+    }
+    if (k < n) {
+        const u64 last = block_select(sh, item, one, k, &before);
+#pragma unroll
+        for (int c = 0; c < kOwn; ++c)
+            if (item[c] > last) q[c] = 0;
+    }
+    if (total == 0) {
+        u64 sum = 0;
+#pragma unroll
+        for (int c = 0; c < kOwn; ++c) sum += q[c];
+        total = block_total(sum, sh.warp_a);
+    }
+    if (cut_p) {
+        const u64 last = block_select(sh, item, q, top_p_target(p, total), &before);
+#pragma unroll
+        for (int c = 0; c < kOwn; ++c)
+            if (item[c] > last) q[c] = 0;
+        total = before + item_weight(last, rule);
+    }
+#pragma unroll
+    for (int c = 0; c < kOwn; ++c) item[c] &= 0xffffffffull;  // the index: the draw's order
+    const u64 index = block_select(sh, item, q, draw_of(word, total) + 1, &before);
+#pragma unroll
+    for (int c = 0; c < kOwn; ++c)
+        if (q[c] && item[c] == index) write_token(a, row, (uint32_t)index, q[c], total);
+}
+
+// The key at which the running total over the items up to `last`, keys in
+// descending order, of counts or of weights (MASS), first reaches `target`
 // (1 <= target <= the whole total), and what is missing above it (>= 1).
 // `level` numbers the levels of a row's selections (their two buffers swap:
 // a slow block may still read the last level's).
 template <bool MASS, typename T>
-__device__ __noinline__ void radix_select(SampleShared &sh, const Slice<T> &sl, const RowRule &rule,
-                                          uint32_t floor_key, u64 target, int &level, uint32_t *tau, u64 *missing) {
-    const int lane = threadIdx.x & 31;
+__device__ __noinline__ void radix_select(SampleShared &sh, const Slice<T> &sl, const RowRule &rule, u64 last,
+                                          u64 target, int &level, uint32_t *tau, u64 *missing) {
     uint32_t prefix = 0, mask = 0;
     for (int shift = 24; shift >= 0; shift -= 8, ++level) {
         SumBins<256> &hist = sh.digits[level & 1];
         hist.clear();
         __syncthreads();
-        sl.each(lane, [&](const uint4 &r, unsigned int) {
+        sl.each(threadIdx.x & 31, [&](const uint4 &r, unsigned int v) {
             float x[Vec<T>::N];
             Vec<T>::unpack(r, x);
-#pragma unroll
+#pragma unroll 1
             for (int e = 0; e < Vec<T>::N; ++e) {
                 if (x[e] != x[e]) x[e] = -INFINITY;
                 const uint32_t k = key_of(x[e]);
-                if ((k & mask) != prefix || k < floor_key) continue;
+                if ((k & mask) != prefix || item_of(k, sl.index(v, e)) > last) continue;
                 const uint32_t w = MASS ? token_weight(x[e], rule) : 1u;
                 if (w) hist.add((k >> shift) & 255u, w);
             }
@@ -473,259 +741,75 @@ __device__ __noinline__ void radix_select(SampleShared &sh, const Slice<T> &sl, 
     *missing = target;
 }
 
-__device__ __forceinline__ void write_token(const SampleArgs &a, u64 row, uint32_t index, u64 q, u64 total) {
-    a.tokens[row] = (int32_t)index;
-    if (a.probs) a.probs[row] = (float)((double)q / (double)total);
-}
-
-__device__ __forceinline__ u64 draw_of(uint32_t word, u64 total) { return __umul64hi((u64)word << 32, total); }
-
-__device__ __forceinline__ u64 top_p_target(float p, u64 total) {
-    return (u64)ceil(__dmul_rn((double)p, (double)total));
-}
-
-// The draw among what `cut` leaves, in index order. mass and ties: what this
-// warp's vectors hold above tau and at it.
+// The `nth` logit (from 1, by index) with key tau, as an item; -inf entries
+// past the row's ends do not count.
 template <typename T>
-__device__ __noinline__ void draw(SampleShared &sh, const Slice<T> &sl, const RowRule &rule, const Cut &cut,
-                                  u64 q_tau, u64 total, u64 mass, u64 ties, const SampleArgs &a, u64 row) {
+__device__ __noinline__ u64 nth_tie(SampleShared &sh, const Slice<T> &sl, uint32_t tau, u64 nth, Slot ties_slot,
+                                    Slot at_slot) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const u64 r = draw_of(a.random[row], total);
-    __syncthreads();
-    if (lane == 0) {
-        sh.warp_a[warp] = mass;
-        sh.warp_b[warp] = ties;
-    }
-    __syncthreads();
-    u64 block_mass = 0, block_ties = 0;
+    auto tied = [&](const uint4 &r, unsigned int v) {  // by element
+        float x[Vec<T>::N];
+        Vec<T>::unpack(r, x);
+        unsigned int t = 0;
 #pragma unroll
+        for (int e = 0; e < Vec<T>::N; ++e) {
+            if (x[e] != x[e]) x[e] = -INFINITY;
+            if (key_of(x[e]) == tau && sl.index(v, e) < sl.n) t |= 1u << e;
+        }
+        return t;
+    };
+    u64 mine = 0;
+    sl.each(lane, [&](const uint4 &r, unsigned int v) { mine += __popc(tied(r, v)); });
+    mine = warp_total(mine);
+    __syncthreads();
+    if (lane == 0) sh.warp_a[warp] = mine;
+    if (threadIdx.x == 0) sh.cast[0] = ~0ull;
+    __syncthreads();
+    u64 before = 0, block_ties = 0;
     for (int w = 0; w < kSWarps; ++w) {
-        block_mass += sh.warp_a[w];
-        block_ties += sh.warp_b[w];
+        before += w < warp ? sh.warp_a[w] : 0ull;
+        block_ties += sh.warp_a[w];
     }
-    exchange(sh, kSlotDraw, block_mass, block_ties);
-    u64 before = 0, tie_left = cut.ties;
-    for (uint32_t c = 0; c < cluster_rank(); ++c) {
-        const u64 t = min(tie_left, sh.slots[kSlotDraw][c][1]);
-        before += sh.slots[kSlotDraw][c][0] + t * q_tau;
-        tie_left -= t;
-    }
-    for (int w = 0; w < warp; ++w) {
-        const u64 t = min(tie_left, sh.warp_b[w]);
-        before += sh.warp_a[w] + t * q_tau;
-        tie_left -= t;
-    }
-    if (!(before <= r && r - before < mass + min(tie_left, ties) * q_tau)) return;
-    // this warp's: 32 vectors a turn
-    for (unsigned int j0 = 0, it = 0; j0 < sl.per_warp && sl.v0 + j0 < sl.nv; j0 += 32, ++it) {
-        const unsigned int j = j0 + lane;
-        float x[Vec<T>::N];
-        const bool in = j < sl.per_warp && sl.v0 + j < sl.nv;
-        if (in) Vec<T>::unpack(it < sl.staged_iters ? sl.stage[32 * it] : sl.load(sl.v0 + j), x);
-        unsigned int tied = 0;  // by element
-        u64 sum = 0;
+    exchange(sh, ties_slot, block_ties, 0);
+    for (uint32_t c = 0; c < cluster_rank(); ++c) before += sh.slots[ties_slot][c][0];
+    if (before < nth && nth <= before + mine)  // this warp's
+        for (unsigned int j0 = 0, it = 0; j0 < sl.per_warp; j0 += 32, ++it) {
+            const unsigned int j = j0 + lane;
+            unsigned int t = 0;
+            if (j < sl.per_warp && sl.v0 + j < sl.nv)
+                t = tied(it < sl.staged_iters ? sl.stage[32 * it] : sl.load(sl.v0 + j), sl.v0 + j);
+            u64 inc = __popc(t);
 #pragma unroll
-        for (int e = 0; e < Vec<T>::N; ++e) {
-            if (!in || x[e] != x[e]) x[e] = -INFINITY;
-            const uint32_t k = key_of(x[e]);
-            if (k > cut.tau) sum += token_weight(x[e], rule);
-            if (k == cut.tau) tied |= 1u << e;
-        }
-        u64 t_inc = __popc(tied);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const u64 o = __shfl_up_sync(0xffffffffu, t_inc, d);
-            if (lane >= d) t_inc += o;
-        }
-        u64 my_ties = t_inc - __popc(tied);  // before this lane's
-        my_ties = my_ties < tie_left ? tie_left - my_ties : 0ull;
-        sum += min(my_ties, (u64)__popc(tied)) * q_tau;
-        u64 inc = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const u64 o = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += o;
-        }
-        const unsigned int hit = __ballot_sync(0xffffffffu, before + inc > r);
-        if (hit) {
-            if (lane != __ffs(hit) - 1) return;
-            u64 at = before + inc - sum;
-#pragma unroll
-            for (int e = 0; e < Vec<T>::N; ++e) {
-                u64 q = 0;
-                if (key_of(x[e]) > cut.tau) q = token_weight(x[e], rule);
-                else if ((tied >> e & 1u) && my_ties > 0) {
-                    q = q_tau;
-                    --my_ties;
-                }
-                if (at <= r && r < at + q) write_token(a, row, sl.index(sl.v0 + j, e), q, total);
-                at += q;
+            for (int d = 1; d < 32; d <<= 1) {
+                const u64 o = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += o;
             }
-            return;
+            const u64 at = before + inc - __popc(t);
+            if (at < nth && nth <= before + inc) {
+                for (u64 skip = nth - at - 1; skip > 0; --skip) t &= t - 1;
+                sh.cast[0] = item_of(tau, sl.index(sl.v0 + j, __ffs(t) - 1));
+            }
+            before += __shfl_sync(0xffffffffu, inc, 31);
         }
-        before += __shfl_sync(0xffffffffu, inc, 31);
-        const u64 used = __shfl_sync(0xffffffffu, t_inc, 31);
-        tie_left -= min(tie_left, used);
-    }
+    __syncthreads();
+    exchange(sh, at_slot, sh.cast[0], 0);
+    u64 item = ~0ull;
+    for (uint32_t c = 0; c < cluster_size(); ++c) item = min(item, sh.slots[at_slot][c][0]);
+    return item;
 }
 
-// What the vectors of this warp hold above the cut's key, and at it.
+// What this warp keeps of the items up to `last`.
 template <typename T>
-__device__ __forceinline__ void cut_pass(const Slice<T> &sl, const RowRule &rule, const Cut &cut, u64 *mass,
-                                         u64 *ties) {
-    const float thr = cut.tau ? key_logit(cut.tau) : -INFINITY;
+__device__ __forceinline__ u64 kept_mass(const Slice<T> &sl, const RowRule &rule, u64 last) {
     u64 m = 0;
-    unsigned int t = 0;
-    sl.each(threadIdx.x & 31, [&](const uint4 &r, unsigned int) {
-        if (!(Vec<T>::max(r) >= thr)) return;
-        float x[Vec<T>::N];
-        Vec<T>::unpack(r, x);
-#pragma unroll
-        for (int e = 0; e < Vec<T>::N; ++e) {
-            if (x[e] > thr) m += token_weight(x[e], rule);
-            t += x[e] == thr;
-        }
-    });
-    *mass = warp_total(m);
-    *ties = __reduce_add_sync(0xffffffffu, t);
-}
-
-// Gathers the logits that keep(x) names into this block's list.
-template <typename T, typename Keep>
-__device__ __forceinline__ void collect(SampleShared &sh, const Slice<T> &sl, float thr, Keep keep) {
     sl.each(threadIdx.x & 31, [&](const uint4 &r, unsigned int v) {
-        if (!(Vec<T>::max(r) >= thr)) return;
         float x[Vec<T>::N];
         Vec<T>::unpack(r, x);
-#pragma unroll
+#pragma unroll 1
         for (int e = 0; e < Vec<T>::N; ++e)
-            if (x[e] >= thr && x[e] > -INFINITY && keep(x[e])) {
-                const uint32_t at = atomicAdd(&sh.n_list, 1u);
-                if (at < kLocal) sh.list[at] = (u64)~key_of(x[e]) << 32 | sl.index(v, e);
-            }
+            if (x[e] > -INFINITY && item_of(key_of(x[e]), sl.index(v, e)) <= last) m += token_weight(x[e], rule);
     });
-    __syncthreads();
-}
-
-// The length of all blocks' lists, after an exchange of their lengths as
-// `slot`'s first word; over kList when one of them or all do not fit.
-__device__ __forceinline__ uint32_t gathered(const SampleShared &sh, Slot slot) {
-    uint32_t n = 0;
-    for (uint32_t c = 0; c < cluster_size(); ++c) {
-        const uint32_t one = (uint32_t)sh.slots[slot][c][0];
-        n += one <= kLocal ? one : kList + 1;
-    }
-    return n;
-}
-
-// All blocks' lists, one after another in rank 0's gather (called there, when
-// they fit).
-__device__ __forceinline__ void pull(SampleShared &sh, Slot slot) {
-    uint32_t at = 0;
-    for (uint32_t c = 0; c < cluster_size(); ++c) {
-        const uint32_t n = (uint32_t)sh.slots[slot][c][0];
-        for (uint32_t i = threadIdx.x; i < n; i += kSThreads) sh.gather[at + i] = ld_cluster_u64(at_rank(sh.list + i, c));
-        at += n;
-    }
-    __syncthreads();
-}
-
-__device__ __forceinline__ uint32_t item_weight(u64 item, const RowRule &rule) {
-    return token_weight(key_logit(~(uint32_t)(item >> 32)), rule);
-}
-
-// The token among the n gathered logits, which hold all that the filters
-// keep: the first k of them in order, and of those the top-p prefix (p < 1),
-// measured against `total` if that is not 0, else against their own sum.
-__device__ __noinline__ void finish_list(SampleShared &sh, uint32_t n, uint32_t k, float p, u64 total,
-                                         const RowRule &rule, const SampleArgs &a, u64 row) {
-    const bool cut_p = p > 0.0f && p < 1.0f;
-    const uint32_t word = a.random[row];
-    u64 *weight = sh.list;  // pulled: free
-    if (n <= kRanked) {
-        // two threads an item count what stands before it
-        const uint32_t i = threadIdx.x >> 1, half = threadIdx.x & 1;
-        const u64 item = i < n ? sh.gather[i] : ~0ull;
-        const u64 q = i < n ? item_weight(item, rule) : 0u;
-        if (half == 0) weight[i] = q;
-        __syncthreads();
-        uint32_t rank = 0;
-        u64 before = 0;
-        for (uint32_t j = half; j < n; j += 2)
-            if (sh.gather[j] < item) {
-                ++rank;
-                before += weight[j];
-            }
-        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-        before += __shfl_xor_sync(0xffffffffu, before, 1);
-        u64 kept = i < n && rank < k ? q : 0ull;
-        if (total == 0) total = block_total(half == 0 ? kept : 0ull, sh.warp_a);
-        if (cut_p) {
-            if (before >= top_p_target(p, total)) kept = 0;
-            total = block_total(half == 0 ? kept : 0ull, sh.warp_a);
-        }
-        __syncthreads();
-        if (half == 0) weight[i] = kept;
-        __syncthreads();
-        u64 at = 0;
-        for (uint32_t j = half; j < n; j += 2)
-            if ((uint32_t)sh.gather[j] < (uint32_t)item) at += weight[j];
-        at += __shfl_xor_sync(0xffffffffu, at, 1);
-        const u64 r = draw_of(word, total);
-        if (half == 0 && at <= r && r < at + kept) write_token(a, row, (uint32_t)item, kept, total);
-        return;
-    }
-    unsigned int size = 512;
-    while (size < n) size <<= 1;
-    for (unsigned int i = n + threadIdx.x; i < size; i += kSThreads) sh.gather[i] = ~0ull;
-    __syncthreads();
-    block_sort(sh.gather, size);
-    constexpr int C = kList / kSThreads;
-    const unsigned int per = size / kSThreads;
-    u64 q[C], sum = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const unsigned int i = threadIdx.x * per + c;
-        q[c] = c < (int)per && i < n && i < k ? item_weight(sh.gather[i], rule) : 0u;
-        sum += q[c];
-    }
-    if (total == 0) total = block_total(sum, sh.warp_a);
-    if (cut_p) {
-        const u64 want = top_p_target(p, total);
-        u64 before = block_before(sum, sh.warp_a);
-        sum = 0;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const u64 own = q[c];
-            if (before >= want) q[c] = 0;
-            before += own;
-            sum += q[c];
-        }
-        total = block_total(sum, sh.warp_a);
-    }
-    // the same items by index
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const unsigned int i = threadIdx.x * per + c;
-        if (c < (int)per) sh.gather[i] = i < n ? sh.gather[i] << 32 | q[c] : ~0ull << 32;
-    }
-    __syncthreads();
-    block_sort(sh.gather, size);
-    sum = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        q[c] = c < (int)per ? (uint32_t)sh.gather[threadIdx.x * per + c] : 0u;
-        sum += q[c];
-    }
-    u64 at = block_before(sum, sh.warp_a);
-    const u64 r = draw_of(word, total);
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        if (at <= r && r < at + q[c])
-            write_token(a, row, (uint32_t)(sh.gather[threadIdx.x * per + c] >> 32), q[c], total);
-        at += q[c];
-    }
+    return warp_total(m);
 }
 
 // The filters by selection on the logits' bits, then the draw: right for
@@ -733,32 +817,25 @@ __device__ __noinline__ void finish_list(SampleShared &sh, uint32_t n, uint32_t 
 template <typename T>
 __device__ __noinline__ void sample_by_selection(SampleShared &sh, const Slice<T> &sl, const RowRule &rule, uint32_t k,
                                                  float p, const SampleArgs &a, u64 row) {
-    Cut cut{0u, 0ull};  // no key is 0: everything stays
+    u64 last = kKeepAll, missing;
+    uint32_t tau;
     int level = 0;
-    if (k > 0) radix_select<false>(sh, sl, rule, 0u, k, level, &cut.tau, &cut.ties);
-    u64 q_tau = k > 0 ? token_weight(key_logit(cut.tau), rule) : 0u;
-    u64 mass, ties;
-    cut_pass(sl, rule, cut, &mass, &ties);
-    const u64 above_block = block_total((threadIdx.x & 31) == 0 ? mass : 0ull, sh.warp_c);
-    exchange(sh, kSlotAbove, above_block, 0);
-    u64 above = 0;
-    for (uint32_t c = 0; c < cluster_size(); ++c) above += sh.slots[kSlotAbove][c][0];
-    u64 total = above + cut.ties * q_tau;
+    if (k > 0) {
+        radix_select<false>(sh, sl, rule, kKeepAll, k, level, &tau, &missing);
+        if (tau > kKeyOfMinusInf) last = nth_tie(sh, sl, tau, missing, kSlotTies, kSlotTieAt);
+    }
+    u64 mass = kept_mass(sl, rule, last);
+    exchange(sh, kSlotSum, block_total((threadIdx.x & 31) == 0 ? mass : 0ull, sh.warp_c), 0);
+    u64 total = slot_total(sh, kSlotSum);
     if (p > 0.0f && p < 1.0f) {
         const u64 want = top_p_target(p, total);
-        if (want > above) {  // ends among the ties
-            cut.ties = (want - above + q_tau - 1) / q_tau;
-            total = above + cut.ties * q_tau;
-        } else {
-            u64 missing;
-            radix_select<true>(sh, sl, rule, cut.tau + 1u, want, level, &cut.tau, &missing);
-            q_tau = token_weight(key_logit(cut.tau), rule);
-            cut.ties = (missing + q_tau - 1) / q_tau;
-            total = want - missing + cut.ties * q_tau;
-            cut_pass(sl, rule, cut, &mass, &ties);
-        }
+        radix_select<true>(sh, sl, rule, last, want, level, &tau, &missing);
+        const u64 q = token_weight(key_logit(tau), rule), ties = (missing + q - 1) / q;
+        last = nth_tie(sh, sl, tau, ties, kSlotTies2, kSlotTieAt2);
+        total = want - missing + ties * q;
+        mass = kept_mass(sl, rule, last);
     }
-    draw(sh, sl, rule, cut, q_tau, total, mass, ties, a, row);
+    draw(sh, sl, rule, last, total, mass, a, row);
 }
 
 template <typename T>
@@ -800,9 +877,34 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     const bool bounded = k > 0 && (sl.n <= kLocal || share <= kSThreads / 2);
     uint32_t bound = 0;
     if (bounded && sl.n > kLocal) {
-        // the largest 16-bit prefix that at least `share` thread maxima reach
-        for (uint32_t bit = 0x80000000u; bit >= 0x10000u; bit >>= 1)
-            if (__syncthreads_count(thread_key >= (bound | bit)) >= (int)share) bound |= bit;
+        // maxima of groups of threads, at least twice as many groups as the share (fewer groups bound
+        // less tightly, more cost more to rank); the one of rank `share` - 1 is the bound
+        uint32_t group = 32, key = warp_key;
+        while (group > 1 && kSThreads / group < 2 * share) group /= 2;
+        if (group < 32) {
+            key = thread_key;
+            for (uint32_t d = 1; d < group; d *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, d));
+        }
+        const uint32_t groups = kSThreads / group, g = threadIdx.x / group;
+        if (threadIdx.x % group == 0) sh.group_max[g] = key;
+        __syncthreads();
+        if (threadIdx.x < groups) {
+            const uint32_t mine = sh.group_max[threadIdx.x];
+            uint32_t above = 0;
+            const uint4 *four = reinterpret_cast<const uint4 *>(sh.group_max);
+#pragma unroll 4
+            for (uint32_t j = 0; j < groups / 4; ++j) {
+                const uint4 o = four[j];
+                const uint32_t at = 4 * j;
+                above += (o.x > mine || (o.x == mine && at < threadIdx.x)) +
+                         (o.y > mine || (o.y == mine && at + 1 < threadIdx.x)) +
+                         (o.z > mine || (o.z == mine && at + 2 < threadIdx.x)) +
+                         (o.w > mine || (o.w == mine && at + 3 < threadIdx.x));
+            }
+            if (above == share - 1) sh.cast[0] = mine;
+        }
+        __syncthreads();
+        bound = (uint32_t)sh.cast[0];
     } else {
         __syncthreads();
     }
@@ -854,27 +956,56 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     }
     const bool finite = rule.m < INFINITY && rule.scale < INFINITY;
     if (finite && bounded) {
-        collect(sh, sl, bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY, [](float) { return true; });
+        const float thr = bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY;
+        sl.each(lane, [&](const uint4 &r, unsigned int v) {
+            if (!(V::max(r) >= thr)) return;
+            float x[V::N];
+            V::unpack(r, x);
+#pragma unroll
+            for (int e = 0; e < V::N; ++e)
+                if (x[e] >= thr && x[e] > -INFINITY) put(sh, item_of(key_of(x[e]), sl.index(v, e)));
+        });
+        __syncthreads();
         exchange(sh, kSlotFirst, sh.n_list, 0);
         const uint32_t n = gathered(sh, kSlotFirst);
         if (n <= kList) {
-            if (rank == 0) pull(sh, kSlotFirst);
+            if (rank == 0) pull(sh, kSlotFirst, n);
             cluster_arrive();
             if (rank == 0) finish_list(sh, n, k, p, 0ull, rule, a, row);
             cluster_wait();
             return;
         }
     } else if (finite && k == 0) {
-        // all weights; for top-p also the histogram of the distances that can matter: past
-        // cut_y the row holds less than (1 - p) of the largest weight
-        const float cut_y = cut_p ? fminf(31.0f, log2f((float)sl.n / (1.0f - p)) + 0.1f) : 0.0f;
-        if (cut_p) {
-            sh.bins.clear();
-            __syncthreads();
-        }
+        // All weights; for top-p also their histogram by distance, as far as it can matter: past
+        // cut_y the row holds less than (1 - p) of the largest weight. Logits below `zero` weigh
+        // nothing (y > 31).
         const u64 m2 = pack2(rule.m, rule.m), scale2 = pack2(rule.scale, rule.scale);
+        const float zero = __fsub_rd(rule.m, __fdiv_ru(31.5f, rule.scale));
         u64 mass = 0;
+        if (!cut_p) {
+            sl.each(lane, [&](const uint4 &r, unsigned int) {
+                if (!(V::max(r) >= zero)) return;
+                float x[V::N];
+                V::unpack(r, x);
+#pragma unroll
+                for (int e = 0; e < V::N; e += 2) {
+                    float y[2];
+                    uint32_t q[2];
+                    weigh2(x[e], x[e + 1], m2, scale2, y, q);
+                    mass += q[0] >= rule.qmin ? q[0] : 0u;
+                    mass += q[1] >= rule.qmin ? q[1] : 0u;
+                }
+            });
+            mass = warp_total(mass);
+            exchange(sh, kSlotFirst, block_total(lane == 0 ? mass : 0ull, sh.warp_c), 0);
+            draw(sh, sl, rule, kKeepAll, slot_total(sh, kSlotFirst), mass, a, row);
+            return;
+        }
+        const float cut_y = fminf(31.0f, log2f((float)sl.n / (1.0f - p)) + 0.1f);
+        sh.bins.clear();
+        __syncthreads();
         sl.each(lane, [&](const uint4 &r, unsigned int) {
+            if (!(V::max(r) >= zero)) return;
             float x[V::N];
             V::unpack(r, x);
 #pragma unroll
@@ -890,27 +1021,20 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
                 }
             }
         });
-        mass = warp_total(mass);
-        if (!cut_p) {
-            const u64 block_mass = block_total(lane == 0 ? mass : 0ull, sh.warp_c);
-            exchange(sh, kSlotFirst, block_mass, 0);
-            u64 total = 0;
-            for (uint32_t c = 0; c < blocks; ++c) total += sh.slots[kSlotFirst][c][0];
-            draw(sh, sl, rule, Cut{0u, 0ull}, 0ull, total, mass, 0ull, a, row);
-            return;
-        }
-        const u64 block_mass = block_total(lane == 0 ? mass : 0ull, sh.warp_c);
-        exchange(sh, kSlotFirst, block_mass, 0);
-        u64 total = 0;
-        for (uint32_t c = 0; c < blocks; ++c) total += sh.slots[kSlotFirst][c][0];
-        const u64 want = top_p_target(p, total);
+        exchange(sh, kSlotFirst, block_total(mass, sh.warp_c), 0);
+        const u64 total = slot_total(sh, kSlotFirst), want = top_p_target(p, total);
         // the bin in which the running sum reaches `want`, two bins a thread
+        u64 low[kMaxCluster], high[kMaxCluster];
+#pragma unroll
+        for (uint32_t c = 0; c < kMaxCluster; ++c) {
+            low[c] = c < blocks ? ld_cluster_u64(at_rank(&sh.bins.low[2 * threadIdx.x], c)) : 0ull;
+            high[c] = c < blocks ? ld_cluster_u64(at_rank(&sh.bins.high[2 * threadIdx.x], c)) : 0ull;
+        }
         u64 bin_mass[2] = {0, 0};
-        for (uint32_t c = 0; c < blocks; ++c) {
-            const u64 low = ld_cluster_u64(at_rank(&sh.bins.low[2 * threadIdx.x], c));
-            const u64 high = ld_cluster_u64(at_rank(&sh.bins.high[2 * threadIdx.x], c));
-            bin_mass[0] += (low & 0xffffffffull) | high << 32;
-            bin_mass[1] += low >> 32 | (high >> 32) << 32;
+#pragma unroll
+        for (uint32_t c = 0; c < kMaxCluster; ++c) {
+            bin_mass[0] += (low[c] & 0xffffffffull) | high[c] << 32;
+            bin_mass[1] += low[c] >> 32 | (high[c] >> 32) << 32;
         }
         // at most so many logits with a weight lie in a bin: none weighs less than its far end,
         // less more than the recipe's error
@@ -934,62 +1058,64 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         const uint32_t bin = (uint32_t)sh.cast[0];
         const u64 above = sh.cast[1];
         const bool all = sh.cast[2] <= kList;
-        // every logit in a bin up to this one is at or above
+        // every logit in a bin up to this one is at or above thr
         const float thr = __fsub_rd(rule.m, __fdiv_ru(((float)bin + 1.0f) * (1.0f / 32.0f), rule.scale));
-        collect(sh, sl, thr, [&](float x) {
-            const float y = __fmul_rn(__fsub_rn(rule.m, x), rule.scale);
-            if (!(y < cut_y) || token_weight(x, rule) == 0u) return false;
-            const uint32_t b = bin_of(y);
-            return all ? b <= bin : b == bin;
+        mass = 0;  // of the bins before it
+        sl.each(lane, [&](const uint4 &r, unsigned int v) {
+            if (!(V::max(r) >= thr)) return;
+            float x[V::N];
+            V::unpack(r, x);
+#pragma unroll
+            for (int e = 0; e < V::N; e += 2) {
+                float y[2];
+                uint32_t q[2];
+                weigh2(x[e], x[e + 1], m2, scale2, y, q);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!(y[i] < cut_y) || q[i] < max(rule.qmin, 1u)) continue;
+                    const uint32_t b = bin_of(y[i]);
+                    if (b < bin && !all) mass += q[i];
+                    else if (b <= bin) put(sh, item_of(key_of(x[e + i]), sl.index(v, e + i)));
+                }
+            }
         });
+        __syncthreads();
         exchange(sh, kSlotSecond, sh.n_list, 0);
         const uint32_t n = gathered(sh, kSlotSecond);
         if (n <= kList) {
-            if (rank == 0) pull(sh, kSlotSecond);
+            if (rank == 0) pull(sh, kSlotSecond, n);
             if (all) {
                 cluster_arrive();
                 if (rank == 0) finish_list(sh, n, 0xffffffffu, p, total, rule, a, row);
                 cluster_wait();
                 return;
             }
-            u64 tau = 0, ties = 0;
+            u64 last = 0, left = 0;
             if (rank == 0) {  // the crossing among the gathered
-                unsigned int size = 512;
-                while (size < n) size <<= 1;
-                for (unsigned int i = n + threadIdx.x; i < size; i += kSThreads) sh.gather[i] = ~0ull;
-                __syncthreads();
-                block_sort(sh.gather, size);
-                const unsigned int per = size / kSThreads;
-                u64 sum = 0;
-                for (unsigned int c = 0; c < per; ++c) {
-                    const unsigned int i = threadIdx.x * per + c;
-                    if (i < n) sum += item_weight(sh.gather[i], rule);
+                u64 item[kOwn];
+                uint32_t q[kOwn];
+#pragma unroll
+                for (int c = 0; c < kOwn; ++c) {
+                    const uint32_t i = threadIdx.x + c * kSThreads;
+                    item[c] = i < n ? sh.gather[i] : ~0ull;
+                    q[c] = i < n ? item_weight(item[c], rule) : 0u;
                 }
-                u64 at = above + block_before(sum, sh.warp_a);
-                for (unsigned int c = 0; c < per; ++c) {
-                    const unsigned int i = threadIdx.x * per + c;
-                    if (i >= n) break;
-                    const u64 q = item_weight(sh.gather[i], rule);
-                    if (at < want && want <= at + q) {
-                        const uint32_t high = (uint32_t)(sh.gather[i] >> 32);
-                        unsigned int first = i;
-                        while (first > 0 && (uint32_t)(sh.gather[first - 1] >> 32) == high) --first;
-                        sh.cast[0] = (u64)~high << 32 | (i - first + 1);
-                        sh.cast[1] = at + q;
-                    }
-                    at += q;
-                }
-                __syncthreads();
-                tau = sh.cast[0];
-                ties = sh.cast[1];
+                last = block_select(sh, item, q, want - above, &left);
+                left += above + item_weight(last, rule);
             }
-            exchange(sh, kSlotThird, tau, ties);
-            const u64 packed = sh.slots[kSlotThird][0][0], left = sh.slots[kSlotThird][0][1];
-            const Cut cut{(uint32_t)(packed >> 32), packed & 0xffffffffull};
-            const u64 q_tau = token_weight(key_logit(cut.tau), rule);
-            u64 kept, tied;
-            cut_pass(sl, rule, cut, &kept, &tied);
-            draw(sh, sl, rule, cut, q_tau, left, kept, tied, a, row);
+            exchange(sh, kSlotThird, last, left);
+            last = sh.slots[kSlotThird][0][0];
+            left = sh.slots[kSlotThird][0][1];
+            // the warps' shares of the crossing bin
+            if (threadIdx.x < kSWarps) sh.digits[0].low[threadIdx.x] = sh.digits[0].high[threadIdx.x] = 0u;
+            __syncthreads();
+            for (uint32_t i = threadIdx.x; i < sh.n_list; i += kSThreads)
+                if (sh.list[i] <= last)
+                    sh.digits[0].add(((uint32_t)sh.list[i] + sl.pad) / V::N / sl.per_warp - rank * kSWarps,
+                                     item_weight(sh.list[i], rule));
+            __syncthreads();
+            mass = warp_total(mass) + ((u64)sh.digits[0].high[warp] << 32) + sh.digits[0].low[warp];
+            draw(sh, sl, rule, last, left, mass, a, row);
             return;
         }
     }
