@@ -23,14 +23,15 @@
 // One cluster of blocks takes a row: each block reads its slice once from
 // HBM and keeps it in shared memory (what does not fit is read again, from
 // L2), so the passes after the maximum touch no HBM. No row is sorted:
-//   top-k   the ceil(k / blocks)-th largest of the maxima of groups of each
-//           block's threads is a bound below which no kept token lies; the
-//           few logits at or above it are gathered into one block, which
+//   top-k   the k-th largest of the maxima of groups of threads is a bound
+//           below which no kept token lies; the few logits at or above it
+//           (with 2 k groups some 1.4 k) are gathered into one block, which
 //           makes the draw.
 //   top-p   a histogram of the weights by y (32 bins an octave) gives the bin
 //           in which the prefix sum crosses; that bin's logits are gathered
 //           (or all above it too, if they are few: then the gathering block
-//           makes the draw as well).
+//           makes the draw as well). The histogram also tells each block what
+//           it keeps, so that only the block with the draw weighs again.
 //   else    (huge k, long ties, infinite logits) radix selection on the
 //           logits' bits, 8 a level, on counts or sums of weights.
 // A filter ends at an item, (~key, index) as one u64: what stands at or
@@ -68,6 +69,7 @@ struct SampleArgs {
     float *probs;
     unsigned int per_warp;      // 16-byte vectors of a row a warp takes
     unsigned int staged_iters;  // of its ceil(per_warp / 32) turns, those kept in shared memory
+    unsigned int ahead;         // rows between a block's row and the one it asks L2 to fetch, or 0
 };
 
 // Exchanges between a cluster's blocks: one slot each, so that none is
@@ -99,7 +101,6 @@ struct alignas(16) SampleShared {
             SumBins<kSThreads> sums;
             uint32_t counts[kSThreads];
         } picks;
-        uint32_t group_max[kSThreads];
     };
     u64 slots[kSlots][kMaxCluster][2];
     u64 warp_a[kSWarps], warp_b[kSWarps], warp_c[kSWarps];
@@ -299,6 +300,9 @@ __device__ __forceinline__ uint32_t at_rank(const void *p, uint32_t rank) {
 __device__ __forceinline__ void st_cluster(uint32_t addr, u64 a, u64 b) {
     asm volatile("st.shared::cluster.v2.u64 [%0], {%1, %2};" ::"r"(addr), "l"(a), "l"(b) : "memory");
 }
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
@@ -356,58 +360,62 @@ __device__ __forceinline__ u64 block_before(u64 v, u64 *s_warp) {
 }
 
 __device__ __forceinline__ u64 warp_min(u64 v) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
+    const uint32_t high = __reduce_min_sync(0xffffffffu, (uint32_t)(v >> 32));
+    const uint32_t low = __reduce_min_sync(0xffffffffu, (uint32_t)(v >> 32) == high ? (uint32_t)v : 0xffffffffu);
+    return (u64)high << 32 | low;
 }
 
 constexpr int kOwn = kList / kSThreads;  // gathered items a thread holds
 
 // Over the block's items with a weight (those at distinct places): the place
 // at which the running sum of weights, in ascending order of place, reaches
-// `target` (1 <= target <= the sum of all), and the sum before it. Histograms
-// of the places still in question, 512 bins a turn, the next turn within the
-// bin that holds the crossing, until that is one item.
-__device__ __noinline__ u64 block_select(SampleShared &sh, const u64 (&place)[kOwn], const uint32_t (&weight)[kOwn],
+// `target` (1 <= target <= the sum of all), and the sum before it. A histogram
+// of the places still in question, 512 bins between the least and the
+// greatest, then the same within the bin that holds the crossing, until that
+// is one item.
+__device__ __noinline__ u64 block_select(SampleShared &sh, const u64 (&places)[kOwn], const uint32_t (&weights)[kOwn],
                                          u64 target, u64 *before_it) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    u64 lo = ~0ull, hi = ~0ull;  // hi: complemented, so that both are minima
+    u64 place[kOwn], base = 0;
+    uint32_t weight[kOwn];
 #pragma unroll
-    for (int c = 0; c < kOwn; ++c)
-        if (weight[c]) {
-            lo = min(lo, place[c]);
-            hi = min(hi, ~place[c]);
-        }
-    lo = warp_min(lo);
-    hi = warp_min(hi);
-    __syncthreads();
-    if (lane == 0) {
-        sh.warp_a[warp] = lo;
-        sh.warp_b[warp] = hi;
+    for (int c = 0; c < kOwn; ++c) {
+        place[c] = places[c];
+        weight[c] = weights[c];
     }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSWarps; ++w) {
-        lo = min(lo, sh.warp_a[w]);
-        hi = min(hi, sh.warp_b[w]);
-    }
-    int shift = 64 - __clzll((~hi - lo) | 511ull) - 9;
-    u64 base = 0;
     while (true) {
+        u64 lo = ~0ull, hi = ~0ull;  // hi: complemented, so that both are minima
+#pragma unroll
+        for (int c = 0; c < kOwn; ++c)
+            if (weight[c]) {
+                lo = min(lo, place[c]);
+                hi = min(hi, ~place[c]);
+            }
+        lo = warp_min(lo);
+        hi = warp_min(hi);
         sh.picks.sums.clear();
         sh.picks.counts[threadIdx.x] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int c = 0; c < kOwn; ++c) {
-            const u64 bin = (place[c] - lo) >> shift;  // places below lo wrap to large bins
-            if (weight[c] && bin < kSThreads) {
-                sh.picks.sums.add((uint32_t)bin, weight[c]);
-                atomicAdd(&sh.picks.counts[bin], 1u);
-            }
+        if (lane == 0) {
+            sh.warp_a[warp] = lo;
+            sh.warp_b[warp] = hi;
         }
         __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kSWarps; ++w) {
+            lo = min(lo, sh.warp_a[w]);
+            hi = min(hi, sh.warp_b[w]);
+        }
+        const int shift = 55 - __clzll((~hi - lo) | 511ull);
+#pragma unroll
+        for (int c = 0; c < kOwn; ++c)
+            if (weight[c]) {
+                const uint32_t bin = (uint32_t)((place[c] - lo) >> shift);
+                sh.picks.sums.add(bin, weight[c]);
+                atomicAdd(&sh.picks.counts[bin], 1u);
+            }
+        __syncthreads();
         const u64 mine = (u64)sh.picks.sums.high[threadIdx.x] << 32 | sh.picks.sums.low[threadIdx.x];
-        const u64 before = base + block_before(mine, sh.warp_a);
+        const u64 before = base + block_before(mine, sh.warp_c);
         if (before < target && target <= before + mine) {
             sh.cast[0] = threadIdx.x;
             sh.cast[1] = before;
@@ -416,17 +424,19 @@ __device__ __noinline__ u64 block_select(SampleShared &sh, const u64 (&place)[kO
         __syncthreads();
         const u64 bin = sh.cast[0], left = sh.cast[2];
         base = sh.cast[1];
-        if (left == 1 || shift == 0) {
+        u64 found = ~0ull;
 #pragma unroll
-            for (int c = 0; c < kOwn; ++c)
-                if (weight[c] && (place[c] - lo) >> shift == bin) sh.cast[3] = place[c];
+        for (int c = 0; c < kOwn; ++c) {
+            if ((place[c] - lo) >> shift != bin) weight[c] = 0;
+            if (weight[c]) found = place[c];
+        }
+        if (left == 1) {
+            if (found != ~0ull) sh.cast[3] = found;
             __syncthreads();
             *before_it = base;
             return sh.cast[3];
         }
-        lo += bin << shift;
-        shift = shift > 9 ? shift - 9 : 0;
-        __syncthreads();  // cast is written again
+        __syncthreads();  // cast and the bins are written again
     }
 }
 
@@ -518,25 +528,54 @@ __device__ __forceinline__ u64 slot_total(const SampleShared &sh, Slot slot) {
     return t;
 }
 
-// The draw among the items up to `last`, in index order; mass: what this
-// warp's vectors keep. The block that holds the draw walks the one warp's
-// share that does, a turn of 32 vectors a warp.
-template <typename T>
-__device__ __forceinline__ void draw(SampleShared &sh, const Slice<T> &own, const RowRule &rule, u64 last, u64 total,
-                                     u64 mass, const SampleArgs &a, u64 row) {
+// What this warp keeps of the items up to `last`; FINITE: m and scale are.
+template <bool FINITE, typename T>
+__device__ __forceinline__ u64 kept_mass(const Slice<T> &sl, const RowRule &rule, u64 last) {
+    const float thr = last == kKeepAll ? -INFINITY : key_logit(~(uint32_t)(last >> 32));
+    const u64 m2 = pack2(rule.m, rule.m), scale2 = pack2(rule.scale, rule.scale);
+    u64 mass = 0;
+    sl.each(threadIdx.x & 31, [&](const uint4 &r, unsigned int v) {
+        if (!(Vec<T>::max(r) >= thr)) return;
+        float x[Vec<T>::N];
+        Vec<T>::unpack(r, x);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; e += 2) {
+            uint32_t q[2];
+            if (FINITE) {
+                float y[2];
+                weigh2(x[e], x[e + 1], m2, scale2, y, q);
+            } else {
+                q[0] = token_weight(x[e], rule);
+                q[1] = token_weight(x[e + 1], rule);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool keep = x[e + i] > thr || (x[e + i] == thr && sl.index(v, e + i) <= (uint32_t)last);
+                mass += keep && q[i] >= rule.qmin ? q[i] : 0u;
+            }
+        }
+    });
+    return warp_total(mass);
+}
+
+// The draw among the items up to `last`, in index order, from what each block
+// keeps (the first words of `slot`) and, where it is known, this warp (else m
+// and scale are finite). The
+// block that holds the draw finds the warp's share that does, and walks it a
+// turn of 32 vectors a warp.
+template <bool WARPS_KNOWN, typename T>
+__device__ __noinline__ void draw(SampleShared &sh, const Slice<T> &own, const RowRule &rule, u64 last, u64 total,
+                                  Slot slot, u64 warp_mass, const SampleArgs &a, u64 row) {
     constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const u64 r = draw_of(a.random[row], total);
-    __syncthreads();
-    if (lane == 0) sh.warp_a[warp] = mass;
-    __syncthreads();
-    u64 block_mass = 0;
-#pragma unroll
-    for (int w = 0; w < kSWarps; ++w) block_mass += sh.warp_a[w];
-    exchange(sh, kSlotDraw, block_mass, 0);
     u64 before = 0;
-    for (uint32_t c = 0; c < cluster_rank(); ++c) before += sh.slots[kSlotDraw][c][0];
-    if (r < before || r - before >= block_mass) return;
+    for (uint32_t c = 0; c < cluster_rank(); ++c) before += sh.slots[slot][c][0];
+    if (r < before || r - before >= sh.slots[slot][cluster_rank()][0]) return;
+    if (!WARPS_KNOWN) warp_mass = kept_mass<true>(own, rule, last);
+    __syncthreads();
+    if (lane == 0) sh.warp_a[warp] = warp_mass;
+    __syncthreads();
     int w = 0;
     while (r - before >= sh.warp_a[w]) before += sh.warp_a[w++];
     const Slice<T> sl = own.of_warp(w - warp);
@@ -580,6 +619,48 @@ __device__ __forceinline__ void draw(SampleShared &sh, const Slice<T> &own, cons
         if (r < turn) return;
         before = turn;
     }
+}
+
+// A key that at least k of the n maxima reach: the lower edge of the bin that
+// holds the k-th largest, of 512 between the least and row_key, the greatest;
+// then of 512 in that bin, while it spans more than 1/64 of an octave (a
+// maximum of -inf widens the first).
+__device__ __forceinline__ uint32_t kth_bound(SampleShared &sh, const uint32_t *maxima, uint32_t n, uint32_t k,
+                                              uint32_t row_key) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t *counts = sh.picks.counts;
+    uint32_t least = row_key;
+    for (uint32_t i = threadIdx.x; i < n; i += kSThreads) least = min(least, maxima[i]);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) sh.warp_a[warp] = least;
+    counts[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSWarps; ++w) least = min(least, (uint32_t)sh.warp_a[w]);
+    int shift = 23 - __clz((row_key - least) | 511u);
+    uint32_t nearest = 0;  // distance from row_key at which the bins start
+    while (true) {
+        for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
+            const uint32_t d = row_key - maxima[i];
+            if (d >= nearest && (d - nearest) >> shift < kSThreads) atomicAdd(&counts[(d - nearest) >> shift], 1u);
+        }
+        __syncthreads();
+        const uint32_t mine = counts[threadIdx.x];
+        const uint32_t before = (uint32_t)block_before(mine, sh.warp_b);
+        if (before < k && k <= before + mine) {
+            sh.cast[0] = nearest + (threadIdx.x << shift);
+            sh.cast[1] = before;
+        }
+        counts[threadIdx.x] = 0;
+        __syncthreads();
+        nearest = (uint32_t)sh.cast[0];
+        if (shift <= 17) break;
+        k -= (uint32_t)sh.cast[1];
+        shift -= 9;
+        __syncthreads();  // cast is written again
+    }
+    const u64 far = (u64)nearest + (1ull << shift) - 1;  // the bin's farthest distance
+    return far < row_key ? row_key - (uint32_t)far : 0u;
 }
 
 // Puts an item into this block's list.
@@ -798,20 +879,6 @@ __device__ __noinline__ u64 nth_tie(SampleShared &sh, const Slice<T> &sl, uint32
     return item;
 }
 
-// What this warp keeps of the items up to `last`.
-template <typename T>
-__device__ __forceinline__ u64 kept_mass(const Slice<T> &sl, const RowRule &rule, u64 last) {
-    u64 m = 0;
-    sl.each(threadIdx.x & 31, [&](const uint4 &r, unsigned int v) {
-        float x[Vec<T>::N];
-        Vec<T>::unpack(r, x);
-#pragma unroll 1
-        for (int e = 0; e < Vec<T>::N; ++e)
-            if (x[e] > -INFINITY && item_of(key_of(x[e]), sl.index(v, e)) <= last) m += token_weight(x[e], rule);
-    });
-    return warp_total(m);
-}
-
 // The filters by selection on the logits' bits, then the draw: right for
 // every row, and the way of those the other paths do not take.
 template <typename T>
@@ -824,7 +891,7 @@ __device__ __noinline__ void sample_by_selection(SampleShared &sh, const Slice<T
         radix_select<false>(sh, sl, rule, kKeepAll, k, level, &tau, &missing);
         if (tau > kKeyOfMinusInf) last = nth_tie(sh, sl, tau, missing, kSlotTies, kSlotTieAt);
     }
-    u64 mass = kept_mass(sl, rule, last);
+    u64 mass = kept_mass<false>(sl, rule, last);
     exchange(sh, kSlotSum, block_total((threadIdx.x & 31) == 0 ? mass : 0ull, sh.warp_c), 0);
     u64 total = slot_total(sh, kSlotSum);
     if (p > 0.0f && p < 1.0f) {
@@ -833,9 +900,12 @@ __device__ __noinline__ void sample_by_selection(SampleShared &sh, const Slice<T
         const u64 q = token_weight(key_logit(tau), rule), ties = (missing + q - 1) / q;
         last = nth_tie(sh, sl, tau, ties, kSlotTies2, kSlotTieAt2);
         total = want - missing + ties * q;
-        mass = kept_mass(sl, rule, last);
+        mass = kept_mass<false>(sl, rule, last);
+        exchange(sh, kSlotDraw, block_total((threadIdx.x & 31) == 0 ? mass : 0ull, sh.warp_c), 0);
+        draw<true>(sh, sl, rule, last, total, kSlotDraw, mass, a, row);
+        return;
     }
-    draw(sh, sl, rule, last, total, mass, a, row);
+    draw<true>(sh, sl, rule, last, total, kSlotSum, mass, a, row);
 }
 
 template <typename T>
@@ -868,56 +938,47 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     const uint32_t k = k_arg > 0 && (uint32_t)k_arg < sl.n ? (uint32_t)k_arg : 0u;
     const bool cut_p = p > 0.0f && p < 1.0f;
 
-    // the row's largest logit, and for top-k the bound
+    // The blocks that run after these find their rows in L2: HBM stays busy while these compute
+    // (256 rows of 262144 f32: @@ us without, @@ with).
+    if (a.ahead && threadIdx.x == 0 && row + a.ahead < a.rows) {
+        const uintptr_t from = reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) +
+                                                           (row + a.ahead) * a.row_stride);
+        const uintptr_t first = (from + 15) & ~(uintptr_t)15, end = (from + a.vocab * sizeof(T)) & ~(uintptr_t)15;
+        const uintptr_t at = first + (uintptr_t)rank * kSWarps * a.per_warp * 16;
+        if (at < end) {
+            const uintptr_t bytes = min(end - at, (uintptr_t)kSWarps * a.per_warp * 16);
+            bulk_prefetch_l2(reinterpret_cast<const void *>(at), (unsigned int)bytes);
+        }
+    }
+
+    // the row's largest logit, and for top-k the maxima its bound comes from
     const float thread_max = sl.first_pass(lane);
     const uint32_t thread_key = key_of(thread_max == thread_max ? thread_max : -INFINITY);
     const uint32_t warp_key = __reduce_max_sync(0xffffffffu, thread_key);
     if (lane == 0) sh.warp_a[warp] = warp_key;
-    const uint32_t share = (k + blocks - 1) / blocks;
-    const bool bounded = k > 0 && (sl.n <= kLocal || share <= kSThreads / 2);
-    uint32_t bound = 0;
-    if (bounded && sl.n > kLocal) {
-        // maxima of groups of threads, at least twice as many groups as the share (fewer groups bound
-        // less tightly, more cost more to rank); the one of rank `share` - 1 is the bound
-        uint32_t group = 32, key = warp_key;
-        while (group > 1 && kSThreads / group < 2 * share) group /= 2;
-        if (group < 32) {
-            key = thread_key;
-            for (uint32_t d = 1; d < group; d *= 2) key = max(key, __shfl_xor_sync(0xffffffffu, key, d));
-        }
-        const uint32_t groups = kSThreads / group, g = threadIdx.x / group;
-        if (threadIdx.x % group == 0) sh.group_max[g] = key;
-        __syncthreads();
-        if (threadIdx.x < groups) {
-            const uint32_t mine = sh.group_max[threadIdx.x];
-            uint32_t above = 0;
-            const uint4 *four = reinterpret_cast<const uint4 *>(sh.group_max);
-#pragma unroll 4
-            for (uint32_t j = 0; j < groups / 4; ++j) {
-                const uint4 o = four[j];
-                const uint32_t at = 4 * j;
-                above += (o.x > mine || (o.x == mine && at < threadIdx.x)) +
-                         (o.y > mine || (o.y == mine && at + 1 < threadIdx.x)) +
-                         (o.z > mine || (o.z == mine && at + 2 < threadIdx.x)) +
-                         (o.w > mine || (o.w == mine && at + 3 < threadIdx.x));
-            }
-            if (above == share - 1) sh.cast[0] = mine;
-        }
-        __syncthreads();
-        bound = (uint32_t)sh.cast[0];
-    } else {
-        __syncthreads();
+    // top-k: maxima of groups of threads, at least 2 k groups in the row
+    uint32_t group = 32;
+    while (group > 1 && kSThreads / group * blocks < 2 * k) group /= 2;
+    const uint32_t groups = kSThreads / group;
+    const bool bounded = k > 0 && (sl.n <= kLocal || 2 * k <= groups * blocks);
+    const bool by_groups = bounded && sl.n > kLocal;
+    uint32_t group_key = warp_key;
+    if (by_groups && group < 32) {
+        group_key = thread_key;
+        for (uint32_t d = 1; d < group; d *= 2) group_key = max(group_key, __shfl_xor_sync(0xffffffffu, group_key, d));
     }
+    __syncthreads();
     uint32_t block_key = 0;
 #pragma unroll
     for (int w = 0; w < kSWarps; ++w) block_key = max(block_key, (uint32_t)sh.warp_a[w]);
     cluster_wait();
-    exchange(sh, kSlotMax, block_key, bound);
+    uint32_t *maxima = reinterpret_cast<uint32_t *>(sh.gather);  // of all the row's groups
+    if (by_groups && threadIdx.x % group == 0)
+        for (uint32_t c = 0; c < blocks; ++c)
+            st_cluster(at_rank(maxima + rank * groups + threadIdx.x / group, c), group_key);
+    exchange(sh, kSlotMax, block_key, 0);
     uint32_t row_key = 0;
-    for (uint32_t c = 0; c < blocks; ++c) {
-        row_key = max(row_key, (uint32_t)sh.slots[kSlotMax][c][0]);
-        bound = min(bound, (uint32_t)sh.slots[kSlotMax][c][1]);
-    }
+    for (uint32_t c = 0; c < blocks; ++c) row_key = max(row_key, (uint32_t)sh.slots[kSlotMax][c][0]);
     if (row_key <= kKeyOfMinusInf) {  // the mask leaves nothing
         if (rank == 0 && threadIdx.x == 0) {
             a.tokens[row] = -1;
@@ -956,6 +1017,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     }
     const bool finite = rule.m < INFINITY && rule.scale < INFINITY;
     if (finite && bounded) {
+        const uint32_t bound = by_groups ? kth_bound(sh, maxima, groups * blocks, k, row_key) : 0u;
         const float thr = bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY;
         sl.each(lane, [&](const uint4 &r, unsigned int v) {
             if (!(V::max(r) >= thr)) return;
@@ -998,10 +1060,11 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
             });
             mass = warp_total(mass);
             exchange(sh, kSlotFirst, block_total(lane == 0 ? mass : 0ull, sh.warp_c), 0);
-            draw(sh, sl, rule, kKeepAll, slot_total(sh, kSlotFirst), mass, a, row);
+            draw<true>(sh, sl, rule, kKeepAll, slot_total(sh, kSlotFirst), kSlotFirst, mass, a, row);
             return;
         }
         const float cut_y = fminf(31.0f, log2f((float)sl.n / (1.0f - p)) + 0.1f);
+        const uint32_t floor_q = max(max(rule.qmin, exp2_weight(cut_y)), 1u);  // the histogram's least weight
         sh.bins.clear();
         __syncthreads();
         sl.each(lane, [&](const uint4 &r, unsigned int) {
@@ -1015,9 +1078,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
                 weigh2(x[e], x[e + 1], m2, scale2, y, q);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t w = q[i] >= rule.qmin ? q[i] : 0u;
-                    mass += w;
-                    if (y[i] < cut_y && w) sh.bins.add(bin_of(y[i]), w);
+                    mass += q[i] >= rule.qmin ? q[i] : 0u;
+                    if (q[i] >= floor_q) sh.bins.add(bin_of(y[i]), q[i]);
                 }
             }
         });
@@ -1043,9 +1105,11 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         for (int i = 0; i < 2; ++i) {
             const uint32_t far = exp2_weight(((float)(2 * threadIdx.x + i) + 0.5f) * (1.0f / 32.0f));
             const uint32_t slack = (far >> 16) + 2;
-            const uint32_t least = max(far > slack ? far - slack : 0u, max(rule.qmin, 1u));
-            at_most[i] = (u64)((float)bin_mass[i] / (float)least * 1.001f) + (bin_mass[i] ? 1u : 0u);
+            const uint32_t least = max(far > slack ? far - slack : 0u, floor_q);
+            at_most[i] = (u64)(__fdividef((float)bin_mass[i], (float)least) * 1.001f) + (bin_mass[i] ? 1u : 0u);
         }
+        const u64 own[2] = {(u64)sh.bins.high[2 * threadIdx.x] << 32 | sh.bins.low[2 * threadIdx.x],
+                            (u64)sh.bins.high[2 * threadIdx.x + 1] << 32 | sh.bins.low[2 * threadIdx.x + 1]};
         const u64 before = block_before(bin_mass[0] + bin_mass[1], sh.warp_a);
         const u64 count_before = block_before(at_most[0] + at_most[1], sh.warp_b);
         if (before < want && want <= before + bin_mass[0] + bin_mass[1]) {
@@ -1058,25 +1122,31 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         const uint32_t bin = (uint32_t)sh.cast[0];
         const u64 above = sh.cast[1];
         const bool all = sh.cast[2] <= kList;
-        // every logit in a bin up to this one is at or above thr
+        const u64 block_above = block_total((2 * threadIdx.x < bin ? own[0] : 0ull) +
+                                                (2 * threadIdx.x + 1 < bin ? own[1] : 0ull), sh.warp_c);
+        // every logit in a bin up to this one is at or above thr, every one in a bin from it on at
+        // or below cap
         const float thr = __fsub_rd(rule.m, __fdiv_ru(((float)bin + 1.0f) * (1.0f / 32.0f), rule.scale));
-        mass = 0;  // of the bins before it
+        const float cap = all || bin == 0 ? INFINITY
+                                          : __fsub_ru(rule.m, __fdiv_rd(((float)bin - 1.0f) * (1.0f / 32.0f), rule.scale));
         sl.each(lane, [&](const uint4 &r, unsigned int v) {
             if (!(V::max(r) >= thr)) return;
             float x[V::N];
             V::unpack(r, x);
+            unsigned int near = 0;
 #pragma unroll
-            for (int e = 0; e < V::N; e += 2) {
-                float y[2];
-                uint32_t q[2];
-                weigh2(x[e], x[e + 1], m2, scale2, y, q);
+            for (int e = 0; e < V::N; ++e)
+                if (x[e] >= thr && x[e] <= cap) near |= 1u << e;
+#pragma unroll 1
+            for (; near; near &= near - 1) {
+                const int e = __ffs(near) - 1;
+                float xe = x[0];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (!(y[i] < cut_y) || q[i] < max(rule.qmin, 1u)) continue;
-                    const uint32_t b = bin_of(y[i]);
-                    if (b < bin && !all) mass += q[i];
-                    else if (b <= bin) put(sh, item_of(key_of(x[e + i]), sl.index(v, e + i)));
-                }
+                for (int i = 1; i < V::N; ++i) xe = e == i ? x[i] : xe;
+                const float y = __fmul_rn(__fsub_rn(rule.m, xe), rule.scale);
+                if (!(y < 32.0f) || exp2_weight(y) < floor_q) continue;
+                const uint32_t b = bin_of(y);
+                if (all ? b <= bin : b == bin) put(sh, item_of(key_of(xe), sl.index(v, e)));
             }
         });
         __syncthreads();
@@ -1106,16 +1176,12 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
             exchange(sh, kSlotThird, last, left);
             last = sh.slots[kSlotThird][0][0];
             left = sh.slots[kSlotThird][0][1];
-            // the warps' shares of the crossing bin
-            if (threadIdx.x < kSWarps) sh.digits[0].low[threadIdx.x] = sh.digits[0].high[threadIdx.x] = 0u;
-            __syncthreads();
+            // this block's part: its bins before the crossing one, and its items up to the crossing
+            u64 part = 0;
             for (uint32_t i = threadIdx.x; i < sh.n_list; i += kSThreads)
-                if (sh.list[i] <= last)
-                    sh.digits[0].add(((uint32_t)sh.list[i] + sl.pad) / V::N / sl.per_warp - rank * kSWarps,
-                                     item_weight(sh.list[i], rule));
-            __syncthreads();
-            mass = warp_total(mass) + ((u64)sh.digits[0].high[warp] << 32) + sh.digits[0].low[warp];
-            draw(sh, sl, rule, last, left, mass, a, row);
+                if (sh.list[i] <= last) part += item_weight(sh.list[i], rule);
+            exchange(sh, kSlotDraw, block_total(part, sh.warp_c) + block_above, 0);
+            draw<false>(sh, sl, rule, last, left, kSlotDraw, 0ull, a, row);
             return;
         }
     }
@@ -1149,6 +1215,8 @@ static int sample_launch(SampleArgs a, cudaStream_t stream) {
     if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(sizeof(SampleShared) + kMaxStaged * kStageBytes)) != cudaSuccess)
         return U32SCAN_ECUDA;
+    const unsigned int resident = 2 * 152 / blocks;  // rows at a time
+    a.ahead = a.rows > resident ? resident : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned int)a.rows * blocks);
     cfg.blockDim = dim3(kSThreads);
@@ -1179,7 +1247,7 @@ extern "C" int sample_tokens(const void *logits, int type, size_t rows, size_t v
     for (const void *p : {(const void *)temperature, (const void *)top_k, (const void *)top_p, (const void *)min_p,
                           (const void *)random, (const void *)tokens, (const void *)probs})
         if (reinterpret_cast<uintptr_t>(p) & 3) return U32SCAN_EINVAL;
-    const SampleArgs a{logits, rows, vocab, row_stride, temperature, top_k, top_p, min_p, random, tokens, probs, 0, 0};
+    const SampleArgs a{logits, rows, vocab, row_stride, temperature, top_k, top_p, min_p, random, tokens, probs, 0, 0, 0};
     const cudaStream_t s = (cudaStream_t)stream;
     if (type == U32SCAN_F32) return sample_launch<float>(a, s);
     if (type == U32SCAN_F16) return sample_launch<__half>(a, s);
