@@ -30,8 +30,9 @@
 //   top-p   a histogram of the weights by y (32 bins an octave) gives the bin
 //           in which the prefix sum crosses; that bin's logits are gathered
 //           (or all above it too, if they are few: then the gathering block
-//           makes the draw as well). The histogram also tells each block what
-//           it keeps, so that only the block with the draw weighs again.
+//           makes the draw as well). The histogram also tells each half of a
+//           block what it keeps, so that only the half with the draw weighs
+//           again.
 //   else    (huge k, long ties, infinite logits) radix selection on the
 //           logits' bits, 8 a level, on counts or sums of weights.
 // A filter ends at an item, (~key, index) as one u64: what stands at or
@@ -69,13 +70,22 @@ struct SampleArgs {
     float *probs;
     unsigned int per_warp;      // 16-byte vectors of a row a warp takes
     unsigned int staged_iters;  // of its ceil(per_warp / 32) turns, those kept in shared memory
-    unsigned int ahead;         // rows between a block's row and the one it asks L2 to fetch, or 0
 };
 
 // Exchanges between a cluster's blocks: one slot each, so that none is
 // written again while a slow block still reads it.
-enum Slot { kSlotMax, kSlotFirst, kSlotSecond, kSlotThird, kSlotSum, kSlotTies, kSlotTieAt, kSlotTies2, kSlotTieAt2, kSlotDraw,
-            kSlots };
+enum Slot {
+    kSlotMax,
+    kSlotFirst,
+    kSlotSecond,
+    kSlotSum,
+    kSlotTies,
+    kSlotTieAt,
+    kSlotTies2,
+    kSlotTieAt2,
+    kSlotDraw,
+    kSlots
+};
 
 // Sums of u32 by bin, exact in 64 bits at one native shared-memory atomic an
 // addition: the carries out of the low words are counted in the high ones.
@@ -92,10 +102,9 @@ struct SumBins {
 };
 
 struct alignas(16) SampleShared {
-    u64 list[kLocal];   // this block's: (~key, index), ascending = in order
-    u64 gather[kList];  // the cluster's, in the block of rank 0
+    u64 items[kLocal + kList];  // (~key, index), ascending = in order: this block's list, then all blocks'
     union {
-        SumBins<kBins> bins;
+        SumBins<kBins> bins[2];  // of the block's two halves
         SumBins<256> digits[2];
         struct {
             SumBins<kSThreads> sums;
@@ -103,10 +112,17 @@ struct alignas(16) SampleShared {
         } picks;
     };
     u64 slots[kSlots][kMaxCluster][2];
-    u64 warp_a[kSWarps], warp_b[kSWarps], warp_c[kSWarps];
+    u64 warp[3][kSWarps];
     u64 cast[4];
     uint32_t n_list;
 };
+
+// The block's, at the start of its dynamic shared memory; named here and not
+// handed on by reference, so that every access is known to be to shared memory.
+__device__ __forceinline__ SampleShared &block_shared() {
+    extern __shared__ __align__(16) unsigned char s_mem[];
+    return *reinterpret_cast<SampleShared *>(s_mem);
+}
 
 // ---------------------------------------------------------------------------
 // Logits, keys, weights
@@ -212,7 +228,7 @@ struct RowRule {
 };
 
 // A logit's weight, any logit, any rule.
-__device__ __forceinline__ uint32_t token_weight(float x, const RowRule &rule) {
+__device__ __noinline__ uint32_t token_weight(float x, RowRule rule) {
     if (x == rule.m) return 0x80000000u;
     const float y = __fmul_rn(__fsub_rn(rule.m, x), rule.scale);
     if (!(y < 32.0f) || x == -INFINITY) return 0u;
@@ -308,6 +324,9 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ void ld_cluster_u64x2(uint32_t addr, u64 &a, u64 &b) {
+    asm volatile("ld.shared::cluster.v2.u64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
     u64 v;
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
@@ -317,46 +336,18 @@ __device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
 // Every block's (a, b), given by its threads below the cluster's size, then
 // in sh.slots[slot] of every block. A cluster barrier: what blocks wrote to
 // their shared memory before it can be read by the others after it.
-__device__ __forceinline__ void exchange(SampleShared &sh, Slot slot, u64 a, u64 b) {
+__device__ __noinline__ void exchange(Slot slot, u64 a, u64 b) {
+    SampleShared &sh = block_shared();
     if (threadIdx.x < cluster_size()) st_cluster(at_rank(sh.slots[slot][cluster_rank()], threadIdx.x), a, b);
     cluster_arrive();
     cluster_wait();
 }
 
+// The sum over the warp of values below 2^54 (a row's sums are below 2^53).
 __device__ __forceinline__ u64 warp_total(u64 v) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-}
-
-// The sum over the block, in every thread.
-__device__ __forceinline__ u64 block_total(u64 v, u64 *s_warp) {
-    v = warp_total(v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
-    __syncthreads();
-    u64 t = 0;
-#pragma unroll
-    for (int w = 0; w < kSWarps; ++w) t += s_warp[w];
-    return t;
-}
-
-// The sum over the threads before this one.
-__device__ __forceinline__ u64 block_before(u64 v, u64 *s_warp) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    u64 inc = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const u64 o = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += o;
-    }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = inc;
-    __syncthreads();
-    u64 base = 0;
-#pragma unroll
-    for (int w = 0; w < kSWarps; ++w) base += w < warp ? s_warp[w] : 0ull;
-    return base + inc - v;
+    const uint32_t low = __reduce_add_sync(0xffffffffu, (uint32_t)v & 0x7ffffffu);
+    const uint32_t high = __reduce_add_sync(0xffffffffu, (uint32_t)(v >> 27));
+    return ((u64)high << 27) + low;
 }
 
 __device__ __forceinline__ u64 warp_min(u64 v) {
@@ -365,84 +356,64 @@ __device__ __forceinline__ u64 warp_min(u64 v) {
     return (u64)high << 32 | low;
 }
 
-constexpr int kOwn = kList / kSThreads;  // gathered items a thread holds
-
-// Over the block's items with a weight (those at distinct places): the place
-// at which the running sum of weights, in ascending order of place, reaches
-// `target` (1 <= target <= the sum of all), and the sum before it. A histogram
-// of the places still in question, 512 bins between the least and the
-// greatest, then the same within the bin that holds the crossing, until that
-// is one item.
-__device__ __noinline__ u64 block_select(SampleShared &sh, const u64 (&places)[kOwn], const uint32_t (&weights)[kOwn],
-                                         u64 target, u64 *before_it) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    u64 place[kOwn], base = 0;
-    uint32_t weight[kOwn];
-#pragma unroll
-    for (int c = 0; c < kOwn; ++c) {
-        place[c] = places[c];
-        weight[c] = weights[c];
+__device__ __forceinline__ u64 warp_inclusive(u64 v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int d = 1; d < 32; d <<= 1) {
+        const u64 o = __shfl_up_sync(0xffffffffu, v, d);
+        if (lane >= d) v += o;
     }
-    while (true) {
-        u64 lo = ~0ull, hi = ~0ull;  // hi: complemented, so that both are minima
-#pragma unroll
-        for (int c = 0; c < kOwn; ++c)
-            if (weight[c]) {
-                lo = min(lo, place[c]);
-                hi = min(hi, ~place[c]);
-            }
-        lo = warp_min(lo);
-        hi = warp_min(hi);
-        sh.picks.sums.clear();
-        sh.picks.counts[threadIdx.x] = 0;
-        if (lane == 0) {
-            sh.warp_a[warp] = lo;
-            sh.warp_b[warp] = hi;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kSWarps; ++w) {
-            lo = min(lo, sh.warp_a[w]);
-            hi = min(hi, sh.warp_b[w]);
-        }
-        const int shift = 55 - __clzll((~hi - lo) | 511ull);
-#pragma unroll
-        for (int c = 0; c < kOwn; ++c)
-            if (weight[c]) {
-                const uint32_t bin = (uint32_t)((place[c] - lo) >> shift);
-                sh.picks.sums.add(bin, weight[c]);
-                atomicAdd(&sh.picks.counts[bin], 1u);
-            }
-        __syncthreads();
-        const u64 mine = (u64)sh.picks.sums.high[threadIdx.x] << 32 | sh.picks.sums.low[threadIdx.x];
-        const u64 before = base + block_before(mine, sh.warp_c);
-        if (before < target && target <= before + mine) {
-            sh.cast[0] = threadIdx.x;
-            sh.cast[1] = before;
-            sh.cast[2] = sh.picks.counts[threadIdx.x];
-        }
-        __syncthreads();
-        const u64 bin = sh.cast[0], left = sh.cast[2];
-        base = sh.cast[1];
-        u64 found = ~0ull;
-#pragma unroll
-        for (int c = 0; c < kOwn; ++c) {
-            if ((place[c] - lo) >> shift != bin) weight[c] = 0;
-            if (weight[c]) found = place[c];
-        }
-        if (left == 1) {
-            if (found != ~0ull) sh.cast[3] = found;
-            __syncthreads();
-            *before_it = base;
-            return sh.cast[3];
-        }
-        __syncthreads();  // cast and the bins are written again
-    }
+    return v;
 }
+
+// Warp w's value of sh.warp[which], for lanes w below the number of warps,
+// after every warp has given one.
+__device__ __forceinline__ u64 of_warps(u64 v, int which, u64 none) {
+    SampleShared &sh = block_shared();
+    const int lane = threadIdx.x & 31;
+    __syncthreads();
+    if (lane == 0) sh.warp[which][threadIdx.x >> 5] = v;
+    __syncthreads();
+    return lane < kSWarps ? sh.warp[which][lane] : none;
+}
+
+// The sum over the block, in every thread.
+__device__ __noinline__ u64 block_total(u64 v) { return warp_total(of_warps(warp_total(v), 0, 0ull)); }
+
+// The sum over the threads before this one.
+__device__ __noinline__ u64 block_before(u64 v) {
+    const u64 inc = warp_inclusive(v);
+    const u64 warps = of_warps(__shfl_sync(0xffffffffu, inc, 31), 1, 0ull);
+    return warp_total((threadIdx.x & 31) < (threadIdx.x >> 5) ? warps : 0ull) + inc - v;
+}
+
+// The least over the block, in every thread.
+__device__ __noinline__ u64 block_min(u64 v) { return warp_min(of_warps(warp_min(v), 2, ~0ull)); }
 
 // ---------------------------------------------------------------------------
 // A block's slice of a row
 // ---------------------------------------------------------------------------
+// Elements p .. of base, those outside [first, end) as -inf.
+template <typename T>
+__device__ __noinline__ uint4 load_edge(const T *base, unsigned int p, unsigned int first, unsigned int end) {
+    constexpr int bits = 8 * sizeof(T), per_word = 32 / bits;
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        w[j] = Vec<T>::kFill;
+#pragma unroll
+        for (int i = 0; i < per_word; ++i) {
+            const unsigned int at = p + j * per_word + i;
+            if (at >= first && at < end) {
+                const uint32_t one = sizeof(T) == 4 ? reinterpret_cast<const uint32_t *>(base)[at]
+                                                    : reinterpret_cast<const uint16_t *>(base)[at];
+                w[j] = sizeof(T) == 4 ? one : (w[j] & ~(0xffffu << bits * i)) | one << bits * i;
+            }
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <typename T>
 struct Slice {
     using V = Vec<T>;
@@ -456,18 +427,14 @@ struct Slice {
     __device__ __forceinline__ uint4 load(unsigned int v) const {
         const unsigned int p = v * V::N;
         if (p >= pad && p + V::N <= pad + n) return __ldg(reinterpret_cast<const uint4 *>(base) + v);
-        uint32_t w[4] = {V::kFill, V::kFill, V::kFill, V::kFill};
-        T *e = reinterpret_cast<T *>(w);
-#pragma unroll
-        for (int j = 0; j < V::N; ++j)
-            if (p + j >= pad && p + j < pad + n) e[j] = reinterpret_cast<const T *>(base)[p + j];
-        return make_uint4(w[0], w[1], w[2], w[3]);
+        return load_edge<T>(reinterpret_cast<const T *>(base), p, pad, pad + n);
     }
 
     // First reading: keeps the staged vectors, returns this thread's maximum.
     __device__ __forceinline__ float first_pass(int lane) const {
         constexpr int U = 4;
         float m = -INFINITY;
+#pragma unroll 1
         for (unsigned int j = lane, it = 0; j < per_warp && v0 + j < nv; j += 32 * U, it += U) {
             uint4 r[U];
 #pragma unroll
@@ -485,11 +452,28 @@ struct Slice {
         return m;
     }
 
-    // f(vector, its number) for this lane's vectors, in ascending order.
+    __device__ __forceinline__ bool has(unsigned int j) const { return j < per_warp && v0 + j < nv; }
+    __device__ __forceinline__ uint4 turn(unsigned int it, unsigned int j) const {
+        return it < staged_iters ? stage[32 * it] : load(v0 + j);
+    }
+
+    // f(vector, its number) for this lane's vectors, in ascending order, the
+    // next one on its way meanwhile.
     template <typename F>
     __device__ __forceinline__ void each(int lane, F f) const {
-        for (unsigned int j = lane, it = 0; j < per_warp && v0 + j < nv; j += 32, ++it)
-            f(it < staged_iters ? stage[32 * it] : load(v0 + j), v0 + j);
+        unsigned int j = lane, it = 0;
+        bool more = has(j);
+        uint4 next = make_uint4(0, 0, 0, 0);
+        if (more) next = turn(it, j);
+#pragma unroll 1
+        while (more) {
+            const uint4 r = next;
+            const unsigned int v = v0 + j;
+            j += 32;
+            more = has(j);
+            if (more) next = turn(++it, j);
+            f(r, v);
+        }
     }
 
     __device__ __forceinline__ uint32_t index(unsigned int v, int e) const { return v * V::N + e - pad; }
@@ -505,12 +489,77 @@ struct Slice {
 
 // A logit's place in the filters' order, ascending.
 __device__ __forceinline__ u64 item_of(uint32_t key, uint32_t index) { return (u64)~key << 32 | index; }
-__device__ __forceinline__ uint32_t item_weight(u64 item, const RowRule &rule) {
+__device__ __noinline__ uint32_t item_weight(u64 item, RowRule rule) {
     return token_weight(key_logit(~(uint32_t)(item >> 32)), rule);
 }
 constexpr u64 kKeepAll = ~0ull;
 
-__device__ __forceinline__ void write_token(const SampleArgs &a, u64 row, uint32_t index, u64 q, u64 total) {
+// Over the n gathered items up to `limit` that have a weight (of one each
+// with COUNT): the first, in order (or by index), at which the running sum of
+// weights reaches `target` (1 <= target <= the sum of all), and the sum
+// before it. A histogram of the places still in question, 512 bins between
+// the least and the greatest, then the same within the bin that holds the
+// crossing, until that is one item.
+template <bool COUNT>
+__device__ __noinline__ u64 block_select(uint32_t n, u64 limit, bool by_index, u64 target, const RowRule rule,
+                                         u64 *before_it) {
+    SampleShared &sh = block_shared();
+    u64 low = 0, high = ~0ull, base = 0;  // the places still in question
+    while (true) {
+        u64 lo = ~0ull, hi = ~0ull;  // hi: complemented, so that both are minima
+        sh.picks.sums.clear();
+        sh.picks.counts[threadIdx.x] = 0;
+        int shift = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+            for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
+                const u64 item = sh.items[kLocal + i], place = by_index ? item & 0xffffffffull : item;
+                if (item > limit || place < low || place > high) continue;
+                const uint32_t w = COUNT ? 1u : item_weight(item, rule);
+                if (w == 0) continue;
+                if (pass == 0) {
+                    lo = min(lo, place);
+                    hi = min(hi, ~place);
+                } else {
+                    const uint32_t bin = (uint32_t)((place - lo) >> shift);
+                    sh.picks.sums.add(bin, w);
+                    atomicAdd(&sh.picks.counts[bin], 1u);
+                }
+            }
+            if (pass == 0) {
+                lo = block_min(lo);
+                hi = ~block_min(hi);
+                shift = 55 - __clzll((hi - lo) | 511ull);
+            }
+        }
+        __syncthreads();
+        const u64 mine = (u64)sh.picks.sums.high[threadIdx.x] << 32 | sh.picks.sums.low[threadIdx.x];
+        const u64 before = base + block_before(mine);
+        if (before < target && target <= before + mine) {
+            sh.cast[0] = threadIdx.x;
+            sh.cast[1] = before;
+            sh.cast[2] = sh.picks.counts[threadIdx.x];
+        }
+        __syncthreads();
+        base = sh.cast[1];
+        low = lo + (sh.cast[0] << shift);
+        high = low + ((1ull << shift) - 1);
+        const bool one = sh.cast[2] == 1;
+        __syncthreads();  // cast and the bins are written again
+        if (one) break;
+    }
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
+        const u64 item = sh.items[kLocal + i], place = by_index ? item & 0xffffffffull : item;
+        if (item <= limit && place >= low && place <= high && (COUNT || item_weight(item, rule))) sh.cast[3] = item;
+    }
+    __syncthreads();
+    *before_it = base;
+    return sh.cast[3];
+}
+
+__device__ __noinline__ void write_token(const SampleArgs &a, u64 row, uint32_t index, u64 q, u64 total) {
     a.tokens[row] = (int32_t)index;
     if (a.probs) a.probs[row] = (float)((double)q / (double)total);
 }
@@ -521,103 +570,115 @@ __device__ __forceinline__ u64 top_p_target(float p, u64 total) {
     return (u64)ceil(__dmul_rn((double)p, (double)total));
 }
 
-// The sum of what the blocks put into a slot's first word.
-__device__ __forceinline__ u64 slot_total(const SampleShared &sh, Slot slot) {
-    u64 t = 0;
-    for (uint32_t c = 0; c < cluster_size(); ++c) t += sh.slots[slot][c][0];
-    return t;
+// The sum of what the first `blocks` blocks put into a slot.
+__device__ __noinline__ u64 slot_total(Slot slot, uint32_t blocks, int word = 0) {
+    SampleShared &sh = block_shared();
+    const uint32_t lane = threadIdx.x & 31;
+    return warp_total(lane < blocks ? sh.slots[slot][lane][word] : 0ull);
 }
 
-// What this warp keeps of the items up to `last`; FINITE: m and scale are.
-template <bool FINITE, typename T>
-__device__ __forceinline__ u64 kept_mass(const Slice<T> &sl, const RowRule &rule, u64 last) {
+// What the block's halves hold, from what its warps do (lane 0's word counts).
+__device__ __forceinline__ void halves_of(u64 warp_mass, u64 (&half)[2]) {
+    const u64 one = (threadIdx.x & 31) == 0 ? warp_mass : 0ull;
+    half[0] = block_total(threadIdx.x < kSThreads / 2 ? one : 0ull);
+    half[1] = block_total(threadIdx.x < kSThreads / 2 ? 0ull : one);
+}
+
+// The weights of a vector's logits up to `last`, 0 for the others; `finite`
+// says that m and scale are.
+template <typename T>
+__device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const uint4 &r, unsigned int v, RowRule rule,
+                                            bool finite, u64 last, uint32_t (&q)[Vec<T>::N]) {
     const float thr = last == kKeepAll ? -INFINITY : key_logit(~(uint32_t)(last >> 32));
-    const u64 m2 = pack2(rule.m, rule.m), scale2 = pack2(rule.scale, rule.scale);
-    u64 mass = 0;
-    sl.each(threadIdx.x & 31, [&](const uint4 &r, unsigned int v) {
-        if (!(Vec<T>::max(r) >= thr)) return;
-        float x[Vec<T>::N];
-        Vec<T>::unpack(r, x);
+    float x[Vec<T>::N];
+    Vec<T>::unpack(r, x);
+    u64 sum = 0;
 #pragma unroll
-        for (int e = 0; e < Vec<T>::N; e += 2) {
-            uint32_t q[2];
-            if (FINITE) {
-                float y[2];
-                weigh2(x[e], x[e + 1], m2, scale2, y, q);
-            } else {
-                q[0] = token_weight(x[e], rule);
-                q[1] = token_weight(x[e + 1], rule);
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool keep = x[e + i] > thr || (x[e + i] == thr && sl.index(v, e + i) <= (uint32_t)last);
-                mass += keep && q[i] >= rule.qmin ? q[i] : 0u;
-            }
+    for (int e = 0; e < Vec<T>::N; e += 2) {
+        uint32_t w[2];
+        if (finite) {
+            float y[2];
+            weigh2(x[e], x[e + 1], pack2(rule.m, rule.m), pack2(rule.scale, rule.scale), y, w);
+        } else {
+            w[0] = token_weight(x[e], rule);
+            w[1] = token_weight(x[e + 1], rule);
         }
-    });
-    return warp_total(mass);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bool keep = x[e + i] > thr || (x[e + i] == thr && sl.index(v, e + i) <= (uint32_t)last);
+            q[e + i] = keep && w[i] >= rule.qmin ? w[i] : 0u;
+            sum += q[e + i];
+        }
+    }
+    return sum;
 }
 
-// The draw among the items up to `last`, in index order, from what each block
-// keeps (the first words of `slot`) and, where it is known, this warp (else m
-// and scale are finite). The
-// block that holds the draw finds the warp's share that does, and walks it a
-// turn of 32 vectors a warp.
-template <bool WARPS_KNOWN, typename T>
-__device__ __noinline__ void draw(SampleShared &sh, const Slice<T> &own, const RowRule &rule, u64 last, u64 total,
-                                  Slot slot, u64 warp_mass, const SampleArgs &a, u64 row) {
+// The draw among the items up to `last`, in index order, by the block that
+// holds it: `before` is what the blocks before this one keep, `half` what
+// this one's halves do. It weighs that half again, a turn of 32 vectors a
+// warp, and walks the turn with the draw.
+template <typename T>
+__device__ __noinline__ void draw(const Slice<T> &own, RowRule rule, bool finite, u64 last, u64 total, u64 before,
+                                  const u64 (&half)[2], const SampleArgs &a, u64 row) {
+    SampleShared &sh = block_shared();
     constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const u64 r = draw_of(a.random[row], total);
-    u64 before = 0;
-    for (uint32_t c = 0; c < cluster_rank(); ++c) before += sh.slots[slot][c][0];
-    if (r < before || r - before >= sh.slots[slot][cluster_rank()][0]) return;
-    if (!WARPS_KNOWN) warp_mass = kept_mass<true>(own, rule, last);
-    __syncthreads();
-    if (lane == 0) sh.warp_a[warp] = warp_mass;
-    __syncthreads();
-    int w = 0;
-    while (r - before >= sh.warp_a[w]) before += sh.warp_a[w++];
-    const Slice<T> sl = own.of_warp(w - warp);
-    for (unsigned int j0 = 0, it0 = 0; j0 < sl.per_warp; j0 += 32 * kSWarps, it0 += kSWarps) {
-        const unsigned int it = it0 + warp, j = 32 * it + lane;
-        float x[N];
+    if (r < before || r - before >= half[0] + half[1]) return;
+    const bool second = r - before >= half[0];
+    if (second) before += half[0];
+    const int warp0 = second ? kSWarps / 2 : 0;
+    const unsigned int per = (own.per_warp + 31) / 32, turns = kSWarps / 2 * per;
+    u64 *mass = sh.items;  // by turn
+    u64 at = 0;
+    bool walk = false;  // first all turns, then the one
+    unsigned int t = warp;
+#pragma unroll 1
+    while (true) {
         uint32_t q[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) q[e] = 0;
         u64 sum = 0;
-        const bool in = j < sl.per_warp && sl.v0 + j < sl.nv;
-        if (in) Vec<T>::unpack(it < sl.staged_iters ? sl.stage[32 * it] : sl.load(sl.v0 + j), x);
+        const Slice<T> sl = own.of_warp(warp0 + (int)(t / per) - warp);
+        const unsigned int it = t % per, j = 32 * it + lane;
+        if (t < turns && sl.has(j)) sum = kept_weights(sl, sl.turn(it, j), sl.v0 + j, rule, finite, last, q);
+        if (walk) {
+            at += warp_inclusive(sum) - sum;
+            if (at <= r && r - at < sum) {
+                int chosen = 0;
+                uint32_t weight = 0;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            q[e] = 0;
-            if (in && x[e] > -INFINITY && item_of(key_of(x[e]), sl.index(sl.v0 + j, e)) <= last)
-                q[e] = token_weight(x[e], rule);
-            sum += q[e];
-        }
-        u64 inc = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const u64 o = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += o;
-        }
-        __syncthreads();
-        if (lane == 31) sh.warp_b[warp] = inc;
-        __syncthreads();
-        u64 turn = before, at = before;
-#pragma unroll
-        for (int o = 0; o < kSWarps; ++o) {
-            if (o == warp) at = turn;
-            turn += sh.warp_b[o];
-        }
-        at += inc - sum;
-        if (at <= r && r - at < sum) {
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                if (at <= r && r - at < q[e]) write_token(a, row, sl.index(sl.v0 + j, e), q[e], total);
-                at += q[e];
+                for (int e = 0; e < N; ++e) {
+                    if (at <= r && r - at < q[e]) {
+                        chosen = e;
+                        weight = q[e];
+                    }
+                    at += q[e];
+                }
+                write_token(a, row, sl.index(sl.v0 + j, chosen), weight, total);
             }
+            return;
         }
-        if (r < turn) return;
-        before = turn;
+        sum = warp_total(sum);
+        if (lane == 0 && t < turns) mass[t] = sum;
+        t += kSWarps;
+        if (t < turns) continue;
+        __syncthreads();
+        const unsigned int each = (turns + kSThreads - 1) / kSThreads, first = threadIdx.x * each;
+        sum = 0;
+        for (t = first; t < first + each && t < turns; ++t) sum += mass[t];
+        at = before + block_before(sum);
+        if (at <= r && r - at < sum) {
+            t = first;
+            while (r - at >= mass[t]) at += mass[t++];
+            sh.cast[0] = t;
+            sh.cast[1] = at;
+        }
+        __syncthreads();
+        if (warp != 0) return;
+        t = (unsigned int)sh.cast[0];
+        at = sh.cast[1];
+        walk = true;
     }
 }
 
@@ -625,18 +686,14 @@ __device__ __noinline__ void draw(SampleShared &sh, const Slice<T> &own, const R
 // holds the k-th largest, of 512 between the least and row_key, the greatest;
 // then of 512 in that bin, while it spans more than 1/64 of an octave (a
 // maximum of -inf widens the first).
-__device__ __forceinline__ uint32_t kth_bound(SampleShared &sh, const uint32_t *maxima, uint32_t n, uint32_t k,
+__device__ __forceinline__ uint32_t kth_bound(const uint32_t *maxima, uint32_t n, uint32_t k,
                                               uint32_t row_key) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    SampleShared &sh = block_shared();
     uint32_t *counts = sh.picks.counts;
     uint32_t least = row_key;
     for (uint32_t i = threadIdx.x; i < n; i += kSThreads) least = min(least, maxima[i]);
-    least = __reduce_min_sync(0xffffffffu, least);
-    if (lane == 0) sh.warp_a[warp] = least;
     counts[threadIdx.x] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSWarps; ++w) least = min(least, (uint32_t)sh.warp_a[w]);
+    least = (uint32_t)block_min(least);
     int shift = 23 - __clz((row_key - least) | 511u);
     uint32_t nearest = 0;  // distance from row_key at which the bins start
     while (true) {
@@ -646,7 +703,7 @@ __device__ __forceinline__ uint32_t kth_bound(SampleShared &sh, const uint32_t *
         }
         __syncthreads();
         const uint32_t mine = counts[threadIdx.x];
-        const uint32_t before = (uint32_t)block_before(mine, sh.warp_b);
+        const uint32_t before = (uint32_t)block_before(mine);
         if (before < k && k <= before + mine) {
             sh.cast[0] = nearest + (threadIdx.x << shift);
             sh.cast[1] = before;
@@ -664,30 +721,46 @@ __device__ __forceinline__ uint32_t kth_bound(SampleShared &sh, const uint32_t *
 }
 
 // Puts an item into this block's list.
-__device__ __forceinline__ void put(SampleShared &sh, u64 item) {
+__device__ __forceinline__ void put(u64 item) {
+    SampleShared &sh = block_shared();
     const uint32_t at = atomicAdd(&sh.n_list, 1u);
-    if (at < kLocal) sh.list[at] = item;
+    if (at < kLocal) sh.items[at] = item;
+}
+
+// f(x[e], e) for the elements that `test` names: few, so one copy of f.
+template <int N, typename Test, typename F>
+__device__ __forceinline__ void each_of(const float (&x)[N], Test test, F f) {
+    unsigned int mask = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+        if (test(x[e])) mask |= 1u << e;
+#pragma unroll 1
+    for (; mask; mask &= mask - 1) {
+        const int e = __ffs(mask) - 1;
+        float xe = x[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) xe = e == i ? x[i] : xe;
+        f(xe, e);
+    }
 }
 
 // The length of all blocks' lists, after an exchange of their lengths as
 // `slot`'s first word; over kList when one of them or all do not fit.
-__device__ __forceinline__ uint32_t gathered(const SampleShared &sh, Slot slot) {
-    uint32_t n = 0;
-    for (uint32_t c = 0; c < cluster_size(); ++c) {
-        const uint32_t one = (uint32_t)sh.slots[slot][c][0];
-        n += one <= kLocal ? one : kList + 1;
-    }
-    return n;
+__device__ __forceinline__ uint32_t gathered(Slot slot) {
+    SampleShared &sh = block_shared();
+    const uint32_t lane = threadIdx.x & 31, one = lane < cluster_size() ? (uint32_t)sh.slots[slot][lane][0] : 0u;
+    return __reduce_add_sync(0xffffffffu, one <= kLocal ? one : kList + 1);
 }
 
-// All blocks' n items, one list after another, in rank 0's gather (called
-// there, when they fit): every thread finds its items' blocks by itself, so
-// that all of them are on their way at once.
-__device__ __forceinline__ void pull(SampleShared &sh, Slot slot, uint32_t n) {
+// All blocks' n items, one list after another, in this block (when they fit):
+// every thread finds its items' blocks by itself, so that all of them are on
+// their way at once.
+__device__ __forceinline__ void pull(Slot slot, uint32_t n) {
+    SampleShared &sh = block_shared();
     for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
         uint32_t c = 0, at = i;
         while (at >= (uint32_t)sh.slots[slot][c][0]) at -= (uint32_t)sh.slots[slot][c++][0];
-        sh.gather[i] = ld_cluster_u64(at_rank(sh.list + at, c));
+        sh.items[kLocal + i] = ld_cluster_u64(at_rank(sh.items + at, c));
     }
     __syncthreads();
 }
@@ -695,8 +768,9 @@ __device__ __forceinline__ void pull(SampleShared &sh, Slot slot, uint32_t n) {
 // The token among the n gathered items, which hold all that the filters keep:
 // the first k of them in order, and of those the top-p prefix (0 < p < 1),
 // measured against `total` if that is not 0, else against their own sum.
-__device__ __noinline__ void finish_list(SampleShared &sh, uint32_t n, uint32_t k, float p, u64 total,
+__device__ __noinline__ void finish_list(uint32_t n, uint32_t k, float p, u64 total,
                                          const RowRule &rule, const SampleArgs &a, u64 row) {
+    SampleShared &sh = block_shared();
     const bool cut_p = p > 0.0f && p < 1.0f;
     const uint32_t word = a.random[row];
     if (n <= kRanked) {
@@ -704,16 +778,16 @@ __device__ __noinline__ void finish_list(SampleShared &sh, uint32_t n, uint32_t 
         uint32_t team = 2;
         while (team < 16 && 2 * team * n <= kSThreads) team *= 2;
         const uint32_t i = threadIdx.x / team, part = threadIdx.x % team;
-        u64 *weight = sh.list;  // pulled: free
-        const u64 item = i < n ? sh.gather[i] : ~0ull;
+        u64 *weight = sh.items;  // pulled: free
+        const u64 item = i < n ? sh.items[kLocal + i] : ~0ull;
         const u64 q = i < n ? item_weight(item, rule) : 0u;
         if (part == 0) weight[i] = q;
         __syncthreads();
         uint32_t rank = 0;
         u64 before = 0;
-#pragma unroll 4
+#pragma unroll 2
         for (uint32_t j = part; j < n; j += team) {
-            const bool first = sh.gather[j] < item;
+            const bool first = sh.items[kLocal + j] < item;
             rank += first;
             before += first ? weight[j] : 0ull;
         }
@@ -722,56 +796,38 @@ __device__ __noinline__ void finish_list(SampleShared &sh, uint32_t n, uint32_t 
             before += __shfl_xor_sync(0xffffffffu, before, d);
         }
         u64 kept = i < n && rank < k ? q : 0ull;
-        if (total == 0) total = block_total(part == 0 ? kept : 0ull, sh.warp_a);
+        if (total == 0) total = block_total(part == 0 ? kept : 0ull);
         if (cut_p) {
             if (before >= top_p_target(p, total)) kept = 0;
-            total = block_total(part == 0 ? kept : 0ull, sh.warp_b);
+            total = block_total(part == 0 ? kept : 0ull);
         }
         __syncthreads();
         if (part == 0) weight[i] = kept;
         __syncthreads();
         u64 at = 0;
-#pragma unroll 4
-        for (uint32_t j = part; j < n; j += team) at += (uint32_t)sh.gather[j] < (uint32_t)item ? weight[j] : 0ull;
+#pragma unroll 2
+        for (uint32_t j = part; j < n; j += team)
+            at += (uint32_t)sh.items[kLocal + j] < (uint32_t)item ? weight[j] : 0ull;
         for (uint32_t d = 1; d < team; d *= 2) at += __shfl_xor_sync(0xffffffffu, at, d);
         const u64 r = draw_of(word, total);
         if (part == 0 && at <= r && r < at + kept) write_token(a, row, (uint32_t)item, kept, total);
         return;
     }
-    u64 item[kOwn], before;
-    uint32_t q[kOwn], one[kOwn];
-#pragma unroll
-    for (int c = 0; c < kOwn; ++c) {
-        const uint32_t i = threadIdx.x + c * kSThreads;
-        one[c] = i < n;
-        item[c] = i < n ? sh.gather[i] : ~0ull;
-        q[c] = i < n ? item_weight(item[c], rule) : 0u;
-    }
-    if (k < n) {
-        const u64 last = block_select(sh, item, one, k, &before);
-#pragma unroll
-        for (int c = 0; c < kOwn; ++c)
-            if (item[c] > last) q[c] = 0;
-    }
+    u64 last = kKeepAll, before;
+    if (k < n) last = block_select<true>(n, last, false, k, rule, &before);
     if (total == 0) {
         u64 sum = 0;
-#pragma unroll
-        for (int c = 0; c < kOwn; ++c) sum += q[c];
-        total = block_total(sum, sh.warp_a);
+#pragma unroll 1
+        for (uint32_t i = threadIdx.x; i < n; i += kSThreads)
+            if (sh.items[kLocal + i] <= last) sum += item_weight(sh.items[kLocal + i], rule);
+        total = block_total(sum);
     }
     if (cut_p) {
-        const u64 last = block_select(sh, item, q, top_p_target(p, total), &before);
-#pragma unroll
-        for (int c = 0; c < kOwn; ++c)
-            if (item[c] > last) q[c] = 0;
+        last = block_select<false>(n, last, false, top_p_target(p, total), rule, &before);
         total = before + item_weight(last, rule);
     }
-#pragma unroll
-    for (int c = 0; c < kOwn; ++c) item[c] &= 0xffffffffull;  // the index: the draw's order
-    const u64 index = block_select(sh, item, q, draw_of(word, total) + 1, &before);
-#pragma unroll
-    for (int c = 0; c < kOwn; ++c)
-        if (q[c] && item[c] == index) write_token(a, row, (uint32_t)index, q[c], total);
+    const u64 chosen = block_select<false>(n, last, true, draw_of(word, total) + 1, rule, &before);
+    if (threadIdx.x == 0) write_token(a, row, (uint32_t)chosen, item_weight(chosen, rule), total);
 }
 
 // The key at which the running total over the items up to `last`, keys in
@@ -780,9 +836,11 @@ __device__ __noinline__ void finish_list(SampleShared &sh, uint32_t n, uint32_t 
 // `level` numbers the levels of a row's selections (their two buffers swap:
 // a slow block may still read the last level's).
 template <bool MASS, typename T>
-__device__ __noinline__ void radix_select(SampleShared &sh, const Slice<T> &sl, const RowRule &rule, u64 last,
+__device__ __noinline__ void radix_select(const Slice<T> &sl, const RowRule &rule, u64 last,
                                           u64 target, int &level, uint32_t *tau, u64 *missing) {
+    SampleShared &sh = block_shared();
     uint32_t prefix = 0, mask = 0;
+#pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8, ++level) {
         SumBins<256> &hist = sh.digits[level & 1];
         hist.clear();
@@ -807,7 +865,7 @@ __device__ __noinline__ void radix_select(SampleShared &sh, const Slice<T> &sl, 
             for (uint32_t c = 0; c < cluster_size(); ++c)
                 mine += (u64)ld_cluster(at_rank(&hist.low[255 - threadIdx.x], c)) +
                         ((u64)ld_cluster(at_rank(&hist.high[255 - threadIdx.x], c)) << 32);
-        const u64 before = block_before(mine, sh.warp_a);
+        const u64 before = block_before(mine);
         if (before < target && target <= before + mine) {
             sh.cast[0] = 255u - threadIdx.x;
             sh.cast[1] = target - before;
@@ -825,9 +883,10 @@ __device__ __noinline__ void radix_select(SampleShared &sh, const Slice<T> &sl, 
 // The `nth` logit (from 1, by index) with key tau, as an item; -inf entries
 // past the row's ends do not count.
 template <typename T>
-__device__ __noinline__ u64 nth_tie(SampleShared &sh, const Slice<T> &sl, uint32_t tau, u64 nth, Slot ties_slot,
+__device__ __noinline__ u64 nth_tie(const Slice<T> &sl, uint32_t tau, u64 nth, Slot ties_slot,
                                     Slot at_slot) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    SampleShared &sh = block_shared();
+    const int lane = threadIdx.x & 31;
     auto tied = [&](const uint4 &r, unsigned int v) {  // by element
         float x[Vec<T>::N];
         Vec<T>::unpack(r, x);
@@ -842,29 +901,18 @@ __device__ __noinline__ u64 nth_tie(SampleShared &sh, const Slice<T> &sl, uint32
     u64 mine = 0;
     sl.each(lane, [&](const uint4 &r, unsigned int v) { mine += __popc(tied(r, v)); });
     mine = warp_total(mine);
-    __syncthreads();
-    if (lane == 0) sh.warp_a[warp] = mine;
     if (threadIdx.x == 0) sh.cast[0] = ~0ull;
-    __syncthreads();
-    u64 before = 0, block_ties = 0;
-    for (int w = 0; w < kSWarps; ++w) {
-        before += w < warp ? sh.warp_a[w] : 0ull;
-        block_ties += sh.warp_a[w];
-    }
-    exchange(sh, ties_slot, block_ties, 0);
-    for (uint32_t c = 0; c < cluster_rank(); ++c) before += sh.slots[ties_slot][c][0];
+    u64 before = block_before(lane == 0 ? mine : 0ull);  // of lane 0: the warps' before
+    before = __shfl_sync(0xffffffffu, before, 0);
+    exchange(ties_slot, block_total(lane == 0 ? mine : 0ull), 0);
+    before += slot_total(ties_slot, cluster_rank());
     if (before < nth && nth <= before + mine)  // this warp's
         for (unsigned int j0 = 0, it = 0; j0 < sl.per_warp; j0 += 32, ++it) {
             const unsigned int j = j0 + lane;
             unsigned int t = 0;
             if (j < sl.per_warp && sl.v0 + j < sl.nv)
                 t = tied(it < sl.staged_iters ? sl.stage[32 * it] : sl.load(sl.v0 + j), sl.v0 + j);
-            u64 inc = __popc(t);
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const u64 o = __shfl_up_sync(0xffffffffu, inc, d);
-                if (lane >= d) inc += o;
-            }
+            const u64 inc = warp_inclusive(__popc(t));
             const u64 at = before + inc - __popc(t);
             if (at < nth && nth <= before + inc) {
                 for (u64 skip = nth - at - 1; skip > 0; --skip) t &= t - 1;
@@ -873,45 +921,51 @@ __device__ __noinline__ u64 nth_tie(SampleShared &sh, const Slice<T> &sl, uint32
             before += __shfl_sync(0xffffffffu, inc, 31);
         }
     __syncthreads();
-    exchange(sh, at_slot, sh.cast[0], 0);
-    u64 item = ~0ull;
-    for (uint32_t c = 0; c < cluster_size(); ++c) item = min(item, sh.slots[at_slot][c][0]);
-    return item;
+    exchange(at_slot, sh.cast[0], 0);
+    return warp_min(lane < (int)cluster_size() ? sh.slots[at_slot][lane][0] : ~0ull);
 }
 
 // The filters by selection on the logits' bits, then the draw: right for
 // every row, and the way of those the other paths do not take.
 template <typename T>
-__device__ __noinline__ void sample_by_selection(SampleShared &sh, const Slice<T> &sl, const RowRule &rule, uint32_t k,
+__device__ __noinline__ void sample_by_selection(const Slice<T> &sl, const RowRule &rule, uint32_t k,
                                                  float p, const SampleArgs &a, u64 row) {
     u64 last = kKeepAll, missing;
     uint32_t tau;
     int level = 0;
     if (k > 0) {
-        radix_select<false>(sh, sl, rule, kKeepAll, k, level, &tau, &missing);
-        if (tau > kKeyOfMinusInf) last = nth_tie(sh, sl, tau, missing, kSlotTies, kSlotTieAt);
+        radix_select<false>(sl, rule, kKeepAll, k, level, &tau, &missing);
+        if (tau > kKeyOfMinusInf) last = nth_tie(sl, tau, missing, kSlotTies, kSlotTieAt);
     }
-    u64 mass = kept_mass<false>(sl, rule, last);
-    exchange(sh, kSlotSum, block_total((threadIdx.x & 31) == 0 ? mass : 0ull, sh.warp_c), 0);
-    u64 total = slot_total(sh, kSlotSum);
+    auto kept = [&](u64 (&half)[2]) {
+        u64 mass = 0;
+        sl.each(threadIdx.x & 31, [&](const uint4 &r, unsigned int v) {
+            uint32_t q[Vec<T>::N];
+            mass += kept_weights(sl, r, v, rule, false, last, q);
+        });
+        halves_of(warp_total(mass), half);
+    };
+    u64 half[2];
+    kept(half);
+    exchange(kSlotSum, half[0] + half[1], 0);
+    u64 total = slot_total(kSlotSum, cluster_size());
+    Slot slot = kSlotSum;
     if (p > 0.0f && p < 1.0f) {
         const u64 want = top_p_target(p, total);
-        radix_select<true>(sh, sl, rule, last, want, level, &tau, &missing);
+        radix_select<true>(sl, rule, last, want, level, &tau, &missing);
         const u64 q = token_weight(key_logit(tau), rule), ties = (missing + q - 1) / q;
-        last = nth_tie(sh, sl, tau, ties, kSlotTies2, kSlotTieAt2);
+        last = nth_tie(sl, tau, ties, kSlotTies2, kSlotTieAt2);
         total = want - missing + ties * q;
-        mass = kept_mass<false>(sl, rule, last);
-        exchange(sh, kSlotDraw, block_total((threadIdx.x & 31) == 0 ? mass : 0ull, sh.warp_c), 0);
-        draw<true>(sh, sl, rule, last, total, kSlotDraw, mass, a, row);
-        return;
+        kept(half);
+        exchange(kSlotDraw, half[0] + half[1], 0);
+        slot = kSlotDraw;
     }
-    draw<true>(sh, sl, rule, last, total, kSlotSum, mass, a, row);
+    draw(sl, rule, false, last, total, slot_total(slot, cluster_rank()), half, a, row);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a) {
-    extern __shared__ __align__(16) unsigned char s_mem[];
-    SampleShared &sh = *reinterpret_cast<SampleShared *>(s_mem);
+    SampleShared &sh = block_shared();
     using V = Vec<T>;
     const uint32_t rank = cluster_rank(), blocks = cluster_size();
     const u64 row = blockIdx.x / blocks;
@@ -929,7 +983,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         sl.per_warp = a.per_warp;
         sl.staged_iters = a.staged_iters;
         sl.v0 = (rank * kSWarps + warp) * a.per_warp;
-        sl.stage = reinterpret_cast<uint4 *>(s_mem + sizeof(SampleShared)) + warp * 32 * a.staged_iters + lane;
+        sl.stage = reinterpret_cast<uint4 *>(&sh + 1) + warp * 32 * a.staged_iters + lane;
     }
     const float t = a.temperature ? a.temperature[row] : 1.0f;
     const int k_arg = a.top_k ? a.top_k[row] : 0;
@@ -938,24 +992,10 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     const uint32_t k = k_arg > 0 && (uint32_t)k_arg < sl.n ? (uint32_t)k_arg : 0u;
     const bool cut_p = p > 0.0f && p < 1.0f;
 
-    // The blocks that run after these find their rows in L2: HBM stays busy while these compute
-    // (256 rows of 262144 f32: @@ us without, @@ with).
-    if (a.ahead && threadIdx.x == 0 && row + a.ahead < a.rows) {
-        const uintptr_t from = reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) +
-                                                           (row + a.ahead) * a.row_stride);
-        const uintptr_t first = (from + 15) & ~(uintptr_t)15, end = (from + a.vocab * sizeof(T)) & ~(uintptr_t)15;
-        const uintptr_t at = first + (uintptr_t)rank * kSWarps * a.per_warp * 16;
-        if (at < end) {
-            const uintptr_t bytes = min(end - at, (uintptr_t)kSWarps * a.per_warp * 16);
-            bulk_prefetch_l2(reinterpret_cast<const void *>(at), (unsigned int)bytes);
-        }
-    }
-
     // the row's largest logit, and for top-k the maxima its bound comes from
     const float thread_max = sl.first_pass(lane);
     const uint32_t thread_key = key_of(thread_max == thread_max ? thread_max : -INFINITY);
     const uint32_t warp_key = __reduce_max_sync(0xffffffffu, thread_key);
-    if (lane == 0) sh.warp_a[warp] = warp_key;
     // top-k: maxima of groups of threads, at least 2 k groups in the row
     uint32_t group = 32;
     while (group > 1 && kSThreads / group * blocks < 2 * k) group /= 2;
@@ -967,18 +1007,15 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         group_key = thread_key;
         for (uint32_t d = 1; d < group; d *= 2) group_key = max(group_key, __shfl_xor_sync(0xffffffffu, group_key, d));
     }
-    __syncthreads();
-    uint32_t block_key = 0;
-#pragma unroll
-    for (int w = 0; w < kSWarps; ++w) block_key = max(block_key, (uint32_t)sh.warp_a[w]);
+    const uint32_t block_key = ~(uint32_t)block_min(~warp_key);
     cluster_wait();
-    uint32_t *maxima = reinterpret_cast<uint32_t *>(sh.gather);  // of all the row's groups
+    uint32_t *maxima = reinterpret_cast<uint32_t *>(sh.items + kLocal);  // of all the row's groups
     if (by_groups && threadIdx.x % group == 0)
         for (uint32_t c = 0; c < blocks; ++c)
             st_cluster(at_rank(maxima + rank * groups + threadIdx.x / group, c), group_key);
-    exchange(sh, kSlotMax, block_key, 0);
-    uint32_t row_key = 0;
-    for (uint32_t c = 0; c < blocks; ++c) row_key = max(row_key, (uint32_t)sh.slots[kSlotMax][c][0]);
+    exchange(kSlotMax, block_key, 0);
+    const uint32_t row_key =
+        __reduce_max_sync(0xffffffffu, lane < (int)blocks ? (uint32_t)sh.slots[kSlotMax][lane][0] : 0u);
     if (row_key <= kKeyOfMinusInf) {  // the mask leaves nothing
         if (rank == 0 && threadIdx.x == 0) {
             a.tokens[row] = -1;
@@ -1002,14 +1039,9 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
                 for (int e = V::N - 1; e >= 0; --e)
                     if (x[e] == rule.m) first = sl.index(v, e);
             });
-        first = __reduce_min_sync(0xffffffffu, first);
-        if (lane == 0) sh.warp_b[warp] = first;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kSWarps; ++w) first = min(first, (uint32_t)sh.warp_b[w]);
-        exchange(sh, kSlotFirst, first, 0);
+        exchange(kSlotFirst, block_min(first), 0);
+        first = __reduce_min_sync(0xffffffffu, lane < (int)blocks ? (uint32_t)sh.slots[kSlotFirst][lane][0] : first);
         if (rank == 0 && threadIdx.x == 0) {
-            for (uint32_t c = 0; c < blocks; ++c) first = min(first, (uint32_t)sh.slots[kSlotFirst][c][0]);
             a.tokens[row] = (int32_t)first;
             if (a.probs) a.probs[row] = 1.0f;
         }
@@ -1017,23 +1049,22 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     }
     const bool finite = rule.m < INFINITY && rule.scale < INFINITY;
     if (finite && bounded) {
-        const uint32_t bound = by_groups ? kth_bound(sh, maxima, groups * blocks, k, row_key) : 0u;
+        const uint32_t bound = by_groups ? kth_bound(maxima, groups * blocks, k, row_key) : 0u;
         const float thr = bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY;
         sl.each(lane, [&](const uint4 &r, unsigned int v) {
             if (!(V::max(r) >= thr)) return;
             float x[V::N];
             V::unpack(r, x);
-#pragma unroll
-            for (int e = 0; e < V::N; ++e)
-                if (x[e] >= thr && x[e] > -INFINITY) put(sh, item_of(key_of(x[e]), sl.index(v, e)));
+            each_of<V::N>(x, [&](float xe) { return xe >= thr && xe > -INFINITY; },
+                          [&](float xe, int e) { put(item_of(key_of(xe), sl.index(v, e))); });
         });
         __syncthreads();
-        exchange(sh, kSlotFirst, sh.n_list, 0);
-        const uint32_t n = gathered(sh, kSlotFirst);
+        exchange(kSlotFirst, sh.n_list, 0);
+        const uint32_t n = gathered(kSlotFirst);
         if (n <= kList) {
-            if (rank == 0) pull(sh, kSlotFirst, n);
+            if (rank == 0) pull(kSlotFirst, n);
             cluster_arrive();
-            if (rank == 0) finish_list(sh, n, k, p, 0ull, rule, a, row);
+            if (rank == 0) finish_list(n, k, p, 0ull, rule, a, row);
             cluster_wait();
             return;
         }
@@ -1058,15 +1089,18 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
                     mass += q[1] >= rule.qmin ? q[1] : 0u;
                 }
             });
-            mass = warp_total(mass);
-            exchange(sh, kSlotFirst, block_total(lane == 0 ? mass : 0ull, sh.warp_c), 0);
-            draw<true>(sh, sl, rule, kKeepAll, slot_total(sh, kSlotFirst), kSlotFirst, mass, a, row);
+            u64 half[2];
+            halves_of(warp_total(mass), half);
+            exchange(kSlotFirst, half[0] + half[1], 0);
+            draw(sl, rule, true, kKeepAll, slot_total(kSlotFirst, blocks), slot_total(kSlotFirst, rank), half, a, row);
             return;
         }
         const float cut_y = fminf(31.0f, log2f((float)sl.n / (1.0f - p)) + 0.1f);
         const uint32_t floor_q = max(max(rule.qmin, exp2_weight(cut_y)), 1u);  // the histogram's least weight
-        sh.bins.clear();
+        sh.bins[0].clear();
+        sh.bins[1].clear();
         __syncthreads();
+        SumBins<kBins> &bins = sh.bins[warp / (kSWarps / 2)];
         sl.each(lane, [&](const uint4 &r, unsigned int) {
             if (!(V::max(r) >= zero)) return;
             float x[V::N];
@@ -1079,113 +1113,107 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     mass += q[i] >= rule.qmin ? q[i] : 0u;
-                    if (q[i] >= floor_q) sh.bins.add(bin_of(y[i]), q[i]);
+                    if (q[i] >= floor_q) bins.add(bin_of(y[i]), q[i]);
                 }
             }
         });
-        exchange(sh, kSlotFirst, block_total(mass, sh.warp_c), 0);
-        const u64 total = slot_total(sh, kSlotFirst), want = top_p_target(p, total);
-        // the bin in which the running sum reaches `want`, two bins a thread
-        u64 low[kMaxCluster], high[kMaxCluster];
+        __syncthreads();
+        // two bins a thread, of both halves and (for the other blocks) their sum
+        u64 own[2][2], *sums = sh.items + kLocal;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int b = 2 * threadIdx.x + i;
+            own[0][i] = (u64)sh.bins[0].high[b] << 32 | sh.bins[0].low[b];
+            own[1][i] = (u64)sh.bins[1].high[b] << 32 | sh.bins[1].low[b];
+            sums[b] = own[0][i] + own[1][i];
+        }
+        exchange(kSlotFirst, block_total(mass), 0);
+        const u64 total = slot_total(kSlotFirst, blocks), want = top_p_target(p, total);
+        // the bin in which the running sum reaches `want`
+        u64 part[kMaxCluster][2];
 #pragma unroll
         for (uint32_t c = 0; c < kMaxCluster; ++c) {
-            low[c] = c < blocks ? ld_cluster_u64(at_rank(&sh.bins.low[2 * threadIdx.x], c)) : 0ull;
-            high[c] = c < blocks ? ld_cluster_u64(at_rank(&sh.bins.high[2 * threadIdx.x], c)) : 0ull;
+            part[c][0] = part[c][1] = 0;
+            if (c < blocks) ld_cluster_u64x2(at_rank(sums + 2 * threadIdx.x, c), part[c][0], part[c][1]);
         }
         u64 bin_mass[2] = {0, 0};
 #pragma unroll
         for (uint32_t c = 0; c < kMaxCluster; ++c) {
-            bin_mass[0] += (low[c] & 0xffffffffull) | high[c] << 32;
-            bin_mass[1] += low[c] >> 32 | (high[c] >> 32) << 32;
+            bin_mass[0] += part[c][0];
+            bin_mass[1] += part[c][1];
         }
-        // at most so many logits with a weight lie in a bin: none weighs less than its far end,
-        // less more than the recipe's error
-        u64 at_most[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t far = exp2_weight(((float)(2 * threadIdx.x + i) + 0.5f) * (1.0f / 32.0f));
-            const uint32_t slack = (far >> 16) + 2;
-            const uint32_t least = max(far > slack ? far - slack : 0u, floor_q);
-            at_most[i] = (u64)(__fdividef((float)bin_mass[i], (float)least) * 1.001f) + (bin_mass[i] ? 1u : 0u);
-        }
-        const u64 own[2] = {(u64)sh.bins.high[2 * threadIdx.x] << 32 | sh.bins.low[2 * threadIdx.x],
-                            (u64)sh.bins.high[2 * threadIdx.x + 1] << 32 | sh.bins.low[2 * threadIdx.x + 1]};
-        const u64 before = block_before(bin_mass[0] + bin_mass[1], sh.warp_a);
-        const u64 count_before = block_before(at_most[0] + at_most[1], sh.warp_b);
+        const u64 before = block_before(bin_mass[0] + bin_mass[1]);
         if (before < want && want <= before + bin_mass[0] + bin_mass[1]) {
             const bool second = want > before + bin_mass[0];
             sh.cast[0] = 2 * threadIdx.x + second;
             sh.cast[1] = before + (second ? bin_mass[0] : 0ull);
-            sh.cast[2] = count_before + at_most[0] + (second ? at_most[1] : 0ull);
+            sh.cast[2] = before + bin_mass[0] + (second ? bin_mass[1] : 0ull);
         }
         __syncthreads();
         const uint32_t bin = (uint32_t)sh.cast[0];
         const u64 above = sh.cast[1];
-        const bool all = sh.cast[2] <= kList;
-        const u64 block_above = block_total((2 * threadIdx.x < bin ? own[0] : 0ull) +
-                                                (2 * threadIdx.x + 1 < bin ? own[1] : 0ull), sh.warp_c);
+        // none in a bin up to this one weighs less than its far end, less more than the recipe's
+        // error: are there few enough to gather all of them?
+        const uint32_t far = exp2_weight(((float)bin + 0.5f) * (1.0f / 32.0f)), slack = (far >> 16) + 2;
+        const bool all = sh.cast[2] <= (u64)max(far > slack ? far - slack : 0u, floor_q) * kList;
+        u64 half[2];  // of the bins before it
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            half[h] = block_total((2 * threadIdx.x < bin ? own[h][0] : 0ull) +
+                                  (2 * threadIdx.x + 1 < bin ? own[h][1] : 0ull));
         // every logit in a bin up to this one is at or above thr, every one in a bin from it on at
         // or below cap
         const float thr = __fsub_rd(rule.m, __fdiv_ru(((float)bin + 1.0f) * (1.0f / 32.0f), rule.scale));
-        const float cap = all || bin == 0 ? INFINITY
-                                          : __fsub_ru(rule.m, __fdiv_rd(((float)bin - 1.0f) * (1.0f / 32.0f), rule.scale));
+        const float cap = all || bin == 0
+                              ? INFINITY
+                              : __fsub_ru(rule.m, __fdiv_rd(((float)bin - 1.0f) * (1.0f / 32.0f), rule.scale));
         sl.each(lane, [&](const uint4 &r, unsigned int v) {
             if (!(V::max(r) >= thr)) return;
             float x[V::N];
             V::unpack(r, x);
-            unsigned int near = 0;
-#pragma unroll
-            for (int e = 0; e < V::N; ++e)
-                if (x[e] >= thr && x[e] <= cap) near |= 1u << e;
-#pragma unroll 1
-            for (; near; near &= near - 1) {
-                const int e = __ffs(near) - 1;
-                float xe = x[0];
-#pragma unroll
-                for (int i = 1; i < V::N; ++i) xe = e == i ? x[i] : xe;
-                const float y = __fmul_rn(__fsub_rn(rule.m, xe), rule.scale);
-                if (!(y < 32.0f) || exp2_weight(y) < floor_q) continue;
-                const uint32_t b = bin_of(y);
-                if (all ? b <= bin : b == bin) put(sh, item_of(key_of(xe), sl.index(v, e)));
-            }
+            each_of<V::N>(x, [&](float xe) { return xe >= thr && xe <= cap; },
+                          [&](float xe, int e) {
+                              const float y = __fmul_rn(__fsub_rn(rule.m, xe), rule.scale);
+                              if (!(y < 32.0f) || exp2_weight(y) < floor_q) return;
+                              const uint32_t b = bin_of(y);
+                              if (all ? b <= bin : b == bin) put(item_of(key_of(xe), sl.index(v, e)));
+                          });
         });
         __syncthreads();
-        exchange(sh, kSlotSecond, sh.n_list, 0);
-        const uint32_t n = gathered(sh, kSlotSecond);
+        exchange(kSlotSecond, sh.n_list, half[0] + half[1]);
+        const uint32_t n = gathered(kSlotSecond);
         if (n <= kList) {
-            if (rank == 0) pull(sh, kSlotSecond, n);
+            if (!all || rank == 0) pull(kSlotSecond, n);
+            cluster_arrive();  // no block leaves, or writes over its list, while others read it
             if (all) {
-                cluster_arrive();
-                if (rank == 0) finish_list(sh, n, 0xffffffffu, p, total, rule, a, row);
+                if (rank == 0) finish_list(n, 0xffffffffu, p, total, rule, a, row);
                 cluster_wait();
-                return;
-            }
-            u64 last = 0, left = 0;
-            if (rank == 0) {  // the crossing among the gathered
-                u64 item[kOwn];
-                uint32_t q[kOwn];
-#pragma unroll
-                for (int c = 0; c < kOwn; ++c) {
-                    const uint32_t i = threadIdx.x + c * kSThreads;
-                    item[c] = i < n ? sh.gather[i] : ~0ull;
-                    q[c] = i < n ? item_weight(item[c], rule) : 0u;
-                }
-                last = block_select(sh, item, q, want - above, &left);
+            } else {  // every block finds the crossing among the gathered, and what is kept of them where
+                u64 left;
+                const u64 last = block_select<false>(n, kKeepAll, false, want - above, rule, &left);
                 left += above + item_weight(last, rule);
+                const uint32_t from = (uint32_t)slot_total(kSlotSecond, rank), to = from + sh.n_list;
+                const uint32_t second = (rank * kSWarps + kSWarps / 2) * sl.per_warp * V::N;  // its first element
+                u64 ahead = 0, in[2] = {0, 0};
+#pragma unroll 1
+                for (uint32_t i = threadIdx.x; i < to; i += kSThreads) {
+                    const u64 item = sh.items[kLocal + i];
+                    if (item > last) continue;
+                    const u64 q = item_weight(item, rule);
+                    if (i < from) ahead += q;
+                    else if ((uint32_t)item + sl.pad < second) in[0] += q;
+                    else in[1] += q;
+                }
+                ahead = block_total(ahead);
+                half[0] += block_total(in[0]);
+                half[1] += block_total(in[1]);
+                cluster_wait();
+                draw(sl, rule, true, last, left, ahead + slot_total(kSlotSecond, rank, 1), half, a, row);
             }
-            exchange(sh, kSlotThird, last, left);
-            last = sh.slots[kSlotThird][0][0];
-            left = sh.slots[kSlotThird][0][1];
-            // this block's part: its bins before the crossing one, and its items up to the crossing
-            u64 part = 0;
-            for (uint32_t i = threadIdx.x; i < sh.n_list; i += kSThreads)
-                if (sh.list[i] <= last) part += item_weight(sh.list[i], rule);
-            exchange(sh, kSlotDraw, block_total(part, sh.warp_c) + block_above, 0);
-            draw<false>(sh, sl, rule, last, left, kSlotDraw, 0ull, a, row);
             return;
         }
     }
-    sample_by_selection(sh, sl, rule, k, p, a, row);
+    sample_by_selection(sl, rule, k, p, a, row);
 }
 
 // ---------------------------------------------------------------------------
@@ -1194,15 +1222,17 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
 
 // Turns of 32 vectors a warp keeps in shared memory: two blocks an SM.
 constexpr unsigned int kStageBytes = kSWarps * 32 * 16;
-constexpr unsigned int kMaxStaged = 9;
-static_assert(sizeof(SampleShared) % 16 == 0 && offsetof(SampleShared, slots) % 16 == 0, "16-byte accesses");
+constexpr unsigned int kMaxStaged = 8;
+static_assert(sizeof(SampleShared) % 16 == 0 && offsetof(SampleShared, slots) % 16 == 0 && kLocal % 2 == 0,
+              "16-byte accesses");
 static_assert(2 * (sizeof(SampleShared) + kMaxStaged * kStageBytes + 1024) <= 228 * 1024, "two blocks an SM");
 
 template <typename T>
 static int sample_launch(SampleArgs a, cudaStream_t stream) {
     // The smallest cluster whose slices fit shared memory, then larger while
     // blocks are fewer than the GPU holds and a thread keeps a vector.
-    const unsigned int nv = (unsigned int)((a.vocab + 2 * Vec<T>::N - 2) / Vec<T>::N);
+    const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride % Vec<T>::N == 0;
+    const unsigned int nv = (unsigned int)((a.vocab + (aligned ? 1 : 2) * (Vec<T>::N - 1)) / Vec<T>::N);
     unsigned int blocks = 1;
     while (blocks < kMaxCluster &&
            (nv > blocks * kMaxStaged * kSThreads || (a.rows * blocks < 256 && nv > blocks * kSThreads)))
@@ -1215,8 +1245,6 @@ static int sample_launch(SampleArgs a, cudaStream_t stream) {
     if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)(sizeof(SampleShared) + kMaxStaged * kStageBytes)) != cudaSuccess)
         return U32SCAN_ECUDA;
-    const unsigned int resident = 2 * 152 / blocks;  // rows at a time
-    a.ahead = a.rows > resident ? resident : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned int)a.rows * blocks);
     cfg.blockDim = dim3(kSThreads);
@@ -1247,7 +1275,7 @@ extern "C" int sample_tokens(const void *logits, int type, size_t rows, size_t v
     for (const void *p : {(const void *)temperature, (const void *)top_k, (const void *)top_p, (const void *)min_p,
                           (const void *)random, (const void *)tokens, (const void *)probs})
         if (reinterpret_cast<uintptr_t>(p) & 3) return U32SCAN_EINVAL;
-    const SampleArgs a{logits, rows, vocab, row_stride, temperature, top_k, top_p, min_p, random, tokens, probs, 0, 0, 0};
+    const SampleArgs a{logits, rows, vocab, row_stride, temperature, top_k, top_p, min_p, random, tokens, probs, 0, 0};
     const cudaStream_t s = (cudaStream_t)stream;
     if (type == U32SCAN_F32) return sample_launch<float>(a, s);
     if (type == U32SCAN_F16) return sample_launch<__half>(a, s);
