@@ -22,7 +22,8 @@
 //
 // One cluster of blocks takes a row: each block reads its slice once from
 // HBM and keeps it in shared memory (what does not fit is read again, from
-// L2), so the passes after the maximum touch no HBM. No row is sorted:
+// L2), so the passes after the maximum touch no HBM, and skips what lies below
+// a bound 32 vectors at a time. No row is sorted:
 //   top-k   the k-th largest of the maxima of groups of threads is a bound
 //           below which no kept token lies; the few logits at or above it
 //           (with 2 k groups some 1.4 k) are gathered into one block, which
@@ -54,6 +55,7 @@ constexpr int kMaxCluster = 8;
 constexpr int kLocal = 1024;  // logits a block may put forward
 constexpr int kList = 2048;   // and all blocks of a row together
 constexpr int kRanked = 256;  // up to here items are ranked by counting, past it selected by histograms
+constexpr int kTurns = 64;    // turns (of 32 vectors) a warp remembers the maximum of
 constexpr int kBins = 1024;   // histogram of y: 32 bins an octave, 31 octaves
 constexpr float kLog2e = 0x1.715476p+0f;
 constexpr uint32_t kKeyOfMinusInf = 0x007fffffu;
@@ -96,6 +98,20 @@ struct SumBins {
         const uint32_t old = atomicAdd(&low[bin], v);
         if (old + v < v) atomicAdd(&high[bin], 1u);
     }
+    // add() of those that are at least floor, all on their way before the
+    // first carry is looked at.
+    template <int M>
+    __device__ __forceinline__ void add_from(uint32_t floor, const uint32_t (&bin)[M], const uint32_t (&v)[M]) {
+        uint32_t old[M];
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            old[i] = 0;
+            if (v[i] >= floor) old[i] = atomicAdd(&low[bin[i]], v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+            if (old[i] + v[i] < old[i]) atomicAdd(&high[bin[i]], 1u);
+    }
     __device__ __forceinline__ void clear() {
         for (int b = threadIdx.x; b < N; b += kSThreads) low[b] = high[b] = 0u;
     }
@@ -112,6 +128,7 @@ struct alignas(16) SampleShared {
         } picks;
     };
     u64 slots[kSlots][kMaxCluster][2];
+    uint32_t turn_key[kSWarps][kTurns];  // the key of a turn's largest logit
     u64 warp[3][kSWarps];
     u64 cast[4];
     uint32_t n_list;
@@ -419,59 +436,98 @@ struct Slice {
     using V = Vec<T>;
     const char *base;           // the row's address rounded down to 16 bytes
     unsigned int pad, n;        // elements between base and the row, and in the row
-    unsigned int v0, nv;        // this warp's first vector; the row's vectors
-    unsigned int per_warp, staged_iters;
+    unsigned int v0, count;     // this warp's first vector and how many it has
+    unsigned int staged_iters;
     uint4 *stage;               // this lane's vectors: turn i at stage[32 * i]
 
     // Vector v; past the row's ends filled with -inf.
     __device__ __forceinline__ uint4 load(unsigned int v) const {
-        const unsigned int p = v * V::N;
-        if (p >= pad && p + V::N <= pad + n) return __ldg(reinterpret_cast<const uint4 *>(base) + v);
-        return load_edge<T>(reinterpret_cast<const T *>(base), p, pad, pad + n);
+        const unsigned int first = pad ? 1u : 0u, end = (pad + n) / V::N;  // those between are whole
+        if (v - first < end - first) return __ldg(reinterpret_cast<const uint4 *>(base) + v);
+        return load_edge<T>(reinterpret_cast<const T *>(base), v * V::N, pad, pad + n);
     }
 
-    // First reading: keeps the staged vectors, returns this thread's maximum.
-    __device__ __forceinline__ float first_pass(int lane) const {
+    // First reading: keeps the staged vectors and the turns' maxima, returns the
+    // warp's (as a key) and, if asked, this thread's.
+    __device__ __forceinline__ uint32_t first_pass(uint32_t *thread_key) const {
         constexpr int U = 4;
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        uint32_t *turn_key = block_shared().turn_key[warp];
+        const uint4 *whole = reinterpret_cast<const uint4 *>(base) + v0 + lane;
+        const unsigned int whole_end = (pad + n) / V::N;  // vectors from here on, and 0 with a pad, are cut
         float m = -INFINITY;
+        uint32_t most = 0;
 #pragma unroll 1
-        for (unsigned int j = lane, it = 0; j < per_warp && v0 + j < nv; j += 32 * U, it += U) {
+        for (unsigned int it = 0; 32 * it < count; it += U) {
             uint4 r[U];
+            const unsigned int end = 32 * (it + U);
+            if (end <= count && v0 + end <= whole_end && (pad == 0 || v0 + it > 0)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const unsigned int ju = j + 32 * u;
-                if (ju < per_warp && v0 + ju < nv) r[u] = load(v0 + ju);
-                else r[u] = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
+                for (int u = 0; u < U; ++u) r[u] = __ldg(whole + 32 * (it + u));
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const unsigned int j = 32 * (it + u) + lane;
+                    r[u] = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
+                    if (has(j)) r[u] = load(v0 + j);
+                }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                m = fmaxf(m, V::max(r[u]));
+                const float top = V::max(r[u]);
+                m = fmaxf(m, top);
+                const uint32_t key = __reduce_max_sync(0xffffffffu, key_of(top == top ? top : -INFINITY));
+                most = max(most, key);
+                if (it + u < kTurns && lane == 0) turn_key[it + u] = key;
                 if (it + u < staged_iters) stage[32 * (it + u)] = r[u];
             }
         }
-        return m;
+        __syncwarp();
+        *thread_key = key_of(m);
+        return max(most, kKeyOfMinusInf);
     }
 
-    __device__ __forceinline__ bool has(unsigned int j) const { return j < per_warp && v0 + j < nv; }
+    __device__ __forceinline__ bool has(unsigned int j) const { return j < count; }
     __device__ __forceinline__ uint4 turn(unsigned int it, unsigned int j) const {
         return it < staged_iters ? stage[32 * it] : load(v0 + j);
     }
 
-    // f(vector, its number) for this lane's vectors, in ascending order, the
-    // next one on its way meanwhile.
+    // f(vector, its number) for this lane's vectors, in ascending order, in
+    // the turns that may hold a logit at or above thr; the next one is on its
+    // way meanwhile.
     template <typename F>
-    __device__ __forceinline__ void each(int lane, F f) const {
-        unsigned int j = lane, it = 0;
-        bool more = has(j);
+    __device__ __forceinline__ void each(float thr, F f) const {
+        const unsigned int lane = threadIdx.x & 31;
+        const uint32_t *turn_key = block_shared().turn_key[threadIdx.x >> 5];
+        static_assert(kTurns == 64, "two words of turns");
+        const uint32_t key = key_of(thr);
+        const unsigned int turns = (count + 31) / 32;
+        // the remembered turns to take; those past them are all taken
+        unsigned int low = __ballot_sync(0xffffffffu, lane < turns && turn_key[lane] >= key);
+        unsigned int high = __ballot_sync(0xffffffffu, 32 + lane < turns && turn_key[32 + lane] >= key);
+        unsigned int past = kTurns - 1;
+        auto take = [&]() -> unsigned int {
+            if (low) {
+                const unsigned int it = __ffs(low) - 1;
+                low &= low - 1;
+                return it;
+            }
+            if (high) {
+                const unsigned int it = __ffs(high) + 31;
+                high &= high - 1;
+                return it;
+            }
+            return ++past;
+        };
+        unsigned int j = 32 * take() + lane;
         uint4 next = make_uint4(0, 0, 0, 0);
-        if (more) next = turn(it, j);
+        if (has(j)) next = turn(j / 32, j);
 #pragma unroll 1
-        while (more) {
+        while (has(j)) {
             const uint4 r = next;
             const unsigned int v = v0 + j;
-            j += 32;
-            more = has(j);
-            if (more) next = turn(++it, j);
+            j = 32 * take() + lane;
+            if (has(j)) next = turn(j / 32, j);
             f(r, v);
         }
     }
@@ -479,9 +535,10 @@ struct Slice {
     __device__ __forceinline__ uint32_t index(unsigned int v, int e) const { return v * V::N + e - pad; }
 
     // The share of the warp `by` warps on in this block.
-    __device__ __forceinline__ Slice of_warp(int by) const {
+    __device__ __forceinline__ Slice of_warp(int by, unsigned int per_warp, unsigned int nv) const {
         Slice s = *this;
         s.v0 += by * (int)per_warp;
+        s.count = s.v0 < nv ? min(per_warp, nv - s.v0) : 0u;
         s.stage += by * 32 * (int)staged_iters;
         return s;
     }
@@ -493,6 +550,7 @@ __device__ __noinline__ uint32_t item_weight(u64 item, RowRule rule) {
     return token_weight(key_logit(~(uint32_t)(item >> 32)), rule);
 }
 constexpr u64 kKeepAll = ~0ull;
+constexpr u64 kNoItem = ~0ull;  // an item without weight, past all others
 
 // Over the n gathered items up to `limit` that have a weight (of one each
 // with COUNT): the first, in order (or by index), at which the running sum of
@@ -628,7 +686,8 @@ __device__ __noinline__ void draw(const Slice<T> &own, RowRule rule, bool finite
     const bool second = r - before >= half[0];
     if (second) before += half[0];
     const int warp0 = second ? kSWarps / 2 : 0;
-    const unsigned int per = (own.per_warp + 31) / 32, turns = kSWarps / 2 * per;
+    const unsigned int per_warp = a.per_warp, nv = (own.pad + own.n + N - 1) / N;
+    const unsigned int per = (per_warp + 31) / 32, turns = kSWarps / 2 * per;
     u64 *mass = sh.items;  // by turn
     u64 at = 0;
     bool walk = false;  // first all turns, then the one
@@ -639,7 +698,7 @@ __device__ __noinline__ void draw(const Slice<T> &own, RowRule rule, bool finite
 #pragma unroll
         for (int e = 0; e < N; ++e) q[e] = 0;
         u64 sum = 0;
-        const Slice<T> sl = own.of_warp(warp0 + (int)(t / per) - warp);
+        const Slice<T> sl = own.of_warp(warp0 + (int)(t / per) - warp, per_warp, nv);
         const unsigned int it = t % per, j = 32 * it + lane;
         if (t < turns && sl.has(j)) sum = kept_weights(sl, sl.turn(it, j), sl.v0 + j, rule, finite, last, q);
         if (walk) {
@@ -845,7 +904,7 @@ __device__ __noinline__ void radix_select(const Slice<T> &sl, const RowRule &rul
         SumBins<256> &hist = sh.digits[level & 1];
         hist.clear();
         __syncthreads();
-        sl.each(threadIdx.x & 31, [&](const uint4 &r, unsigned int v) {
+        sl.each(-INFINITY, [&](const uint4 &r, unsigned int v) {
             float x[Vec<T>::N];
             Vec<T>::unpack(r, x);
 #pragma unroll 1
@@ -899,7 +958,7 @@ __device__ __noinline__ u64 nth_tie(const Slice<T> &sl, uint32_t tau, u64 nth, S
         return t;
     };
     u64 mine = 0;
-    sl.each(lane, [&](const uint4 &r, unsigned int v) { mine += __popc(tied(r, v)); });
+    sl.each(-INFINITY, [&](const uint4 &r, unsigned int v) { mine += __popc(tied(r, v)); });
     mine = warp_total(mine);
     if (threadIdx.x == 0) sh.cast[0] = ~0ull;
     u64 before = block_before(lane == 0 ? mine : 0ull);  // of lane 0: the warps' before
@@ -907,11 +966,10 @@ __device__ __noinline__ u64 nth_tie(const Slice<T> &sl, uint32_t tau, u64 nth, S
     exchange(ties_slot, block_total(lane == 0 ? mine : 0ull), 0);
     before += slot_total(ties_slot, cluster_rank());
     if (before < nth && nth <= before + mine)  // this warp's
-        for (unsigned int j0 = 0, it = 0; j0 < sl.per_warp; j0 += 32, ++it) {
+        for (unsigned int j0 = 0, it = 0; j0 < sl.count; j0 += 32, ++it) {
             const unsigned int j = j0 + lane;
             unsigned int t = 0;
-            if (j < sl.per_warp && sl.v0 + j < sl.nv)
-                t = tied(it < sl.staged_iters ? sl.stage[32 * it] : sl.load(sl.v0 + j), sl.v0 + j);
+            if (sl.has(j)) t = tied(sl.turn(it, j), sl.v0 + j);
             const u64 inc = warp_inclusive(__popc(t));
             const u64 at = before + inc - __popc(t);
             if (at < nth && nth <= before + inc) {
@@ -939,7 +997,7 @@ __device__ __noinline__ void sample_by_selection(const Slice<T> &sl, const RowRu
     }
     auto kept = [&](u64 (&half)[2]) {
         u64 mass = 0;
-        sl.each(threadIdx.x & 31, [&](const uint4 &r, unsigned int v) {
+        sl.each(-INFINITY, [&](const uint4 &r, unsigned int v) {
             uint32_t q[Vec<T>::N];
             mass += kept_weights(sl, r, v, rule, false, last, q);
         });
@@ -979,10 +1037,10 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         sl.base = reinterpret_cast<const char *>(at & ~(uintptr_t)15);
         sl.pad = (unsigned int)(at & 15) / sizeof(T);
         sl.n = (unsigned int)a.vocab;
-        sl.nv = (sl.pad + sl.n + V::N - 1) / V::N;
-        sl.per_warp = a.per_warp;
+        const unsigned int nv = (sl.pad + sl.n + V::N - 1) / V::N;
         sl.staged_iters = a.staged_iters;
         sl.v0 = (rank * kSWarps + warp) * a.per_warp;
+        sl.count = sl.v0 < nv ? min(a.per_warp, nv - sl.v0) : 0u;
         sl.stage = reinterpret_cast<uint4 *>(&sh + 1) + warp * 32 * a.staged_iters + lane;
     }
     const float t = a.temperature ? a.temperature[row] : 1.0f;
@@ -993,9 +1051,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     const bool cut_p = p > 0.0f && p < 1.0f;
 
     // the row's largest logit, and for top-k the maxima its bound comes from
-    const float thread_max = sl.first_pass(lane);
-    const uint32_t thread_key = key_of(thread_max == thread_max ? thread_max : -INFINITY);
-    const uint32_t warp_key = __reduce_max_sync(0xffffffffu, thread_key);
+    uint32_t thread_key;
+    const uint32_t warp_key = sl.first_pass(&thread_key);
     // top-k: maxima of groups of threads, at least 2 k groups in the row
     uint32_t group = 32;
     while (group > 1 && kSThreads / group * blocks < 2 * k) group /= 2;
@@ -1031,7 +1088,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     if (!(t > 0.0f)) {  // the first of the largest
         uint32_t first = 0xffffffffu;
         if (block_key == row_key)
-            sl.each(lane, [&](const uint4 &r, unsigned int v) {
+            sl.each(rule.m, [&](const uint4 &r, unsigned int v) {
                 if (first != 0xffffffffu || !(V::max(r) >= rule.m)) return;
                 float x[V::N];
                 V::unpack(r, x);
@@ -1051,7 +1108,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     if (finite && bounded) {
         const uint32_t bound = by_groups ? kth_bound(maxima, groups * blocks, k, row_key) : 0u;
         const float thr = bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY;
-        sl.each(lane, [&](const uint4 &r, unsigned int v) {
+        sl.each(thr, [&](const uint4 &r, unsigned int v) {
             if (!(V::max(r) >= thr)) return;
             float x[V::N];
             V::unpack(r, x);
@@ -1070,13 +1127,13 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         }
     } else if (finite && k == 0) {
         // All weights; for top-p also their histogram by distance, as far as it can matter: past
-        // cut_y the row holds less than (1 - p) of the largest weight. Logits below `zero` weigh
-        // nothing (y > 31).
+        // cut_y the row holds less than (1 - p) of the largest weight. (With min-p: all of those
+        // kept, so that the histogram's sum is the row's.) Logits below `zero` weigh nothing (y > 31).
         const u64 m2 = pack2(rule.m, rule.m), scale2 = pack2(rule.scale, rule.scale);
         const float zero = __fsub_rd(rule.m, __fdiv_ru(31.5f, rule.scale));
         u64 mass = 0;
         if (!cut_p) {
-            sl.each(lane, [&](const uint4 &r, unsigned int) {
+            sl.each(zero, [&](const uint4 &r, unsigned int) {
                 if (!(V::max(r) >= zero)) return;
                 float x[V::N];
                 V::unpack(r, x);
@@ -1096,25 +1153,31 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
             return;
         }
         const float cut_y = fminf(31.0f, log2f((float)sl.n / (1.0f - p)) + 0.1f);
-        const uint32_t floor_q = max(max(rule.qmin, exp2_weight(cut_y)), 1u);  // the histogram's least weight
+        const bool min_p = rule.qmin > 0;
+        const uint32_t floor_q = min_p ? rule.qmin : max(exp2_weight(cut_y), 1u);  // the histogram's least weight
         sh.bins[0].clear();
         sh.bins[1].clear();
         __syncthreads();
         SumBins<kBins> &bins = sh.bins[warp / (kSWarps / 2)];
-        sl.each(lane, [&](const uint4 &r, unsigned int) {
+        sl.each(zero, [&](const uint4 &r, unsigned int) {
             if (!(V::max(r) >= zero)) return;
             float x[V::N];
             V::unpack(r, x);
 #pragma unroll
-            for (int e = 0; e < V::N; e += 2) {
-                float y[2];
-                uint32_t q[2];
-                weigh2(x[e], x[e + 1], m2, scale2, y, q);
+            for (int e = 0; e < V::N; e += 4) {
+                uint32_t b[4], q[4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    mass += q[i] >= rule.qmin ? q[i] : 0u;
-                    if (q[i] >= floor_q) bins.add(bin_of(y[i]), q[i]);
+                for (int i = 0; i < 4; i += 2) {
+                    float y2[2];
+                    uint32_t q2[2];
+                    weigh2(x[e + i], x[e + i + 1], m2, scale2, y2, q2);
+                    mass += (u64)q2[0] + q2[1];
+                    q[i] = q2[0];
+                    q[i + 1] = q2[1];
+                    b[i] = bin_of(y2[0]);
+                    b[i + 1] = bin_of(y2[1]);
                 }
+                bins.add_from(floor_q, b, q);
             }
         });
         __syncthreads();
@@ -1127,7 +1190,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
             own[1][i] = (u64)sh.bins[1].high[b] << 32 | sh.bins[1].low[b];
             sums[b] = own[0][i] + own[1][i];
         }
-        exchange(kSlotFirst, block_total(mass), 0);
+        exchange(kSlotFirst, block_total(min_p ? own[0][0] + own[0][1] + own[1][0] + own[1][1] : mass), 0);
         const u64 total = slot_total(kSlotFirst, blocks), want = top_p_target(p, total);
         // the bin in which the running sum reaches `want`
         u64 part[kMaxCluster][2];
@@ -1161,24 +1224,27 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         for (int h = 0; h < 2; ++h)
             half[h] = block_total((2 * threadIdx.x < bin ? own[h][0] : 0ull) +
                                   (2 * threadIdx.x + 1 < bin ? own[h][1] : 0ull));
-        // every logit in a bin up to this one is at or above thr, every one in a bin from it on at
-        // or below cap
-        const float thr = __fsub_rd(rule.m, __fdiv_ru(((float)bin + 1.0f) * (1.0f / 32.0f), rule.scale));
+        // Every logit in a bin up to this one is at or above thr, every one in a bin from it on at
+        // or below cap; the few others between them are taken out of the list afterwards.
+        const float thr = __fsub_rd(rule.m, __fdiv_ru(((float)bin + 0.51f) * (1.0f / 32.0f), rule.scale));
         const float cap = all || bin == 0
                               ? INFINITY
-                              : __fsub_ru(rule.m, __fdiv_rd(((float)bin - 1.0f) * (1.0f / 32.0f), rule.scale));
-        sl.each(lane, [&](const uint4 &r, unsigned int v) {
+                              : __fsub_ru(rule.m, __fdiv_rd(((float)bin - 0.51f) * (1.0f / 32.0f), rule.scale));
+        sl.each(thr, [&](const uint4 &r, unsigned int v) {
             if (!(V::max(r) >= thr)) return;
             float x[V::N];
             V::unpack(r, x);
             each_of<V::N>(x, [&](float xe) { return xe >= thr && xe <= cap; },
-                          [&](float xe, int e) {
-                              const float y = __fmul_rn(__fsub_rn(rule.m, xe), rule.scale);
-                              if (!(y < 32.0f) || exp2_weight(y) < floor_q) return;
-                              const uint32_t b = bin_of(y);
-                              if (all ? b <= bin : b == bin) put(item_of(key_of(xe), sl.index(v, e)));
-                          });
+                          [&](float xe, int e) { put(item_of(key_of(xe), sl.index(v, e))); });
         });
+        __syncthreads();
+#pragma unroll 1
+        for (uint32_t i = threadIdx.x; i < min(sh.n_list, (uint32_t)kLocal); i += kSThreads) {
+            const float x = key_logit(~(uint32_t)(sh.items[i] >> 32));
+            const float y = __fmul_rn(__fsub_rn(rule.m, x), rule.scale);
+            if (!(y < 32.0f) || exp2_weight(y) < floor_q || bin_of(y) > bin || (!all && bin_of(y) < bin))
+                sh.items[i] = kNoItem;
+        }
         __syncthreads();
         exchange(kSlotSecond, sh.n_list, half[0] + half[1]);
         const uint32_t n = gathered(kSlotSecond);
@@ -1193,7 +1259,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
                 const u64 last = block_select<false>(n, kKeepAll, false, want - above, rule, &left);
                 left += above + item_weight(last, rule);
                 const uint32_t from = (uint32_t)slot_total(kSlotSecond, rank), to = from + sh.n_list;
-                const uint32_t second = (rank * kSWarps + kSWarps / 2) * sl.per_warp * V::N;  // its first element
+                const uint32_t second = (rank * kSWarps + kSWarps / 2) * a.per_warp * V::N;  // its first element
                 u64 ahead = 0, in[2] = {0, 0};
 #pragma unroll 1
                 for (uint32_t i = threadIdx.x; i < to; i += kSThreads) {
