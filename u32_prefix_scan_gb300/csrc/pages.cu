@@ -15,10 +15,14 @@
 //            so all pages move at once).
 // All of it is integer, so results do not depend on the order of atomics.
 //
-// Reduce, then scan: the count kernel reads refs once in tiles and its last
-// block scans the tiles' counts and the rows' needs, so the second kernel
-// knows every base without waiting on other blocks. refs is read twice, the
-// second time from L2 (4 MB at a million pages).
+// Three launches, each reading what the one before wrote: plan (count the free
+// or live pages of every 16384 refs; the last block scans the counts and the
+// rows' needs), place (list the pages by rank) and act (table entries, refs,
+// bytes). A cache of up to 16384 pages is planned and placed by one block in
+// one launch. refs is read twice, the second time from L2 (4 MB at a million
+// pages): a single pass that carries the rank from tile to tile would have
+// every tile wait for the one before, and the rows' needs, which decide how
+// far the list goes, are known only after the scan.
 #include <cstdint>
 #include <mutex>
 #include <cuda_runtime.h>
@@ -29,9 +33,13 @@ namespace u32scan {
 
 typedef unsigned long long u64;
 
-constexpr int kPThreads = 256;
+constexpr int kPThreads = 256;      // free, copies and act
 constexpr int kPWarps = kPThreads / 32;
-constexpr int kRefTile = 4096;      // refs counted by one block
+constexpr int kPlanThreads = 1024;  // plan and place
+constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPerThread = 16;      // refs of a thread of plan and place
+constexpr int kRefTile = kPlanThreads * kPerThread;
+constexpr u64 kOneBlockRows = 16384;  // rows up to which one block plans (16 a thread)
 constexpr int kEntryChunk = 512;    // table entries handled by one warp
 constexpr size_t kCopyUnit = 16384; // bytes of a page copied by one block at a time
 
@@ -44,10 +52,11 @@ struct Pool {
 // past every other operation's tile words).
 struct PagesCtrl {
     u64 free_pages;    // fork: F
-    u64 jobs;          // fork: rows whose partly filled page is copied
+    u64 taken;         // fork: fresh pages of the rows that are served
+    u64 jobs;          // fork: children whose parent's last page is partly filled
     u64 live;          // compact: L
     u64 moved;         // compact: pages that move
-    u64 pad[28];
+    u64 pad[27];
 };
 static_assert(sizeof(PagesCtrl) == 256, "one line group");
 
@@ -58,13 +67,15 @@ struct PagesWs {
     u64 *ends;        // fork: [rows]
     int32_t *old_len; // fork: [rows] length before the call (of the parent, for a child)
     int32_t *jobs;    // fork: [rows]
+    int32_t *fresh;   // fork: [pages] the free pages by rank
     uint32_t *freed;  // free: [blocks]
     int32_t *holes, *movers, *rank;  // compact: [pages] each
 };
 
 static u64 ref_tiles(u64 pages) { return (pages + kRefTile - 1) / kRefTile; }
 
-// n = pages + rows: 8 bytes a tile and at most 16 bytes a row or 12 a page.
+// n = pages + rows: 8 bytes a tile, and at most 16 bytes a row and 4 a page
+// (fork) or 12 a page (compact).
 size_t pages_workspace_bytes(u64 n) {
     return round_up(tile_word_reach(), 256) + sizeof(PagesCtrl) + round_up(8 * (n / kRefTile + 2), 256) +
            round_up(16 * n, 256) + 4 * 256;
@@ -81,6 +92,7 @@ static PagesWs carve(void *ws, u64 pages, u64 rows) {
     w.ends = reinterpret_cast<u64 *>(p);
     w.old_len = reinterpret_cast<int32_t *>(p + round_up(8 * rows, 256));
     w.jobs = reinterpret_cast<int32_t *>(p + round_up(8 * rows, 256) + round_up(4 * rows, 256));
+    w.fresh = reinterpret_cast<int32_t *>(p + round_up(8 * rows, 256) + 2 * round_up(4 * rows, 256));
     w.freed = reinterpret_cast<uint32_t *>(p);
     w.holes = reinterpret_cast<int32_t *>(p);
     w.movers = reinterpret_cast<int32_t *>(p + round_up(4 * pages, 256));
@@ -101,21 +113,17 @@ __device__ __forceinline__ u64 warp_inclusive_u64(u64 x, int lane) {
 }
 
 // Exclusive sum over the block's threads; *total is the block's (all threads
-// call it; s_warp holds kPWarps values).
+// call it; s_warp holds one value a warp, at most 32).
 __device__ __forceinline__ u64 block_exclusive(u64 x, u64 *s_warp, u64 *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const u64 inc = warp_inclusive_u64(x, lane);
     __syncthreads();
     if (lane == 31) s_warp[warp] = inc;
     __syncthreads();
-    u64 base = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kPWarps; ++w) {
-        if (w < warp) base += s_warp[w];
-        all += s_warp[w];
-    }
-    *total = all;
-    return base + inc - x;
+    const u64 sums = warp_inclusive_u64(lane < warps ? s_warp[lane] : 0ull, lane);
+    *total = __shfl_sync(0xffffffffu, sums, 31);
+    const u64 base = __shfl_sync(0xffffffffu, sums, warp ? warp - 1 : 0);
+    return (warp ? base : 0ull) + inc - x;
 }
 
 // True in every thread of the block that finishes last (each block's earlier
@@ -133,30 +141,56 @@ __device__ __forceinline__ bool last_block(WsHeader *hdr) {
     return s_last != 0u;
 }
 
-// a[i] <- a[0] + .. + a[i] (INCLUSIVE) or a[i-1], by one block; returns the
-// total. The values are read past L1: other blocks wrote them.
-template <bool INCLUSIVE>
-__device__ __forceinline__ u64 scan_by_block(u64 *a, u64 n, u64 *s_warp) {
+// f(i, base) for i < n by one block, where base is the sum of the values v(k),
+// k < i; returns the sum of all. A thread takes neighbouring i, so that one
+// block-wide scan serves many (4 a thread at a time).
+template <typename V, typename F>
+__device__ __forceinline__ u64 scan_by_block(u64 n, u64 *s_warp, V v, F f) {
+    constexpr int C = 4;
     u64 carry = 0;
-    for (u64 i0 = 0; i0 < n; i0 += kPThreads) {
-        const u64 i = i0 + threadIdx.x;
-        const u64 x = i < n ? ld_relaxed(a + i) : 0ull;
-        u64 total;
-        const u64 ex = block_exclusive(x, s_warp, &total);
-        if (i < n) a[i] = carry + ex + (INCLUSIVE ? x : 0ull);
+    for (u64 i0 = 0; i0 < n; i0 += (u64)C * blockDim.x) {
+        const u64 left = n - i0, per = left < (u64)C * blockDim.x ? (left + blockDim.x - 1) / blockDim.x : C;
+        const u64 first = i0 + threadIdx.x * per;
+        u64 x[C], sum = 0;
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c] = c < (int)per && first + c < n ? v(first + c) : 0ull;
+#pragma unroll
+        for (int c = 0; c < C; ++c) sum += x[c];
+        u64 total, base = carry + block_exclusive(sum, s_warp, &total);
         carry += total;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (c < (int)per && first + c < n) f(first + c, base, x[c]);
+            base += x[c];
+        }
     }
     return carry;
 }
 
-// Number of refs in [begin, end) that are zero (ZERO) or not, by one block.
-template <bool ZERO>
-__device__ __forceinline__ u64 count_refs(const int32_t *refs, u64 begin, u64 end, u64 *s_warp) {
-    u64 c = 0;
-    for (u64 i = begin + threadIdx.x; i < end; i += kPThreads) c += (refs[i] == 0) == ZERO;
-    u64 total;
-    block_exclusive(c, s_warp, &total);
-    return total;
+// Which of this thread's kPerThread refs of a tile are free (zero), a bit each.
+__device__ __forceinline__ unsigned int free_mask(const int32_t *refs, u64 tile, u64 pages) {
+    const u64 first = tile * kRefTile + (u64)threadIdx.x * kPerThread;
+    unsigned int m = 0;
+    if (first + kPerThread <= pages && (reinterpret_cast<uintptr_t>(refs) & 15) == 0) {
+        int4 r[kPerThread / 4];
+#pragma unroll
+        for (int j = 0; j < kPerThread / 4; ++j) r[j] = reinterpret_cast<const int4 *>(refs + first)[j];
+#pragma unroll
+        for (int j = 0; j < kPerThread / 4; ++j)
+            m |= ((r[j].x == 0) | (r[j].y == 0) << 1 | (r[j].z == 0) << 2 | (r[j].w == 0) << 3) << (4 * j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPerThread; ++j)
+            if (first + j < pages && refs[first + j] == 0) m |= 1u << j;
+    }
+    return m;
+}
+
+// The bits of free_mask's refs that exist.
+__device__ __forceinline__ unsigned int page_mask(u64 tile, u64 pages) {
+    const u64 first = tile * kRefTile + (u64)threadIdx.x * kPerThread;
+    if (first >= pages) return 0u;
+    return pages - first >= kPerThread ? 0xffffu : (1u << (unsigned int)(pages - first)) - 1u;
 }
 
 // ---------------------------------------------------------------------------
@@ -230,20 +264,21 @@ struct ForkArgs {
     int32_t *lens;
     int32_t *refs;
     u64 pages;
-    u64 page_tokens;
+    uint32_t page_tokens;
     const int32_t *parent, *grow;
     int32_t *status, *free_pages;
 };
 
 constexpr int32_t kBadRow = -1;  // old_len of a row whose arguments are refused
 
-__device__ __forceinline__ u64 pages_for(u64 tokens, u64 page_tokens) {
+// Both below 2^31, so that 32 bits are enough.
+__device__ __forceinline__ uint32_t pages_for(uint32_t tokens, uint32_t page_tokens) {
     return (tokens + page_tokens - 1) / page_tokens;
 }
 
 // Pages row s holds before its fresh ones: a child's shared full pages, or
 // the row's own.
-__device__ __forceinline__ u64 held_pages(bool child, u64 old_len, u64 page_tokens) {
+__device__ __forceinline__ uint32_t held_pages(bool child, uint32_t old_len, uint32_t page_tokens) {
     return child ? old_len / page_tokens : pages_for(old_len, page_tokens);
 }
 
@@ -261,146 +296,165 @@ __device__ __forceinline__ u64 row_need(const ForkArgs &a, u64 s, int32_t *old_l
     }
     const int32_t g = a.grow ? a.grow[s] : 0;
     if (old < 0 || g < 0) return 0;
-    const u64 total = (u64)old + (u64)g;
-    if (total > 0x7fffffffull || pages_for(total, a.page_tokens) > a.width) return 0;
+    const uint32_t total = (uint32_t)old + (uint32_t)g;
+    if (total > 0x7fffffffu || pages_for(total, a.page_tokens) > a.width) return 0;
     *old_len = old;
-    return pages_for(total, a.page_tokens) - held_pages(child, (u64)old, a.page_tokens);
+    return pages_for(total, a.page_tokens) - held_pages(child, (uint32_t)old, a.page_tokens);
 }
 
-__global__ void __launch_bounds__(kPThreads) fork_count_kernel(ForkArgs a, PagesWs w, u64 tiles) {
-    __shared__ u64 s_warp[kPWarps];
-    if (blockIdx.x < tiles) {
-        const u64 begin = (u64)blockIdx.x * kRefTile;
-        const u64 c = count_refs<true>(a.refs, begin, min(begin + kRefTile, a.pages), s_warp);
-        if (threadIdx.x == 0) w.tile_base[blockIdx.x] = c;
-    } else {
-        const u64 s = (blockIdx.x - tiles) * kPThreads + threadIdx.x;
-        if (s < a.rows) {
+// What the rows ask for, by one block: ends, the jobs, and the number of pages
+// the served rows take (returned).
+__device__ __forceinline__ u64 plan_rows(const ForkArgs &a, const PagesWs &w, u64 free_pages, u64 *s_warp) {
+    __shared__ u64 s_taken;
+    u64 taken = 0;
+    if (threadIdx.x == 0) s_taken = 0;
+    scan_by_block(
+        a.rows, s_warp,
+        [&](u64 s) -> u64 {
             int32_t old;
-            w.ends[s] = row_need(a, s, &old);
+            const u64 need = row_need(a, s, &old);
             w.old_len[s] = old;
-        }
-    }
-    if (!last_block(w.hdr)) return;
-    const u64 free_pages = scan_by_block<false>(w.tile_base, tiles, s_warp);
-    scan_by_block<true>(w.ends, a.rows, s_warp);
-    // the children whose parent's last page is partly filled, in row order
-    u64 jobs = 0;
-    for (u64 s0 = 0; s0 < a.rows; s0 += kPThreads) {
-        const u64 s = s0 + threadIdx.x;
-        bool job = false;
-        if (s < a.rows && is_child(a, s)) {
-            const int32_t old = (int32_t)ld_relaxed_u32(reinterpret_cast<const unsigned int *>(w.old_len + s));
-            job = old > 0 && (u64)old % a.page_tokens != 0;
-        }
-        u64 total;
-        const u64 at = jobs + block_exclusive(job ? 1ull : 0ull, s_warp, &total);
-        if (job) w.jobs[at] = (int32_t)s;
-        jobs += total;
-    }
+            return need;
+        },
+        [&](u64 s, u64 base, u64 need) {
+            w.ends[s] = base + need;
+            if (need && base + need <= free_pages) taken = base + need;
+        });
+    if (taken) atomicMax(&s_taken, taken);
+    // children whose parent's last page is partly filled, in row order (a thread reads what it wrote)
+    const u64 jobs = !a.parent ? 0ull
+                               : scan_by_block(
+                                     a.rows, s_warp,
+                                     [&](u64 s) -> u64 {
+                                         const int32_t old = w.old_len[s];
+                                         return old > 0 && is_child(a, s) && (uint32_t)old % a.page_tokens != 0;
+                                     },
+                                     [&](u64 s, u64 base, u64 job) {
+                                         if (job) w.jobs[base] = (int32_t)s;
+                                     });
+    __syncthreads();
     if (threadIdx.x == 0) {
         w.ctrl->free_pages = free_pages;
+        w.ctrl->taken = s_taken;
         w.ctrl->jobs = jobs;
+        if (a.free_pages) *a.free_pages = (int32_t)(free_pages - s_taken);
     }
+    return s_taken;
+}
+
+// The tile's free pages of rank below `taken` become fresh ones.
+__device__ __forceinline__ void place_fresh(const ForkArgs &a, const PagesWs &w, u64 tile, unsigned int mask, u64 rank,
+                                            u64 taken) {
+    const u64 first = tile * kRefTile + (u64)threadIdx.x * kPerThread;
+    for (; mask && rank < taken; mask &= mask - 1, ++rank) {
+        const u64 page = first + (__ffs(mask) - 1);
+        w.fresh[rank] = (int32_t)page;
+        a.refs[page] = 1;
+    }
+}
+
+// ONE: a single block, which also places (a cache of one tile).
+template <bool ONE>
+__global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a, PagesWs w, u64 tiles) {
+    __shared__ u64 s_warp[kPlanWarps];
+    u64 total;
+    const unsigned int mask = blockIdx.x < tiles ? free_mask(a.refs, blockIdx.x, a.pages) : 0u;
+    const u64 rank = block_exclusive(__popc(mask), s_warp, &total);
+    if (ONE) {
+        const u64 taken = plan_rows(a, w, total, s_warp);
+        place_fresh(a, w, 0, mask, rank, taken);
+        return;
+    }
+    if (threadIdx.x == 0) w.tile_base[blockIdx.x] = total;
+    if (!last_block(w.hdr)) return;
+    const u64 free_pages = scan_by_block(
+        tiles, s_warp, [&](u64 t) { return ld_relaxed(w.tile_base + t); },
+        [&](u64 t, u64 base, u64) { w.tile_base[t] = base; });
+    plan_rows(a, w, free_pages, s_warp);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) fork_place_kernel(ForkArgs a, PagesWs w) {
+    __shared__ u64 s_warp[kPlanWarps];
+    const u64 base = w.tile_base[blockIdx.x], taken = w.ctrl->taken;
+    if (base >= taken) return;
+    const unsigned int mask = free_mask(a.refs, blockIdx.x, a.pages);
+    u64 total;
+    const u64 rank = base + block_exclusive(__popc(mask), s_warp, &total);
+    place_fresh(a, w, blockIdx.x, mask, rank, taken);
 }
 
 // Row s gets all it asks for.
-__device__ __forceinline__ bool row_served(const PagesWs &w, u64 s, u64 free_pages) {
-    if (w.old_len[s] == kBadRow) return false;
-    const u64 end = w.ends[s], begin = s ? w.ends[s - 1] : 0ull;
-    return end == begin || end <= free_pages;
+__device__ __forceinline__ bool row_served(const PagesWs &w, u64 s, u64 begin, u64 free_pages) {
+    return w.old_len[s] != kBadRow && (w.ends[s] == begin || w.ends[s] <= free_pages);
 }
 
-// The number of ends at or below x.
-__device__ __forceinline__ u64 ends_upto(const u64 *ends, u64 rows, u64 x) {
-    u64 lo = 0, hi = rows;
-    while (lo < hi) {
-        const u64 mid = (lo + hi) / 2;
-        if (ends[mid] <= x) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
+__device__ __forceinline__ u64 row_begin(const PagesWs &w, u64 s) { return s ? w.ends[s - 1] : 0ull; }
 
-__global__ void __launch_bounds__(kPThreads) fork_assign_kernel(ForkArgs a, PagesWs w, u64 tiles, u64 chunks) {
-    __shared__ u64 s_warp[kPWarps];
+// Table entries, lengths and states (the first row_blocks blocks, a warp to
+// kEntryChunk entries of a row), and the bytes of the partly filled pages.
+__global__ void __launch_bounds__(kPThreads)
+fork_act_kernel(ForkArgs a, PagesWs w, Pool pool, unsigned int row_blocks, u64 chunks) {
     const u64 free_pages = w.ctrl->free_pages;
-    const u64 asked = a.rows ? w.ends[a.rows - 1] : 0ull;
-    if (blockIdx.x < tiles) {  // hand out this tile's free pages
-        u64 rank = w.tile_base[blockIdx.x];
-        const u64 begin = (u64)blockIdx.x * kRefTile, end = min(begin + kRefTile, a.pages);
-        for (u64 i0 = begin; i0 < end && rank < asked; i0 += kPThreads) {
-            const u64 i = i0 + threadIdx.x;
-            const bool is_free = i < end && a.refs[i] == 0;
-            u64 total;
-            const u64 f = rank + block_exclusive(is_free ? 1ull : 0ull, s_warp, &total);
-            rank += total;
-            if (!is_free || f >= asked) continue;
-            const u64 s = ends_upto(w.ends, a.rows, f);  // the row with ends[s-1] <= f < ends[s]
-            if (w.ends[s] > free_pages) continue;        // it cannot have all its pages: it takes none
-            const u64 first = s ? w.ends[s - 1] : 0ull;
-            const u64 slot = held_pages(is_child(a, s), (u64)w.old_len[s], a.page_tokens) + (f - first);
-            a.table[s * a.stride + slot] = (int32_t)i;
-            a.refs[i] = 1;
-        }
+    if (blockIdx.x >= row_blocks) {
+        copy_pages(pool, w.ctrl->jobs, blockIdx.x - row_blocks, gridDim.x - row_blocks,
+                   [&](u64 k, u64 *src, u64 *dst) {
+                       const u64 s = (u64)w.jobs[k], begin = row_begin(w, s);
+                       if (!row_served(w, s, begin, free_pages)) return false;
+                       *src = page_of(a.table[(u64)a.parent[s] * a.stride + (uint32_t)w.old_len[s] / a.page_tokens]);
+                       *dst = page_of(w.fresh[begin]);
+                       return true;
+                   });
         return;
     }
-    const u64 item = (blockIdx.x - tiles) * kPWarps + (threadIdx.x >> 5);
+    const u64 item = (u64)blockIdx.x * kPWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const u64 s = item / chunks, chunk = item - s * chunks;
-    if (item == 0 && lane == 0 && a.free_pages) {  // what the served rows leave
-        const u64 fit = ends_upto(w.ends, a.rows, free_pages);
-        *a.free_pages = (int32_t)(free_pages - (fit ? w.ends[fit - 1] : 0ull));
-    }
     if (s >= a.rows) return;
-    const bool served = row_served(w, s, free_pages);
-    const bool child = is_child(a, s);
+    const u64 begin = row_begin(w, s), need = w.ends[s] - begin;
+    const bool served = row_served(w, s, begin, free_pages), child = is_child(a, s);
+    const int32_t old = w.old_len[s];
     if (chunk == 0 && lane == 0) {
-        const u64 need = w.ends[s] - (s ? w.ends[s - 1] : 0ull);
-        a.status[s] = served ? (int32_t)need : w.old_len[s] == kBadRow ? -1 : -2;
-        if (served) a.lens[s] = w.old_len[s] + (a.grow ? a.grow[s] : 0);
+        a.status[s] = served ? (int32_t)need : old == kBadRow ? -1 : -2;
+        if (served) a.lens[s] = old + (a.grow ? a.grow[s] : 0);
     }
-    if (!served || !child) return;
-    const u64 shared = (u64)w.old_len[s] / a.page_tokens;
-    const int32_t *from = a.table + (u64)a.parent[s] * a.stride;
+    if (!served) return;
+    const u64 held = held_pages(child, (uint32_t)old, a.page_tokens), total = held + need;
+    const int32_t *from = a.table + (child ? (u64)a.parent[s] : s) * a.stride;
     int32_t *to = a.table + s * a.stride;
-    for (u64 j = chunk * kEntryChunk + lane; j < min(shared, (chunk + 1) * kEntryChunk); j += 32) {
-        const int32_t e = from[j];
+    const u64 first = chunk * kEntryChunk, end = chunk + 1 == chunks ? total : min(total, first + kEntryChunk);
+    for (u64 j = (child ? first : max(first, held)) + lane; j < end; j += 32) {
+        const int32_t e = j < held ? from[j] : w.fresh[begin + (j - held)];
         to[j] = e;
-        if (page_of(e) < a.pages) atomicAdd(a.refs + e, 1);
+        if (j < held && page_of(e) < a.pages) atomicAdd(a.refs + e, 1);
     }
-}
-
-__global__ void __launch_bounds__(kPThreads) fork_copy_kernel(ForkArgs a, PagesWs w, Pool pool) {
-    const u64 free_pages = w.ctrl->free_pages;
-    copy_pages(pool, w.ctrl->jobs, blockIdx.x, gridDim.x, [&](u64 k, u64 *src, u64 *dst) {
-        const u64 s = (u64)w.jobs[k];
-        if (!row_served(w, s, free_pages)) return false;
-        const u64 slot = (u64)w.old_len[s] / a.page_tokens;
-        *src = page_of(a.table[(u64)a.parent[s] * a.stride + slot]);
-        *dst = page_of(a.table[s * a.stride + slot]);
-        return true;
-    });
 }
 
 // ---------------------------------------------------------------------------
 // free
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPThreads)
-free_kernel(int32_t *table, u64 stride, u64 rows, u64 width, int32_t *lens, int32_t *refs, u64 pages, u64 page_tokens,
-            const int32_t *release, int32_t *freed, PagesWs w) {
+free_kernel(int32_t *table, u64 stride, u64 rows, u64 width, int32_t *lens, int32_t *refs, u64 pages,
+            uint32_t page_tokens, const int32_t *release, int32_t *freed, PagesWs w) {
+    constexpr int U = 4;
     __shared__ u64 s_warp[kPWarps];
     const int lane = threadIdx.x & 31;
     u64 gone = 0;
     for (u64 s = (u64)blockIdx.x * kPWarps + (threadIdx.x >> 5); s < rows; s += (u64)gridDim.x * kPWarps) {
         if (release[s] == 0) continue;
         const int32_t len = lens[s];
-        const u64 n = len > 0 ? min(pages_for((u64)len, page_tokens), width) : 0ull;
+        const u64 n = len > 0 ? min((u64)pages_for((uint32_t)len, page_tokens), width) : 0ull;
         int32_t *row = table + s * stride;
-        for (u64 j = lane; j < n; j += 32) {
-            const int32_t e = row[j];
-            row[j] = -1;
-            if (page_of(e) < pages && atomicSub(refs + e, 1) == 1) ++gone;
+        for (u64 j = lane; j < n; j += 32 * U) {  // U entries and their counts on the way together
+            int32_t e[U], was[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) e[u] = j + 32 * u < n ? row[j + 32 * u] : -1;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                was[u] = page_of(e[u]) < pages ? atomicSub(refs + e[u], 1) : 0;
+                if (j + 32 * u < n) row[j + 32 * u] = -1;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) gone += was[u] == 1;
         }
         __syncwarp();
         if (lane == 0) lens[s] = 0;
@@ -423,59 +477,90 @@ struct CompactArgs {
     u64 stride, rows, width;
     const int32_t *lens;
     int32_t *refs;
-    u64 pages, page_tokens;
+    u64 pages;
+    uint32_t page_tokens;
     int32_t *live, *remap;
 };
 
-__global__ void __launch_bounds__(kPThreads) compact_count_kernel(CompactArgs a, PagesWs w) {
-    __shared__ u64 s_warp[kPWarps];
-    const u64 begin = (u64)blockIdx.x * kRefTile;
-    const u64 c = count_refs<false>(a.refs, begin, min(begin + kRefTile, a.pages), s_warp);
-    if (threadIdx.x == 0) w.tile_base[blockIdx.x] = c;
-    if (!last_block(w.hdr)) return;
-    const u64 live = scan_by_block<false>(w.tile_base, gridDim.x, s_warp);
-    __syncthreads();
-    u64 below = live;  // live pages below `live`: those that stay
-    if (live < a.pages) {
-        const u64 tile = live / kRefTile;
-        below = w.tile_base[tile] + count_refs<false>(a.refs, tile * kRefTile, live, s_warp);
-    }
-    if (threadIdx.x == 0) {
-        w.ctrl->live = live;
-        w.ctrl->moved = live - below;
-        if (a.live) *a.live = (int32_t)live;
+// The tile's free pages below `live` are holes, its live ones from there on
+// movers; `rank` counts the live pages before this thread's, `stay` those
+// below `live`.
+__device__ __forceinline__ void place_moves(const CompactArgs &a, const PagesWs &w, u64 tile, unsigned int live_mask,
+                                            u64 rank, u64 live, u64 stay) {
+    const u64 first = tile * kRefTile + (u64)threadIdx.x * kPerThread;
+#pragma unroll
+    for (int j = 0; j < kPerThread; ++j) {
+        const u64 i = first + j;
+        if (i >= a.pages) break;
+        const bool is_live = live_mask >> j & 1u;
+        if (i < live && !is_live) w.holes[i - rank] = (int32_t)i;
+        if (i >= live && is_live) {
+            w.movers[rank - stay] = (int32_t)i;
+            w.rank[i] = (int32_t)(rank - stay);
+        }
+        if (a.remap && !(i >= live && is_live)) a.remap[i] = is_live ? (int32_t)i : -1;
+        rank += is_live;
     }
 }
 
-__global__ void __launch_bounds__(kPThreads) compact_pair_kernel(CompactArgs a, PagesWs w) {
-    __shared__ u64 s_warp[kPWarps];
-    const u64 live = w.ctrl->live, stay = live - w.ctrl->moved;
-    u64 rank = w.tile_base[blockIdx.x];
-    const u64 begin = (u64)blockIdx.x * kRefTile, end = min(begin + kRefTile, a.pages);
-    for (u64 i0 = begin; i0 < end; i0 += kPThreads) {
-        const u64 i = i0 + threadIdx.x;
-        const bool is_live = i < end && a.refs[i] != 0;
-        u64 total;
-        const u64 r = rank + block_exclusive(is_live ? 1ull : 0ull, s_warp, &total);
-        rank += total;
-        if (i >= end) continue;
-        if (i < live && !is_live) w.holes[i - r] = (int32_t)i;
-        if (i >= live && is_live) {
-            w.movers[r - stay] = (int32_t)i;
-            w.rank[i] = (int32_t)(r - stay);
+// How many of the live pages lie below page `live`, given the tile that holds
+// it (`rank`: those before this thread's refs).
+__device__ __forceinline__ void count_below(u64 tile, unsigned int live_mask, u64 rank, u64 live, u64 *below) {
+    const u64 first = tile * kRefTile + (u64)threadIdx.x * kPerThread;
+    if (first <= live && live < first + kPerThread)
+        *below = rank + __popc(live_mask & ((1u << (unsigned int)(live - first)) - 1u));
+}
+
+template <bool ONE>
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactArgs a, PagesWs w) {
+    __shared__ u64 s_warp[kPlanWarps];
+    __shared__ u64 s_below;
+    unsigned int mask = ~free_mask(a.refs, blockIdx.x, a.pages) & page_mask(blockIdx.x, a.pages);
+    u64 total, tile = blockIdx.x;
+    u64 rank = block_exclusive(__popc(mask), s_warp, &total);
+    u64 live = total;
+    if (!ONE) {
+        if (threadIdx.x == 0) w.tile_base[blockIdx.x] = total;
+        if (!last_block(w.hdr)) return;
+        live = scan_by_block(
+            gridDim.x, s_warp, [&](u64 t) { return ld_relaxed(w.tile_base + t); },
+            [&](u64 t, u64 base, u64) { w.tile_base[t] = base; });
+        __syncthreads();
+        tile = live / kRefTile;
+        if (live < a.pages) {
+            mask = ~free_mask(a.refs, tile, a.pages) & page_mask(tile, a.pages);
+            rank = w.tile_base[tile] + block_exclusive(__popc(mask), s_warp, &total);
         }
-        if (a.remap && !(i >= live && is_live)) a.remap[i] = is_live ? (int32_t)i : -1;
     }
+    if (threadIdx.x == 0) s_below = live;
+    __syncthreads();
+    if (live < a.pages) count_below(tile, mask, rank, live, &s_below);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        w.ctrl->live = live;
+        w.ctrl->moved = live - s_below;
+        if (a.live) *a.live = (int32_t)live;
+    }
+    if (ONE) place_moves(a, w, 0, mask, rank, live, s_below);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) compact_place_kernel(CompactArgs a, PagesWs w) {
+    __shared__ u64 s_warp[kPlanWarps];
+    const u64 live = w.ctrl->live, stay = live - w.ctrl->moved;
+    const unsigned int mask = ~free_mask(a.refs, blockIdx.x, a.pages) & page_mask(blockIdx.x, a.pages);
+    u64 total;
+    const u64 rank = w.tile_base[blockIdx.x] + block_exclusive(__popc(mask), s_warp, &total);
+    place_moves(a, w, blockIdx.x, mask, rank, live, stay);
 }
 
 __global__ void __launch_bounds__(kPThreads)
-compact_move_kernel(CompactArgs a, PagesWs w, Pool pool, unsigned int row_blocks, unsigned int ref_blocks) {
+compact_act_kernel(CompactArgs a, PagesWs w, Pool pool, unsigned int row_blocks, unsigned int ref_blocks) {
     const u64 live = w.ctrl->live, moved = w.ctrl->moved;
     const int lane = threadIdx.x & 31;
     if (blockIdx.x < row_blocks) {  // table entries
         for (u64 s = (u64)blockIdx.x * kPWarps + (threadIdx.x >> 5); s < a.rows; s += (u64)row_blocks * kPWarps) {
             const int32_t len = a.lens[s];
-            const u64 n = len > 0 ? min(pages_for((u64)len, a.page_tokens), a.width) : 0ull;
+            const u64 n = len > 0 ? min((u64)pages_for((uint32_t)len, a.page_tokens), a.width) : 0ull;
             int32_t *row = a.table + s * a.stride;
             for (u64 j = lane; j < n; j += 32) {
                 const u64 e = page_of(row[j]);
@@ -529,7 +614,8 @@ static bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) &
 static bool pool_ok(const u32scan_page_pool *pool, size_t pages, Pool *out) {
     *out = Pool{nullptr, 0, pages, 0, 0};
     if (pool == nullptr || pool->n_planes == 0 || pool->page_bytes == 0) return pool == nullptr || pool->pages == pages;
-    if (pool->pages != pages || pool->planes == nullptr || (reinterpret_cast<uintptr_t>(pool->planes) & 7)) return false;
+    if (pool->pages != pages || pool->planes == nullptr || (reinterpret_cast<uintptr_t>(pool->planes) & 7))
+        return false;
     if (pool->n_planes >= (1u << 20) || pool->page_bytes >= (1ull << 40) || pool->page_stride < pool->page_bytes ||
         pool->page_stride >= (1ull << 40))
         return false;
@@ -542,7 +628,8 @@ static bool table_ok(const int32_t *table, size_t stride, size_t rows, size_t wi
                      const int32_t *refs, size_t pages, size_t page_tokens) {
     if (rows >= (1ull << 31) || width >= (1ull << 31) || pages >= (1ull << 31)) return false;
     if (page_tokens == 0 || page_tokens >= (1ull << 31) || stride < width || stride >= (1ull << 31)) return false;
-    if ((rows > 0 && (lens == nullptr || (width > 0 && table == nullptr))) || (pages > 0 && refs == nullptr)) return false;
+    if (rows > 0 && (lens == nullptr || (width > 0 && table == nullptr))) return false;
+    if (pages > 0 && refs == nullptr) return false;
     return !misaligned(table) && !misaligned(lens) && !misaligned(refs);
 }
 
@@ -594,16 +681,22 @@ extern "C" int pages_fork(int32_t *table, size_t table_stride, size_t rows, size
     int rc = sm_count(&sms);
     if (rc != U32SCAN_OK) return rc;
     const cudaStream_t s = (cudaStream_t)stream;
-    const ForkArgs a{table, table_stride, rows, width, lens, refs, pages, page_tokens, parent, grow, status, free_pages};
+    const ForkArgs a{table, table_stride, rows,   width, lens,   refs,
+                     pages, (uint32_t)page_tokens, parent, grow, status, free_pages};
     const PagesWs w = carve(ws, pages, rows);
-    const u64 tiles = ref_tiles(pages), row_blocks = (rows + kPThreads - 1) / kPThreads;
-    const u64 chunks = parent ? (width + kEntryChunk - 1) / kEntryChunk + (width == 0) : 1;
-    const u64 warps = (rows ? rows : 1) * chunks, assign_blocks = (warps + kPWarps - 1) / kPWarps;
-    if (tiles + assign_blocks >= (1ull << 31)) return U32SCAN_EINVAL;
-    fork_count_kernel<<<(unsigned int)(tiles + row_blocks + (tiles + row_blocks == 0)), kPThreads, 0, s>>>(a, w, tiles);
-    fork_assign_kernel<<<(unsigned int)(tiles + assign_blocks), kPThreads, 0, s>>>(a, w, tiles, chunks);
-    if (parent && p.n_planes)
-        fork_copy_kernel<<<copy_grid(rows * units_per_pair(p), sms), kPThreads, 0, s>>>(a, w, p);
+    const u64 tiles = ref_tiles(pages), chunks = parent && width ? (width + kEntryChunk - 1) / kEntryChunk : 1;
+    const u64 row_blocks = (rows * chunks + kPWarps - 1) / kPWarps;
+    const unsigned int data_blocks = parent && p.n_planes ? copy_grid(rows * units_per_pair(p), sms) : 0u;
+    if (row_blocks + data_blocks >= (1ull << 31)) return U32SCAN_EINVAL;
+    if (tiles <= 1 && rows <= kOneBlockRows) {
+        fork_plan_kernel<true><<<1, kPlanThreads, 0, s>>>(a, w, tiles);
+    } else {
+        fork_plan_kernel<false><<<(unsigned int)(tiles ? tiles : 1), kPlanThreads, 0, s>>>(a, w, tiles);
+        if (tiles) fork_place_kernel<<<(unsigned int)tiles, kPlanThreads, 0, s>>>(a, w);
+    }
+    if (row_blocks)
+        fork_act_kernel<<<(unsigned int)row_blocks + data_blocks, kPThreads, 0, s>>>(a, w, p, (unsigned int)row_blocks,
+                                                                                   chunks);
     return launched();
 }
 
@@ -620,7 +713,7 @@ extern "C" int pages_free(int32_t *table, size_t table_stride, size_t rows, size
     const u64 want = (rows + kPWarps - 1) / kPWarps, full = (u64)sms * 8;
     const unsigned int grid = (unsigned int)(want < full ? (want ? want : 1) : full);
     free_kernel<<<grid, kPThreads, 0, (cudaStream_t)stream>>>(table, table_stride, rows, width, lens, refs, pages,
-                                                              page_tokens, release, freed, carve(ws, pages, rows));
+                                                              (uint32_t)page_tokens, release, freed, carve(ws, pages, rows));
     return launched();
 }
 
@@ -640,15 +733,19 @@ extern "C" int pages_compact(const u32scan_page_pool *pool, int32_t *table, size
     int sms = 0;
     const int rc = sm_count(&sms);
     if (rc != U32SCAN_OK) return rc;
-    const CompactArgs a{table, table_stride, rows, width, lens, refs, pages, page_tokens, live, remap};
+    const CompactArgs a{table, table_stride, rows, width, lens, refs, pages, (uint32_t)page_tokens, live, remap};
     const PagesWs w = carve(ws, pages, rows);
     const unsigned int tiles = (unsigned int)ref_tiles(pages);
-    compact_count_kernel<<<tiles, kPThreads, 0, s>>>(a, w);
-    compact_pair_kernel<<<tiles, kPThreads, 0, s>>>(a, w);
+    if (tiles == 1) {
+        compact_plan_kernel<true><<<1, kPlanThreads, 0, s>>>(a, w);
+    } else {
+        compact_plan_kernel<false><<<tiles, kPlanThreads, 0, s>>>(a, w);
+        compact_place_kernel<<<tiles, kPlanThreads, 0, s>>>(a, w);
+    }
     const u64 want = (rows + kPWarps - 1) / kPWarps, ref_want = (pages / 2 + kPThreads - 1) / kPThreads;
     const unsigned int row_blocks = (unsigned int)(want < (u64)sms ? want : (u64)sms);
     const unsigned int ref_blocks = (unsigned int)(ref_want < (u64)sms ? (ref_want ? ref_want : 1) : (u64)sms);
     const unsigned int data_blocks = p.n_planes ? copy_grid(pages / 2 * units_per_pair(p), sms) : 0u;
-    compact_move_kernel<<<row_blocks + ref_blocks + data_blocks, kPThreads, 0, s>>>(a, w, p, row_blocks, ref_blocks);
+    compact_act_kernel<<<row_blocks + ref_blocks + data_blocks, kPThreads, 0, s>>>(a, w, p, row_blocks, ref_blocks);
     return launched();
 }
