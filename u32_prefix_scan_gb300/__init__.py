@@ -45,5 +45,6 @@ def __getattr__(name):
     if name in _API:
         from . import api
 
-        return getattr(api, name)
+        globals()[name] = getattr(api, name)  # found directly from now on
+        return globals()[name]
     raise AttributeError(name)

@@ -16,9 +16,9 @@
 // All of it is integer, so results do not depend on the order of atomics.
 //
 // Three launches, each reading what the one before wrote: plan (count the free
-// or live pages of every 16384 refs; the last block scans the counts and the
+// or live pages of every 4096 refs; the last block scans the counts and the
 // rows' needs), place (list the pages by rank) and act (table entries, refs,
-// bytes). A cache of up to 16384 pages is planned and placed by one block in
+// bytes). A cache of up to 4096 pages is planned and placed by one block in
 // one launch. refs is read twice, the second time from L2 (4 MB at a million
 // pages): a single pass that carries the rank from tile to tile would have
 // every tile wait for the one before, and the rows' needs, which decide how
@@ -37,7 +37,7 @@ constexpr int kPThreads = 256;      // free, copies and act
 constexpr int kPWarps = kPThreads / 32;
 constexpr int kPlanThreads = 1024;  // plan and place
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPerThread = 16;      // refs of a thread of plan and place
+constexpr int kPerThread = 4;       // refs of a thread of plan and place
 constexpr int kRefTile = kPlanThreads * kPerThread;
 constexpr u64 kOneBlockRows = 16384;  // rows up to which one block plans (16 a thread)
 constexpr int kEntryChunk = 512;    // table entries handled by one warp
@@ -190,7 +190,7 @@ __device__ __forceinline__ unsigned int free_mask(const int32_t *refs, u64 tile,
 __device__ __forceinline__ unsigned int page_mask(u64 tile, u64 pages) {
     const u64 first = tile * kRefTile + (u64)threadIdx.x * kPerThread;
     if (first >= pages) return 0u;
-    return pages - first >= kPerThread ? 0xffffu : (1u << (unsigned int)(pages - first)) - 1u;
+    return pages - first >= kPerThread ? (1u << kPerThread) - 1u : (1u << (unsigned int)(pages - first)) - 1u;
 }
 
 // ---------------------------------------------------------------------------
@@ -713,7 +713,8 @@ extern "C" int pages_free(int32_t *table, size_t table_stride, size_t rows, size
     const u64 want = (rows + kPWarps - 1) / kPWarps, full = (u64)sms * 8;
     const unsigned int grid = (unsigned int)(want < full ? (want ? want : 1) : full);
     free_kernel<<<grid, kPThreads, 0, (cudaStream_t)stream>>>(table, table_stride, rows, width, lens, refs, pages,
-                                                              (uint32_t)page_tokens, release, freed, carve(ws, pages, rows));
+                                                              (uint32_t)page_tokens, release, freed,
+                                                              carve(ws, pages, rows));
     return launched();
 }
 
