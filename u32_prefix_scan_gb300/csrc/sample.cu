@@ -108,9 +108,14 @@ struct SumBins {
             old[i] = 0;
             if (v[i] >= floor) old[i] = atomicAdd(&low[bin[i]], v[i]);
         }
+        bool carry = false;
 #pragma unroll
-        for (int i = 0; i < M; ++i)
-            if (old[i] + v[i] < old[i]) atomicAdd(&high[bin[i]], 1u);
+        for (int i = 0; i < M; ++i) carry |= old[i] > ~v[i];
+        if (carry) {
+#pragma unroll
+            for (int i = 0; i < M; ++i)
+                if (old[i] > ~v[i]) atomicAdd(&high[bin[i]], 1u);
+        }
     }
     __device__ __forceinline__ void clear() {
         for (int b = threadIdx.x; b < N; b += kSThreads) low[b] = high[b] = 0u;
@@ -125,6 +130,7 @@ struct alignas(16) SampleShared {
         struct {
             SumBins<kSThreads> sums;
             uint32_t counts[kSThreads];
+            uint32_t weights[kList];
         } picks;
     };
     u64 slots[kSlots][kMaxCluster][2];
@@ -407,6 +413,22 @@ __device__ __noinline__ u64 block_before(u64 v) {
 // The least over the block, in every thread.
 __device__ __noinline__ u64 block_min(u64 v) { return warp_min(of_warps(warp_min(v), 2, ~0ull)); }
 
+// The least lo and the greatest hi over the block, in every thread.
+__device__ __noinline__ void block_range(u64 &lo, u64 &hi) {
+    SampleShared &sh = block_shared();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    lo = warp_min(lo);
+    hi = warp_min(~hi);
+    __syncthreads();
+    if (lane == 0) {
+        sh.warp[0][warp] = lo;
+        sh.warp[1][warp] = hi;
+    }
+    __syncthreads();
+    lo = warp_min(lane < kSWarps ? sh.warp[0][lane] : ~0ull);
+    hi = ~warp_min(lane < kSWarps ? sh.warp[1][lane] : ~0ull);
+}
+
 // ---------------------------------------------------------------------------
 // A block's slice of a row
 // ---------------------------------------------------------------------------
@@ -493,8 +515,8 @@ struct Slice {
     }
 
     // f(vector, its number) for this lane's vectors, in ascending order, in
-    // the turns that may hold a logit at or above thr; the next one is on its
-    // way meanwhile.
+    // the turns that may hold a logit at or above thr; the next one that is
+    // not in shared memory is on its way meanwhile.
     template <typename F>
     __device__ __forceinline__ void each(float thr, F f) const {
         const unsigned int lane = threadIdx.x & 31;
@@ -519,15 +541,16 @@ struct Slice {
             }
             return ++past;
         };
-        unsigned int j = 32 * take() + lane;
-        uint4 next = make_uint4(0, 0, 0, 0);
-        if (has(j)) next = turn(j / 32, j);
+        unsigned int it = take();
+        uint4 ahead = make_uint4(0, 0, 0, 0);
+        if (it >= staged_iters && has(32 * it + lane)) ahead = load(v0 + 32 * it + lane);
 #pragma unroll 1
-        while (has(j)) {
-            const uint4 r = next;
-            const unsigned int v = v0 + j;
-            j = 32 * take() + lane;
-            if (has(j)) next = turn(j / 32, j);
+        while (has(32 * it + lane)) {
+            const unsigned int v = v0 + 32 * it + lane;
+            uint4 r = ahead;
+            if (it < staged_iters) r = stage[32 * it];
+            it = take();
+            if (it >= staged_iters && has(32 * it + lane)) ahead = load(v0 + 32 * it + lane);
             f(r, v);
         }
     }
@@ -552,43 +575,49 @@ __device__ __noinline__ uint32_t item_weight(u64 item, RowRule rule) {
 constexpr u64 kKeepAll = ~0ull;
 constexpr u64 kNoItem = ~0ull;  // an item without weight, past all others
 
-// Over the n gathered items up to `limit` that have a weight (of one each
-// with COUNT): the first, in order (or by index), at which the running sum of
-// weights reaches `target` (1 <= target <= the sum of all), and the sum
-// before it. A histogram of the places still in question, 512 bins between
-// the least and the greatest, then the same within the bin that holds the
-// crossing, until that is one item.
+// The gathered items' weights (of one each with COUNT), 0 past `limit`, for
+// block_select.
 template <bool COUNT>
-__device__ __noinline__ u64 block_select(uint32_t n, u64 limit, bool by_index, u64 target, const RowRule rule,
-                                         u64 *before_it) {
+__device__ __forceinline__ void weigh_items(uint32_t n, u64 limit, RowRule rule) {
     SampleShared &sh = block_shared();
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
+        const u64 item = sh.items[kLocal + i];
+        sh.picks.weights[i] = item > limit || item == kNoItem ? 0u : COUNT ? 1u : item_weight(item, rule);
+    }
+}
+
+// Over the n gathered items with a weight (weigh_items, by the same threads):
+// the first, in order (or by index), at which the running sum of weights
+// reaches `target` (1 <= target <= the sum of all), and the sum before it. A
+// histogram of the places still in question, 512 bins between the least and
+// the greatest, then the same within the bin that holds the crossing, until
+// that is one item.
+__device__ __noinline__ u64 block_select(uint32_t n, bool by_index, u64 target, u64 *before_it) {
+    SampleShared &sh = block_shared();
+    const u64 place_bits = by_index ? 0xffffffffull : ~0ull;
     u64 low = 0, high = ~0ull, base = 0;  // the places still in question
     while (true) {
-        u64 lo = ~0ull, hi = ~0ull;  // hi: complemented, so that both are minima
-        sh.picks.sums.clear();
-        sh.picks.counts[threadIdx.x] = 0;
-        int shift = 0;
+        u64 lo = ~0ull, hi = 0;
 #pragma unroll 1
-        for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll 1
-            for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
-                const u64 item = sh.items[kLocal + i], place = by_index ? item & 0xffffffffull : item;
-                if (item > limit || place < low || place > high) continue;
-                const uint32_t w = COUNT ? 1u : item_weight(item, rule);
-                if (w == 0) continue;
-                if (pass == 0) {
-                    lo = min(lo, place);
-                    hi = min(hi, ~place);
-                } else {
-                    const uint32_t bin = (uint32_t)((place - lo) >> shift);
-                    sh.picks.sums.add(bin, w);
-                    atomicAdd(&sh.picks.counts[bin], 1u);
-                }
+        for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
+            const u64 place = sh.items[kLocal + i] & place_bits;
+            if (sh.picks.weights[i] && place >= low && place <= high) {
+                lo = min(lo, place);
+                hi = max(hi, place);
             }
-            if (pass == 0) {
-                lo = block_min(lo);
-                hi = ~block_min(hi);
-                shift = 55 - __clzll((hi - lo) | 511ull);
+        }
+        sh.picks.sums.low[threadIdx.x] = sh.picks.sums.high[threadIdx.x] = sh.picks.counts[threadIdx.x] = 0;
+        block_range(lo, hi);
+        const int shift = 55 - __clzll((hi - lo) | 511ull);
+#pragma unroll 1
+        for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
+            const u64 place = sh.items[kLocal + i] & place_bits;
+            const uint32_t w = sh.picks.weights[i];
+            if (w && place >= low && place <= high) {
+                const uint32_t bin = (uint32_t)((place - lo) >> shift);
+                sh.picks.sums.add(bin, w);
+                atomicAdd(&sh.picks.counts[bin], 1u);
             }
         }
         __syncthreads();
@@ -609,8 +638,8 @@ __device__ __noinline__ u64 block_select(uint32_t n, u64 limit, bool by_index, u
     }
 #pragma unroll 1
     for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
-        const u64 item = sh.items[kLocal + i], place = by_index ? item & 0xffffffffull : item;
-        if (item <= limit && place >= low && place <= high && (COUNT || item_weight(item, rule))) sh.cast[3] = item;
+        const u64 place = sh.items[kLocal + i] & place_bits;
+        if (sh.picks.weights[i] && place >= low && place <= high) sh.cast[3] = sh.items[kLocal + i];
     }
     __syncthreads();
     *before_it = base;
@@ -873,19 +902,23 @@ __device__ __noinline__ void finish_list(uint32_t n, uint32_t k, float p, u64 to
         return;
     }
     u64 last = kKeepAll, before;
-    if (k < n) last = block_select<true>(n, last, false, k, rule, &before);
+    if (k < n) {
+        weigh_items<true>(n, last, rule);
+        last = block_select(n, false, k, &before);
+    }
+    weigh_items<false>(n, last, rule);
     if (total == 0) {
         u64 sum = 0;
 #pragma unroll 1
-        for (uint32_t i = threadIdx.x; i < n; i += kSThreads)
-            if (sh.items[kLocal + i] <= last) sum += item_weight(sh.items[kLocal + i], rule);
+        for (uint32_t i = threadIdx.x; i < n; i += kSThreads) sum += sh.picks.weights[i];
         total = block_total(sum);
     }
     if (cut_p) {
-        last = block_select<false>(n, last, false, top_p_target(p, total), rule, &before);
+        last = block_select(n, false, top_p_target(p, total), &before);
         total = before + item_weight(last, rule);
+        weigh_items<false>(n, last, rule);
     }
-    const u64 chosen = block_select<false>(n, last, true, draw_of(word, total) + 1, rule, &before);
+    const u64 chosen = block_select(n, true, draw_of(word, total) + 1, &before);
     if (threadIdx.x == 0) write_token(a, row, (uint32_t)chosen, item_weight(chosen, rule), total);
 }
 
@@ -1134,7 +1167,6 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         u64 mass = 0;
         if (!cut_p) {
             sl.each(zero, [&](const uint4 &r, unsigned int) {
-                if (!(V::max(r) >= zero)) return;
                 float x[V::N];
                 V::unpack(r, x);
 #pragma unroll
@@ -1160,7 +1192,6 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         __syncthreads();
         SumBins<kBins> &bins = sh.bins[warp / (kSWarps / 2)];
         sl.each(zero, [&](const uint4 &r, unsigned int) {
-            if (!(V::max(r) >= zero)) return;
             float x[V::N];
             V::unpack(r, x);
 #pragma unroll
@@ -1256,7 +1287,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
                 cluster_wait();
             } else {  // every block finds the crossing among the gathered, and what is kept of them where
                 u64 left;
-                const u64 last = block_select<false>(n, kKeepAll, false, want - above, rule, &left);
+                weigh_items<false>(n, kKeepAll, rule);
+                const u64 last = block_select(n, false, want - above, &left);
                 left += above + item_weight(last, rule);
                 const uint32_t from = (uint32_t)slot_total(kSlotSecond, rank), to = from + sh.n_list;
                 const uint32_t second = (rank * kSWarps + kSWarps / 2) * a.per_warp * V::N;  // its first element
@@ -1265,7 +1297,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
                 for (uint32_t i = threadIdx.x; i < to; i += kSThreads) {
                     const u64 item = sh.items[kLocal + i];
                     if (item > last) continue;
-                    const u64 q = item_weight(item, rule);
+                    const u64 q = sh.picks.weights[i];
                     if (i < from) ahead += q;
                     else if ((uint32_t)item + sl.pad < second) in[0] += q;
                     else in[1] += q;
