@@ -27,15 +27,15 @@
 //   top-k   the k-th largest of the maxima of groups of threads is a bound
 //           below which no kept token lies; the few logits at or above it
 //           (with 2 k groups some 1.4 k) are gathered into one block, which
-//           makes the draw.
+//           makes the draw. Where a row has fewer than 2 k groups: as top-p,
+//           with counts for weights.
 //   top-p   a histogram of the weights by y (32 bins an octave) gives the bin
 //           in which the prefix sum crosses; that bin's logits are gathered
 //           (or all above it too, if they are few: then the gathering block
 //           makes the draw as well). The histogram also tells each half of a
 //           block what it keeps, so that only the half with the draw weighs
-//           again.
-//   else    (huge k, long ties, infinite logits) radix selection on the
-//           logits' bits, 8 a level, on counts or sums of weights.
+//           again. A bin with more logits than are gathered (long ties, flat
+//           rows) is searched by radix selection on its logits' bits.
 // A filter ends at an item, (~key, index) as one u64: what stands at or
 // before it in order stays, so ties need no count of their own.
 #include <cstdint>
@@ -77,14 +77,17 @@ struct SampleArgs {
 // Exchanges between a cluster's blocks: one slot each, so that none is
 // written again while a slow block still reads it.
 enum Slot {
-    kSlotMax,
-    kSlotFirst,
-    kSlotSecond,
-    kSlotSum,
-    kSlotTies,
-    kSlotTieAt,
-    kSlotTies2,
-    kSlotTieAt2,
+    kSlotMax,       // the largest logit
+    kSlotBound,     // lengths of the lists above the bound
+    kSlotFirst,     // greedy: the least index; no top-p: weights
+    kSlotCounts,    // top-k by histogram: counts, lengths of lists, ties, the tie
+    kSlotCountList,
+    kSlotCountTies,
+    kSlotCountTie,
+    kSlotSums,      // top-p: weights, lengths of lists and weights above, ties, the tie, weights kept
+    kSlotSumList,
+    kSlotSumTies,
+    kSlotSumTie,
     kSlotDraw,
     kSlots
 };
@@ -248,6 +251,14 @@ __device__ __forceinline__ uint32_t exp2_weight(float y) {
 struct RowRule {
     float m, scale;
     uint32_t qmin;
+};
+
+// Where a row's result goes, and the word it is drawn with.
+struct RowEnd {
+    int32_t *token;
+    float *prob;
+    uint32_t word;
+    unsigned int per_warp;
 };
 
 // A logit's weight, any logit, any rule.
@@ -631,7 +642,7 @@ __device__ __noinline__ u64 block_select(uint32_t n, bool by_index, u64 target, 
         __syncthreads();
         base = sh.cast[1];
         low = lo + (sh.cast[0] << shift);
-        high = low + ((1ull << shift) - 1);
+        high = min(high, low + ((1ull << shift) - 1));  // the last bin may reach past the places in question
         const bool one = sh.cast[2] == 1;
         __syncthreads();  // cast and the bins are written again
         if (one) break;
@@ -646,9 +657,9 @@ __device__ __noinline__ u64 block_select(uint32_t n, bool by_index, u64 target, 
     return sh.cast[3];
 }
 
-__device__ __noinline__ void write_token(const SampleArgs &a, u64 row, uint32_t index, u64 q, u64 total) {
-    a.tokens[row] = (int32_t)index;
-    if (a.probs) a.probs[row] = (float)((double)q / (double)total);
+__device__ __noinline__ void write_token(RowEnd end, uint32_t index, u64 q, u64 total) {
+    *end.token = (int32_t)index;
+    if (end.prob) *end.prob = (float)((double)q / (double)total);
 }
 
 __device__ __forceinline__ u64 draw_of(uint32_t word, u64 total) { return __umul64hi((u64)word << 32, total); }
@@ -671,32 +682,30 @@ __device__ __forceinline__ void halves_of(u64 warp_mass, u64 (&half)[2]) {
     half[1] = block_total(threadIdx.x < kSThreads / 2 ? 0ull : one);
 }
 
-// The weights of a vector's logits up to `last`, 0 for the others; `finite`
-// says that m and scale are.
+// The weights of a vector's logits up to `last`, 0 for the others, for a
+// finite m and scale.
 template <typename T>
-__device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const uint4 &r, unsigned int v, RowRule rule,
-                                            bool finite, u64 last, uint32_t (&q)[Vec<T>::N]) {
-    const float thr = last == kKeepAll ? -INFINITY : key_logit(~(uint32_t)(last >> 32));
+__device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const uint4 &r, unsigned int v, RowRule rule, u64 last,
+                                            uint32_t (&q)[Vec<T>::N]) {
     float x[Vec<T>::N];
     Vec<T>::unpack(r, x);
-    u64 sum = 0;
 #pragma unroll
     for (int e = 0; e < Vec<T>::N; e += 2) {
+        float y[2];
         uint32_t w[2];
-        if (finite) {
-            float y[2];
-            weigh2(x[e], x[e + 1], pack2(rule.m, rule.m), pack2(rule.scale, rule.scale), y, w);
-        } else {
-            w[0] = token_weight(x[e], rule);
-            w[1] = token_weight(x[e + 1], rule);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool keep = x[e + i] > thr || (x[e + i] == thr && sl.index(v, e + i) <= (uint32_t)last);
-            q[e + i] = keep && w[i] >= rule.qmin ? w[i] : 0u;
-            sum += q[e + i];
-        }
+        weigh2(x[e], x[e + 1], pack2(rule.m, rule.m), pack2(rule.scale, rule.scale), y, w);
+        q[e] = w[0] >= rule.qmin ? w[0] : 0u;
+        q[e + 1] = w[1] >= rule.qmin ? w[1] : 0u;
     }
+    if (last != kKeepAll) {
+        const float thr = key_logit(~(uint32_t)(last >> 32));
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; ++e)
+            if (x[e] < thr || (x[e] == thr && sl.index(v, e) > (uint32_t)last)) q[e] = 0;
+    }
+    u64 sum = 0;
+#pragma unroll
+    for (int e = 0; e < Vec<T>::N; ++e) sum += q[e];
     return sum;
 }
 
@@ -705,17 +714,17 @@ __device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const uint4 &r, 
 // this one's halves do. It weighs that half again, a turn of 32 vectors a
 // warp, and walks the turn with the draw.
 template <typename T>
-__device__ __noinline__ void draw(const Slice<T> &own, RowRule rule, bool finite, u64 last, u64 total, u64 before,
-                                  const u64 (&half)[2], const SampleArgs &a, u64 row) {
+__device__ __noinline__ void draw(Slice<T> own, RowRule rule, u64 last, u64 total, u64 before,
+                                  const u64 (&half)[2], RowEnd end) {
     SampleShared &sh = block_shared();
     constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const u64 r = draw_of(a.random[row], total);
+    const u64 r = draw_of(end.word, total);
     if (r < before || r - before >= half[0] + half[1]) return;
     const bool second = r - before >= half[0];
     if (second) before += half[0];
     const int warp0 = second ? kSWarps / 2 : 0;
-    const unsigned int per_warp = a.per_warp, nv = (own.pad + own.n + N - 1) / N;
+    const unsigned int per_warp = end.per_warp, nv = (own.pad + own.n + N - 1) / N;
     const unsigned int per = (per_warp + 31) / 32, turns = kSWarps / 2 * per;
     u64 *mass = sh.items;  // by turn
     u64 at = 0;
@@ -729,7 +738,7 @@ __device__ __noinline__ void draw(const Slice<T> &own, RowRule rule, bool finite
         u64 sum = 0;
         const Slice<T> sl = own.of_warp(warp0 + (int)(t / per) - warp, per_warp, nv);
         const unsigned int it = t % per, j = 32 * it + lane;
-        if (t < turns && sl.has(j)) sum = kept_weights(sl, sl.turn(it, j), sl.v0 + j, rule, finite, last, q);
+        if (t < turns && sl.has(j)) sum = kept_weights(sl, sl.turn(it, j), sl.v0 + j, rule, last, q);
         if (walk) {
             at += warp_inclusive(sum) - sum;
             if (at <= r && r - at < sum) {
@@ -743,7 +752,7 @@ __device__ __noinline__ void draw(const Slice<T> &own, RowRule rule, bool finite
                     }
                     at += q[e];
                 }
-                write_token(a, row, sl.index(sl.v0 + j, chosen), weight, total);
+                write_token(end, sl.index(sl.v0 + j, chosen), weight, total);
             }
             return;
         }
@@ -832,6 +841,19 @@ __device__ __forceinline__ void each_of(const float (&x)[N], Test test, F f) {
     }
 }
 
+// Gathers the logits in [thr, cap] (-inf not among them) into this block's list.
+template <typename T>
+__device__ __noinline__ void collect(Slice<T> sl, float thr, float cap) {
+    sl.each(thr, [&](const uint4 &r, unsigned int v) {
+        if (!(Vec<T>::max(r) >= thr)) return;
+        float x[Vec<T>::N];
+        Vec<T>::unpack(r, x);
+        each_of<Vec<T>::N>(x, [&](float xe) { return xe >= thr && xe <= cap && xe > -INFINITY; },
+                           [&](float xe, int e) { put(item_of(key_of(xe), sl.index(v, e))); });
+    });
+    __syncthreads();
+}
+
 // The length of all blocks' lists, after an exchange of their lengths as
 // `slot`'s first word; over kList when one of them or all do not fit.
 __device__ __forceinline__ uint32_t gathered(Slot slot) {
@@ -857,10 +879,10 @@ __device__ __forceinline__ void pull(Slot slot, uint32_t n) {
 // the first k of them in order, and of those the top-p prefix (0 < p < 1),
 // measured against `total` if that is not 0, else against their own sum.
 __device__ __noinline__ void finish_list(uint32_t n, uint32_t k, float p, u64 total,
-                                         const RowRule &rule, const SampleArgs &a, u64 row) {
+                                         RowRule rule, RowEnd end) {
     SampleShared &sh = block_shared();
     const bool cut_p = p > 0.0f && p < 1.0f;
-    const uint32_t word = a.random[row];
+    const uint32_t word = end.word;
     if (n <= kRanked) {
         // `team` threads an item count what stands before it
         uint32_t team = 2;
@@ -898,7 +920,7 @@ __device__ __noinline__ void finish_list(uint32_t n, uint32_t k, float p, u64 to
             at += (uint32_t)sh.items[kLocal + j] < (uint32_t)item ? weight[j] : 0ull;
         for (uint32_t d = 1; d < team; d *= 2) at += __shfl_xor_sync(0xffffffffu, at, d);
         const u64 r = draw_of(word, total);
-        if (part == 0 && at <= r && r < at + kept) write_token(a, row, (uint32_t)item, kept, total);
+        if (part == 0 && at <= r && r < at + kept) write_token(end, (uint32_t)item, kept, total);
         return;
     }
     u64 last = kKeepAll, before;
@@ -919,63 +941,13 @@ __device__ __noinline__ void finish_list(uint32_t n, uint32_t k, float p, u64 to
         weigh_items<false>(n, last, rule);
     }
     const u64 chosen = block_select(n, true, draw_of(word, total) + 1, &before);
-    if (threadIdx.x == 0) write_token(a, row, (uint32_t)chosen, item_weight(chosen, rule), total);
-}
-
-// The key at which the running total over the items up to `last`, keys in
-// descending order, of counts or of weights (MASS), first reaches `target`
-// (1 <= target <= the whole total), and what is missing above it (>= 1).
-// `level` numbers the levels of a row's selections (their two buffers swap:
-// a slow block may still read the last level's).
-template <bool MASS, typename T>
-__device__ __noinline__ void radix_select(const Slice<T> &sl, const RowRule &rule, u64 last,
-                                          u64 target, int &level, uint32_t *tau, u64 *missing) {
-    SampleShared &sh = block_shared();
-    uint32_t prefix = 0, mask = 0;
-#pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8, ++level) {
-        SumBins<256> &hist = sh.digits[level & 1];
-        hist.clear();
-        __syncthreads();
-        sl.each(-INFINITY, [&](const uint4 &r, unsigned int v) {
-            float x[Vec<T>::N];
-            Vec<T>::unpack(r, x);
-#pragma unroll 1
-            for (int e = 0; e < Vec<T>::N; ++e) {
-                if (x[e] != x[e]) x[e] = -INFINITY;
-                const uint32_t k = key_of(x[e]);
-                if ((k & mask) != prefix || item_of(k, sl.index(v, e)) > last) continue;
-                const uint32_t w = MASS ? token_weight(x[e], rule) : 1u;
-                if (w) hist.add((k >> shift) & 255u, w);
-            }
-        });
-        cluster_arrive();
-        cluster_wait();
-        // the digits in descending order: thread t has digit 255 - t
-        u64 mine = 0;
-        if (threadIdx.x < 256)
-            for (uint32_t c = 0; c < cluster_size(); ++c)
-                mine += (u64)ld_cluster(at_rank(&hist.low[255 - threadIdx.x], c)) +
-                        ((u64)ld_cluster(at_rank(&hist.high[255 - threadIdx.x], c)) << 32);
-        const u64 before = block_before(mine);
-        if (before < target && target <= before + mine) {
-            sh.cast[0] = 255u - threadIdx.x;
-            sh.cast[1] = target - before;
-        }
-        __syncthreads();
-        prefix |= (uint32_t)sh.cast[0] << shift;
-        mask |= 255u << shift;
-        target = sh.cast[1];
-        __syncthreads();
-    }
-    *tau = prefix;
-    *missing = target;
+    if (threadIdx.x == 0) write_token(end, (uint32_t)chosen, item_weight(chosen, rule), total);
 }
 
 // The `nth` logit (from 1, by index) with key tau, as an item; -inf entries
 // past the row's ends do not count.
 template <typename T>
-__device__ __noinline__ u64 nth_tie(const Slice<T> &sl, uint32_t tau, u64 nth, Slot ties_slot,
+__device__ __noinline__ u64 nth_tie(Slice<T> sl, uint32_t tau, u64 nth, Slot ties_slot,
                                     Slot at_slot) {
     SampleShared &sh = block_shared();
     const int lane = threadIdx.x & 31;
@@ -991,7 +963,7 @@ __device__ __noinline__ u64 nth_tie(const Slice<T> &sl, uint32_t tau, u64 nth, S
         return t;
     };
     u64 mine = 0;
-    sl.each(-INFINITY, [&](const uint4 &r, unsigned int v) { mine += __popc(tied(r, v)); });
+    sl.each(key_logit(tau), [&](const uint4 &r, unsigned int v) { mine += __popc(tied(r, v)); });
     mine = warp_total(mine);
     if (threadIdx.x == 0) sh.cast[0] = ~0ull;
     u64 before = block_before(lane == 0 ? mine : 0ull);  // of lane 0: the warps' before
@@ -1016,42 +988,270 @@ __device__ __noinline__ u64 nth_tie(const Slice<T> &sl, uint32_t tau, u64 nth, S
     return warp_min(lane < (int)cluster_size() ? sh.slots[at_slot][lane][0] : ~0ull);
 }
 
-// The filters by selection on the logits' bits, then the draw: right for
-// every row, and the way of those the other paths do not take.
-template <typename T>
-__device__ __noinline__ void sample_by_selection(const Slice<T> &sl, const RowRule &rule, uint32_t k,
-                                                 float p, const SampleArgs &a, u64 row) {
-    u64 last = kKeepAll, missing;
-    uint32_t tau;
-    int level = 0;
-    if (k > 0) {
-        radix_select<false>(sl, rule, kKeepAll, k, level, &tau, &missing);
-        if (tau > kKeyOfMinusInf) last = nth_tie(sl, tau, missing, kSlotTies, kSlotTieAt);
-    }
-    auto kept = [&](u64 (&half)[2]) {
-        u64 mass = 0;
-        sl.each(-INFINITY, [&](const uint4 &r, unsigned int v) {
-            uint32_t q[Vec<T>::N];
-            mass += kept_weights(sl, r, v, rule, false, last, q);
+// The histogram bin in which a filter ends, and what lies in it.
+struct Crossing {
+    uint32_t bin;
+    uint32_t floor_q;  // the least weight in the histogram (counts: 1, as far as y < 31)
+    float thr, cap;    // every logit of the bin is in [thr, cap], few others are
+    u64 limit;         // items past it do not count
+    bool upto;         // the bins before it too
+};
+
+// Is the logit x (in [thr, cap]) with this index one of the crossing's?
+template <bool COUNT>
+__device__ __forceinline__ bool in_crossing(const Crossing &c, RowRule rule, float x, u64 item) {
+    const float y = __fmul_rn(__fsub_rn(rule.m, x), rule.scale);
+    if (!(y < (COUNT ? 31.0f : 32.0f))) return false;
+    const uint32_t b = bin_of(y);
+    return (c.upto ? b <= c.bin : b == c.bin) && (COUNT || (exp2_weight(y) >= c.floor_q && item <= c.limit));
+}
+
+// The item at which the running sum of the bin's weights (counts) reaches
+// target, over the whole cluster: its key by radix selection, 8 bits a level,
+// then the tie. *left: the sum up to it.
+template <bool COUNT, typename T>
+__device__ __noinline__ u64 select_in_bin(Slice<T> sl, RowRule rule, const Crossing &c, u64 target, u64 *left) {
+    SampleShared &sh = block_shared();
+    uint32_t prefix = 0, mask = 0;
+    u64 missing = target;
+#pragma unroll 1
+    for (int shift = 24; shift >= 0; shift -= 8) {
+        SumBins<256> &hist = sh.digits[shift / 8 & 1];  // two in turn: a slow block may still read the last one
+        __syncthreads();
+        hist.clear();
+        __syncthreads();
+        sl.each(c.thr, [&](const uint4 &r, unsigned int v) {
+            if (!(Vec<T>::max(r) >= c.thr)) return;
+            float x[Vec<T>::N];
+            Vec<T>::unpack(r, x);
+            each_of<Vec<T>::N>(x, [&](float xe) { return xe >= c.thr && xe <= c.cap; },
+                               [&](float xe, int e) {
+                                   const uint32_t k = key_of(xe);
+                                   if ((k & mask) != prefix) return;
+                                   if (!in_crossing<COUNT>(c, rule, xe, item_of(k, sl.index(v, e)))) return;
+                                   hist.add((k >> shift) & 255u, COUNT ? 1u : token_weight(xe, rule));
+                               });
         });
-        halves_of(warp_total(mass), half);
-    };
-    u64 half[2];
-    kept(half);
-    exchange(kSlotSum, half[0] + half[1], 0);
-    u64 total = slot_total(kSlotSum, cluster_size());
-    Slot slot = kSlotSum;
-    if (p > 0.0f && p < 1.0f) {
-        const u64 want = top_p_target(p, total);
-        radix_select<true>(sl, rule, last, want, level, &tau, &missing);
-        const u64 q = token_weight(key_logit(tau), rule), ties = (missing + q - 1) / q;
-        last = nth_tie(sl, tau, ties, kSlotTies2, kSlotTieAt2);
-        total = want - missing + ties * q;
-        kept(half);
-        exchange(kSlotDraw, half[0] + half[1], 0);
-        slot = kSlotDraw;
+        cluster_arrive();
+        cluster_wait();
+        // the digits in descending order: thread t has digit 255 - t
+        u64 mine = 0;
+        if (threadIdx.x < 256)
+            for (uint32_t b = 0; b < cluster_size(); ++b)
+                mine += (u64)ld_cluster(at_rank(&hist.low[255 - threadIdx.x], b)) +
+                        ((u64)ld_cluster(at_rank(&hist.high[255 - threadIdx.x], b)) << 32);
+        const u64 before = block_before(mine);
+        if (before < missing && missing <= before + mine) {
+            sh.cast[0] = 255u - threadIdx.x;
+            sh.cast[1] = missing - before;
+        }
+        __syncthreads();
+        prefix |= (uint32_t)sh.cast[0] << shift;
+        mask |= 255u << shift;
+        missing = sh.cast[1];
     }
-    draw(sl, rule, false, last, total, slot_total(slot, cluster_rank()), half, a, row);
+    const u64 q = COUNT ? 1ull : token_weight(key_logit(prefix), rule), ties = (missing + q - 1) / q;
+    *left = target - missing + ties * q;
+    return nth_tie(sl, prefix, ties, COUNT ? kSlotCountTies : kSlotSumTies, COUNT ? kSlotCountTie : kSlotSumTie);
+}
+
+// A filter over a row of finite m and scale: top-k (COUNT) or top-p over the
+// items up to `limit`, by a histogram of counts or weights. Returns true when
+// the row's token is written (top-p: always), else *last is the item at
+// which the filter ends.
+template <bool COUNT, typename T>
+__device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float p, u64 limit,
+                                    RowEnd end, u64 *last) {
+    SampleShared &sh = block_shared();
+    using V = Vec<T>;
+    const uint32_t rank = cluster_rank(), blocks = cluster_size();
+    const int warp = threadIdx.x >> 5;
+    const Slot sums_slot = COUNT ? kSlotCounts : kSlotSums, list_slot = COUNT ? kSlotCountList : kSlotSumList;
+    // top-p: the histogram goes as far as it can matter (past cut_y the row holds less than (1 - p)
+    // of the largest weight); with min-p it takes all that is kept, and its sum is the row's
+    const float cut_y = fminf(31.0f, log2f((float)sl.n / (1.0f - p)) + 0.1f);
+    const bool min_p = rule.qmin > 0;
+    Crossing c;
+    c.limit = limit;
+    c.floor_q = COUNT ? 1u : min_p ? rule.qmin : max(exp2_weight(cut_y), 1u);
+    __syncthreads();
+    sh.bins[0].clear();
+    sh.bins[1].clear();
+    if (threadIdx.x == 0) sh.n_list = 0;
+    __syncthreads();
+    SumBins<kBins> &bins = sh.bins[warp / (kSWarps / 2)];
+    const u64 m2 = pack2(rule.m, rule.m), scale2 = pack2(rule.scale, rule.scale);
+    const float zero = __fsub_rd(rule.m, __fdiv_ru(31.5f, rule.scale));  // logits below it weigh nothing
+    const bool limited = limit != kKeepAll;
+    const float limit_x = limited ? key_logit(~(uint32_t)(limit >> 32)) : -INFINITY;
+    u64 mass = 0;
+    sl.each(zero, [&](const uint4 &r, unsigned int v) {
+        float x[V::N];
+        V::unpack(r, x);
+#pragma unroll
+        for (int e = 0; e < V::N; e += 4) {
+            if constexpr (COUNT) {
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    float y[2];
+                    unpack2(mul2(sub2(m2, pack2(x[e + i], x[e + i + 1])), scale2), y[0], y[1]);
+                    if (y[0] < 31.0f) atomicAdd(&bins.low[bin_of(y[0])], 1u);
+                    if (y[1] < 31.0f) atomicAdd(&bins.low[bin_of(y[1])], 1u);
+                }
+            } else {
+                uint32_t b[4], q[4];
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    float y2[2];
+                    uint32_t q2[2];
+                    weigh2(x[e + i], x[e + i + 1], m2, scale2, y2, q2);
+                    q[i] = q2[0];
+                    q[i + 1] = q2[1];
+                    b[i] = bin_of(y2[0]);
+                    b[i + 1] = bin_of(y2[1]);
+                }
+                if (limited)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool past = x[e + i] == limit_x && sl.index(v, e + i) > (uint32_t)limit;
+                        if (x[e + i] < limit_x || past) q[i] = 0;
+                    }
+                mass += (u64)q[0] + q[1];
+                mass += (u64)q[2] + q[3];
+                bins.add_from(c.floor_q, b, q);
+            }
+        }
+    });
+    __syncthreads();
+    // two bins a thread, of both halves and (for the other blocks) their sum
+    u64 own[2][2], *sums = sh.items + kLocal;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int b = 2 * threadIdx.x + i;
+        own[0][i] = (u64)sh.bins[0].high[b] << 32 | sh.bins[0].low[b];
+        own[1][i] = (u64)sh.bins[1].high[b] << 32 | sh.bins[1].low[b];
+        sums[b] = own[0][i] + own[1][i];
+    }
+    exchange(sums_slot, block_total(COUNT || min_p ? own[0][0] + own[0][1] + own[1][0] + own[1][1] : mass), 0);
+    const u64 total = slot_total(sums_slot, blocks), want = COUNT ? k : top_p_target(p, total);
+    if (COUNT && total <= want) {  // all that have a weight are kept
+        *last = limit;
+        return false;
+    }
+    // the bin in which the running sum reaches `want`
+    u64 part[kMaxCluster][2];
+#pragma unroll
+    for (uint32_t b = 0; b < kMaxCluster; ++b) {
+        part[b][0] = part[b][1] = 0;
+        if (b < blocks) ld_cluster_u64x2(at_rank(sums + 2 * threadIdx.x, b), part[b][0], part[b][1]);
+    }
+    u64 bin_mass[2] = {0, 0};
+#pragma unroll
+    for (uint32_t b = 0; b < kMaxCluster; ++b) {
+        bin_mass[0] += part[b][0];
+        bin_mass[1] += part[b][1];
+    }
+    const u64 before = block_before(bin_mass[0] + bin_mass[1]);
+    if (before < want && want <= before + bin_mass[0] + bin_mass[1]) {
+        const bool second = want > before + bin_mass[0];
+        sh.cast[0] = 2 * threadIdx.x + second;
+        sh.cast[1] = before + (second ? bin_mass[0] : 0ull);
+        sh.cast[2] = before + bin_mass[0] + (second ? bin_mass[1] : 0ull);
+    }
+    __syncthreads();
+    c.bin = (uint32_t)sh.cast[0];
+    const u64 above = sh.cast[1];
+    // Are there few enough to gather all up to this bin? None there weighs less than the bin's far
+    // end, less more than the recipe's error.
+    const uint32_t far = exp2_weight(((float)c.bin + 0.5f) * (1.0f / 32.0f)), slack = (far >> 16) + 2;
+    c.upto = sh.cast[2] <= (COUNT ? (u64)kList : (u64)max(far > slack ? far - slack : 0u, c.floor_q) * kList);
+    u64 half[2] = {0, 0};  // weights of the bins before it
+    if (!COUNT)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            half[h] = block_total((2 * threadIdx.x < c.bin ? own[h][0] : 0ull) +
+                                  (2 * threadIdx.x + 1 < c.bin ? own[h][1] : 0ull));
+    // Every logit in a bin up to this one is at or above thr, every one in a bin from it on at or
+    // below cap; the few others between them are taken out of the list afterwards.
+    c.thr = __fsub_rd(rule.m, __fdiv_ru(((float)c.bin + 0.51f) * (1.0f / 32.0f), rule.scale));
+    c.cap = c.upto || c.bin == 0
+                ? INFINITY
+                : __fsub_ru(rule.m, __fdiv_rd(((float)c.bin - 0.51f) * (1.0f / 32.0f), rule.scale));
+    collect(sl, c.thr, c.cap);
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < min(sh.n_list, (uint32_t)kLocal); i += kSThreads)
+        if (!in_crossing<COUNT>(c, rule, key_logit(~(uint32_t)(sh.items[i] >> 32)), sh.items[i])) sh.items[i] = kNoItem;
+    exchange(list_slot, sh.n_list, half[0] + half[1]);
+    const uint32_t n = gathered(list_slot);
+    u64 left;
+    if (n > kList) {
+        c.upto = false;
+        *last = select_in_bin<COUNT>(sl, rule, c, want - above, &left);
+        if (COUNT) return false;
+        u64 kept = 0;
+        sl.each(zero, [&](const uint4 &r, unsigned int v) {
+            uint32_t q[V::N];
+            kept += kept_weights(sl, r, v, rule, *last, q);
+        });
+        halves_of(warp_total(kept), half);
+        exchange(kSlotDraw, half[0] + half[1], 0);
+        draw(sl, rule, *last, above + left, slot_total(kSlotDraw, rank), half, end);
+        return true;
+    }
+    if (!c.upto || rank == 0) pull(list_slot, n);
+    cluster_arrive();  // no block leaves, or writes over its list, while others read it
+    if (c.upto) {
+        if (rank == 0) finish_list(n, COUNT ? k : 0xffffffffu, p, COUNT ? 0ull : total, rule, end);
+        cluster_wait();
+        return true;
+    }
+    // every block finds the crossing among the gathered, and what is kept of them where
+    weigh_items<COUNT>(n, kKeepAll, rule);
+    *last = block_select(n, false, want - above, &left);
+    if (!COUNT) {
+        left += above + item_weight(*last, rule);
+        const uint32_t from = (uint32_t)slot_total(list_slot, rank), to = from + sh.n_list;
+        const uint32_t second = (rank * kSWarps + kSWarps / 2) * end.per_warp * V::N;  // its first element
+        u64 ahead = 0, in[2] = {0, 0};
+#pragma unroll 1
+        for (uint32_t i = threadIdx.x; i < to; i += kSThreads) {
+            const u64 item = sh.items[kLocal + i];
+            if (item > *last) continue;
+            const u64 q = sh.picks.weights[i];
+            if (i < from) ahead += q;
+            else if ((uint32_t)item + sl.pad < second) in[0] += q;
+            else in[1] += q;
+        }
+        ahead = block_total(ahead) + slot_total(list_slot, rank, 1);
+        half[0] += block_total(in[0]);
+        half[1] += block_total(in[1]);
+        cluster_wait();
+        draw(sl, rule, *last, left, ahead, half, end);
+        return true;
+    }
+    cluster_wait();
+    return false;
+}
+
+// A row whose largest logit is infinite, or whose scale is: only the largest
+// have a weight, 2^31 each.
+template <typename T>
+__device__ __noinline__ void sample_largest(Slice<T> sl, uint32_t row_key, uint32_t k, float p,
+                                            RowEnd end) {
+    u64 ties = 0;
+    sl.each(key_logit(row_key), [&](const uint4 &r, unsigned int) {
+        float x[Vec<T>::N];
+        Vec<T>::unpack(r, x);
+#pragma unroll
+        for (int e = 0; e < Vec<T>::N; ++e) ties += x[e] == key_logit(row_key);
+    });
+    exchange(kSlotFirst, block_total(ties), 0);
+    ties = slot_total(kSlotFirst, cluster_size());
+    if (k > 0 && k < ties) ties = k;
+    if (p > 0.0f && p < 1.0f) ties = (top_p_target(p, ties << 31) + (1ull << 31) - 1) >> 31;
+    const u64 nth = (draw_of(end.word, ties << 31) >> 31) + 1;
+    const u64 item = nth_tie(sl, row_key, nth, kSlotSumTies, kSlotSumTie);
+    if (cluster_rank() == 0 && threadIdx.x == 0) write_token(end, (uint32_t)item, 1ull << 31, ties << 31);
 }
 
 template <typename T>
@@ -1060,6 +1260,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     using V = Vec<T>;
     const uint32_t rank = cluster_rank(), blocks = cluster_size();
     const u64 row = blockIdx.x / blocks;
+    const RowEnd end{a.tokens + row, a.probs ? a.probs + row : nullptr, a.random[row], a.per_warp};
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     cluster_arrive();  // paired with the wait before the first exchange: every block has started
     if (threadIdx.x == 0) sh.n_list = 0;
@@ -1108,8 +1309,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         __reduce_max_sync(0xffffffffu, lane < (int)blocks ? (uint32_t)sh.slots[kSlotMax][lane][0] : 0u);
     if (row_key <= kKeyOfMinusInf) {  // the mask leaves nothing
         if (rank == 0 && threadIdx.x == 0) {
-            a.tokens[row] = -1;
-            if (a.probs) a.probs[row] = 0.0f;
+            *end.token = -1;
+            if (end.prob) *end.prob = 0.0f;
         }
         return;
     }
@@ -1132,191 +1333,53 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         exchange(kSlotFirst, block_min(first), 0);
         first = __reduce_min_sync(0xffffffffu, lane < (int)blocks ? (uint32_t)sh.slots[kSlotFirst][lane][0] : first);
         if (rank == 0 && threadIdx.x == 0) {
-            a.tokens[row] = (int32_t)first;
-            if (a.probs) a.probs[row] = 1.0f;
+            *end.token = (int32_t)first;
+            if (end.prob) *end.prob = 1.0f;
         }
         return;
     }
-    const bool finite = rule.m < INFINITY && rule.scale < INFINITY;
-    if (finite && bounded) {
+    if (!(rule.m < INFINITY) || !(rule.scale < INFINITY)) {
+        sample_largest(sl, row_key, k, p, end);
+        return;
+    }
+    if (bounded) {
         const uint32_t bound = by_groups ? kth_bound(maxima, groups * blocks, k, row_key) : 0u;
-        const float thr = bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY;
-        sl.each(thr, [&](const uint4 &r, unsigned int v) {
-            if (!(V::max(r) >= thr)) return;
-            float x[V::N];
-            V::unpack(r, x);
-            each_of<V::N>(x, [&](float xe) { return xe >= thr && xe > -INFINITY; },
-                          [&](float xe, int e) { put(item_of(key_of(xe), sl.index(v, e))); });
-        });
-        __syncthreads();
-        exchange(kSlotFirst, sh.n_list, 0);
-        const uint32_t n = gathered(kSlotFirst);
+        collect(sl, bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY, INFINITY);
+        exchange(kSlotBound, sh.n_list, 0);
+        const uint32_t n = gathered(kSlotBound);
         if (n <= kList) {
-            if (rank == 0) pull(kSlotFirst, n);
+            if (rank == 0) pull(kSlotBound, n);
             cluster_arrive();
-            if (rank == 0) finish_list(n, k, p, 0ull, rule, a, row);
+            if (rank == 0) finish_list(n, k, p, 0ull, rule, end);
             cluster_wait();
             return;
         }
-    } else if (finite && k == 0) {
-        // All weights; for top-p also their histogram by distance, as far as it can matter: past
-        // cut_y the row holds less than (1 - p) of the largest weight. (With min-p: all of those
-        // kept, so that the histogram's sum is the row's.) Logits below `zero` weigh nothing (y > 31).
-        const u64 m2 = pack2(rule.m, rule.m), scale2 = pack2(rule.scale, rule.scale);
-        const float zero = __fsub_rd(rule.m, __fdiv_ru(31.5f, rule.scale));
-        u64 mass = 0;
-        if (!cut_p) {
-            sl.each(zero, [&](const uint4 &r, unsigned int) {
-                float x[V::N];
-                V::unpack(r, x);
-#pragma unroll
-                for (int e = 0; e < V::N; e += 2) {
-                    float y[2];
-                    uint32_t q[2];
-                    weigh2(x[e], x[e + 1], m2, scale2, y, q);
-                    mass += q[0] >= rule.qmin ? q[0] : 0u;
-                    mass += q[1] >= rule.qmin ? q[1] : 0u;
-                }
-            });
-            u64 half[2];
-            halves_of(warp_total(mass), half);
-            exchange(kSlotFirst, half[0] + half[1], 0);
-            draw(sl, rule, true, kKeepAll, slot_total(kSlotFirst, blocks), slot_total(kSlotFirst, rank), half, a, row);
-            return;
-        }
-        const float cut_y = fminf(31.0f, log2f((float)sl.n / (1.0f - p)) + 0.1f);
-        const bool min_p = rule.qmin > 0;
-        const uint32_t floor_q = min_p ? rule.qmin : max(exp2_weight(cut_y), 1u);  // the histogram's least weight
-        sh.bins[0].clear();
-        sh.bins[1].clear();
-        __syncthreads();
-        SumBins<kBins> &bins = sh.bins[warp / (kSWarps / 2)];
-        sl.each(zero, [&](const uint4 &r, unsigned int) {
-            float x[V::N];
-            V::unpack(r, x);
-#pragma unroll
-            for (int e = 0; e < V::N; e += 4) {
-                uint32_t b[4], q[4];
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    float y2[2];
-                    uint32_t q2[2];
-                    weigh2(x[e + i], x[e + i + 1], m2, scale2, y2, q2);
-                    mass += (u64)q2[0] + q2[1];
-                    q[i] = q2[0];
-                    q[i + 1] = q2[1];
-                    b[i] = bin_of(y2[0]);
-                    b[i + 1] = bin_of(y2[1]);
-                }
-                bins.add_from(floor_q, b, q);
-            }
-        });
-        __syncthreads();
-        // two bins a thread, of both halves and (for the other blocks) their sum
-        u64 own[2][2], *sums = sh.items + kLocal;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int b = 2 * threadIdx.x + i;
-            own[0][i] = (u64)sh.bins[0].high[b] << 32 | sh.bins[0].low[b];
-            own[1][i] = (u64)sh.bins[1].high[b] << 32 | sh.bins[1].low[b];
-            sums[b] = own[0][i] + own[1][i];
-        }
-        exchange(kSlotFirst, block_total(min_p ? own[0][0] + own[0][1] + own[1][0] + own[1][1] : mass), 0);
-        const u64 total = slot_total(kSlotFirst, blocks), want = top_p_target(p, total);
-        // the bin in which the running sum reaches `want`
-        u64 part[kMaxCluster][2];
-#pragma unroll
-        for (uint32_t c = 0; c < kMaxCluster; ++c) {
-            part[c][0] = part[c][1] = 0;
-            if (c < blocks) ld_cluster_u64x2(at_rank(sums + 2 * threadIdx.x, c), part[c][0], part[c][1]);
-        }
-        u64 bin_mass[2] = {0, 0};
-#pragma unroll
-        for (uint32_t c = 0; c < kMaxCluster; ++c) {
-            bin_mass[0] += part[c][0];
-            bin_mass[1] += part[c][1];
-        }
-        const u64 before = block_before(bin_mass[0] + bin_mass[1]);
-        if (before < want && want <= before + bin_mass[0] + bin_mass[1]) {
-            const bool second = want > before + bin_mass[0];
-            sh.cast[0] = 2 * threadIdx.x + second;
-            sh.cast[1] = before + (second ? bin_mass[0] : 0ull);
-            sh.cast[2] = before + bin_mass[0] + (second ? bin_mass[1] : 0ull);
-        }
-        __syncthreads();
-        const uint32_t bin = (uint32_t)sh.cast[0];
-        const u64 above = sh.cast[1];
-        // none in a bin up to this one weighs less than its far end, less more than the recipe's
-        // error: are there few enough to gather all of them?
-        const uint32_t far = exp2_weight(((float)bin + 0.5f) * (1.0f / 32.0f)), slack = (far >> 16) + 2;
-        const bool all = sh.cast[2] <= (u64)max(far > slack ? far - slack : 0u, floor_q) * kList;
-        u64 half[2];  // of the bins before it
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            half[h] = block_total((2 * threadIdx.x < bin ? own[h][0] : 0ull) +
-                                  (2 * threadIdx.x + 1 < bin ? own[h][1] : 0ull));
-        // Every logit in a bin up to this one is at or above thr, every one in a bin from it on at
-        // or below cap; the few others between them are taken out of the list afterwards.
-        const float thr = __fsub_rd(rule.m, __fdiv_ru(((float)bin + 0.51f) * (1.0f / 32.0f), rule.scale));
-        const float cap = all || bin == 0
-                              ? INFINITY
-                              : __fsub_ru(rule.m, __fdiv_rd(((float)bin - 0.51f) * (1.0f / 32.0f), rule.scale));
-        sl.each(thr, [&](const uint4 &r, unsigned int v) {
-            if (!(V::max(r) >= thr)) return;
-            float x[V::N];
-            V::unpack(r, x);
-            each_of<V::N>(x, [&](float xe) { return xe >= thr && xe <= cap; },
-                          [&](float xe, int e) { put(item_of(key_of(xe), sl.index(v, e))); });
-        });
-        __syncthreads();
-#pragma unroll 1
-        for (uint32_t i = threadIdx.x; i < min(sh.n_list, (uint32_t)kLocal); i += kSThreads) {
-            const float x = key_logit(~(uint32_t)(sh.items[i] >> 32));
-            const float y = __fmul_rn(__fsub_rn(rule.m, x), rule.scale);
-            if (!(y < 32.0f) || exp2_weight(y) < floor_q || bin_of(y) > bin || (!all && bin_of(y) < bin))
-                sh.items[i] = kNoItem;
-        }
-        __syncthreads();
-        exchange(kSlotSecond, sh.n_list, half[0] + half[1]);
-        const uint32_t n = gathered(kSlotSecond);
-        if (n <= kList) {
-            if (!all || rank == 0) pull(kSlotSecond, n);
-            cluster_arrive();  // no block leaves, or writes over its list, while others read it
-            if (all) {
-                if (rank == 0) finish_list(n, 0xffffffffu, p, total, rule, a, row);
-                cluster_wait();
-            } else {  // every block finds the crossing among the gathered, and what is kept of them where
-                u64 left;
-                weigh_items<false>(n, kKeepAll, rule);
-                const u64 last = block_select(n, false, want - above, &left);
-                left += above + item_weight(last, rule);
-                const uint32_t from = (uint32_t)slot_total(kSlotSecond, rank), to = from + sh.n_list;
-                const uint32_t second = (rank * kSWarps + kSWarps / 2) * a.per_warp * V::N;  // its first element
-                u64 ahead = 0, in[2] = {0, 0};
-#pragma unroll 1
-                for (uint32_t i = threadIdx.x; i < to; i += kSThreads) {
-                    const u64 item = sh.items[kLocal + i];
-                    if (item > last) continue;
-                    const u64 q = sh.picks.weights[i];
-                    if (i < from) ahead += q;
-                    else if ((uint32_t)item + sl.pad < second) in[0] += q;
-                    else in[1] += q;
-                }
-                ahead = block_total(ahead);
-                half[0] += block_total(in[0]);
-                half[1] += block_total(in[1]);
-                cluster_wait();
-                draw(sl, rule, true, last, left, ahead + slot_total(kSlotSecond, rank, 1), half, a, row);
-            }
-            return;
-        }
     }
-    sample_by_selection(sl, rule, k, p, a, row);
+    u64 last = kKeepAll;
+    if (k > 0 && filter<true>(sl, rule, k, p, kKeepAll, end, &last)) return;
+    if (cut_p) {
+        u64 cut;
+        filter<false>(sl, rule, k, p, last, end, &cut);
+        return;
+    }
+    u64 mass = 0, half[2];
+    sl.each(__fsub_rd(rule.m, __fdiv_ru(31.5f, rule.scale)), [&](const uint4 &r, unsigned int v) {
+        uint32_t q[V::N];
+        mass += kept_weights(sl, r, v, rule, last, q);
+    });
+    halves_of(warp_total(mass), half);
+    exchange(kSlotFirst, half[0] + half[1], 0);
+    draw(sl, rule, last, slot_total(kSlotFirst, blocks), slot_total(kSlotFirst, rank), half, end);
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
+
+// Blocks a row, where a test fixes them; 0: by the rule in sample_launch.
+#ifndef U32SCAN_SAMPLE_BLOCKS
+#define U32SCAN_SAMPLE_BLOCKS 0
+#endif
 
 // Turns of 32 vectors a warp keeps in shared memory: two blocks an SM.
 constexpr unsigned int kStageBytes = kSWarps * 32 * 16;
@@ -1327,14 +1390,20 @@ static_assert(2 * (sizeof(SampleShared) + kMaxStaged * kStageBytes + 1024) <= 22
 
 template <typename T>
 static int sample_launch(SampleArgs a, cudaStream_t stream) {
-    // The smallest cluster whose slices fit shared memory, then larger while
-    // blocks are fewer than the GPU holds and a thread keeps a vector.
+    // The smallest cluster that gives the GPU 256 blocks (of the 304 it holds), a thread still having
+    // a vector, and slices of at most 65536 logits. Fewer and larger slices pay the barriers and the
+    // serial steps less often, more and smaller ones share a long row's passes: 256 x 262144 f32 mixed
+    // takes 182, 139, 149 us with 2, 4, 8 blocks a row, 64 x 131072 bf16 top-p 54, 46, 62, 256 x 32000
+    // bf16 top-p 45, 55, 80 with 1, 2, 4, one row of 128000 under top-p 78, 46, 30, 24 with 1, 2, 4, 8.
     const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride % Vec<T>::N == 0;
     const unsigned int nv = (unsigned int)((a.vocab + (aligned ? 1 : 2) * (Vec<T>::N - 1)) / Vec<T>::N);
     unsigned int blocks = 1;
     while (blocks < kMaxCluster &&
-           (nv > blocks * kMaxStaged * kSThreads || (a.rows * blocks < 256 && nv > blocks * kSThreads)))
+           (a.vocab > blocks * 65536ull || (a.rows * blocks < 256 && nv > blocks * kSThreads)))
         blocks *= 2;
+#if U32SCAN_SAMPLE_BLOCKS
+    blocks = U32SCAN_SAMPLE_BLOCKS;
+#endif
     const unsigned int per_block = (nv + blocks - 1) / blocks;
     a.per_warp = ((per_block + kSWarps - 1) / kSWarps + 7) / 8 * 8;
     const unsigned int iters = (a.per_warp + 31) / 32;
