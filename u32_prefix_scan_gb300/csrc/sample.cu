@@ -779,13 +779,32 @@ __device__ __noinline__ void draw(Slice<T> own, RowRule rule, u64 last, u64 tota
     }
 }
 
-// A key that at least k of the n maxima reach: the lower edge of the bin that
-// holds the k-th largest, of 512 between the least and row_key, the greatest;
-// then of 512 in that bin, while it spans more than 1/64 of an octave (a
-// maximum of -inf widens the first).
+// A key that at least k of the n maxima reach. Of up to 512 (a multiple of 16)
+// the k-th largest, by counting; of more the lower edge of the bin that holds
+// it, of 512 between the least and row_key, the greatest, then of 512 in that
+// bin, while it spans more than 1/64 of an octave (a maximum of -inf widens
+// the first).
 __device__ __forceinline__ uint32_t kth_bound(const uint32_t *maxima, uint32_t n, uint32_t k,
                                               uint32_t row_key) {
     SampleShared &sh = block_shared();
+    if (n <= kSThreads) {
+        if (threadIdx.x < n) {
+            const uint32_t mine = maxima[threadIdx.x];
+            const uint4 *four = reinterpret_cast<const uint4 *>(maxima);
+            uint32_t above = 0;
+#pragma unroll 2
+            for (uint32_t j = 0; j < n; j += 4) {
+                const uint4 o = four[j / 4];
+                above += (o.x > mine || (o.x == mine && j < threadIdx.x)) +
+                         (o.y > mine || (o.y == mine && j + 1 < threadIdx.x)) +
+                         (o.z > mine || (o.z == mine && j + 2 < threadIdx.x)) +
+                         (o.w > mine || (o.w == mine && j + 3 < threadIdx.x));
+            }
+            if (above == k - 1) sh.cast[0] = mine;
+        }
+        __syncthreads();
+        return (uint32_t)sh.cast[0];
+    }
     uint32_t *counts = sh.picks.counts;
     uint32_t least = row_key;
     for (uint32_t i = threadIdx.x; i < n; i += kSThreads) least = min(least, maxima[i]);
