@@ -1403,14 +1403,15 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
 // Turns of 32 vectors a warp keeps in shared memory: two blocks an SM.
 constexpr unsigned int kStageBytes = kSWarps * 32 * 16;
 constexpr unsigned int kMaxStaged = 8;
+constexpr unsigned int kResident = 304;  // blocks at a time: two on each of 152 SMs
 static_assert(sizeof(SampleShared) % 16 == 0 && offsetof(SampleShared, slots) % 16 == 0 && kLocal % 2 == 0,
               "16-byte accesses");
 static_assert(2 * (sizeof(SampleShared) + kMaxStaged * kStageBytes + 1024) <= 228 * 1024, "two blocks an SM");
 
 template <typename T>
 static int sample_launch(SampleArgs a, cudaStream_t stream) {
-    // The smallest cluster that gives the GPU 256 blocks (of the 304 it holds), a thread still having
-    // a vector, and slices of at most 65536 logits. Fewer and larger slices pay the barriers and the
+    // The largest cluster with which all rows run at a time, a thread still having a vector, and
+    // slices of at most 65536 logits. Fewer and larger slices pay the barriers and the
     // serial steps less often, more and smaller ones share a long row's passes: 256 x 262144 f32 mixed
     // takes 182, 139, 149 us with 2, 4, 8 blocks a row, 64 x 131072 bf16 top-p 54, 46, 62, 256 x 32000
     // bf16 top-p 45, 55, 80 with 1, 2, 4, one row of 128000 under top-p 78, 46, 30, 24 with 1, 2, 4, 8.
@@ -1418,7 +1419,7 @@ static int sample_launch(SampleArgs a, cudaStream_t stream) {
     const unsigned int nv = (unsigned int)((a.vocab + (aligned ? 1 : 2) * (Vec<T>::N - 1)) / Vec<T>::N);
     unsigned int blocks = 1;
     while (blocks < kMaxCluster &&
-           (a.vocab > blocks * 65536ull || (a.rows * blocks < 256 && nv > blocks * kSThreads)))
+           (a.vocab > blocks * 65536ull || (2 * a.rows * blocks <= kResident && nv > blocks * kSThreads)))
         blocks *= 2;
 #if U32SCAN_SAMPLE_BLOCKS
     blocks = U32SCAN_SAMPLE_BLOCKS;
