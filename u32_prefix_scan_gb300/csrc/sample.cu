@@ -56,6 +56,7 @@ constexpr int kLocal = 1024;  // logits a block may put forward
 constexpr int kList = 2048;   // and all blocks of a row together
 constexpr int kRanked = 256;  // up to here items are ranked by counting, past it selected by histograms
 constexpr int kTurns = 64;    // turns (of 32 vectors) a warp remembers the maximum of
+constexpr int kFew = 64;      // up to here a selection's last items are (eight threads each)
 constexpr int kBins = 1024;   // histogram of y: 32 bins an octave, 31 octaves
 constexpr float kLog2e = 0x1.715476p+0f;
 constexpr uint32_t kKeyOfMinusInf = 0x007fffffu;
@@ -131,7 +132,13 @@ struct alignas(16) SampleShared {
         SumBins<kBins> bins[2];  // of the block's two halves
         SumBins<256> digits[2];
         struct {
-            SumBins<kSThreads> sums;
+            union {
+                SumBins<kSThreads> sums;
+                struct {
+                    u64 place[kFew];
+                    uint32_t weight[kFew], from[kFew];
+                } few;
+            };
             uint32_t counts[kSThreads];
             uint32_t weights[kList];
         } picks;
@@ -602,8 +609,9 @@ __device__ __forceinline__ void weigh_items(uint32_t n, u64 limit, RowRule rule)
 // the first, in order (or by index), at which the running sum of weights
 // reaches `target` (1 <= target <= the sum of all), and the sum before it. A
 // histogram of the places still in question, 512 bins between the least and
-// the greatest, then the same within the bin that holds the crossing, until
-// that is one item.
+// the greatest, gives the bin that holds the crossing; its items, where they
+// are at most kFew, find it by counting what stands before them, else
+// they are the next histogram's.
 __device__ __noinline__ u64 block_select(uint32_t n, bool by_index, u64 target, u64 *before_it) {
     SampleShared &sh = block_shared();
     const u64 place_bits = by_index ? 0xffffffffull : ~0ull;
@@ -643,18 +651,39 @@ __device__ __noinline__ u64 block_select(uint32_t n, bool by_index, u64 target, 
         base = sh.cast[1];
         low = lo + (sh.cast[0] << shift);
         high = min(high, low + ((1ull << shift) - 1));  // the last bin may reach past the places in question
-        const bool one = sh.cast[2] == 1;
+        const uint32_t few = (uint32_t)sh.cast[2];
         __syncthreads();  // cast and the bins are written again
-        if (one) break;
-    }
+        if (few > kFew) continue;
+        if (threadIdx.x == 0) sh.picks.counts[0] = 0;
+        __syncthreads();
 #pragma unroll 1
-    for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
-        const u64 place = sh.items[kLocal + i] & place_bits;
-        if (sh.picks.weights[i] && place >= low && place <= high) sh.cast[3] = sh.items[kLocal + i];
+        for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
+            const u64 place = sh.items[kLocal + i] & place_bits;
+            if (sh.picks.weights[i] && place >= low && place <= high) {
+                const uint32_t at = atomicAdd(&sh.picks.counts[0], 1u);
+                sh.picks.few.place[at] = place;
+                sh.picks.few.weight[at] = sh.picks.weights[i];
+                sh.picks.few.from[at] = i;
+            }
+        }
+        __syncthreads();
+        constexpr uint32_t team = kSThreads / kFew;
+        const uint32_t i = threadIdx.x / team, part = threadIdx.x % team;
+        const u64 place = i < few ? sh.picks.few.place[i] : 0ull;
+        u64 sum = 0;
+        for (uint32_t j = part; j < few; j += team)
+            sum += sh.picks.few.place[j] < place ? sh.picks.few.weight[j] : 0u;
+#pragma unroll
+        for (uint32_t d = 1; d < team; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        sum += base;
+        if (part == 0 && i < few && sum < target && target <= sum + sh.picks.few.weight[i]) {
+            sh.cast[0] = sh.items[kLocal + sh.picks.few.from[i]];
+            sh.cast[1] = sum;
+        }
+        __syncthreads();
+        *before_it = sh.cast[1];
+        return sh.cast[0];
     }
-    __syncthreads();
-    *before_it = base;
-    return sh.cast[3];
 }
 
 __device__ __noinline__ void write_token(RowEnd end, uint32_t index, u64 q, u64 total) {
@@ -914,12 +943,13 @@ __device__ __noinline__ void finish_list(uint32_t n, uint32_t k, float p, u64 to
         __syncthreads();
         uint32_t rank = 0;
         u64 before = 0;
+        if (i < n)
 #pragma unroll 2
-        for (uint32_t j = part; j < n; j += team) {
-            const bool first = sh.items[kLocal + j] < item;
-            rank += first;
-            before += first ? weight[j] : 0ull;
-        }
+            for (uint32_t j = part; j < n; j += team) {
+                const bool first = sh.items[kLocal + j] < item;
+                rank += first;
+                before += first ? weight[j] : 0ull;
+            }
         for (uint32_t d = 1; d < team; d *= 2) {
             rank += __shfl_xor_sync(0xffffffffu, rank, d);
             before += __shfl_xor_sync(0xffffffffu, before, d);
@@ -934,9 +964,10 @@ __device__ __noinline__ void finish_list(uint32_t n, uint32_t k, float p, u64 to
         if (part == 0) weight[i] = kept;
         __syncthreads();
         u64 at = 0;
+        if (i < n)
 #pragma unroll 2
-        for (uint32_t j = part; j < n; j += team)
-            at += (uint32_t)sh.items[kLocal + j] < (uint32_t)item ? weight[j] : 0ull;
+            for (uint32_t j = part; j < n; j += team)
+                at += (uint32_t)sh.items[kLocal + j] < (uint32_t)item ? weight[j] : 0ull;
         for (uint32_t d = 1; d < team; d *= 2) at += __shfl_xor_sync(0xffffffffu, at, d);
         const u64 r = draw_of(word, total);
         if (part == 0 && at <= r && r < at + kept) write_token(end, (uint32_t)item, kept, total);
