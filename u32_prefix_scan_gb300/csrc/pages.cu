@@ -306,32 +306,51 @@ __device__ __forceinline__ u64 row_need(const ForkArgs &a, u64 s, int32_t *old_l
 // the served rows take (returned).
 __device__ __forceinline__ u64 plan_rows(const ForkArgs &a, const PagesWs &w, u64 free_pages, u64 *s_warp) {
     __shared__ u64 s_taken;
-    u64 taken = 0;
+    u64 taken = 0, jobs = 0;
     if (threadIdx.x == 0) s_taken = 0;
-    scan_by_block(
-        a.rows, s_warp,
-        [&](u64 s) -> u64 {
-            int32_t old;
-            const u64 need = row_need(a, s, &old);
-            w.old_len[s] = old;
-            return need;
-        },
-        [&](u64 s, u64 base, u64 need) {
-            w.ends[s] = base + need;
-            if (need && base + need <= free_pages) taken = base + need;
-        });
+    auto need_of = [&](u64 s, int32_t *old) {
+        const u64 need = row_need(a, s, old);
+        w.old_len[s] = *old;
+        return need;
+    };
+    auto place_row = [&](u64 s, u64 base, u64 need) {
+        w.ends[s] = base + need;
+        if (need && base + need <= free_pages) taken = base + need;
+    };
+    // a child whose parent's last page is partly filled
+    auto is_job = [&](u64 s, int32_t old) {
+        return old > 0 && is_child(a, s) && (uint32_t)old % a.page_tokens != 0;
+    };
+    if (a.rows <= 65535) {
+        // one scan of both: needs (their sum is below 65535 * 2^31) and, from bit 48 on, jobs
+        constexpr u64 kNeeds = (1ull << 48) - 1;
+        const u64 sums = scan_by_block(
+            a.rows, s_warp,
+            [&](u64 s) -> u64 {
+                int32_t old;
+                const u64 need = need_of(s, &old);
+                return need | (is_job(s, old) ? 1ull << 48 : 0ull);
+            },
+            [&](u64 s, u64 base, u64 x) {
+                place_row(s, base & kNeeds, x & kNeeds);
+                if (x >> 48) w.jobs[base >> 48] = (int32_t)s;
+            });
+        jobs = sums >> 48;
+    } else {
+        scan_by_block(
+            a.rows, s_warp,
+            [&](u64 s) -> u64 {
+                int32_t old;
+                return need_of(s, &old);
+            },
+            place_row);
+        jobs = scan_by_block(  // a thread reads what it wrote
+            a.rows, s_warp, [&](u64 s) -> u64 { return is_job(s, w.old_len[s]); },
+            [&](u64 s, u64 base, u64 job) {
+                if (job) w.jobs[base] = (int32_t)s;
+            });
+    }
     if (taken) atomicMax(&s_taken, taken);
-    // children whose parent's last page is partly filled, in row order (a thread reads what it wrote)
-    const u64 jobs = !a.parent ? 0ull
-                               : scan_by_block(
-                                     a.rows, s_warp,
-                                     [&](u64 s) -> u64 {
-                                         const int32_t old = w.old_len[s];
-                                         return old > 0 && is_child(a, s) && (uint32_t)old % a.page_tokens != 0;
-                                     },
-                                     [&](u64 s, u64 base, u64 job) {
-                                         if (job) w.jobs[base] = (int32_t)s;
-                                     });
     __syncthreads();
     if (threadIdx.x == 0) {
         w.ctrl->free_pages = free_pages;
@@ -440,8 +459,8 @@ free_kernel(int32_t *table, u64 stride, u64 rows, u64 width, int32_t *lens, int3
     const int lane = threadIdx.x & 31;
     u64 gone = 0;
     for (u64 s = (u64)blockIdx.x * kPWarps + (threadIdx.x >> 5); s < rows; s += (u64)gridDim.x * kPWarps) {
-        if (release[s] == 0) continue;
-        const int32_t len = lens[s];
+        const int32_t gone_row = release[s], len = lens[s];  // on their way together
+        if (gone_row == 0) continue;
         const u64 n = len > 0 ? min((u64)pages_for((uint32_t)len, page_tokens), width) : 0ull;
         int32_t *row = table + s * stride;
         for (u64 j = lane; j < n; j += 32 * U) {  // U entries and their counts on the way together
