@@ -205,7 +205,8 @@ def sample_call(lib, **kw):
     return lib.sample_tokens(*a.values(), None)
 
 
-@pytest.mark.parametrize("bad", [dict(logits=None), dict(logits=FAKE + 2), dict(type=3), dict(type=-1), dict(rows=1 << 31),
+@pytest.mark.parametrize("bad", [dict(logits=None), dict(logits=FAKE + 2), dict(type=3), dict(type=-1),
+                                 dict(rows=1 << 31), dict(rows=1 << 28),
                                  dict(vocab=_native.MAX_VOCAB + 1), dict(stride=1 << 32), dict(random=None),
                                  dict(tokens=None), dict(t=FAKE + 1), dict(k=FAKE + 2), dict(p=FAKE + 3),
                                  dict(a=FAKE + 1), dict(random=FAKE + 2), dict(tokens=FAKE + 1), dict(probs=FAKE + 2),

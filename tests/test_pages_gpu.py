@@ -156,6 +156,26 @@ def test_fork_no_free_and_all_free(u):
                np.array([0, 0, 1], np.int32), None)
 
 
+@pytest.mark.parametrize("rows", [65535, 65536, 70001])
+@pytest.mark.parametrize("pages", [3000, 300000])
+def test_fork_many_rows(u, rows, pages):
+    """More rows than one packed scan takes; pages for some and for all."""
+    rng = np.random.default_rng(rows)
+    table = np.full((rows, 3), -1, np.int32)
+    lens, refs = np.zeros(rows, np.int32), np.zeros(pages, np.int32)
+    active = 1000
+    lens[:active] = rng.integers(0, 9, active)
+    n = -(-lens // 4)
+    place = rng.permutation(pages)
+    for j in range(3):
+        hold = np.flatnonzero(n > j)
+        table[hold, j], place = place[: hold.size], place[hold.size :]
+    refs[table[table >= 0]] = 1
+    parent = np.full(rows, -1, np.int32)
+    parent[active:] = np.where(rng.random(rows - active) < 0.5, rng.integers(0, active, rows - active), -1)
+    check_fork(u, table, lens, refs, 4, parent, rng.integers(0, 5, rows).astype(np.int32), random_pool(3, 1, pages, 16))
+
+
 def test_fork_long_rows(u):
     """A prefix of many table chunks shared by many children."""
     rows, width, pages, page_tokens = 40, 3001, 8000, 2
@@ -276,7 +296,8 @@ def test_strided_tables(u):
     t2, l2, r2, _ = oracle.pages_free(t2, l2, r2, 4, release)
     t2, r2, _, _, _ = oracle.pages_compact(t2, l2, r2, 4)
     got = host(w)
-    assert np.array_equal(got[:, 2 : 2 + width], t2) and np.all(got[:, :2] == 7777) and np.all(got[:, 2 + width :] == 7777)
+    assert np.array_equal(got[:, 2 : 2 + width], t2)
+    assert np.all(got[:, :2] == 7777) and np.all(got[:, 2 + width :] == 7777)
     assert np.array_equal(host(l), l2) and np.array_equal(host(r), r2)
 
 

@@ -138,7 +138,8 @@ def test_largest_vocabulary(u, kind):
 @pytest.mark.parametrize("rows", [1, 2, 17, 151, 153, 700])
 def test_row_counts(u, rows):
     n = 2000
-    check(u, logits_for("peaked", rows, n, rows), "f32", inputs.splitmix_u32(14, 0, rows), params_for("mixed", rows, rows))
+    check(u, logits_for("peaked", rows, n, rows), "f32", inputs.splitmix_u32(14, 0, rows),
+          params_for("mixed", rows, rows))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -252,3 +253,70 @@ def test_refusals(u):
         u.sample_tokens(x, r, top_k=x[0])
     with pytest.raises(TypeError, match="tokens"):
         u.sample_tokens(x, r, tokens=torch.zeros(4, dtype=torch.int64, device="cuda"))
+
+
+@pytest.mark.parametrize("kind", ["peaked", "flat", "equal", "tied", "up", "wide"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_rows_of_every_shape(u, kind, dtype):
+    """Rows too long or too even for the lists: the selections within a bin."""
+    n, rows = 300007, 3
+    x = logits_for(kind, rows, n, 31)
+    words = inputs.splitmix_u32(20, 0, rows)
+    f, i = np.float32, np.int32
+    for params in (dict(top_p=np.array([0.2, 0.9, 0.9999], f)),
+                   dict(top_k=np.array([1500, 2047, 200000], i)),
+                   dict(top_k=np.array([2049, 60000, 299999], i), top_p=np.array([0.5, 0.97, 0.999], f)),
+                   dict(top_k=np.array([5000, 0, 1000], i), top_p=np.array([0.9] * 3, f),
+                        min_p=np.array([0.3, 0.01, 1e-6], f)),
+                   dict(temperature=np.array([1e4, 0.01, 50.0], f), top_k=np.array([3000, 40, 0], i),
+                        top_p=np.array([0.7] * 3, f))):
+        check(u, x, dtype, words, params)
+
+
+def test_largest_f32_vocabulary(u):
+    n = 1 << 22
+    x = logits_for("peaked", 2, n, 33)
+    words = inputs.splitmix_u32(21, 0, 2)
+    check(u, x, "f32", words, dict(top_p=np.array([0.9, 1.0], np.float32), top_k=np.array([0, 700], np.int32)))
+    check(u, x, "f32", np.array([0xFFFFFFFF, 0], np.uint32), {})
+
+
+@pytest.fixture(scope="module")
+def one_block(u):
+    """The library with one block a row: long slices, most of them read again."""
+    from u32_prefix_scan_gb300 import _native, build
+
+    return _native.load(build.build_variant("sample_one_block", ["-DU32SCAN_SAMPLE_BLOCKS=1"]))
+
+
+@pytest.mark.parametrize("kind", ["peaked", "flat", "tied", "masked", "inf"])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_any_number_of_blocks_gives_the_same_bits(u, one_block, monkeypatch, kind, dtype):
+    from u32_prefix_scan_gb300 import _native
+
+    for n, rows in ((257, 5), (40001, 7), (600011, 2)):
+        dev, _ = as_type(logits_for(kind, rows, n, n), dtype)
+        for mode in ("plain", "mixed", "top_p", "top_k", "greedy"):
+            words, params = inputs.splitmix_u32(22, 0, rows, start=n), params_for(mode, rows, n)
+            want = run(u, dev, words, params)
+            with monkeypatch.context() as m:
+                m.setattr(_native, "_lib", one_block)
+                got = run(u, dev, words, params)
+            assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_probabilities_against_softmax_in_64_bits(u, dtype):
+    """Without filters the probability is the softmax of the logits held: the
+    weight is off by the roundings of its exponent (1.5 ulp of at most 2^-19,
+    times ln 2), the polynomial (2e-7) and its floor (2^-31 of the largest),
+    the sum by as much, the result by its rounding to float."""
+    n, rows = 20011, 64
+    dev, held = as_type(logits_for("peaked", rows, n, 41), dtype)
+    t = np.linspace(0.4, 3.0, rows).astype(np.float32)
+    tok, prob = run(u, dev, inputs.splitmix_u32(23, 0, rows), dict(temperature=t))
+    z = held.astype(np.float64) / t[:, None]
+    w = np.exp(z - z.max(1, keepdims=True))
+    p = (w / w.sum(1, keepdims=True))[np.arange(rows), tok]
+    rel = 2 * (1.5 * 2.0**-19 * np.log(2.0) + 2e-7) + n * 2.0**-31 + 2.0**-24
+    assert np.all(np.abs(prob - p) <= p * rel + 2.0**-31)
