@@ -53,6 +53,7 @@ constexpr int kSThreads = 512;
 constexpr int kSWarps = kSThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kLocal = 1024;  // logits a block may put forward
+constexpr int kHits = kLocal;  // vectors with such logits
 constexpr int kList = 2048;   // and all blocks of a row together
 constexpr int kRanked = 256;  // up to here items are ranked by counting, past it selected by histograms
 constexpr int kTurns = 64;    // turns (of 32 vectors) a warp remembers the maximum of
@@ -142,12 +143,13 @@ struct alignas(16) SampleShared {
             uint32_t counts[kSThreads];
             uint32_t weights[kList];
         } picks;
+        uint32_t hits[kHits];
     };
     u64 slots[kSlots][kMaxCluster][2];
     uint32_t turn_key[kSWarps][kTurns];  // the key of a turn's largest logit
     u64 warp[3][kSWarps];
     u64 cast[4];
-    uint32_t n_list;
+    uint32_t n_list, n_hits;
 };
 
 // The block's, at the start of its dynamic shared memory; named here and not
@@ -170,8 +172,9 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// Sixteen bytes of a row as floats, and their maximum (of those that are not
-// NaN; -inf or NaN if there is none).
+// Sixteen bytes of a row as floats; their maximum (of those that are not NaN;
+// -inf or NaN if there is none); whether any lies in [from(lo), upto(hi)], the
+// bounds rounded inwards to the logits' type.
 template <typename T>
 struct Vec;
 
@@ -184,6 +187,17 @@ struct Vec<float> {
         x[1] = __uint_as_float(r.y);
         x[2] = __uint_as_float(r.z);
         x[3] = __uint_as_float(r.w);
+    }
+    typedef float Bound;
+    static __device__ __forceinline__ Bound from(float lo) { return lo; }
+    static __device__ __forceinline__ Bound upto(float hi) { return hi; }
+    static __device__ __forceinline__ bool any_in(const uint4 &r, Bound lo, Bound hi) {
+        float x[4];
+        unpack(r, x);
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= x[e] >= lo && x[e] <= hi;
+        return any;
     }
     static __device__ __forceinline__ float max(const uint4 &r) {
         return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
@@ -202,6 +216,16 @@ struct Vec<__nv_bfloat16> {
             x[2 * j] = __uint_as_float(w[j] << 16);
             x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
         }
+    }
+    typedef __nv_bfloat162 Bound;
+    static __device__ __forceinline__ Bound from(float lo) { return __bfloat162bfloat162(__float2bfloat16_ru(lo)); }
+    static __device__ __forceinline__ Bound upto(float hi) { return __bfloat162bfloat162(__float2bfloat16_rd(hi)); }
+    static __device__ __forceinline__ bool any_in(const uint4 &r, Bound lo, Bound hi) {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r);
+        unsigned int any = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) any |= __hge2_mask(h[j], lo) & __hle2_mask(h[j], hi);
+        return any != 0;
     }
     static __device__ __forceinline__ float max(const uint4 &r) {
         const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r);
@@ -222,6 +246,16 @@ struct Vec<__half> {
             x[2 * j] = f.x;
             x[2 * j + 1] = f.y;
         }
+    }
+    typedef __half2 Bound;
+    static __device__ __forceinline__ Bound from(float lo) { return __half2half2(__float2half_ru(lo)); }
+    static __device__ __forceinline__ Bound upto(float hi) { return __half2half2(__float2half_rd(hi)); }
+    static __device__ __forceinline__ bool any_in(const uint4 &r, Bound lo, Bound hi) {
+        const __half2 *h = reinterpret_cast<const __half2 *>(&r);
+        unsigned int any = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) any |= __hge2_mask(h[j], lo) & __hle2_mask(h[j], hi);
+        return any != 0;
     }
     static __device__ __forceinline__ float max(const uint4 &r) {
         const __half2 *h = reinterpret_cast<const __half2 *>(&r);
@@ -277,10 +311,7 @@ __device__ __noinline__ uint32_t token_weight(float x, RowRule rule) {
     return q >= rule.qmin ? q : 0u;
 }
 
-// Two logits' distances y and weights before min-p, two operations an
-// instruction (each of the pair rounded alone, as above), for a finite m and
-// scale: x = m gives y = 0 by itself, -inf and NaN give the clamp's 40 and
-// so weight 0.
+// Two f32 operations an instruction, each of the pair rounded alone.
 __device__ __forceinline__ u64 pack2(float a, float b) {
     u64 r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -309,29 +340,54 @@ __device__ __forceinline__ u64 sub2(u64 a, u64 b) {
     return r;
 }
 
-__device__ __forceinline__ void weigh2(float x0, float x1, u64 m2, u64 scale2, float (&y)[2], uint32_t (&q)[2]) {
-    unpack2(mul2(sub2(m2, pack2(x0, x1)), scale2), y[0], y[1]);
-    y[0] = fminf(y[0], 40.0f);
-    y[1] = fminf(y[1], 40.0f);
-    const u64 y2 = pack2(y[0], y[1]);
-    const u64 t2 = add2(y2, pack2(kRound, kRound));
-    const u64 f2 = sub2(y2, add2(t2, pack2(-kRound, -kRound)));
-    u64 p2 = add2(mul2(pack2(kC5, kC5), f2), pack2(kC4, kC4));
-    p2 = add2(mul2(p2, f2), pack2(kC3, kC3));
-    p2 = add2(mul2(p2, f2), pack2(kC2, kC2));
-    p2 = add2(mul2(p2, f2), pack2(kC1, kC1));
-    p2 = add2(mul2(p2, f2), pack2(kC0, kC0));
-    float t[2], p[2];
-    unpack2(t2, t[0], t[1]);
-    unpack2(p2, p[0], p[1]);
-    q[0] = scaled_floor(p[0], t[0]);
-    q[1] = scaled_floor(p[1], t[1]);
-}
+// Weighs a vector's logits for a row of finite m and scale, as token_weight
+// does but before min-p: distances y and weights q. x = m gives y = 0 by
+// itself; -inf and NaN give the clamp's 40, past the weights' range. 6 logits a
+// clock and SM from shared memory (clamping 16-bit logits two at a time before
+// they are widened, or rounding the other way round, measured 5.6).
+template <typename T>
+struct Weigher {
+    u64 m2, scale2;
+
+    __device__ __forceinline__ explicit Weigher(const RowRule &rule)
+        : m2(pack2(rule.m, rule.m)), scale2(pack2(rule.scale, rule.scale)) {}
+
+    __device__ __forceinline__ void operator()(const uint4 &r, float (&x)[Vec<T>::N], float (&y)[Vec<T>::N],
+                                               uint32_t (&q)[Vec<T>::N]) const {
+        constexpr int N = Vec<T>::N;
+        Vec<T>::unpack(r, x);
+        u64 y2[N / 2];
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            y2[e / 2] = mul2(sub2(m2, pack2(x[e], x[e + 1])), scale2);
+            unpack2(y2[e / 2], y[e], y[e + 1]);
+            y[e] = fminf(y[e], 40.0f);
+            y[e + 1] = fminf(y[e + 1], 40.0f);
+            y2[e / 2] = pack2(y[e], y[e + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            const u64 t2 = add2(y2[e / 2], pack2(kRound, kRound));
+            const u64 f2 = sub2(y2[e / 2], add2(t2, pack2(-kRound, -kRound)));
+            u64 p2 = add2(mul2(pack2(kC5, kC5), f2), pack2(kC4, kC4));
+            p2 = add2(mul2(p2, f2), pack2(kC3, kC3));
+            p2 = add2(mul2(p2, f2), pack2(kC2, kC2));
+            p2 = add2(mul2(p2, f2), pack2(kC1, kC1));
+            p2 = add2(mul2(p2, f2), pack2(kC0, kC0));
+            float t[2], p[2];
+            unpack2(t2, t[0], t[1]);
+            unpack2(p2, p[0], p[1]);
+            q[e] = scaled_floor(p[0], t[0]);
+            q[e + 1] = scaled_floor(p[1], t[1]);
+        }
+    }
+};
 
 // The histogram's bin of a distance: the nearest of the bins' centres, so
 // bin b holds y in [b - 1/2, b + 1/2] / 32.
+// (y below 31.9.)
 __device__ __forceinline__ uint32_t bin_of(float y) {
-    return __float_as_uint(__fmaf_rn(y, 32.0f, 8388608.0f)) & (kBins - 1);
+    return __float_as_uint(__fmaf_rn(y, 32.0f, 8388608.0f)) - 0x4b000000u;
 }
 
 // ---------------------------------------------------------------------------
@@ -714,18 +770,13 @@ __device__ __forceinline__ void halves_of(u64 warp_mass, u64 (&half)[2]) {
 // The weights of a vector's logits up to `last`, 0 for the others, for a
 // finite m and scale.
 template <typename T>
-__device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const uint4 &r, unsigned int v, RowRule rule, u64 last,
+__device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const uint4 &r, unsigned int v,
+                                            const Weigher<T> &weigh, uint32_t qmin, u64 last,
                                             uint32_t (&q)[Vec<T>::N]) {
-    float x[Vec<T>::N];
-    Vec<T>::unpack(r, x);
+    float x[Vec<T>::N], y[Vec<T>::N];
+    weigh(r, x, y, q);
 #pragma unroll
-    for (int e = 0; e < Vec<T>::N; e += 2) {
-        float y[2];
-        uint32_t w[2];
-        weigh2(x[e], x[e + 1], pack2(rule.m, rule.m), pack2(rule.scale, rule.scale), y, w);
-        q[e] = w[0] >= rule.qmin ? w[0] : 0u;
-        q[e + 1] = w[1] >= rule.qmin ? w[1] : 0u;
-    }
+    for (int e = 0; e < Vec<T>::N; ++e) q[e] = q[e] >= qmin ? q[e] : 0u;
     if (last != kKeepAll) {
         const float thr = key_logit(~(uint32_t)(last >> 32));
 #pragma unroll
@@ -755,6 +806,7 @@ __device__ __noinline__ void draw(Slice<T> own, RowRule rule, u64 last, u64 tota
     const int warp0 = second ? kSWarps / 2 : 0;
     const unsigned int per_warp = end.per_warp, nv = (own.pad + own.n + N - 1) / N;
     const unsigned int per = (per_warp + 31) / 32, turns = kSWarps / 2 * per;
+    const Weigher<T> weigh(rule);
     u64 *mass = sh.items;  // by turn
     u64 at = 0;
     bool walk = false;  // first all turns, then the one
@@ -767,7 +819,7 @@ __device__ __noinline__ void draw(Slice<T> own, RowRule rule, u64 last, u64 tota
         u64 sum = 0;
         const Slice<T> sl = own.of_warp(warp0 + (int)(t / per) - warp, per_warp, nv);
         const unsigned int it = t % per, j = 32 * it + lane;
-        if (t < turns && sl.has(j)) sum = kept_weights(sl, sl.turn(it, j), sl.v0 + j, rule, last, q);
+        if (t < turns && sl.has(j)) sum = kept_weights(sl, sl.turn(it, j), sl.v0 + j, weigh, rule.qmin, last, q);
         if (walk) {
             at += warp_inclusive(sum) - sum;
             if (at <= r && r - at < sum) {
@@ -889,16 +941,47 @@ __device__ __forceinline__ void each_of(const float (&x)[N], Test test, F f) {
     }
 }
 
-// Gathers the logits in [thr, cap] (-inf not among them) into this block's list.
+// Gathers the logits in [thr, cap] (-inf not among them) into this block's
+// list. In a long slice first the vectors that hold one (few, and a few
+// instructions each, where taking such a vector apart would stop its whole
+// warp), then, a thread a vector, the logits: 64 x 131072 bf16 under top-p
+// 43 us, 45 with all at once. In a short slice, up to 64 vectors a warp, all
+// at once: a row of 32000 bf16 under top-k 11.2 us, 11.7 in two steps.
 template <typename T>
-__device__ __noinline__ void collect(Slice<T> sl, float thr, float cap) {
+__device__ __noinline__ void collect(Slice<T> sl, unsigned int per_warp, float thr, float cap) {
+    SampleShared &sh = block_shared();
+    using V = Vec<T>;
+    thr = fmaxf(thr, -3.402823466e38f);  // the least finite logit
+    auto take = [&](const uint4 &r, unsigned int v) {
+        float x[V::N];
+        V::unpack(r, x);
+        each_of<V::N>(x, [&](float xe) { return xe >= thr && xe <= cap; },
+                      [&](float xe, int e) { put(item_of(key_of(xe), sl.index(v, e))); });
+    };
+    const typename V::Bound lo = V::from(thr), hi = V::upto(cap);
+    if (per_warp <= 64) {
+        sl.each(thr, [&](const uint4 &r, unsigned int v) {
+            if (V::any_in(r, lo, hi)) take(r, v);
+        });
+        __syncthreads();
+        return;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) sh.n_hits = 0;
+    __syncthreads();
     sl.each(thr, [&](const uint4 &r, unsigned int v) {
-        if (!(Vec<T>::max(r) >= thr)) return;
-        float x[Vec<T>::N];
-        Vec<T>::unpack(r, x);
-        each_of<Vec<T>::N>(x, [&](float xe) { return xe >= thr && xe <= cap && xe > -INFINITY; },
-                           [&](float xe, int e) { put(item_of(key_of(xe), sl.index(v, e))); });
+        if (!V::any_in(r, lo, hi)) return;
+        const uint32_t at = atomicAdd(&sh.n_hits, 1u);
+        if (at < kHits) sh.hits[at] = v;
     });
+    __syncthreads();
+#pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < min(sh.n_hits, (uint32_t)kHits); i += kSThreads) {
+        const unsigned int v = sh.hits[i];
+        take(sl.load(v), v);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && sh.n_hits > kHits) sh.n_list = kLocal + 1;  // too many
     __syncthreads();
 }
 
@@ -1130,45 +1213,38 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
     if (threadIdx.x == 0) sh.n_list = 0;
     __syncthreads();
     SumBins<kBins> &bins = sh.bins[warp / (kSWarps / 2)];
-    const u64 m2 = pack2(rule.m, rule.m), scale2 = pack2(rule.scale, rule.scale);
-    const float zero = __fsub_rd(rule.m, __fdiv_ru(31.5f, rule.scale));  // logits below it weigh nothing
+    const Weigher<T> weigh(rule);
+    const float octave = __frcp_rn(rule.scale);  // the bounds below leave room for its rounding
+    const float zero = __fsub_rd(rule.m, 31.5f * octave);  // logits below it weigh nothing (y > 31)
     const bool limited = limit != kKeepAll;
     const float limit_x = limited ? key_logit(~(uint32_t)(limit >> 32)) : -INFINITY;
     u64 mass = 0;
     sl.each(zero, [&](const uint4 &r, unsigned int v) {
-        float x[V::N];
-        V::unpack(r, x);
+        float x[V::N], y[V::N];
+        if constexpr (COUNT) {
+            V::unpack(r, x);
 #pragma unroll
-        for (int e = 0; e < V::N; e += 4) {
-            if constexpr (COUNT) {
+            for (int e = 0; e < V::N; e += 2) {
+                unpack2(mul2(sub2(weigh.m2, pack2(x[e], x[e + 1])), weigh.scale2), y[e], y[e + 1]);
+                if (y[e] < 31.0f) atomicAdd(&bins.low[bin_of(y[e])], 1u);
+                if (y[e + 1] < 31.0f) atomicAdd(&bins.low[bin_of(y[e + 1])], 1u);
+            }
+        } else {
+            uint32_t q[V::N];
+            weigh(r, x, y, q);
+            if (limited)
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    float y[2];
-                    unpack2(mul2(sub2(m2, pack2(x[e + i], x[e + i + 1])), scale2), y[0], y[1]);
-                    if (y[0] < 31.0f) atomicAdd(&bins.low[bin_of(y[0])], 1u);
-                    if (y[1] < 31.0f) atomicAdd(&bins.low[bin_of(y[1])], 1u);
+                for (int e = 0; e < V::N; ++e) {
+                    const bool past = x[e] == limit_x && sl.index(v, e) > (uint32_t)limit;
+                    if (x[e] < limit_x || past) q[e] = 0;
                 }
-            } else {
-                uint32_t b[4], q[4];
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    float y2[2];
-                    uint32_t q2[2];
-                    weigh2(x[e + i], x[e + i + 1], m2, scale2, y2, q2);
-                    q[i] = q2[0];
-                    q[i + 1] = q2[1];
-                    b[i] = bin_of(y2[0]);
-                    b[i + 1] = bin_of(y2[1]);
-                }
-                if (limited)
+            for (int e = 0; e < V::N; e += 2) mass += (u64)q[e] + q[e + 1];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool past = x[e + i] == limit_x && sl.index(v, e + i) > (uint32_t)limit;
-                        if (x[e + i] < limit_x || past) q[i] = 0;
-                    }
-                mass += (u64)q[0] + q[1];
-                mass += (u64)q[2] + q[3];
-                bins.add_from(c.floor_q, b, q);
+            for (int e = 0; e < V::N; e += 4) {
+                const uint32_t b[4] = {bin_of(y[e]), bin_of(y[e + 1]), bin_of(y[e + 2]), bin_of(y[e + 3])};
+                const uint32_t w[4] = {q[e], q[e + 1], q[e + 2], q[e + 3]};
+                bins.add_from(c.floor_q, b, w);
             }
         }
     });
@@ -1223,11 +1299,10 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
                                   (2 * threadIdx.x + 1 < c.bin ? own[h][1] : 0ull));
     // Every logit in a bin up to this one is at or above thr, every one in a bin from it on at or
     // below cap; the few others between them are taken out of the list afterwards.
-    c.thr = __fsub_rd(rule.m, __fdiv_ru(((float)c.bin + 0.51f) * (1.0f / 32.0f), rule.scale));
-    c.cap = c.upto || c.bin == 0
-                ? INFINITY
-                : __fsub_ru(rule.m, __fdiv_rd(((float)c.bin - 0.51f) * (1.0f / 32.0f), rule.scale));
-    collect(sl, c.thr, c.cap);
+    c.thr = __fsub_rd(rule.m, __fmul_ru(((float)c.bin + 0.51f) * (1.0f / 32.0f), octave));
+    c.cap = c.upto || c.bin == 0 ? INFINITY
+                                 : __fsub_ru(rule.m, __fmul_rd(((float)c.bin - 0.51f) * (1.0f / 32.0f), octave));
+    collect(sl, end.per_warp, c.thr, c.cap);
 #pragma unroll 1
     for (uint32_t i = threadIdx.x; i < min(sh.n_list, (uint32_t)kLocal); i += kSThreads)
         if (!in_crossing<COUNT>(c, rule, key_logit(~(uint32_t)(sh.items[i] >> 32)), sh.items[i])) sh.items[i] = kNoItem;
@@ -1241,7 +1316,7 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
         u64 kept = 0;
         sl.each(zero, [&](const uint4 &r, unsigned int v) {
             uint32_t q[V::N];
-            kept += kept_weights(sl, r, v, rule, *last, q);
+            kept += kept_weights(sl, r, v, weigh, rule.qmin, *last, q);
         });
         halves_of(warp_total(kept), half);
         exchange(kSlotDraw, half[0] + half[1], 0);
@@ -1394,7 +1469,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     }
     if (bounded) {
         const uint32_t bound = by_groups ? kth_bound(maxima, groups * blocks, k, row_key) : 0u;
-        collect(sl, bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY, INFINITY);
+        collect(sl, end.per_warp, bound > kKeyOfMinusInf ? key_logit(bound) : -INFINITY, INFINITY);
         exchange(kSlotBound, sh.n_list, 0);
         const uint32_t n = gathered(kSlotBound);
         if (n <= kList) {
@@ -1412,10 +1487,11 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         filter<false>(sl, rule, k, p, last, end, &cut);
         return;
     }
+    const Weigher<T> weigh(rule);
     u64 mass = 0, half[2];
-    sl.each(__fsub_rd(rule.m, __fdiv_ru(31.5f, rule.scale)), [&](const uint4 &r, unsigned int v) {
+    sl.each(__fsub_rd(rule.m, 31.5f * __frcp_rn(rule.scale)), [&](const uint4 &r, unsigned int v) {
         uint32_t q[V::N];
-        mass += kept_weights(sl, r, v, rule, last, q);
+        mass += kept_weights(sl, r, v, weigh, rule.qmin, last, q);
     });
     halves_of(warp_total(mass), half);
     exchange(kSlotFirst, half[0] + half[1], 0);
