@@ -38,6 +38,19 @@
 //           rows) is searched by radix selection on its logits' bits.
 // A filter ends at an item, (~key, index) as one u64: what stands at or
 // before it in order stays, so ties need no count of their own.
+//
+// Measured on one GB300, launches back to back: a row of 32000 bf16 under
+// top-k and top-p 11 us; 64 x 131072 bf16 under top-p 42 us; 256 x 262144 f32,
+// a fifth of the rows greedy, most others under top-k, top-p or both, 134 us
+// (268 MB: 2.0 TB/s, where reading alone takes 40 us; DRAM 27 % busy). What bounds it
+// is issue and latency, not reading: of the 68,000 clocks that a block of the
+// 64 rows works, reading is 6,000; weighing its logits (30 instructions each,
+// some 3.6 logits a clock and SM) 18,000, the half with the draw again 11,000;
+// finding the bin and gathering it 16,000 and the selection 17,000, which are
+// short steps between barriers. Instructions are issued in 47 % of the cycles
+// (39 % for the 256 rows, whose rows of unequal work also leave SMs idle at
+// the end). Two blocks of 16 warps an SM, 64 registers a thread: while one
+// waits at a barrier the other weighs.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
