@@ -66,7 +66,7 @@ constexpr int kSThreads = 512;
 constexpr int kSWarps = kSThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kLocal = 1024;  // logits a block may put forward
-constexpr int kHits = kLocal;  // vectors with such logits
+constexpr int kHits = kLocal;  // vectors with such logits (warp, its vector: 16 bits each)
 constexpr int kList = 2048;   // and all blocks of a row together
 constexpr int kRanked = 256;  // up to here items are ranked by counting, past it selected by histograms
 constexpr int kTurns = 64;    // turns (of 32 vectors) a warp remembers the maximum of
@@ -95,12 +95,10 @@ enum Slot {
     kSlotMax,       // the largest logit
     kSlotBound,     // lengths of the lists above the bound
     kSlotFirst,     // greedy: the least index; no top-p: weights
-    kSlotCounts,    // top-k by histogram: counts, lengths of lists, ties, the tie
-    kSlotCountList,
+    kSlotCountList, // top-k by histogram: lengths of lists, ties, the tie
     kSlotCountTies,
     kSlotCountTie,
-    kSlotSums,      // top-p: weights, lengths of lists and weights above, ties, the tie, weights kept
-    kSlotSumList,
+    kSlotSumList,   // top-p: lengths of lists and weights above, ties, the tie, weights kept
     kSlotSumTies,
     kSlotSumTie,
     kSlotDraw,
@@ -490,6 +488,22 @@ __device__ __forceinline__ u64 of_warps(u64 v, int which, u64 none) {
 // The sum over the block, in every thread.
 __device__ __noinline__ u64 block_total(u64 v) { return warp_total(of_warps(warp_total(v), 0, 0ull)); }
 
+// The same of several values at once.
+template <int K>
+__device__ __forceinline__ void block_totals(u64 (&v)[K]) {
+    SampleShared &sh = block_shared();
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = warp_total(v[i]);
+    __syncthreads();
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < K; ++i) sh.warp[i][threadIdx.x >> 5] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = warp_total(lane < kSWarps ? sh.warp[i][lane] : 0ull);
+}
+
 // The sum over the threads before this one.
 __device__ __noinline__ u64 block_before(u64 v) {
     const u64 inc = warp_inclusive(v);
@@ -775,9 +789,10 @@ __device__ __noinline__ u64 slot_total(Slot slot, uint32_t blocks, int word = 0)
 
 // What the block's halves hold, from what its warps do (lane 0's word counts).
 __device__ __forceinline__ void halves_of(u64 warp_mass, u64 (&half)[2]) {
-    const u64 one = (threadIdx.x & 31) == 0 ? warp_mass : 0ull;
-    half[0] = block_total(threadIdx.x < kSThreads / 2 ? one : 0ull);
-    half[1] = block_total(threadIdx.x < kSThreads / 2 ? 0ull : one);
+    const u64 warps = of_warps(warp_mass, 0, 0ull);
+    const bool second = (threadIdx.x & 31) >= kSWarps / 2;
+    half[0] = warp_total(second ? 0ull : warps);
+    half[1] = warp_total(second ? warps : 0ull);
 }
 
 // The weights of a vector's logits up to `last`, 0 for the others, for a
@@ -964,6 +979,7 @@ template <typename T>
 __device__ __noinline__ void collect(Slice<T> sl, unsigned int per_warp, float thr, float cap) {
     SampleShared &sh = block_shared();
     using V = Vec<T>;
+    const int warp = threadIdx.x >> 5;
     thr = fmaxf(thr, -3.402823466e38f);  // the least finite logit
     auto take = [&](const uint4 &r, unsigned int v) {
         float x[V::N];
@@ -985,13 +1001,16 @@ __device__ __noinline__ void collect(Slice<T> sl, unsigned int per_warp, float t
     sl.each(thr, [&](const uint4 &r, unsigned int v) {
         if (!V::any_in(r, lo, hi)) return;
         const uint32_t at = atomicAdd(&sh.n_hits, 1u);
-        if (at < kHits) sh.hits[at] = v;
+        if (at < kHits) sh.hits[at] = (uint32_t)warp << 16 | (v - sl.v0);
     });
     __syncthreads();
 #pragma unroll 1
     for (uint32_t i = threadIdx.x; i < min(sh.n_hits, (uint32_t)kHits); i += kSThreads) {
-        const unsigned int v = sh.hits[i];
-        take(sl.load(v), v);
+        const int by = (int)(sh.hits[i] >> 16) - warp;
+        const unsigned int j = sh.hits[i] & 0xffffu, it = j / 32;
+        const unsigned int v = sl.v0 + by * (int)per_warp + j;
+        const uint4 *stage = sl.stage + by * 32 * (int)sl.staged_iters + (int)(j % 32) - (int)(threadIdx.x % 32);
+        take(it < sl.staged_iters ? stage[32 * it] : sl.load(v), v);
     }
     __syncthreads();
     if (threadIdx.x == 0 && sh.n_hits > kHits) sh.n_list = kLocal + 1;  // too many
@@ -1212,7 +1231,7 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
     using V = Vec<T>;
     const uint32_t rank = cluster_rank(), blocks = cluster_size();
     const int warp = threadIdx.x >> 5;
-    const Slot sums_slot = COUNT ? kSlotCounts : kSlotSums, list_slot = COUNT ? kSlotCountList : kSlotSumList;
+    const Slot list_slot = COUNT ? kSlotCountList : kSlotSumList;
     // top-p: the histogram goes as far as it can matter (past cut_y the row holds less than (1 - p)
     // of the largest weight); with min-p it takes all that is kept, and its sum is the row's
     const float cut_y = fminf(31.0f, log2f((float)sl.n / (1.0f - p)) + 0.1f);
@@ -1262,42 +1281,71 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
         }
     });
     __syncthreads();
-    // two bins a thread, of both halves and (for the other blocks) their sum
-    u64 own[2][2], *sums = sh.items + kLocal;
+    // two bins a thread, of both halves and (for the cluster) their sum, and that of every 16 bins
+    u64 own[2][2], *sums = sh.items + kLocal, *coarse = sums + kBins, *of_block = coarse + kBins / 16;
+    u64 sixteen = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int b = 2 * threadIdx.x + i;
         own[0][i] = (u64)sh.bins[0].high[b] << 32 | sh.bins[0].low[b];
         own[1][i] = (u64)sh.bins[1].high[b] << 32 | sh.bins[1].low[b];
         sums[b] = own[0][i] + own[1][i];
+        sixteen += sums[b];
     }
-    exchange(sums_slot, block_total(COUNT || min_p ? own[0][0] + own[0][1] + own[1][0] + own[1][1] : mass), 0);
-    const u64 total = slot_total(sums_slot, blocks), want = COUNT ? k : top_p_target(p, total);
+#pragma unroll
+    for (int d = 1; d < 8; d *= 2) sixteen += __shfl_xor_sync(0xffffffffu, sixteen, d);
+    if (threadIdx.x % 8 == 0) coarse[threadIdx.x / 8] = sixteen;
+    mass = block_total(COUNT || min_p ? own[0][0] + own[0][1] + own[1][0] + own[1][1] : mass);
+    if (threadIdx.x == 0) *of_block = mass;
+    cluster_arrive();
+    cluster_wait();
+    // The bin in which the running sum reaches what is wanted: of the cluster's sums by 16 bins,
+    // then by bin, by one warp (4 KB from the other blocks; all bins to all threads are 64 KB).
+    if (warp == 0) {
+        const uint32_t lane = threadIdx.x;
+        u64 pair[2] = {0, 0}, one = 0;
+        if (lane < blocks) one = ld_cluster_u64(at_rank(of_block, lane));
+        u64 part[kMaxCluster][2];
+#pragma unroll
+        for (uint32_t b = 0; b < kMaxCluster; ++b) {
+            part[b][0] = part[b][1] = 0;
+            if (b < blocks) ld_cluster_u64x2(at_rank(coarse + 2 * lane, b), part[b][0], part[b][1]);
+        }
+#pragma unroll
+        for (uint32_t b = 0; b < kMaxCluster; ++b) {
+            pair[0] += part[b][0];
+            pair[1] += part[b][1];
+        }
+        const u64 total = warp_total(one), want = COUNT ? k : top_p_target(p, total);
+        u64 inc = warp_inclusive(pair[0] + pair[1]), before = inc - pair[0] - pair[1];
+        unsigned int at = __ffs(__ballot_sync(0xffffffffu, want <= inc)) - 1;  // (none: bin 1023)
+        at = min(at, 31u);
+        const bool upper = want > before + pair[0];
+        if (upper) before += pair[0];
+        before = __shfl_sync(0xffffffffu, before, at);
+        const uint32_t first = 16 * (2 * at + __shfl_sync(0xffffffffu, (unsigned int)upper, at));
+        u64 v = 0;
+#pragma unroll
+        for (uint32_t b = 0; b < kMaxCluster; b += 2)
+            if (b + lane / 16 < blocks) v += ld_cluster_u64(at_rank(sums + first + lane % 16, b + lane / 16));
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        inc = before + warp_inclusive(lane < 16 ? v : 0ull);
+        at = __ffs(__ballot_sync(0xffffffffu, want <= inc)) - 1;
+        if (lane == min(at, 15u)) {
+            sh.cast[0] = first + lane;
+            sh.cast[1] = inc - v;
+            sh.cast[2] = inc;
+            sh.cast[3] = total;
+        }
+    }
+    __syncthreads();
+    const u64 total = sh.cast[3], want = COUNT ? k : top_p_target(p, total);
     if (COUNT && total <= want) {  // all that have a weight are kept
+        cluster_arrive();  // the sums are written again
+        cluster_wait();
         *last = limit;
         return false;
     }
-    // the bin in which the running sum reaches `want`
-    u64 part[kMaxCluster][2];
-#pragma unroll
-    for (uint32_t b = 0; b < kMaxCluster; ++b) {
-        part[b][0] = part[b][1] = 0;
-        if (b < blocks) ld_cluster_u64x2(at_rank(sums + 2 * threadIdx.x, b), part[b][0], part[b][1]);
-    }
-    u64 bin_mass[2] = {0, 0};
-#pragma unroll
-    for (uint32_t b = 0; b < kMaxCluster; ++b) {
-        bin_mass[0] += part[b][0];
-        bin_mass[1] += part[b][1];
-    }
-    const u64 before = block_before(bin_mass[0] + bin_mass[1]);
-    if (before < want && want <= before + bin_mass[0] + bin_mass[1]) {
-        const bool second = want > before + bin_mass[0];
-        sh.cast[0] = 2 * threadIdx.x + second;
-        sh.cast[1] = before + (second ? bin_mass[0] : 0ull);
-        sh.cast[2] = before + bin_mass[0] + (second ? bin_mass[1] : 0ull);
-    }
-    __syncthreads();
     c.bin = (uint32_t)sh.cast[0];
     const u64 above = sh.cast[1];
     // Are there few enough to gather all up to this bin? None there weighs less than the bin's far
@@ -1305,11 +1353,12 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
     const uint32_t far = exp2_weight(((float)c.bin + 0.5f) * (1.0f / 32.0f)), slack = (far >> 16) + 2;
     c.upto = sh.cast[2] <= (COUNT ? (u64)kList : (u64)max(far > slack ? far - slack : 0u, c.floor_q) * kList);
     u64 half[2] = {0, 0};  // weights of the bins before it
-    if (!COUNT)
+    if (!COUNT) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            half[h] = block_total((2 * threadIdx.x < c.bin ? own[h][0] : 0ull) +
-                                  (2 * threadIdx.x + 1 < c.bin ? own[h][1] : 0ull));
+            half[h] = (2 * threadIdx.x < c.bin ? own[h][0] : 0ull) + (2 * threadIdx.x + 1 < c.bin ? own[h][1] : 0ull);
+        block_totals(half);
+    }
     // Every logit in a bin up to this one is at or above thr, every one in a bin from it on at or
     // below cap; the few others between them are taken out of the list afterwards.
     c.thr = __fsub_rd(rule.m, __fmul_ru(((float)c.bin + 0.51f) * (1.0f / 32.0f), octave));
@@ -1350,21 +1399,21 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
         left += above + item_weight(*last, rule);
         const uint32_t from = (uint32_t)slot_total(list_slot, rank), to = from + sh.n_list;
         const uint32_t second = (rank * kSWarps + kSWarps / 2) * end.per_warp * V::N;  // its first element
-        u64 ahead = 0, in[2] = {0, 0};
+        u64 kept[3] = {0, 0, 0};  // by the blocks before, and by this one's halves
 #pragma unroll 1
         for (uint32_t i = threadIdx.x; i < to; i += kSThreads) {
             const u64 item = sh.items[kLocal + i];
             if (item > *last) continue;
             const u64 q = sh.picks.weights[i];
-            if (i < from) ahead += q;
-            else if ((uint32_t)item + sl.pad < second) in[0] += q;
-            else in[1] += q;
+            if (i < from) kept[0] += q;
+            else if ((uint32_t)item + sl.pad < second) kept[1] += q;
+            else kept[2] += q;
         }
-        ahead = block_total(ahead) + slot_total(list_slot, rank, 1);
-        half[0] += block_total(in[0]);
-        half[1] += block_total(in[1]);
+        block_totals(kept);
+        half[0] += kept[1];
+        half[1] += kept[2];
         cluster_wait();
-        draw(sl, rule, *last, left, ahead, half, end);
+        draw(sl, rule, *last, left, kept[0] + slot_total(list_slot, rank, 1), half, end);
         return true;
     }
     cluster_wait();
@@ -1526,6 +1575,7 @@ constexpr unsigned int kMaxStaged = 8;
 constexpr unsigned int kResident = 304;  // blocks at a time: two on each of 152 SMs
 static_assert(sizeof(SampleShared) % 16 == 0 && offsetof(SampleShared, slots) % 16 == 0 && kLocal % 2 == 0,
               "16-byte accesses");
+static_assert(U32SCAN_MAX_VOCAB / 4 / kMaxCluster / kSWarps + 8 < 65536, "a warp's vectors in 16 bits");
 static_assert(2 * (sizeof(SampleShared) + kMaxStaged * kStageBytes + 1024) <= 228 * 1024, "two blocks an SM");
 
 template <typename T>
