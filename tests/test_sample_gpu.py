@@ -320,3 +320,16 @@ def test_probabilities_against_softmax_in_64_bits(u, dtype):
     p = (w / w.sum(1, keepdims=True))[np.arange(rows), tok]
     rel = 2 * (1.5 * 2.0**-19 * np.log(2.0) + 2e-7) + n * 2.0**-31 + 2.0**-24
     assert np.all(np.abs(prob - p) <= p * rel + 2.0**-31)
+
+
+@pytest.mark.parametrize("n", [40, 3000, 70001])
+def test_every_size_of_top_p_and_min_p(u, n):
+    """The targets ceil(top_p * sum) and ceil(min_p * 2^31) are taken as from
+    doubles, from the least float to the last below one."""
+    p = [2.0**-149, 2.0**-126, 3 * 2.0**-130, 1e-30, 2.0**-53, 2.0**-24, 2.0**-22, 0.25, 0.5, 1 / 3, 0.1, 0.7, 0.9,
+         1 - 2.0**-23, 1 - 2.0**-24]
+    p = np.array(p + list(np.random.default_rng(n).random(49)), dtype=np.float32)
+    x = np.concatenate([logits_for("flat", 32, n, 51), logits_for("tied", 32, n, 52)])
+    words = inputs.splitmix_u32(24, 0, 64)
+    check(u, x, "f32", words, dict(top_p=p))
+    check(u, x, "f32", words, dict(min_p=p, top_p=p[::-1].copy()))

@@ -92,7 +92,6 @@ struct SampleArgs {
 // Exchanges between a cluster's blocks: one slot each, so that none is
 // written again while a slow block still reads it.
 enum Slot {
-    kSlotMax,       // the largest logit
     kSlotBound,     // lengths of the lists above the bound
     kSlotFirst,     // greedy: the least index; no top-p: weights
     kSlotCountList, // top-k by histogram: lengths of lists, ties, the tie
@@ -158,8 +157,9 @@ struct alignas(16) SampleShared {
     };
     u64 slots[kSlots][kMaxCluster][2];
     uint32_t turn_key[kSWarps][kTurns];  // the key of a turn's largest logit
+    uint32_t warp_keys[kMaxCluster][kSWarps];  // the keys of all warps' largest logits
     u64 warp[3][kSWarps];
-    u64 cast[4];
+    u64 cast[6];
     uint32_t n_list, n_hits;
 };
 
@@ -466,10 +466,10 @@ __device__ __forceinline__ u64 warp_min(u64 v) {
 
 __device__ __forceinline__ u64 warp_inclusive(u64 v) {
     const int lane = threadIdx.x & 31;
-#pragma unroll 1
+#pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const u64 o = __shfl_up_sync(0xffffffffu, v, d);
-        if (lane >= d) v += o;
+        v += lane >= d ? o : 0ull;
     }
     return v;
 }
@@ -695,22 +695,31 @@ __device__ __forceinline__ void weigh_items(uint32_t n, u64 limit, RowRule rule)
 // the greatest, gives the bin that holds the crossing; its items, where they
 // are at most kFew, find it by counting what stands before them, else
 // they are the next histogram's.
-__device__ __noinline__ u64 block_select(uint32_t n, bool by_index, u64 target, u64 *before_it) {
+__device__ __noinline__ u64 block_select(uint32_t n, bool by_index, u64 target, u64 *before_it, u64 low = 0,
+                                         u64 high = ~0ull) {
     SampleShared &sh = block_shared();
     const u64 place_bits = by_index ? 0xffffffffull : ~0ull;
-    u64 low = 0, high = ~0ull, base = 0;  // the places still in question
+    u64 base = 0;
+    bool narrow = high != ~0ull;
     while (true) {
-        u64 lo = ~0ull, hi = 0;
-#pragma unroll 1
-        for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
-            const u64 place = sh.items[kLocal + i] & place_bits;
-            if (sh.picks.weights[i] && place >= low && place <= high) {
-                lo = min(lo, place);
-                hi = max(hi, place);
-            }
-        }
         sh.picks.sums.low[threadIdx.x] = sh.picks.sums.high[threadIdx.x] = sh.picks.counts[threadIdx.x] = 0;
-        block_range(lo, hi);
+        u64 lo = low, hi = high;
+        if (narrow) {
+            __syncthreads();
+        } else {
+            lo = ~0ull;
+            hi = 0;
+#pragma unroll 1
+            for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
+                const u64 place = sh.items[kLocal + i] & place_bits;
+                if (sh.picks.weights[i] && place >= low && place <= high) {
+                    lo = min(lo, place);
+                    hi = max(hi, place);
+                }
+            }
+            block_range(lo, hi);
+        }
+        narrow = false;
         const int shift = 55 - __clzll((hi - lo) | 511ull);
 #pragma unroll 1
         for (uint32_t i = threadIdx.x; i < n; i += kSThreads) {
@@ -777,7 +786,22 @@ __device__ __noinline__ void write_token(RowEnd end, uint32_t index, u64 q, u64 
 __device__ __forceinline__ u64 draw_of(uint32_t word, u64 total) { return __umul64hi((u64)word << 32, total); }
 
 __device__ __forceinline__ u64 top_p_target(float p, u64 total) {
-    return (u64)ceil(__dmul_rn((double)p, (double)total));
+    // The product's 77 bits in integers (doubles are few on this chip, and slow when every warp
+    // wants one: 780 clocks a block), to 53 bits as a double's are, ties to even, then up.
+    const uint32_t bits = __float_as_uint(p), exponent = max(bits >> 23, 1u);  // p = digits * 2^(exponent - 150)
+    const uint32_t digits = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);
+    u64 low = total * digits, high = __umul64hi(total, digits);
+    int below = 150 - (int)exponent;  // binary places
+    const int length = high ? 128 - __clzll(high) : 64 - __clzll(low);
+    if (length > 53) {
+        const int drop = length - 53;  // at most 24
+        const u64 rest = low & ((1ull << drop) - 1), tie = 1ull << (drop - 1);
+        low = low >> drop | high << (64 - drop);
+        low += rest > tie || (rest == tie && (low & 1));
+        below -= drop;
+    }
+    if (below > 53) return 1;
+    return (low >> below) + ((low & ((1ull << below) - 1)) != 0);
 }
 
 // The sum of what the first `blocks` blocks put into a slot.
@@ -1336,10 +1360,11 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
             sh.cast[1] = inc - v;
             sh.cast[2] = inc;
             sh.cast[3] = total;
+            sh.cast[4] = want;
         }
     }
     __syncthreads();
-    const u64 total = sh.cast[3], want = COUNT ? k : top_p_target(p, total);
+    const u64 total = sh.cast[3], want = sh.cast[4];
     if (COUNT && total <= want) {  // all that have a weight are kept
         cluster_arrive();  // the sums are written again
         cluster_wait();
@@ -1394,7 +1419,8 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
     }
     // every block finds the crossing among the gathered, and what is kept of them where
     weigh_items<COUNT>(n, kKeepAll, rule);
-    *last = block_select(n, false, want - above, &left);
+    *last = block_select(n, false, want - above, &left, item_of(key_of(fminf(c.cap, rule.m)), 0),
+                         item_of(key_of(c.thr), 0xffffffffu));
     if (!COUNT) {
         left += above + item_weight(*last, rule);
         const uint32_t from = (uint32_t)slot_total(list_slot, rank), to = from + sh.n_list;
@@ -1449,7 +1475,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     const u64 row = blockIdx.x / blocks;
     const RowEnd end{a.tokens + row, a.probs ? a.probs + row : nullptr, a.random[row], a.per_warp};
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    cluster_arrive();  // paired with the wait before the first exchange: every block has started
+    // paired with the wait before the first exchange: every block has started (nothing written yet)
+    asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
     if (threadIdx.x == 0) sh.n_list = 0;
 
     Slice<T> sl;
@@ -1485,15 +1512,19 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         group_key = thread_key;
         for (uint32_t d = 1; d < group; d *= 2) group_key = max(group_key, __shfl_xor_sync(0xffffffffu, group_key, d));
     }
-    const uint32_t block_key = ~(uint32_t)block_min(~warp_key);
     cluster_wait();
     uint32_t *maxima = reinterpret_cast<uint32_t *>(sh.items + kLocal);  // of all the row's groups
     if (by_groups && threadIdx.x % group == 0)
         for (uint32_t c = 0; c < blocks; ++c)
             st_cluster(at_rank(maxima + rank * groups + threadIdx.x / group, c), group_key);
-    exchange(kSlotMax, block_key, 0);
-    const uint32_t row_key =
-        __reduce_max_sync(0xffffffffu, lane < (int)blocks ? (uint32_t)sh.slots[kSlotMax][lane][0] : 0u);
+    if (lane < (int)blocks) st_cluster(at_rank(&sh.warp_keys[rank][warp], lane), warp_key);
+    cluster_arrive();
+    cluster_wait();
+    uint32_t row_key = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kMaxCluster; i += 32 / kSWarps)
+        if (i + lane / kSWarps < blocks) row_key = max(row_key, sh.warp_keys[i + lane / kSWarps][lane % kSWarps]);
+    row_key = __reduce_max_sync(0xffffffffu, row_key);
     if (row_key <= kKeyOfMinusInf) {  // the mask leaves nothing
         if (rank == 0 && threadIdx.x == 0) {
             *end.token = -1;
@@ -1504,11 +1535,11 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     RowRule rule;
     rule.m = key_logit(row_key);
     rule.scale = __fdiv_rn(kLog2e, t);
-    rule.qmin = mp > 0.0f ? (uint32_t)ceil((double)fminf(mp, 1.0f) * 2147483648.0) : 0u;
+    rule.qmin = mp > 0.0f ? __float2uint_ru(__fmul_rn(fminf(mp, 1.0f), 0x1p31f)) : 0u;  // (the product is exact)
 
     if (!(t > 0.0f)) {  // the first of the largest
         uint32_t first = 0xffffffffu;
-        if (block_key == row_key)
+        if (warp_key == row_key)
             sl.each(rule.m, [&](const uint4 &r, unsigned int v) {
                 if (first != 0xffffffffu || !(V::max(r) >= rule.m)) return;
                 float x[V::N];
