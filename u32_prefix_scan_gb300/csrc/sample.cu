@@ -93,14 +93,13 @@ struct SampleArgs {
 // written again while a slow block still reads it.
 enum Slot {
     kSlotBound,     // lengths of the lists above the bound
-    kSlotFirst,     // greedy: the least index; no top-p: weights
+    kSlotFirst,     // greedy: the least index; no list: weights
     kSlotCountList, // top-k by histogram: lengths of lists, ties, the tie
     kSlotCountTies,
     kSlotCountTie,
-    kSlotSumList,   // top-p: lengths of lists and weights above, ties, the tie, weights kept
+    kSlotSumList,   // top-p: lengths of lists and weights above, ties, the tie
     kSlotSumTies,
     kSlotSumTie,
-    kSlotDraw,
     kSlots
 };
 
@@ -811,14 +810,6 @@ __device__ __noinline__ u64 slot_total(Slot slot, uint32_t blocks, int word = 0)
     return warp_total(lane < blocks ? sh.slots[slot][lane][word] : 0ull);
 }
 
-// What the block's halves hold, from what its warps do (lane 0's word counts).
-__device__ __forceinline__ void halves_of(u64 warp_mass, u64 (&half)[2]) {
-    const u64 warps = of_warps(warp_mass, 0, 0ull);
-    const bool second = (threadIdx.x & 31) >= kSWarps / 2;
-    half[0] = warp_total(second ? 0ull : warps);
-    half[1] = warp_total(second ? warps : 0ull);
-}
-
 // The weights of a vector's logits up to `last`, 0 for the others, for a
 // finite m and scale.
 template <typename T>
@@ -842,24 +833,24 @@ __device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const uint4 &r, 
 }
 
 // The draw among the items up to `last`, in index order, by the block that
-// holds it: `before` is what the blocks before this one keep, `half` what
-// this one's halves do. It weighs that half again, a turn of 32 vectors a
-// warp, and walks the turn with the draw.
+// holds it: `before` is what the blocks before this one keep, `mass` in lane i
+// what its i-th group of `group` warps does. It weighs the group with the draw
+// again, a turn of 32 vectors a warp, and walks the turn with the draw.
 template <typename T>
-__device__ __noinline__ void draw(Slice<T> own, RowRule rule, u64 last, u64 total, u64 before,
-                                  const u64 (&half)[2], RowEnd end) {
+__device__ __noinline__ void draw(Slice<T> own, RowRule rule, u64 last, u64 total, u64 before, u64 mass,
+                                  unsigned int group, RowEnd end) {
     SampleShared &sh = block_shared();
     constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const u64 r = draw_of(end.word, total);
-    if (r < before || r - before >= half[0] + half[1]) return;
-    const bool second = r - before >= half[0];
-    if (second) before += half[0];
-    const int warp0 = second ? kSWarps / 2 : 0;
+    const u64 r = draw_of(end.word, total), upto = before + warp_inclusive(mass);
+    if (r < before || r >= __shfl_sync(0xffffffffu, upto, 31)) return;
+    const unsigned int at_group = __ffs(__ballot_sync(0xffffffffu, r < upto)) - 1;
+    before = __shfl_sync(0xffffffffu, upto - mass, at_group);
+    const int warp0 = (int)(at_group * group);
     const unsigned int per_warp = end.per_warp, nv = (own.pad + own.n + N - 1) / N;
-    const unsigned int per = (per_warp + 31) / 32, turns = kSWarps / 2 * per;
+    const unsigned int per = (per_warp + 31) / 32, turns = group * per;
     const Weigher<T> weigh(rule);
-    u64 *mass = sh.items;  // by turn
+    u64 *of_turn = sh.items;
     u64 at = 0;
     bool walk = false;  // first all turns, then the one
     unsigned int t = warp;
@@ -890,17 +881,17 @@ __device__ __noinline__ void draw(Slice<T> own, RowRule rule, u64 last, u64 tota
             return;
         }
         sum = warp_total(sum);
-        if (lane == 0 && t < turns) mass[t] = sum;
+        if (lane == 0 && t < turns) of_turn[t] = sum;
         t += kSWarps;
         if (t < turns) continue;
         __syncthreads();
         const unsigned int each = (turns + kSThreads - 1) / kSThreads, first = threadIdx.x * each;
         sum = 0;
-        for (t = first; t < first + each && t < turns; ++t) sum += mass[t];
+        for (t = first; t < first + each && t < turns; ++t) sum += of_turn[t];
         at = before + block_before(sum);
         if (at <= r && r - at < sum) {
             t = first;
-            while (r - at >= mass[t]) at += mass[t++];
+            while (r - at >= of_turn[t]) at += of_turn[t++];
             sh.cast[0] = t;
             sh.cast[1] = at;
         }
@@ -921,20 +912,21 @@ __device__ __forceinline__ uint32_t kth_bound(const uint32_t *maxima, uint32_t n
                                               uint32_t row_key) {
     SampleShared &sh = block_shared();
     if (n <= kSThreads) {
-        if (threadIdx.x < n) {
-            const uint32_t mine = maxima[threadIdx.x];
-            const uint4 *four = reinterpret_cast<const uint4 *>(maxima);
-            uint32_t above = 0;
+        uint32_t team = 1;  // threads that count for one maximum
+        while (team < 16 && 2 * team * n <= kSThreads) team *= 2;
+        const uint32_t i = threadIdx.x / team, part = threadIdx.x % team;
+        const uint32_t mine = i < n ? maxima[i] : 0u;
+        const uint4 *four = reinterpret_cast<const uint4 *>(maxima);
+        uint32_t above = 0;
+        if (i < n)
 #pragma unroll 2
-            for (uint32_t j = 0; j < n; j += 4) {
+            for (uint32_t j = 4 * part; j < n; j += 4 * team) {
                 const uint4 o = four[j / 4];
-                above += (o.x > mine || (o.x == mine && j < threadIdx.x)) +
-                         (o.y > mine || (o.y == mine && j + 1 < threadIdx.x)) +
-                         (o.z > mine || (o.z == mine && j + 2 < threadIdx.x)) +
-                         (o.w > mine || (o.w == mine && j + 3 < threadIdx.x));
+                above += (o.x > mine || (o.x == mine && j < i)) + (o.y > mine || (o.y == mine && j + 1 < i)) +
+                         (o.z > mine || (o.z == mine && j + 2 < i)) + (o.w > mine || (o.w == mine && j + 3 < i));
             }
-            if (above == k - 1) sh.cast[0] = mine;
-        }
+        for (uint32_t d = 1; d < team; d *= 2) above += __shfl_xor_sync(0xffffffffu, above, d);
+        if (part == 0 && i < n && above == k - 1) sh.cast[0] = mine;
         __syncthreads();
         return (uint32_t)sh.cast[0];
     }
@@ -1244,6 +1236,21 @@ __device__ __noinline__ u64 select_in_bin(Slice<T> sl, RowRule rule, const Cross
     return nth_tie(sl, prefix, ties, COUNT ? kSlotCountTies : kSlotSumTies, COUNT ? kSlotCountTie : kSlotSumTie);
 }
 
+// The draw among all items up to `last`, weighed first.
+template <typename T>
+__device__ __noinline__ void weigh_and_draw(Slice<T> sl, RowRule rule, u64 last, RowEnd end) {
+    using V = Vec<T>;
+    const Weigher<T> weigh(rule);
+    u64 mass = 0;
+    sl.each(__fsub_rd(rule.m, 31.5f * __frcp_rn(rule.scale)), [&](const uint4 &r, unsigned int v) {
+        uint32_t q[V::N];
+        mass += kept_weights(sl, r, v, weigh, rule.qmin, last, q);
+    });
+    mass = of_warps(warp_total(mass), 0, 0ull);
+    exchange(kSlotFirst, warp_total(mass), 0);
+    draw(sl, rule, last, slot_total(kSlotFirst, cluster_size()), slot_total(kSlotFirst, cluster_rank()), mass, 1, end);
+}
+
 // A filter over a row of finite m and scale: top-k (COUNT) or top-p over the
 // items up to `limit`, by a histogram of counts or weights. Returns true when
 // the row's token is written (top-p: always), else *last is the item at
@@ -1400,14 +1407,7 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
         c.upto = false;
         *last = select_in_bin<COUNT>(sl, rule, c, want - above, &left);
         if (COUNT) return false;
-        u64 kept = 0;
-        sl.each(zero, [&](const uint4 &r, unsigned int v) {
-            uint32_t q[V::N];
-            kept += kept_weights(sl, r, v, weigh, rule.qmin, *last, q);
-        });
-        halves_of(warp_total(kept), half);
-        exchange(kSlotDraw, half[0] + half[1], 0);
-        draw(sl, rule, *last, above + left, slot_total(kSlotDraw, rank), half, end);
+        weigh_and_draw(sl, rule, *last, end);
         return true;
     }
     if (!c.upto || rank == 0) pull(list_slot, n);
@@ -1439,7 +1439,8 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
         half[0] += kept[1];
         half[1] += kept[2];
         cluster_wait();
-        draw(sl, rule, *last, left, kept[0] + slot_total(list_slot, rank, 1), half, end);
+        draw(sl, rule, *last, left, kept[0] + slot_total(list_slot, rank, 1),
+             threadIdx.x % 32 == 0 ? half[0] : threadIdx.x % 32 == 1 ? half[1] : 0ull, kSWarps / 2, end);
         return true;
     }
     cluster_wait();
@@ -1580,15 +1581,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         filter<false>(sl, rule, k, p, last, end, &cut);
         return;
     }
-    const Weigher<T> weigh(rule);
-    u64 mass = 0, half[2];
-    sl.each(__fsub_rd(rule.m, 31.5f * __frcp_rn(rule.scale)), [&](const uint4 &r, unsigned int v) {
-        uint32_t q[V::N];
-        mass += kept_weights(sl, r, v, weigh, rule.qmin, last, q);
-    });
-    halves_of(warp_total(mass), half);
-    exchange(kSlotFirst, half[0] + half[1], 0);
-    draw(sl, rule, last, slot_total(kSlotFirst, blocks), slot_total(kSlotFirst, rank), half, end);
+    weigh_and_draw(sl, rule, last, end);
 }
 
 // ---------------------------------------------------------------------------
