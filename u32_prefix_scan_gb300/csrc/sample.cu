@@ -85,7 +85,7 @@ struct SampleArgs {
     const uint32_t *random;
     int32_t *tokens;
     float *probs;
-    unsigned int per_warp;      // 16-byte vectors of a row a warp takes
+    unsigned int per_warp;      // vectors of a row a warp takes
     unsigned int staged_iters;  // of its ceil(per_warp / 32) turns, those kept in shared memory
 };
 
@@ -182,44 +182,69 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// Sixteen bytes of a row as floats; their maximum (of those that are not NaN;
-// -inf or NaN if there is none); whether any lies in [from(lo), upto(hi)], the
-// bounds rounded inwards to the logits' type.
+// Eight logits of a row, as they are read (Raw) and as floats; their maximum
+// (of those that are not NaN; -inf or NaN if there is none); whether any lies in
+// [from(lo), upto(hi)], the bounds rounded inwards to the logits' type. Staged,
+// a turn's vectors lie 16 bytes of each lane after 16 bytes of each. (With four
+// f32 a vector the loops' own instructions weigh twice as much: 256 x 131072
+// under top-p 149 us and 138, 256 x 262144 of mixed settings 135 and 130.)
+struct Vec16 {  // what f16 and bf16 share
+    static constexpr int N = 8;
+    typedef uint4 Raw;
+    static __device__ __forceinline__ Raw load(const char *p) { return __ldg(reinterpret_cast<const uint4 *>(p)); }
+    static __device__ __forceinline__ void put(uint4 *stage, const Raw &r) { *stage = r; }
+    static __device__ __forceinline__ Raw get(const uint4 *stage) { return *stage; }
+};
+
 template <typename T>
 struct Vec;
 
 template <>
 struct Vec<float> {
-    static constexpr int N = 4;
+    static constexpr int N = 8;
     static constexpr uint32_t kFill = 0xff800000u;  // -inf
-    static __device__ __forceinline__ void unpack(const uint4 &r, float (&x)[4]) {
-        x[0] = __uint_as_float(r.x);
-        x[1] = __uint_as_float(r.y);
-        x[2] = __uint_as_float(r.z);
-        x[3] = __uint_as_float(r.w);
+    struct Raw {
+        uint4 a, b;
+    };
+    static __device__ __forceinline__ Raw load(const char *p) {
+        Raw r;
+        asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w), "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w)
+            : "l"(p));
+        return r;
+    }
+    static __device__ __forceinline__ void put(uint4 *stage, const Raw &r) {
+        stage[0] = r.a;
+        stage[32] = r.b;
+    }
+    static __device__ __forceinline__ Raw get(const uint4 *stage) { return {stage[0], stage[32]}; }
+    static __device__ __forceinline__ void unpack(const Raw &r, float (&x)[8]) {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(w[e]);
     }
     typedef float Bound;
     static __device__ __forceinline__ Bound from(float lo) { return lo; }
     static __device__ __forceinline__ Bound upto(float hi) { return hi; }
-    static __device__ __forceinline__ bool any_in(const uint4 &r, Bound lo, Bound hi) {
-        float x[4];
+    static __device__ __forceinline__ bool any_in(const Raw &r, Bound lo, Bound hi) {
+        float x[8];
         unpack(r, x);
         bool any = false;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) any |= x[e] >= lo && x[e] <= hi;
+        for (int e = 0; e < 8; ++e) any |= x[e] >= lo && x[e] <= hi;
         return any;
     }
-    static __device__ __forceinline__ float max(const uint4 &r) {
-        return fmaxf(fmaxf(__uint_as_float(r.x), __uint_as_float(r.y)),
-                     fmaxf(__uint_as_float(r.z), __uint_as_float(r.w)));
+    static __device__ __forceinline__ float max(const Raw &r) {
+        float x[8];
+        unpack(r, x);
+        return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
     }
 };
 
 template <>
-struct Vec<__nv_bfloat16> {
-    static constexpr int N = 8;
+struct Vec<__nv_bfloat16> : Vec16 {
     static constexpr uint32_t kFill = 0xff80ff80u;
-    static __device__ __forceinline__ void unpack(const uint4 &r, float (&x)[8]) {
+    static __device__ __forceinline__ void unpack(const Raw &r, float (&x)[8]) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -230,14 +255,14 @@ struct Vec<__nv_bfloat16> {
     typedef __nv_bfloat162 Bound;
     static __device__ __forceinline__ Bound from(float lo) { return __bfloat162bfloat162(__float2bfloat16_ru(lo)); }
     static __device__ __forceinline__ Bound upto(float hi) { return __bfloat162bfloat162(__float2bfloat16_rd(hi)); }
-    static __device__ __forceinline__ bool any_in(const uint4 &r, Bound lo, Bound hi) {
+    static __device__ __forceinline__ bool any_in(const Raw &r, Bound lo, Bound hi) {
         const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r);
         unsigned int any = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) any |= __hge2_mask(h[j], lo) & __hle2_mask(h[j], hi);
         return any != 0;
     }
-    static __device__ __forceinline__ float max(const uint4 &r) {
+    static __device__ __forceinline__ float max(const Raw &r) {
         const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r);
         const float2 f = __bfloat1622float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
         return fmaxf(f.x, f.y);
@@ -245,10 +270,9 @@ struct Vec<__nv_bfloat16> {
 };
 
 template <>
-struct Vec<__half> {
-    static constexpr int N = 8;
+struct Vec<__half> : Vec16 {
     static constexpr uint32_t kFill = 0xfc00fc00u;
-    static __device__ __forceinline__ void unpack(const uint4 &r, float (&x)[8]) {
+    static __device__ __forceinline__ void unpack(const Raw &r, float (&x)[8]) {
         const __half2 *h = reinterpret_cast<const __half2 *>(&r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -260,14 +284,14 @@ struct Vec<__half> {
     typedef __half2 Bound;
     static __device__ __forceinline__ Bound from(float lo) { return __half2half2(__float2half_ru(lo)); }
     static __device__ __forceinline__ Bound upto(float hi) { return __half2half2(__float2half_rd(hi)); }
-    static __device__ __forceinline__ bool any_in(const uint4 &r, Bound lo, Bound hi) {
+    static __device__ __forceinline__ bool any_in(const Raw &r, Bound lo, Bound hi) {
         const __half2 *h = reinterpret_cast<const __half2 *>(&r);
         unsigned int any = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) any |= __hge2_mask(h[j], lo) & __hle2_mask(h[j], hi);
         return any != 0;
     }
-    static __device__ __forceinline__ float max(const uint4 &r) {
+    static __device__ __forceinline__ float max(const Raw &r) {
         const __half2 *h = reinterpret_cast<const __half2 *>(&r);
         const float2 f = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
         return fmaxf(f.x, f.y);
@@ -362,8 +386,8 @@ struct Weigher {
     __device__ __forceinline__ explicit Weigher(const RowRule &rule)
         : m2(pack2(rule.m, rule.m)), scale2(pack2(rule.scale, rule.scale)) {}
 
-    __device__ __forceinline__ void operator()(const uint4 &r, float (&x)[Vec<T>::N], float (&y)[Vec<T>::N],
-                                               uint32_t (&q)[Vec<T>::N]) const {
+    __device__ __forceinline__ void operator()(const typename Vec<T>::Raw &r, float (&x)[Vec<T>::N],
+                                               float (&y)[Vec<T>::N], uint32_t (&q)[Vec<T>::N]) const {
         constexpr int N = Vec<T>::N;
         Vec<T>::unpack(r, x);
         u64 y2[N / 2];
@@ -443,7 +467,7 @@ __device__ __forceinline__ u64 ld_cluster_u64(uint32_t addr) {
 // Every block's (a, b), given by its threads below the cluster's size, then
 // in sh.slots[slot] of every block. A cluster barrier: what blocks wrote to
 // their shared memory before it can be read by the others after it.
-__device__ __noinline__ void exchange(Slot slot, u64 a, u64 b) {
+__device__ __forceinline__ void exchange(Slot slot, u64 a, u64 b) {
     SampleShared &sh = block_shared();
     if (threadIdx.x < cluster_size()) st_cluster(at_rank(sh.slots[slot][cluster_rank()], threadIdx.x), a, b);
     cluster_arrive();
@@ -532,17 +556,22 @@ __device__ __noinline__ void block_range(u64 &lo, u64 &hi) {
 // ---------------------------------------------------------------------------
 // A block's slice of a row
 // ---------------------------------------------------------------------------
-// Elements p .. of base, those outside [first, end) as -inf.
+// Vector v of base, the elements outside [first, end) as -inf.
 template <typename T>
-__device__ __noinline__ uint4 load_edge(const T *base, unsigned int p, unsigned int first, unsigned int end) {
-    constexpr int bits = 8 * sizeof(T), per_word = 32 / bits;
-    uint32_t w[4];
+__device__ __noinline__ typename Vec<T>::Raw load_edge(const T *base, unsigned int v, unsigned int first,
+                                                       unsigned int end) {
+    typedef typename Vec<T>::Raw Raw;
+    constexpr int bits = 8 * sizeof(T), per_word = 32 / bits, words = sizeof(Raw) / 4;
+    union {
+        Raw r;
+        uint32_t w[words];
+    };
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < words; ++j) {
         w[j] = Vec<T>::kFill;
 #pragma unroll
         for (int i = 0; i < per_word; ++i) {
-            const unsigned int at = p + j * per_word + i;
+            const unsigned int at = v * Vec<T>::N + j * per_word + i;
             if (at >= first && at < end) {
                 const uint32_t one = sizeof(T) == 4 ? reinterpret_cast<const uint32_t *>(base)[at]
                                                     : reinterpret_cast<const uint16_t *>(base)[at];
@@ -550,47 +579,49 @@ __device__ __noinline__ uint4 load_edge(const T *base, unsigned int p, unsigned 
             }
         }
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return r;
 }
 
 template <typename T>
 struct Slice {
     using V = Vec<T>;
-    const char *base;           // the row's address rounded down to 16 bytes
+    typedef typename V::Raw Raw;
+    static constexpr int kLane = sizeof(Raw) / 16;  // 16-byte words of a vector
+    const char *base;           // the row's address rounded down to a vector
     unsigned int pad, n;        // elements between base and the row, and in the row
     unsigned int v0, count;     // this warp's first vector and how many it has
     unsigned int staged_iters;
-    uint4 *stage;               // this lane's vectors: turn i at stage[32 * i]
+    uint4 *stage;               // this lane's vectors: turn i at stage + 32 * kLane * i
 
     // Vector v; past the row's ends filled with -inf.
-    __device__ __forceinline__ uint4 load(unsigned int v) const {
+    __device__ __forceinline__ Raw load(unsigned int v) const {
         const unsigned int first = pad ? 1u : 0u, end = (pad + n) / V::N;  // those between are whole
-        if (v - first < end - first) return __ldg(reinterpret_cast<const uint4 *>(base) + v);
-        return load_edge<T>(reinterpret_cast<const T *>(base), v * V::N, pad, pad + n);
+        if (v - first < end - first) return V::load(base + (size_t)v * sizeof(Raw));
+        return load_edge<T>(reinterpret_cast<const T *>(base), v, pad, pad + n);
     }
 
     // First reading: keeps the staged vectors and the turns' maxima, returns the
     // warp's (as a key) and, if asked, this thread's.
     __device__ __forceinline__ uint32_t first_pass(uint32_t *thread_key) const {
-        constexpr int U = 4;
+        constexpr int U = 4 / kLane;
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
         uint32_t *turn_key = block_shared().turn_key[warp];
-        const uint4 *whole = reinterpret_cast<const uint4 *>(base) + v0 + lane;
+        const char *whole = base + (size_t)(v0 + lane) * sizeof(Raw);
         const unsigned int whole_end = (pad + n) / V::N;  // vectors from here on, and 0 with a pad, are cut
         float m = -INFINITY;
         uint32_t most = 0;
 #pragma unroll 1
         for (unsigned int it = 0; 32 * it < count; it += U) {
-            uint4 r[U];
+            Raw r[U];
             const unsigned int end = 32 * (it + U);
             if (end <= count && v0 + end <= whole_end && (pad == 0 || v0 + it > 0)) {
 #pragma unroll
-                for (int u = 0; u < U; ++u) r[u] = __ldg(whole + 32 * (it + u));
+                for (int u = 0; u < U; ++u) r[u] = V::load(whole + 32 * (it + u) * sizeof(Raw));
             } else {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const unsigned int j = 32 * (it + u) + lane;
-                    r[u] = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
+                    r[u] = fill();
                     if (has(j)) r[u] = load(v0 + j);
                 }
             }
@@ -601,7 +632,7 @@ struct Slice {
                 const uint32_t key = __reduce_max_sync(0xffffffffu, key_of(top == top ? top : -INFINITY));
                 most = max(most, key);
                 if (it + u < kTurns && lane == 0) turn_key[it + u] = key;
-                if (it + u < staged_iters) stage[32 * (it + u)] = r[u];
+                if (it + u < staged_iters) V::put(stage + 32 * kLane * (it + u), r[u]);
             }
         }
         __syncwarp();
@@ -610,8 +641,13 @@ struct Slice {
     }
 
     __device__ __forceinline__ bool has(unsigned int j) const { return j < count; }
-    __device__ __forceinline__ uint4 turn(unsigned int it, unsigned int j) const {
-        return it < staged_iters ? stage[32 * it] : load(v0 + j);
+    static __device__ __forceinline__ Raw fill() {
+        const uint4 four = make_uint4(V::kFill, V::kFill, V::kFill, V::kFill);
+        if constexpr (kLane == 2) return {four, four};
+        else return four;
+    }
+    __device__ __forceinline__ Raw turn(unsigned int it, unsigned int j) const {
+        return it < staged_iters ? V::get(stage + 32 * kLane * it) : load(v0 + j);
     }
 
     // f(vector, its number) for this lane's vectors, in ascending order, in
@@ -642,13 +678,13 @@ struct Slice {
             return ++past;
         };
         unsigned int it = take();
-        uint4 ahead = make_uint4(0, 0, 0, 0);
+        Raw ahead = {};
         if (it >= staged_iters && has(32 * it + lane)) ahead = load(v0 + 32 * it + lane);
 #pragma unroll 1
         while (has(32 * it + lane)) {
             const unsigned int v = v0 + 32 * it + lane;
-            uint4 r = ahead;
-            if (it < staged_iters) r = stage[32 * it];
+            Raw r = ahead;
+            if (it < staged_iters) r = V::get(stage + 32 * kLane * it);
             it = take();
             if (it >= staged_iters && has(32 * it + lane)) ahead = load(v0 + 32 * it + lane);
             f(r, v);
@@ -662,7 +698,7 @@ struct Slice {
         Slice s = *this;
         s.v0 += by * (int)per_warp;
         s.count = s.v0 < nv ? min(per_warp, nv - s.v0) : 0u;
-        s.stage += by * 32 * (int)staged_iters;
+        s.stage += by * 32 * kLane * (int)staged_iters;
         return s;
     }
 };
@@ -777,9 +813,42 @@ __device__ __noinline__ u64 block_select(uint32_t n, bool by_index, u64 target, 
     }
 }
 
+// (float)((double)q / (double)total), 1 <= q <= total <= 2^53, q <= 2^31, in
+// integers: the double division takes 0.45 us at every row's end. From a quotient
+// a few units off, the one rounded down (in `units` of the last place) and what
+// is left of it; a remainder that a double would round to half a unit is a tie.
+__device__ __forceinline__ float quotient(u64 q, u64 total) {
+    const uint32_t near = __float_as_uint(__fdividef(__ull2float_rn(q), __ull2float_rn(total)));
+    int exponent = (int)(near >> 23) - 127;
+    u64 units = (near & 0x7fffffu) | 0x800000u;
+    const int shift = 23 - exponent;
+    long long left = (long long)((shift < 64 ? q << shift : 0ull) - units * total);  // modulo 2^64: it is small
+#pragma unroll 1
+    for (; left < 0; left += total) --units;
+#pragma unroll 1
+    for (; left >= (long long)total; left -= total) ++units;
+    if (units < 1u << 23) {  // the quotient lies below a power of two, the one near it does not
+        left *= 2;
+        units *= 2;
+        --exponent;
+        if (left >= (long long)total) {
+            left -= total;
+            ++units;
+        }
+    } else if (units >= 1u << 24) {
+        left += units & 1 ? total : 0ull;
+        total *= 2;
+        units /= 2;
+        ++exponent;
+    }
+    const u64 twice = 2 * (u64)left, apart = twice > total ? twice - total : total - twice;
+    const bool up = apart <= total >> 29 ? units & 1 : twice > total;
+    return __uint_as_float(((uint32_t)(exponent + 127) << 23) + (uint32_t)(units - (1u << 23)) + up);
+}
+
 __device__ __noinline__ void write_token(RowEnd end, uint32_t index, u64 q, u64 total) {
     *end.token = (int32_t)index;
-    if (end.prob) *end.prob = (float)((double)q / (double)total);
+    if (end.prob) *end.prob = quotient(q, total);
 }
 
 __device__ __forceinline__ u64 draw_of(uint32_t word, u64 total) { return __umul64hi((u64)word << 32, total); }
@@ -813,7 +882,7 @@ __device__ __noinline__ u64 slot_total(Slot slot, uint32_t blocks, int word = 0)
 // The weights of a vector's logits up to `last`, 0 for the others, for a
 // finite m and scale.
 template <typename T>
-__device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const uint4 &r, unsigned int v,
+__device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const typename Vec<T>::Raw &r, unsigned int v,
                                             const Weigher<T> &weigh, uint32_t qmin, u64 last,
                                             uint32_t (&q)[Vec<T>::N]) {
     float x[Vec<T>::N], y[Vec<T>::N];
@@ -997,7 +1066,7 @@ __device__ __noinline__ void collect(Slice<T> sl, unsigned int per_warp, float t
     using V = Vec<T>;
     const int warp = threadIdx.x >> 5;
     thr = fmaxf(thr, -3.402823466e38f);  // the least finite logit
-    auto take = [&](const uint4 &r, unsigned int v) {
+    auto take = [&](const auto &r, unsigned int v) {
         float x[V::N];
         V::unpack(r, x);
         each_of<V::N>(x, [&](float xe) { return xe >= thr && xe <= cap; },
@@ -1005,7 +1074,7 @@ __device__ __noinline__ void collect(Slice<T> sl, unsigned int per_warp, float t
     };
     const typename V::Bound lo = V::from(thr), hi = V::upto(cap);
     if (per_warp <= 64) {
-        sl.each(thr, [&](const uint4 &r, unsigned int v) {
+        sl.each(thr, [&](const auto &r, unsigned int v) {
             if (V::any_in(r, lo, hi)) take(r, v);
         });
         __syncthreads();
@@ -1014,7 +1083,7 @@ __device__ __noinline__ void collect(Slice<T> sl, unsigned int per_warp, float t
     __syncthreads();
     if (threadIdx.x == 0) sh.n_hits = 0;
     __syncthreads();
-    sl.each(thr, [&](const uint4 &r, unsigned int v) {
+    sl.each(thr, [&](const auto &r, unsigned int v) {
         if (!V::any_in(r, lo, hi)) return;
         const uint32_t at = atomicAdd(&sh.n_hits, 1u);
         if (at < kHits) sh.hits[at] = (uint32_t)warp << 16 | (v - sl.v0);
@@ -1025,8 +1094,9 @@ __device__ __noinline__ void collect(Slice<T> sl, unsigned int per_warp, float t
         const int by = (int)(sh.hits[i] >> 16) - warp;
         const unsigned int j = sh.hits[i] & 0xffffu, it = j / 32;
         const unsigned int v = sl.v0 + by * (int)per_warp + j;
-        const uint4 *stage = sl.stage + by * 32 * (int)sl.staged_iters + (int)(j % 32) - (int)(threadIdx.x % 32);
-        take(it < sl.staged_iters ? stage[32 * it] : sl.load(v), v);
+        const uint4 *stage = sl.stage + by * 32 * sl.kLane * (int)sl.staged_iters;
+        stage += (int)(j % 32) - (int)(threadIdx.x % 32);
+        take(it < sl.staged_iters ? V::get(stage + 32 * sl.kLane * it) : sl.load(v), v);
     }
     __syncthreads();
     if (threadIdx.x == 0 && sh.n_hits > kHits) sh.n_list = kLocal + 1;  // too many
@@ -1132,7 +1202,7 @@ __device__ __noinline__ u64 nth_tie(Slice<T> sl, uint32_t tau, u64 nth, Slot tie
                                     Slot at_slot) {
     SampleShared &sh = block_shared();
     const int lane = threadIdx.x & 31;
-    auto tied = [&](const uint4 &r, unsigned int v) {  // by element
+    auto tied = [&](const auto &r, unsigned int v) {  // by element
         float x[Vec<T>::N];
         Vec<T>::unpack(r, x);
         unsigned int t = 0;
@@ -1144,7 +1214,7 @@ __device__ __noinline__ u64 nth_tie(Slice<T> sl, uint32_t tau, u64 nth, Slot tie
         return t;
     };
     u64 mine = 0;
-    sl.each(key_logit(tau), [&](const uint4 &r, unsigned int v) { mine += __popc(tied(r, v)); });
+    sl.each(key_logit(tau), [&](const auto &r, unsigned int v) { mine += __popc(tied(r, v)); });
     mine = warp_total(mine);
     if (threadIdx.x == 0) sh.cast[0] = ~0ull;
     u64 before = block_before(lane == 0 ? mine : 0ull);  // of lane 0: the warps' before
@@ -1201,7 +1271,7 @@ __device__ __noinline__ u64 select_in_bin(Slice<T> sl, RowRule rule, const Cross
         __syncthreads();
         hist.clear();
         __syncthreads();
-        sl.each(c.thr, [&](const uint4 &r, unsigned int v) {
+        sl.each(c.thr, [&](const auto &r, unsigned int v) {
             if (!(Vec<T>::max(r) >= c.thr)) return;
             float x[Vec<T>::N];
             Vec<T>::unpack(r, x);
@@ -1242,7 +1312,7 @@ __device__ __noinline__ void weigh_and_draw(Slice<T> sl, RowRule rule, u64 last,
     using V = Vec<T>;
     const Weigher<T> weigh(rule);
     u64 mass = 0;
-    sl.each(__fsub_rd(rule.m, 31.5f * __frcp_rn(rule.scale)), [&](const uint4 &r, unsigned int v) {
+    sl.each(__fsub_rd(rule.m, 31.5f * __frcp_rn(rule.scale)), [&](const auto &r, unsigned int v) {
         uint32_t q[V::N];
         mass += kept_weights(sl, r, v, weigh, rule.qmin, last, q);
     });
@@ -1257,7 +1327,7 @@ __device__ __noinline__ void weigh_and_draw(Slice<T> sl, RowRule rule, u64 last,
 // which the filter ends.
 template <bool COUNT, typename T>
 __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float p, u64 limit,
-                                    RowEnd end, u64 *last) {
+                                    RowEnd end, u64 *last, bool clean) {
     SampleShared &sh = block_shared();
     using V = Vec<T>;
     const uint32_t rank = cluster_rank(), blocks = cluster_size();
@@ -1270,11 +1340,13 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
     Crossing c;
     c.limit = limit;
     c.floor_q = COUNT ? 1u : min_p ? rule.qmin : max(exp2_weight(cut_y), 1u);
-    __syncthreads();
-    sh.bins[0].clear();
-    sh.bins[1].clear();
-    if (threadIdx.x == 0) sh.n_list = 0;
-    __syncthreads();
+    if (!clean) {
+        __syncthreads();
+        sh.bins[0].clear();
+        sh.bins[1].clear();
+        if (threadIdx.x == 0) sh.n_list = 0;
+        __syncthreads();
+    }
     SumBins<kBins> &bins = sh.bins[warp / (kSWarps / 2)];
     const Weigher<T> weigh(rule);
     const float octave = __frcp_rn(rule.scale);  // the bounds below leave room for its rounding
@@ -1282,7 +1354,7 @@ __device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float
     const bool limited = limit != kKeepAll;
     const float limit_x = limited ? key_logit(~(uint32_t)(limit >> 32)) : -INFINITY;
     u64 mass = 0;
-    sl.each(zero, [&](const uint4 &r, unsigned int v) {
+    sl.each(zero, [&](const auto &r, unsigned int v) {
         float x[V::N], y[V::N];
         if constexpr (COUNT) {
             V::unpack(r, x);
@@ -1453,7 +1525,7 @@ template <typename T>
 __device__ __noinline__ void sample_largest(Slice<T> sl, uint32_t row_key, uint32_t k, float p,
                                             RowEnd end) {
     u64 ties = 0;
-    sl.each(key_logit(row_key), [&](const uint4 &r, unsigned int) {
+    sl.each(key_logit(row_key), [&](const auto &r, unsigned int) {
         float x[Vec<T>::N];
         Vec<T>::unpack(r, x);
 #pragma unroll
@@ -1483,14 +1555,15 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     Slice<T> sl;
     {
         const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const T *>(a.logits) + row * a.row_stride);
-        sl.base = reinterpret_cast<const char *>(at & ~(uintptr_t)15);
-        sl.pad = (unsigned int)(at & 15) / sizeof(T);
+        constexpr uintptr_t within = sizeof(typename V::Raw) - 1;
+        sl.base = reinterpret_cast<const char *>(at & ~within);
+        sl.pad = (unsigned int)(at & within) / sizeof(T);
         sl.n = (unsigned int)a.vocab;
         const unsigned int nv = (sl.pad + sl.n + V::N - 1) / V::N;
         sl.staged_iters = a.staged_iters;
         sl.v0 = (rank * kSWarps + warp) * a.per_warp;
         sl.count = sl.v0 < nv ? min(a.per_warp, nv - sl.v0) : 0u;
-        sl.stage = reinterpret_cast<uint4 *>(&sh + 1) + warp * 32 * a.staged_iters + lane;
+        sl.stage = reinterpret_cast<uint4 *>(&sh + 1) + warp * 32 * sl.kLane * a.staged_iters + lane;
     }
     const float t = a.temperature ? a.temperature[row] : 1.0f;
     const int k_arg = a.top_k ? a.top_k[row] : 0;
@@ -1512,6 +1585,10 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     if (by_groups && group < 32) {
         group_key = thread_key;
         for (uint32_t d = 1; d < group; d *= 2) group_key = max(group_key, __shfl_xor_sync(0xffffffffu, group_key, d));
+    }
+    if ((k > 0 || cut_p) && !bounded) {  // a histogram comes first
+        sh.bins[0].clear();
+        sh.bins[1].clear();
     }
     cluster_wait();
     uint32_t *maxima = reinterpret_cast<uint32_t *>(sh.items + kLocal);  // of all the row's groups
@@ -1541,7 +1618,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
     if (!(t > 0.0f)) {  // the first of the largest
         uint32_t first = 0xffffffffu;
         if (warp_key == row_key)
-            sl.each(rule.m, [&](const uint4 &r, unsigned int v) {
+            sl.each(rule.m, [&](const auto &r, unsigned int v) {
                 if (first != 0xffffffffu || !(V::max(r) >= rule.m)) return;
                 float x[V::N];
                 V::unpack(r, x);
@@ -1575,10 +1652,10 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
         }
     }
     u64 last = kKeepAll;
-    if (k > 0 && filter<true>(sl, rule, k, p, kKeepAll, end, &last)) return;
+    if (k > 0 && filter<true>(sl, rule, k, p, kKeepAll, end, &last, !bounded)) return;
     if (cut_p) {
         u64 cut;
-        filter<false>(sl, rule, k, p, last, end, &cut);
+        filter<false>(sl, rule, k, p, last, end, &cut, k == 0);
         return;
     }
     weigh_and_draw(sl, rule, last, end);
@@ -1593,14 +1670,13 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
 #define U32SCAN_SAMPLE_BLOCKS 0
 #endif
 
-// Turns of 32 vectors a warp keeps in shared memory: two blocks an SM.
-constexpr unsigned int kStageBytes = kSWarps * 32 * 16;
-constexpr unsigned int kMaxStaged = 8;
+// Bytes of a row a block keeps in shared memory: two blocks an SM.
+constexpr unsigned int kMaxStage = 64 * 1024;
 constexpr unsigned int kResident = 304;  // blocks at a time: two on each of 152 SMs
 static_assert(sizeof(SampleShared) % 16 == 0 && offsetof(SampleShared, slots) % 16 == 0 && kLocal % 2 == 0,
               "16-byte accesses");
-static_assert(U32SCAN_MAX_VOCAB / 4 / kMaxCluster / kSWarps + 8 < 65536, "a warp's vectors in 16 bits");
-static_assert(2 * (sizeof(SampleShared) + kMaxStaged * kStageBytes + 1024) <= 228 * 1024, "two blocks an SM");
+static_assert(U32SCAN_MAX_VOCAB / 8 / kMaxCluster / kSWarps + 8 < 65536, "a warp's vectors in 16 bits");
+static_assert(2 * (sizeof(SampleShared) + kMaxStage + 1024) <= 228 * 1024, "two blocks an SM");
 
 template <typename T>
 static int sample_launch(SampleArgs a, cudaStream_t stream) {
@@ -1609,7 +1685,8 @@ static int sample_launch(SampleArgs a, cudaStream_t stream) {
     // serial steps less often, more and smaller ones share a long row's passes: 256 x 262144 f32 mixed
     // takes 182, 139, 149 us with 2, 4, 8 blocks a row, 64 x 131072 bf16 top-p 54, 46, 62, 256 x 32000
     // bf16 top-p 45, 55, 80 with 1, 2, 4, one row of 128000 under top-p 78, 46, 30, 24 with 1, 2, 4, 8.
-    const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 && a.row_stride % Vec<T>::N == 0;
+    constexpr unsigned int vec_bytes = sizeof(typename Vec<T>::Raw);
+    const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % vec_bytes == 0 && a.row_stride % Vec<T>::N == 0;
     const unsigned int nv = (unsigned int)((a.vocab + (aligned ? 1 : 2) * (Vec<T>::N - 1)) / Vec<T>::N);
     unsigned int blocks = 1;
     while (blocks < kMaxCluster &&
@@ -1621,10 +1698,11 @@ static int sample_launch(SampleArgs a, cudaStream_t stream) {
     const unsigned int per_block = (nv + blocks - 1) / blocks;
     a.per_warp = ((per_block + kSWarps - 1) / kSWarps + 7) / 8 * 8;
     const unsigned int iters = (a.per_warp + 31) / 32;
-    a.staged_iters = iters < kMaxStaged ? iters : kMaxStaged;
-    const size_t smem = sizeof(SampleShared) + (size_t)a.staged_iters * kStageBytes;
+    constexpr unsigned int turn_bytes = kSThreads * vec_bytes;
+    a.staged_iters = iters < kMaxStage / turn_bytes ? iters : kMaxStage / turn_bytes;
+    const size_t smem = sizeof(SampleShared) + (size_t)a.staged_iters * turn_bytes;
     if (cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(sizeof(SampleShared) + kMaxStaged * kStageBytes)) != cudaSuccess)
+                             (int)(sizeof(SampleShared) + kMaxStage)) != cudaSuccess)
         return U32SCAN_ECUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned int)a.rows * blocks);
