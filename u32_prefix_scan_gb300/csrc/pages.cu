@@ -27,7 +27,7 @@
 // Measured on one GB300, launches back to back: copying 509 pages of 64 x 32
 // KiB 312 us (2.1 GB read and written, 6.8 TB/s, the rate of a plain copy),
 // packing 65537 half-live pages of 2 x 16 KiB 165 us (1.06 GB, 6.4 TB/s): bound
-// by HBM. Forking 512 of 2048 rows in 262147 pages 18 us, releasing half of
+// by HBM. Forking 512 of 2048 rows in 262147 pages 16 us, releasing half of
 // 8192 rows of up to 500 pages 10 us, the same on 16 rows and 1024 pages 8 and 4 us
 // and packing those 7 us: bound by latency, the launches that wait for one
 // another and in each a chain of loads (row, entry, count).
@@ -384,6 +384,7 @@ __device__ __forceinline__ void place_fresh(const ForkArgs &a, const PagesWs &w,
 template <bool ONE>
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a, PagesWs w, u64 tiles) {
     __shared__ u64 s_warp[kPlanWarps];
+    cudaTriggerProgrammaticLaunchCompletion();  // the next launch may come to its wait
     u64 total;
     const unsigned int mask = blockIdx.x < tiles ? free_mask(a.refs, blockIdx.x, a.pages) : 0u;
     const u64 rank = block_exclusive(__popc(mask), s_warp, &total);
@@ -402,6 +403,8 @@ __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(ForkArgs a, Pag
 
 __global__ void __launch_bounds__(kPlanThreads) fork_place_kernel(ForkArgs a, PagesWs w) {
     __shared__ u64 s_warp[kPlanWarps];
+    cudaTriggerProgrammaticLaunchCompletion();  // the next launch may come to its wait
+    cudaGridDependencySynchronize();  // what the launch before wrote
     const u64 base = w.tile_base[blockIdx.x], taken = w.ctrl->taken;
     if (base >= taken) return;
     const unsigned int mask = free_mask(a.refs, blockIdx.x, a.pages);
@@ -421,6 +424,7 @@ __device__ __forceinline__ u64 row_begin(const PagesWs &w, u64 s) { return s ? w
 // kEntryChunk entries of a row), and the bytes of the partly filled pages.
 __global__ void __launch_bounds__(kPThreads)
 fork_act_kernel(ForkArgs a, PagesWs w, Pool pool, unsigned int row_blocks, u64 chunks) {
+    cudaGridDependencySynchronize();  // what the launch before wrote
     const u64 free_pages = w.ctrl->free_pages;
     if (blockIdx.x >= row_blocks) {
         copy_pages(pool, w.ctrl->jobs, blockIdx.x - row_blocks, gridDim.x - row_blocks,
@@ -541,6 +545,7 @@ __device__ __forceinline__ void count_below(u64 tile, unsigned int live_mask, u6
 template <bool ONE>
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactArgs a, PagesWs w) {
     __shared__ u64 s_warp[kPlanWarps];
+    cudaTriggerProgrammaticLaunchCompletion();  // the next launch may come to its wait
     __shared__ u64 s_below;
     unsigned int mask = ~free_mask(a.refs, blockIdx.x, a.pages) & page_mask(blockIdx.x, a.pages);
     u64 total, tile = blockIdx.x;
@@ -573,6 +578,8 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(CompactArgs 
 
 __global__ void __launch_bounds__(kPlanThreads) compact_place_kernel(CompactArgs a, PagesWs w) {
     __shared__ u64 s_warp[kPlanWarps];
+    cudaTriggerProgrammaticLaunchCompletion();  // the next launch may come to its wait
+    cudaGridDependencySynchronize();  // what the launch before wrote
     const u64 live = w.ctrl->live, stay = live - w.ctrl->moved;
     const unsigned int mask = ~free_mask(a.refs, blockIdx.x, a.pages) & page_mask(blockIdx.x, a.pages);
     u64 total;
@@ -582,6 +589,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_place_kernel(CompactArgs
 
 __global__ void __launch_bounds__(kPThreads)
 compact_act_kernel(CompactArgs a, PagesWs w, Pool pool, unsigned int row_blocks, unsigned int ref_blocks) {
+    cudaGridDependencySynchronize();  // what the launch before wrote
     const u64 live = w.ctrl->live, moved = w.ctrl->moved;
     const int lane = threadIdx.x & 31;
     if (blockIdx.x < row_blocks) {  // table entries
@@ -634,6 +642,23 @@ static int sm_count(int *sms) {
 }
 
 static int launched() { return cudaGetLastError() == cudaSuccess ? U32SCAN_OK : U32SCAN_ECUDA; }
+
+// A launch that may be set up while the one before it in the stream (of the
+// same call) still runs, and waits for its end before it reads anything
+// (forking 16 rows 8.2 and 7.7 us, of 2048 rows 16.8 and 16.0).
+template <typename... P, typename... A>
+static void launch_next(void (*kernel)(P...), unsigned int grid, int threads, cudaStream_t s, A... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned int)threads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, P(args)...);  // launched() sees its error
+}
 
 static bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
 
@@ -723,11 +748,11 @@ extern "C" int pages_fork(int32_t *table, size_t table_stride, size_t rows, size
         fork_plan_kernel<true><<<1, kPlanThreads, 0, s>>>(a, w, tiles);
     } else {
         fork_plan_kernel<false><<<(unsigned int)(tiles ? tiles : 1), kPlanThreads, 0, s>>>(a, w, tiles);
-        if (tiles) fork_place_kernel<<<(unsigned int)tiles, kPlanThreads, 0, s>>>(a, w);
+        if (tiles) launch_next(fork_place_kernel, (unsigned int)tiles, kPlanThreads, s, a, w);
     }
     if (row_blocks)
-        fork_act_kernel<<<(unsigned int)row_blocks + data_blocks, kPThreads, 0, s>>>(a, w, p, (unsigned int)row_blocks,
-                                                                                   chunks);
+        launch_next(fork_act_kernel, (unsigned int)row_blocks + data_blocks, kPThreads, s, a, w, p,
+                    (unsigned int)row_blocks, chunks);
     return launched();
 }
 
@@ -772,12 +797,13 @@ extern "C" int pages_compact(const u32scan_page_pool *pool, int32_t *table, size
         compact_plan_kernel<true><<<1, kPlanThreads, 0, s>>>(a, w);
     } else {
         compact_plan_kernel<false><<<tiles, kPlanThreads, 0, s>>>(a, w);
-        compact_place_kernel<<<tiles, kPlanThreads, 0, s>>>(a, w);
+        launch_next(compact_place_kernel, tiles, kPlanThreads, s, a, w);
     }
     const u64 want = (rows + kPWarps - 1) / kPWarps, ref_want = (pages / 2 + kPThreads - 1) / kPThreads;
     const unsigned int row_blocks = (unsigned int)(want < (u64)sms ? want : (u64)sms);
     const unsigned int ref_blocks = (unsigned int)(ref_want < (u64)sms ? (ref_want ? ref_want : 1) : (u64)sms);
     const unsigned int data_blocks = p.n_planes ? copy_grid(pages / 2 * units_per_pair(p), sms) : 0u;
-    compact_act_kernel<<<row_blocks + ref_blocks + data_blocks, kPThreads, 0, s>>>(a, w, p, row_blocks, ref_blocks);
+    launch_next(compact_act_kernel, row_blocks + ref_blocks + data_blocks, kPThreads, s, a, w, p, row_blocks,
+                ref_blocks);
     return launched();
 }
