@@ -39,6 +39,11 @@
 // A filter ends at an item, (~key, index) as one u64: what stands at or
 // before it in order stays, so ties need no count of their own.
 //
+// What every row runs is in line, from the first reading to the draw: a call
+// spills the slice and the rule that stay in registers otherwise (256 x 131072
+// f32 under top-p 137 us with calls, 119 without; 64 x 131072 bf16 38.6, 35.4).
+// Only what few rows need (long ties, rows' ends) and the selections are calls.
+//
 // Measured on one GB300, launches back to back: a row of 32000 bf16 under
 // top-k and top-p 9 us; 7 x 50257 f32 greedy 4, without filters 8, under top-k
 // 50 9.5, under top-p 13 (peaked) to 17 (flat); 64 x 131072 bf16 without
@@ -510,7 +515,7 @@ __device__ __forceinline__ u64 of_warps(u64 v, int which, u64 none) {
 }
 
 // The sum over the block, in every thread.
-__device__ __noinline__ u64 block_total(u64 v) { return warp_total(of_warps(warp_total(v), 0, 0ull)); }
+__device__ __forceinline__ u64 block_total(u64 v) { return warp_total(of_warps(warp_total(v), 0, 0ull)); }
 
 // The same of several values at once.
 template <int K>
@@ -529,17 +534,17 @@ __device__ __forceinline__ void block_totals(u64 (&v)[K]) {
 }
 
 // The sum over the threads before this one.
-__device__ __noinline__ u64 block_before(u64 v) {
+__device__ __forceinline__ u64 block_before(u64 v) {
     const u64 inc = warp_inclusive(v);
     const u64 warps = of_warps(__shfl_sync(0xffffffffu, inc, 31), 1, 0ull);
     return warp_total((threadIdx.x & 31) < (threadIdx.x >> 5) ? warps : 0ull) + inc - v;
 }
 
 // The least over the block, in every thread.
-__device__ __noinline__ u64 block_min(u64 v) { return warp_min(of_warps(warp_min(v), 2, ~0ull)); }
+__device__ __forceinline__ u64 block_min(u64 v) { return warp_min(of_warps(warp_min(v), 2, ~0ull)); }
 
 // The least lo and the greatest hi over the block, in every thread.
-__device__ __noinline__ void block_range(u64 &lo, u64 &hi) {
+__device__ __forceinline__ void block_range(u64 &lo, u64 &hi) {
     SampleShared &sh = block_shared();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     lo = warp_min(lo);
@@ -706,7 +711,7 @@ struct Slice {
 
 // A logit's place in the filters' order, ascending.
 __device__ __forceinline__ u64 item_of(uint32_t key, uint32_t index) { return (u64)~key << 32 | index; }
-__device__ __noinline__ uint32_t item_weight(u64 item, RowRule rule) {
+__device__ __forceinline__ uint32_t item_weight(u64 item, RowRule rule) {
     return token_weight(key_logit(~(uint32_t)(item >> 32)), rule);
 }
 constexpr u64 kKeepAll = ~0ull;
@@ -847,7 +852,7 @@ __device__ __forceinline__ float quotient(u64 q, u64 total) {
     return __uint_as_float(((uint32_t)(exponent + 127) << 23) + (uint32_t)(units - (1u << 23)) + up);
 }
 
-__device__ __noinline__ void write_token(RowEnd end, uint32_t index, u64 q, u64 total) {
+__device__ __forceinline__ void write_token(RowEnd end, uint32_t index, u64 q, u64 total) {
     *end.token = (int32_t)index;
     if (end.prob) *end.prob = quotient(q, total);
 }
@@ -874,7 +879,7 @@ __device__ __forceinline__ u64 top_p_target(float p, u64 total) {
 }
 
 // The sum of what the first `blocks` blocks put into a slot.
-__device__ __noinline__ u64 slot_total(Slot slot, uint32_t blocks, int word = 0) {
+__device__ __forceinline__ u64 slot_total(Slot slot, uint32_t blocks, int word = 0) {
     SampleShared &sh = block_shared();
     const uint32_t lane = threadIdx.x & 31;
     return warp_total(lane < blocks ? sh.slots[slot][lane][word] : 0ull);
@@ -907,7 +912,7 @@ __device__ __forceinline__ u64 kept_weights(const Slice<T> &sl, const typename V
 // what its i-th group of `group` warps does. It weighs the group with the draw
 // again, a turn of 32 vectors a warp, and walks the turn with the draw.
 template <typename T>
-__device__ __noinline__ void draw(Slice<T> own, RowRule rule, u64 last, u64 total, u64 before, u64 mass,
+__device__ __forceinline__ void draw(Slice<T> own, RowRule rule, u64 last, u64 total, u64 before, u64 mass,
                                   unsigned int group, RowEnd end) {
     SampleShared &sh = block_shared();
     constexpr int N = Vec<T>::N;
@@ -1059,10 +1064,10 @@ __device__ __forceinline__ void each_of(const float (&x)[N], Test test, F f) {
 // list. In a long slice first the vectors that hold one (few, and a few
 // instructions each, where taking such a vector apart would stop its whole
 // warp), then, a thread a vector, the logits: 64 x 131072 bf16 under top-p
-// 43 us, 45 with all at once. In a short slice, up to 64 vectors a warp, all
-// at once: a row of 32000 bf16 under top-k 11.2 us, 11.7 in two steps.
+// 38.7 us, 40.2 with all at once. In a short slice, up to 64 vectors a warp,
+// all at once: a row of 32000 bf16 under top-k 8.6 us, 9.0 in two steps.
 template <typename T>
-__device__ __noinline__ void collect(Slice<T> sl, unsigned int per_warp, float thr, float cap) {
+__device__ __forceinline__ void collect(Slice<T> sl, unsigned int per_warp, float thr, float cap) {
     SampleShared &sh = block_shared();
     using V = Vec<T>;
     const int warp = threadIdx.x >> 5;
@@ -1327,7 +1332,7 @@ __device__ __noinline__ void weigh_and_draw(Slice<T> sl, RowRule rule, u64 last,
 // the row's token is written (top-p: always), else *last is the item at
 // which the filter ends.
 template <bool COUNT, typename T>
-__device__ __noinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float p, u64 limit,
+__device__ __forceinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, float p, u64 limit,
                                     RowEnd end, u64 *last, bool clean) {
     SampleShared &sh = block_shared();
     using V = Vec<T>;
