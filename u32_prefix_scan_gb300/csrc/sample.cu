@@ -45,15 +45,15 @@
 // Only what few rows need (long ties, rows' ends) and the selections are calls.
 //
 // Measured on one GB300, launches back to back: a row of 32000 bf16 under
-// top-k and top-p 9 us; 7 x 50257 f32 greedy 4, without filters 8, under top-k
-// 50 9.5, under top-p 13 (peaked) to 17 (flat); 64 x 131072 bf16 without
-// filters 17, under top-p 39; 256 x 262144 f32, a fifth of the rows greedy, most
-// others under top-k, top-p or both, 125 (268 MB: 2.1 TB/s, where reading alone
-// takes 40; DRAM 31 % busy). What bounds it is issue and latency, not reading: a
+// top-k and top-p 8 us; 7 x 50257 f32 greedy 4, without filters 7, under top-k
+// 50 9, under top-p 12 (peaked) to 16 (flat); 64 x 131072 bf16 without
+// filters 16, under top-p 35; 256 x 262144 f32, a fifth of the rows greedy, most
+// others under top-k, top-p or both, 112 (268 MB: 2.4 TB/s, where reading alone
+// takes 40; DRAM 30 % busy). What bounds it is issue and latency, not reading: a
 // logit's weight is 15 f32 operations that round one by one, and some 30
 // instructions with its place in the histogram (3.6 logits a clock and SM);
 // around that are short steps between barriers, a cluster's 500 clocks or more
-// each. Instructions are issued in 47 % of the cycles under top-p (35 % for
+// each. Instructions are issued in 50 % of the cycles under top-p (39 % for
 // the 256 rows, whose rows of unequal work also leave SMs idle at the end). Two
 // blocks of 16 warps an SM, 64 registers a thread: while one waits at a barrier
 // the other weighs.
@@ -1689,8 +1689,8 @@ static int sample_launch(SampleArgs a, cudaStream_t stream) {
     // The largest cluster with which all rows run at a time, a thread still having a vector, and
     // slices of at most 65536 logits. Fewer and larger slices pay the barriers and the
     // serial steps less often, more and smaller ones share a long row's passes: 256 x 262144 f32 mixed
-    // takes 176, 134, 144 us with 2, 4, 8 blocks a row, 64 x 131072 bf16 top-p 42, 38, 50, 256 x 32000
-    // bf16 top-p 35, 41, 60 with 1, 2, 4, 7 x 50257 f32 top-p 45, 29, 22, 18 with 1, 2, 4, 8.
+    // takes 132, 112, 125 us with 2, 4, 8 blocks a row, 64 x 131072 bf16 top-p 38, 35, 46, 256 x 32000
+    // bf16 top-p 32, 38, 53 with 1, 2, 4, 7 x 50257 f32 top-p 34, 24, 19, 16 with 1, 2, 4, 8.
     constexpr unsigned int vec_bytes = sizeof(typename Vec<T>::Raw);
     const bool aligned = reinterpret_cast<uintptr_t>(a.logits) % vec_bytes == 0 && a.row_stride % Vec<T>::N == 0;
     const unsigned int nv = (unsigned int)((a.vocab + (aligned ? 1 : 2) * (Vec<T>::N - 1)) / Vec<T>::N);
