@@ -333,3 +333,26 @@ def test_every_size_of_top_p_and_min_p(u, n):
     words = inputs.splitmix_u32(24, 0, 64)
     check(u, x, "f32", words, dict(top_p=p))
     check(u, x, "f32", words, dict(min_p=p, top_p=p[::-1].copy()))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [5003, 40001, 300007])
+def test_ties_that_most_warps_do_not_hold(u, n, dtype):
+    """Cuts among long ties that lie in the middle or at the end of the row,
+    all else far below: the warps without one are done with the search for
+    the tie at once, while the others still read its key."""
+    rows = 24
+    rng = np.random.default_rng(n)
+    x = np.full((rows, n), -90.0, np.float32)
+    for b in range(rows):
+        first = (n // 2, n - 2400)[b % 2]
+        x[b, first : first + 2400] = 7.25 + 0.5 * (b % 3)  # positive: their keys' last digits are zero
+    words = inputs.splitmix_u32(25, 0, rows)
+    k = rng.choice([2, 40, 1000, 2047, 2399], rows).astype(np.int32)
+    dev, held = as_type(x, dtype)
+    for params in (dict(top_k=k), dict(top_p=rng.choice([0.01, 0.5, 0.999], rows).astype(np.float32)),
+                   dict(top_k=k, top_p=np.full(rows, 0.6, np.float32))):
+        want = oracle.sample_tokens(held, words, **params)
+        for _ in range(20):
+            got = run(u, dev, words, params)
+            assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])

@@ -1222,9 +1222,11 @@ __device__ __noinline__ u64 nth_tie(Slice<T> sl, uint32_t tau, u64 nth, Slot tie
     u64 mine = 0;
     sl.each(key_logit(tau), [&](const auto &r, unsigned int v) { mine += __popc(tied(r, v)); });
     mine = warp_total(mine);
-    if (threadIdx.x == 0) sh.cast[0] = ~0ull;
     u64 before = block_before(lane == 0 ? mine : 0ull);  // of lane 0: the warps' before
     before = __shfl_sync(0xffffffffu, before, 0);
+    // past block_before's barriers every thread has read what the caller left in cast, and the
+    // exchange's barrier comes before the tie is written
+    if (threadIdx.x == 0) sh.cast[0] = ~0ull;
     exchange(ties_slot, block_total(lane == 0 ? mine : 0ull), 0);
     before += slot_total(ties_slot, cluster_rank());
     if (before < nth && nth <= before + mine)  // this warp's
