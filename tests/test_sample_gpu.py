@@ -356,3 +356,36 @@ def test_ties_that_most_warps_do_not_hold(u, n, dtype):
         for _ in range(20):
             got = run(u, dev, words, params)
             assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("scale", [1, 2])
+@pytest.mark.parametrize("n,near", [(5003, 1), (40001, 38001), (100003, 700), (3001, 1500)])
+def test_weights_last_octave(u, n, near, scale, dtype):
+    """Logits whose distance is 31 exactly weigh 1, those past it nothing:
+    `near` logits weigh more, the rest 1 or nothing, and top-k ends before, at
+    and after the last of the heavy ones. With a temperature of log2 e (or half
+    of it) the scale is exactly 1 (or 2). Words at both ends of the range, where
+    the lightest tokens are drawn."""
+    t = np.float32(float.fromhex("0x1.715476p+0") / scale)
+    words = np.array([0, 1, 2, 38, 39, 1 << 31, 2**32 - 40, 2**32 - 2, 2**32 - 1], dtype=np.uint32)
+    last = np.float32(-31.0 / scale)
+    below, above = np.nextafter(last, np.float32(-99)), np.nextafter(last, np.float32(0))
+    x = np.full((4, n), last, np.float32)
+    x[1, n // 2 :] = below
+    x[2, ::2] = above
+    x[3, ::3], x[3, 1::3] = above, below
+    rng = np.random.default_rng(n)
+    for b, kind in enumerate(("front", "back", "apart", "apart")):
+        at = {"front": np.arange(near), "back": np.arange(n - near, n), "apart": rng.permutation(n)[:near]}[kind]
+        x[b, at] = 0.0
+    x = np.repeat(x, words.size, 0)
+    words = np.tile(words, 4)
+    rows = words.size
+    ks = [40, near, near + 1, min(n - 1, 3000), n - 1]
+    for k in ks:
+        k = np.full(rows, k, np.int32)
+        filters = dict(temperature=np.full(rows, t), top_k=k)
+        check(u, x, dtype, words, filters)
+        check(u, x, dtype, words, dict(filters, top_p=np.full(rows, 0.9999999, np.float32)))
+        check(u, x, dtype, words, dict(filters, min_p=np.full(rows, 2.0**-31, np.float32)))

@@ -304,7 +304,7 @@ struct Vec<__half> : Vec16 {
     }
 };
 
-// floor(2^31 * 2^-y) for 0 <= y < 100 (0 from y = 31 on): 2^-n exactly, times
+// floor(2^31 * 2^-y) for 0 <= y < 100 (1 at y = 31, 0 past it): 2^-n exactly, times
 // 2^-f on [-1/2, 1/2] by a degree-5 polynomial with constant term 1 (a minimax
 // fit in relative error, 1.9e-7 in f32). Every operation is rounded alone (no
 // contraction); the coefficients carry the factor 2^31, which changes no
@@ -1250,7 +1250,7 @@ __device__ __noinline__ u64 nth_tie(Slice<T> sl, uint32_t tau, u64 nth, Slot tie
 // The histogram bin in which a filter ends, and what lies in it.
 struct Crossing {
     uint32_t bin;
-    uint32_t floor_q;  // the least weight in the histogram (counts: 1, as far as y < 31)
+    uint32_t floor_q;  // the least weight in the histogram (counts: all that weigh, y <= 31)
     float thr, cap;    // every logit of the bin is in [thr, cap], few others are
     u64 limit;         // items past it do not count
     bool upto;         // the bins before it too
@@ -1260,7 +1260,7 @@ struct Crossing {
 template <bool COUNT>
 __device__ __forceinline__ bool in_crossing(const Crossing &c, RowRule rule, float x, u64 item) {
     const float y = __fmul_rn(__fsub_rn(rule.m, x), rule.scale);
-    if (!(y < (COUNT ? 31.0f : 32.0f))) return false;
+    if (!(y <= 31.0f)) return false;  // it weighs nothing
     const uint32_t b = bin_of(y);
     return (c.upto ? b <= c.bin : b == c.bin) && (COUNT || (exp2_weight(y) >= c.floor_q && item <= c.limit));
 }
@@ -1369,8 +1369,8 @@ __device__ __forceinline__ bool filter(Slice<T> sl, RowRule rule, uint32_t k, fl
 #pragma unroll
             for (int e = 0; e < V::N; e += 2) {
                 unpack2(mul2(sub2(weigh.m2, pack2(x[e], x[e + 1])), weigh.scale2), y[e], y[e + 1]);
-                if (y[e] < 31.0f) atomicAdd(&bins.low[bin_of(y[e])], 1u);
-                if (y[e + 1] < 31.0f) atomicAdd(&bins.low[bin_of(y[e + 1])], 1u);
+                if (y[e] <= 31.0f) atomicAdd(&bins.low[bin_of(y[e])], 1u);
+                if (y[e + 1] <= 31.0f) atomicAdd(&bins.low[bin_of(y[e + 1])], 1u);
             }
         } else {
             uint32_t q[V::N];
