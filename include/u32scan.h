@@ -648,7 +648,8 @@ int u32scan_fill_splitmix_u32(uint32_t *out, size_t n, uint32_t seed, uint32_t s
  *               double; 1 where T is not above 0, 0 where the token is -1.
  * No workspace. Errors: EINVAL (unknown type, null logits with vocab > 0,
  * null random or tokens with rows > 0, misaligned pointers, vocab above
- * U32SCAN_MAX_VOCAB, rows >= 2^28, row_stride >= 2^32), ECUDA.
+ * U32SCAN_MAX_VOCAB, rows >= 2^28, row_stride >= 2^32 with more than one
+ * row), ECUDA.
  */
 int sample_tokens(const void *logits, int type, size_t rows, size_t vocab, size_t row_stride,
                   const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,

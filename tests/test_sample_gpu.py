@@ -389,3 +389,15 @@ def test_weights_last_octave(u, n, near, scale, dtype):
         check(u, x, dtype, words, filters)
         check(u, x, dtype, words, dict(filters, top_p=np.full(rows, 0.9999999, np.float32)))
         check(u, x, dtype, words, dict(filters, min_p=np.full(rows, 2.0**-31, np.float32)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("stride", [2**32, 2**33 + 1, 2**40])
+def test_the_stride_of_one_row_is_not_used(u, stride, dtype):
+    """A view of one row may have any stride (say, one row of a wide buffer)."""
+    x = logits_for("peaked", 1, 5003, 5)
+    dev, held = as_type(x, dtype)
+    view = dev.as_strided((1, 5003), (stride, 1))
+    words, params = inputs.splitmix_u32(26, 0, 1), params_for("top_p", 1, 5)
+    got, want = run(u, view, words, params), oracle.sample_tokens(held, words, **params)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])

@@ -1734,7 +1734,8 @@ extern "C" int sample_tokens(const void *logits, int type, size_t rows, size_t v
                              const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
                              const uint32_t *random, int32_t *tokens, float *probs, u32scan_stream_t stream) {
     if (type != U32SCAN_F32 && type != U32SCAN_F16 && type != U32SCAN_BF16) return U32SCAN_EINVAL;
-    if (rows >= (1ull << 28) || vocab > U32SCAN_MAX_VOCAB || row_stride >= (1ull << 32)) return U32SCAN_EINVAL;
+    if (rows >= (1ull << 28) || vocab > U32SCAN_MAX_VOCAB) return U32SCAN_EINVAL;
+    if (rows > 1 && row_stride >= (1ull << 32)) return U32SCAN_EINVAL;  // one row's is not used
     if (rows == 0) return U32SCAN_OK;
     const uintptr_t elem = type == U32SCAN_F32 ? 3 : 1;
     if ((vocab > 0 && logits == nullptr) || random == nullptr || tokens == nullptr) return U32SCAN_EINVAL;
