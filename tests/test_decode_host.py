@@ -1,0 +1,75 @@
+"""What the decode step's Python calls do before a launch, on stand-ins for
+CUDA tensors and streams (no GPU): which device and stream they take, and
+what they refuse."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import u32_prefix_scan_gb300 as u  # noqa: E402
+from fake_device import Device, Stream  # noqa: E402
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    return Device(monkeypatch)
+
+
+class Args:
+    """The arguments of every call, on one device."""
+
+    def __init__(self, gpu, dev=0):
+        self.logits, self.words = gpu.new(4, 8, dtype=torch.float32, dev=dev), gpu.new(4, dev=dev)
+        self.table, self.lens, self.refs = gpu.new(4, 8, dev=dev), gpu.new(4, dev=dev), gpu.new(50, dev=dev)
+        self.pool = object.__new__(u.PagePool)
+        self.pool.device, self.pool.struct, self.pool.pages = torch.device("cuda", dev), None, 50
+
+    def calls(self):
+        cache = (self.table, self.lens, self.refs, 16)
+        return {
+            "sample_tokens": lambda **kw: u.sample_tokens(self.logits, self.words, **kw),
+            "pages_copy": lambda **kw: u.pages_copy(self.pool, self.lens, self.lens, **kw),
+            "pages_fork": lambda **kw: u.pages_fork(*cache, parent=self.lens, grow=self.lens, pool=self.pool, **kw),
+            "pages_free": lambda **kw: u.pages_free(*cache, self.lens, **kw),
+            "pages_compact": lambda **kw: u.pages_compact(self.pool, *cache, **kw),
+        }
+
+
+CALLS = ["sample_tokens", "pages_copy", "pages_fork", "pages_free", "pages_compact"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_take_the_current_device_and_stream(gpu, name):
+    Args(gpu).calls()[name]()
+    assert [c[0] for c in gpu.lib.calls] == [name] and gpu.lib.calls[0][1][-1] == 1000
+    Args(gpu).calls()[name](stream=Stream(77))
+    assert gpu.lib.calls[1][1][-1] == 77
+    gpu.dev, gpu.current = 1, Stream(2000, 1)
+    Args(gpu, 1).calls()[name]()
+    assert gpu.lib.calls[2][1][-1] == 2000
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_tensors_of_another_device_are_refused(gpu, name):
+    """The library launches on the current device: another's pointers would
+    fault there."""
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0 is current"):
+        Args(gpu, 1).calls()[name]()
+    with pytest.raises(ValueError, match="cuda:1.*cuda:0 is current"):
+        Args(gpu, 1).calls()[name](stream=Stream(77, 1))
+    assert gpu.lib.calls == []
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_a_stream_of_another_device_is_refused(gpu, name):
+    with pytest.raises(ValueError, match="stream must be on cuda:0"):
+        Args(gpu).calls()[name](stream=Stream(77, 1))
+    assert gpu.lib.calls == []
+
+
+@pytest.mark.parametrize("name", ["pages_fork", "pages_free", "pages_compact"])
+def test_a_workspace_of_another_device_is_refused(gpu, name):
+    Args(gpu).calls()[name](workspace=u.Workspace(4096, torch.device("cuda", 0)))
+    with pytest.raises(ValueError, match="workspace must be on cuda:0"):
+        Args(gpu).calls()[name](workspace=u.Workspace(4096, torch.device("cuda", 1)))
+    assert len(gpu.lib.calls) == 1

@@ -7,6 +7,9 @@ kernels; nothing here touches tensor data.
 
 U32 arrays are accepted as torch.int32 or torch.uint32 tensors (the bits are
 the same; wrapping u32 addition and two's-complement int32 addition agree).
+
+The library launches on the current device. sample_tokens and the pages_*
+calls refuse tensors, a stream or a workspace of another one.
 """
 
 from __future__ import annotations
@@ -64,6 +67,18 @@ def _stream_handle(stream) -> int:
     if _raw_stream is None:
         return int(torch.cuda.current_stream().cuda_stream)
     return _raw_stream(torch.cuda.current_device())
+
+
+def _launch_stream(stream, dev: int) -> int:
+    """The handle of the stream for a call on tensors of CUDA device `dev`:
+    the library launches on the current device, where another's pointers
+    would fault."""
+    current = torch.cuda.current_device()
+    if dev != current:
+        raise ValueError(f"the tensors are on cuda:{dev}, but cuda:{current} is current")
+    if stream is not None and getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"stream must be on cuda:{dev}")
+    return _stream_handle(stream)
 
 
 def _require_cuda(t: torch.Tensor, name: str, dtypes=_U32_DTYPES) -> None:
@@ -646,6 +661,7 @@ def sample_tokens(logits: torch.Tensor, random: torch.Tensor, *, temperature: to
     if step != 1 and vocab > 1 and rows > 0:
         raise ValueError("the elements of a row of logits must be adjacent")
     dev = logits.get_device()
+    sh = _launch_stream(stream, dev)
     if tokens is None:
         tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
     if probs is None:
@@ -656,7 +672,7 @@ def sample_tokens(logits: torch.Tensor, random: torch.Tensor, *, temperature: to
         logits.data_ptr(), kind, rows, vocab, row_stride, _optional(temperature, "temperature", f32, rows, dev),
         _optional(top_k, "top_k", i32, rows, dev), _optional(top_p, "top_p", f32, rows, dev),
         _optional(min_p, "min_p", f32, rows, dev), words, _arg(tokens, "tokens", i32, rows, dev),
-        _arg(probs, "probs", f32, rows, dev), _stream_handle(stream)), "sample_tokens")
+        _arg(probs, "probs", f32, rows, dev), sh), "sample_tokens")
     return tokens, probs
 
 
@@ -722,11 +738,11 @@ def pages_copy(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, count: torc
     device."""
     struct, i32 = _pool_struct(pool, pool.device.index if isinstance(pool, PagePool) else -1), torch.int32
     dev, n = pool.device.index, src.numel()
+    sh = _launch_stream(stream, dev)
     if dst.numel() != n:
         raise ValueError("src and dst differ in length")
     _native.check(_native.lib().pages_copy(struct, _arg(src, "src", i32, n, dev), _arg(dst, "dst", i32, n, dev), n,
-                                           _optional(count, "count", i32, 1, dev), _stream_handle(stream)),
-                  "pages_copy")
+                                           _optional(count, "count", i32, 1, dev), sh), "pages_copy")
 
 
 def _cache_args(table, lens, refs, page_tokens):
@@ -757,6 +773,14 @@ def _cache_args(table, lens, refs, page_tokens):
     return (table.data_ptr(), stride, rows, width, lens_ptr, refs_ptr, refs.numel(), page_tokens), dev
 
 
+def _pages_ws(args, table, dev: int, sh: int, workspace) -> Workspace:
+    if workspace is None:
+        return Workspace.get(_native.OP_PAGES, args[6] + args[2], table.device, sh)
+    if workspace.buf.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}")
+    return workspace
+
+
 def _one_out(out, name: str, like: torch.Tensor, dev: int) -> tuple[torch.Tensor, int]:
     if out is None:
         out = torch.empty(1, dtype=torch.int32, device=like.device)
@@ -775,12 +799,12 @@ def pages_fork(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page
     fresh pages taken, -1 (refused) or -2 (out of pages; the row is left as
     it was), and the number of free pages left."""
     args, dev = _cache_args(table, lens, refs, page_tokens)
+    sh = _launch_stream(stream, dev)
     rows, i32 = args[2], torch.int32
     if status is None:
         status = torch.empty(rows, dtype=i32, device=table.device)
     free_pages, free_ptr = _one_out(free_pages, "free_pages", table, dev)
-    sh = _stream_handle(stream)
-    ws = _ws(_native.OP_PAGES, args[6] + rows, table.device, sh, workspace)
+    ws = _pages_ws(args, table, dev, sh, workspace)
     _native.check(_native.lib().pages_fork(
         *args, _optional(parent, "parent", i32, rows, dev), _optional(grow, "grow", i32, rows, dev),
         None if pool is None else _pool_struct(pool, dev), _arg(status, "status", i32, rows, dev), free_ptr, ws.ptr,
@@ -794,9 +818,9 @@ def pages_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page
     pages' refs fall by one, its entries become -1, its length 0. Returns the
     number of pages that became free (one-element device tensor)."""
     args, dev = _cache_args(table, lens, refs, page_tokens)
+    sh = _launch_stream(stream, dev)
     freed, freed_ptr = _one_out(freed, "freed", table, dev)
-    sh = _stream_handle(stream)
-    ws = _ws(_native.OP_PAGES, args[6] + args[2], table.device, sh, workspace)
+    ws = _pages_ws(args, table, dev, sh, workspace)
     _native.check(_native.lib().pages_free(*args, _arg(release, "release", torch.int32, args[2], dev), freed_ptr,
                                            ws.ptr, ws.nbytes, sh), "pages_free")
     return freed
@@ -810,12 +834,12 @@ def pages_compact(pool: PagePool | None, table: torch.Tensor, lens: torch.Tensor
     below L; table and refs follow. Returns (live, remap): L, and each live
     page's new number (-1 for free ones)."""
     args, dev = _cache_args(table, lens, refs, page_tokens)
+    sh = _launch_stream(stream, dev)
     pages = args[6]
     live, live_ptr = _one_out(live, "live", table, dev)
     if remap is None:
         remap = torch.empty(pages, dtype=torch.int32, device=table.device)
-    sh = _stream_handle(stream)
-    ws = _ws(_native.OP_PAGES, pages + args[2], table.device, sh, workspace)
+    ws = _pages_ws(args, table, dev, sh, workspace)
     _native.check(_native.lib().pages_compact(
         None if pool is None else _pool_struct(pool, dev), *args, live_ptr,
         _arg(remap, "remap", torch.int32, pages, dev), ws.ptr, ws.nbytes, sh), "pages_compact")
