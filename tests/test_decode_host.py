@@ -73,3 +73,29 @@ def test_a_workspace_of_another_device_is_refused(gpu, name):
     with pytest.raises(ValueError, match="workspace must be on cuda:0"):
         Args(gpu).calls()[name](workspace=u.Workspace(4096, torch.device("cuda", 1)))
     assert len(gpu.lib.calls) == 1
+
+
+def cleared_workspace(gpu, stream):
+    """The workspace that a first call on `stream` gets; it is filled on the current one."""
+    a = Args(gpu)
+    u.pages_free(a.table, a.lens, a.refs, 16, a.lens, stream=stream)
+    (ws,) = gpu.workspaces.values()
+    assert ws.buf.stream == gpu.current.cuda_stream == 1000
+    return ws
+
+
+def test_a_workspace_is_filled_before_another_stream_uses_it(gpu):
+    ws = cleared_workspace(gpu, Stream(77))
+    (other,) = gpu.external
+    assert (other.cuda_stream, other.waited, ws.buf.recorded) == (77, [1000], (77,))
+
+
+def test_a_workspace_is_filled_before_the_default_stream_uses_it(gpu):
+    """Handle 0 names the default stream, and no other waits in its place."""
+    ws = cleared_workspace(gpu, gpu.default)
+    assert (gpu.default.waited, ws.buf.recorded) == ([1000], (0,))
+
+
+def test_a_workspace_of_the_current_stream_waits_for_nothing(gpu):
+    ws = cleared_workspace(gpu, None)
+    assert (gpu.external, gpu.default.waited, ws.buf.recorded) == ([], [], ())

@@ -354,3 +354,23 @@ def test_host_scan_leaves_nothing_that_passes_for_tile_words(u):
     assert lib.u32scan_check(ws.ptr, stream) == _native.OK
     want, want_total = oracle.scan_exclusive(a)
     assert np.array_equal(host_u32(d), want) and int(host_u32(tot)[0]) == want_total
+
+
+@pytest.mark.parametrize("which", ["default", "other"])
+def test_a_first_call_on_a_stream_that_is_not_current(u, monkeypatch, which):
+    """The workspace is filled on the current stream, which is busy; the call's
+    stream waits for that."""
+    monkeypatch.setattr(u.Workspace, "_cache", {})
+    n = (1 << 22) + 9
+    a = inputs.scan_values(n, 63)
+    d, total = dev32(a), torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    stream = torch.cuda.default_stream() if which == "default" else torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)  # some 50 ms
+        u.scan_exclusive_u32(d, total, stream=stream)
+    torch.cuda.synchronize()
+    u.check(stream=stream)
+    want, want_total = oracle.scan_exclusive(a)
+    assert np.array_equal(host_u32(d), want) and int(host_u32(total)[0]) == want_total

@@ -118,7 +118,9 @@ class Workspace:
                 ws = cls(max(need, 2 * ws.nbytes if ws else need), device)
                 current = torch.cuda.current_stream(device)
                 if stream_handle != current.cuda_stream:  # filled on the current stream, used on the caller's
-                    other = torch.cuda.ExternalStream(stream_handle, device)
+                    # (an ExternalStream of handle 0 would be some stream of torch's pool)
+                    other = (torch.cuda.ExternalStream(stream_handle, device) if stream_handle
+                             else torch.cuda.default_stream(device))
                     other.wait_stream(current)
                     ws.buf.record_stream(other)
                 cls._cache[key] = ws
