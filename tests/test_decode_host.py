@@ -99,3 +99,20 @@ def test_a_workspace_is_filled_before_the_default_stream_uses_it(gpu):
 def test_a_workspace_of_the_current_stream_waits_for_nothing(gpu):
     ws = cleared_workspace(gpu, None)
     assert (gpu.external, gpu.default.waited, ws.buf.recorded) == ([], [], ())
+
+
+@pytest.mark.parametrize("name", ["sample_tokens", "pages_fork", "pages_free", "pages_compact"])
+def test_outputs_lie_in_memory_of_the_stream_that_writes_them(gpu, name):
+    """Memory that the current stream gave back may still be in use there when
+    another stream writes to it; and the outputs may still be in use on the
+    current stream when they are given back."""
+    outs = Args(gpu).calls()[name](stream=Stream(77))
+    for out in [outs] if isinstance(outs, torch.Tensor) else outs:
+        assert (out.stream, out.recorded) == (77, (1000,))
+    outs = Args(gpu).calls()[name](stream=gpu.default)
+    for out in [outs] if isinstance(outs, torch.Tensor) else outs:
+        assert (out.stream, out.recorded) == (0, (1000,))
+    for kw in ({}, dict(stream=gpu.current)):
+        outs = Args(gpu).calls()[name](**kw)
+        for out in [outs] if isinstance(outs, torch.Tensor) else outs:
+            assert (out.stream, out.recorded) == (1000, ())

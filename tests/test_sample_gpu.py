@@ -401,3 +401,24 @@ def test_the_stride_of_one_row_is_not_used(u, stride, dtype):
     words, params = inputs.splitmix_u32(26, 0, 1), params_for("top_p", 1, 5)
     got, want = run(u, view, words, params), oracle.sample_tokens(held, words, **params)
     assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+def test_outputs_on_another_stream_while_the_current_one_is_busy(u):
+    """The current stream gives memory back that it still writes to; a call on
+    another stream gets none of it."""
+    n, rows = 5003, 128
+    x = logits_for("peaked", rows, n, 71)
+    dev, held = as_type(x, "bf16")
+    words = inputs.splitmix_u32(27, 0, rows)
+    r = torch.from_numpy(words.view(np.int32).copy()).cuda()
+    want = oracle.sample_tokens(held, words)
+    side, current = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with torch.cuda.stream(current):
+            torch.cuda._sleep(20_000_000)  # some 10 ms
+            scratch = [torch.full((rows,), 12345, dtype=torch.int32, device="cuda") for _ in range(8)]
+            del scratch
+            tok, prob = u.sample_tokens(dev, r, stream=side)
+        torch.cuda.synchronize()
+        assert np.array_equal(tok.cpu().numpy(), want[0]) and np.array_equal(prob.cpu().numpy(), want[1])

@@ -612,6 +612,19 @@ def runs_owner_u32(ends: torch.Tensor, owner: torch.Tensor | None = None, capaci
     return owner
 
 
+def _new(n: int, dtype, device: torch.device, stream) -> torch.Tensor:
+    """An output for a call on `stream`, in memory of that stream: what the
+    current one gave back may still be in use there. The caller goes on with
+    it on the current stream, so that one is noted too."""
+    if stream is None or stream.cuda_stream == _stream_handle(None):
+        return torch.empty(n, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        out = torch.empty(n, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
 _LOGIT_TYPES = {torch.float32: _native.F32, torch.float16: _native.F16, torch.bfloat16: _native.BF16}
 
 
@@ -665,9 +678,9 @@ def sample_tokens(logits: torch.Tensor, random: torch.Tensor, *, temperature: to
     dev = logits.get_device()
     sh = _launch_stream(stream, dev)
     if tokens is None:
-        tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        tokens = _new(rows, torch.int32, logits.device, stream)
     if probs is None:
-        probs = torch.empty(rows, dtype=torch.float32, device=logits.device)
+        probs = _new(rows, torch.float32, logits.device, stream)
     f32, i32 = torch.float32, torch.int32
     words = _arg(random, "random", i32 if random.dtype is i32 else _U32_DTYPES[1], rows, dev)
     _native.check(_native.lib().sample_tokens(
@@ -783,9 +796,9 @@ def _pages_ws(args, table, dev: int, sh: int, workspace) -> Workspace:
     return workspace
 
 
-def _one_out(out, name: str, like: torch.Tensor, dev: int) -> tuple[torch.Tensor, int]:
+def _one_out(out, name: str, like: torch.Tensor, dev: int, stream) -> tuple[torch.Tensor, int]:
     if out is None:
-        out = torch.empty(1, dtype=torch.int32, device=like.device)
+        out = _new(1, torch.int32, like.device, stream)
     return out, _arg(out, name, torch.int32, 1, dev)
 
 
@@ -804,8 +817,8 @@ def pages_fork(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page
     sh = _launch_stream(stream, dev)
     rows, i32 = args[2], torch.int32
     if status is None:
-        status = torch.empty(rows, dtype=i32, device=table.device)
-    free_pages, free_ptr = _one_out(free_pages, "free_pages", table, dev)
+        status = _new(rows, i32, table.device, stream)
+    free_pages, free_ptr = _one_out(free_pages, "free_pages", table, dev, stream)
     ws = _pages_ws(args, table, dev, sh, workspace)
     _native.check(_native.lib().pages_fork(
         *args, _optional(parent, "parent", i32, rows, dev), _optional(grow, "grow", i32, rows, dev),
@@ -821,7 +834,7 @@ def pages_free(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page
     number of pages that became free (one-element device tensor)."""
     args, dev = _cache_args(table, lens, refs, page_tokens)
     sh = _launch_stream(stream, dev)
-    freed, freed_ptr = _one_out(freed, "freed", table, dev)
+    freed, freed_ptr = _one_out(freed, "freed", table, dev, stream)
     ws = _pages_ws(args, table, dev, sh, workspace)
     _native.check(_native.lib().pages_free(*args, _arg(release, "release", torch.int32, args[2], dev), freed_ptr,
                                            ws.ptr, ws.nbytes, sh), "pages_free")
@@ -838,9 +851,9 @@ def pages_compact(pool: PagePool | None, table: torch.Tensor, lens: torch.Tensor
     args, dev = _cache_args(table, lens, refs, page_tokens)
     sh = _launch_stream(stream, dev)
     pages = args[6]
-    live, live_ptr = _one_out(live, "live", table, dev)
+    live, live_ptr = _one_out(live, "live", table, dev, stream)
     if remap is None:
-        remap = torch.empty(pages, dtype=torch.int32, device=table.device)
+        remap = _new(pages, torch.int32, table.device, stream)
     ws = _pages_ws(args, table, dev, sh, workspace)
     _native.check(_native.lib().pages_compact(
         None if pool is None else _pool_struct(pool, dev), *args, live_ptr,
