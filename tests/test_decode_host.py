@@ -116,3 +116,42 @@ def test_outputs_lie_in_memory_of_the_stream_that_writes_them(gpu, name):
         outs = Args(gpu).calls()[name](**kw)
         for out in [outs] if isinstance(outs, torch.Tensor) else outs:
             assert (out.stream, out.recorded) == (1000, ())
+
+
+@pytest.mark.parametrize("other", [None, 3, [1, 2, 3, 4], "words"])
+def test_arguments_that_are_no_tensors(gpu, other):
+    """A TypeError that names the argument, whichever it is."""
+    a = Args(gpu)
+    cache = (a.table, a.lens, a.refs, 16)
+    calls = {
+        "logits": lambda: u.sample_tokens(other, a.words),
+        "random": lambda: u.sample_tokens(a.logits, other),
+        "src": lambda: u.pages_copy(a.pool, other, a.lens),
+        "dst": lambda: u.pages_copy(a.pool, a.lens, other),
+        "pool": lambda: u.pages_copy(other, a.lens, a.lens),
+        "table": lambda: u.pages_free(other, a.lens, a.refs, 16, a.lens),
+        "lens": lambda: u.pages_free(a.table, other, a.refs, 16, a.lens),
+        "refs": lambda: u.pages_free(a.table, a.lens, other, 16, a.lens),
+        "release": lambda: u.pages_free(*cache, other),
+    }
+    if other is not None:  # may be left out
+        calls |= {
+            "temperature": lambda: u.sample_tokens(a.logits, a.words, temperature=other),
+            "top_k": lambda: u.sample_tokens(a.logits, a.words, top_k=other),
+            "top_p": lambda: u.sample_tokens(a.logits, a.words, top_p=other),
+            "min_p": lambda: u.sample_tokens(a.logits, a.words, min_p=other),
+            "tokens": lambda: u.sample_tokens(a.logits, a.words, tokens=other),
+            "probs": lambda: u.sample_tokens(a.logits, a.words, probs=other),
+            "count": lambda: u.pages_copy(a.pool, a.lens, a.lens, other),
+            "parent": lambda: u.pages_fork(*cache, parent=other),
+            "grow": lambda: u.pages_fork(*cache, grow=other),
+            "status": lambda: u.pages_fork(*cache, status=other),
+            "free_pages": lambda: u.pages_fork(*cache, free_pages=other),
+            "freed": lambda: u.pages_free(*cache, a.lens, freed=other),
+            "live": lambda: u.pages_compact(a.pool, *cache, live=other),
+            "remap": lambda: u.pages_compact(a.pool, *cache, remap=other),
+        }
+    for name, call in calls.items():
+        with pytest.raises(TypeError, match=f"{name} must be a"):
+            call()
+    assert gpu.lib.calls == []

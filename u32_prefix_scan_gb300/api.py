@@ -628,12 +628,16 @@ def _new(n: int, dtype, device: torch.device, stream) -> torch.Tensor:
 _LOGIT_TYPES = {torch.float32: _native.F32, torch.float16: _native.F16, torch.bfloat16: _native.BF16}
 
 
+def _tensor(t, name: str) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
+
+
 def _arg(t, name: str, dtype, numel: int, dev: int) -> int:
     """The device pointer of a contiguous tensor of at least numel elements
     on CUDA device `dev`."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    if not _tensor(t, name).is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
@@ -682,7 +686,7 @@ def sample_tokens(logits: torch.Tensor, random: torch.Tensor, *, temperature: to
     if probs is None:
         probs = _new(rows, torch.float32, logits.device, stream)
     f32, i32 = torch.float32, torch.int32
-    words = _arg(random, "random", i32 if random.dtype is i32 else _U32_DTYPES[1], rows, dev)
+    words = _arg(random, "random", i32 if _tensor(random, "random").dtype is i32 else _U32_DTYPES[1], rows, dev)
     _native.check(_native.lib().sample_tokens(
         logits.data_ptr(), kind, rows, vocab, row_stride, _optional(temperature, "temperature", f32, rows, dev),
         _optional(top_k, "top_k", i32, rows, dev), _optional(top_p, "top_p", f32, rows, dev),
@@ -752,9 +756,9 @@ def pages_copy(pool: PagePool, src: torch.Tensor, dst: torch.Tensor, count: torc
     source). count, a one-element int32 tensor, limits the pairs on the
     device."""
     struct, i32 = _pool_struct(pool, pool.device.index if isinstance(pool, PagePool) else -1), torch.int32
-    dev, n = pool.device.index, src.numel()
+    dev, n = pool.device.index, _tensor(src, "src").numel()
     sh = _launch_stream(stream, dev)
-    if dst.numel() != n:
+    if _tensor(dst, "dst").numel() != n:
         raise ValueError("src and dst differ in length")
     _native.check(_native.lib().pages_copy(struct, _arg(src, "src", i32, n, dev), _arg(dst, "dst", i32, n, dev), n,
                                            _optional(count, "count", i32, 1, dev), sh), "pages_copy")
