@@ -155,3 +155,18 @@ def test_arguments_that_are_no_tensors(gpu, other):
         with pytest.raises(TypeError, match=f"{name} must be a"):
             call()
     assert gpu.lib.calls == []
+
+
+def test_workspace_sizes_are_those_of_the_loaded_library(gpu, monkeypatch):
+    """Another library (other launch shapes, swapped in by tests) may need more
+    for the same operation and size."""
+    from fake_device import Library
+    from u32_prefix_scan_gb300 import api
+
+    args = (u._native.OP_PAGES, 12345, torch.device("cuda", 0), 1000)
+    assert api.Workspace.get(*args).nbytes == 4096
+    first, gpu.lib = gpu.lib, Library(workspace_bytes=8192)
+    assert api.Workspace.get(*args).nbytes == 8192
+    gpu.workspaces.clear()
+    gpu.lib = first
+    assert api.Workspace.get(*args).nbytes == 4096

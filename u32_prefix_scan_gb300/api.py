@@ -110,7 +110,7 @@ class Workspace:
 
     @classmethod
     def get(cls, op: int, n: int, device: torch.device, stream_handle: int) -> "Workspace":
-        need = _workspace_bytes(op, n)
+        need = _workspace_bytes(_native.lib(), op, n)
         key = (device.index, stream_handle)
         with cls._lock:
             ws = cls._cache.get(key)
@@ -128,8 +128,8 @@ class Workspace:
 
 
 @functools.lru_cache(maxsize=1024)
-def _workspace_bytes(op: int, n: int) -> int:
-    return _native.lib().u32scan_workspace_bytes(op, n)
+def _workspace_bytes(lib, op: int, n: int) -> int:
+    return lib.u32scan_workspace_bytes(op, n)
 
 
 def _ws(op: int, n: int, device, stream_handle: int, workspace) -> Workspace:
