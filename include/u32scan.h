@@ -641,7 +641,8 @@ int u32scan_fill_splitmix_u32(uint32_t *out, size_t n, uint32_t seed, uint32_t s
  *               no filter. Values outside the ranges above switch a filter
  *               off.
  *   random      device, uint32_t[rows], uniform words (for instance from
- *               u32scan_fill_splitmix_u32).
+ *               u32scan_fill_splitmix_u32). A draw has their 32 bits: it
+ *               moves in steps of 2^-32 of S'.
  *   tokens      device, int32_t[rows]: the token; -1 for a row in which no
  *               logit is above -inf (or vocab = 0).
  *   probs       device, float[rows] or NULL: q[token] / S' rounded from

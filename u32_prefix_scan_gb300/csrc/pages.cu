@@ -691,8 +691,8 @@ static bool ws_ok(const void *ws, size_t ws_bytes, size_t pages, size_t rows) {
 
 // Blocks for `units` copy units: one a unit up to 128 an SM (8 at a time; the
 // rest are handed out as those finish, which keeps the SMs level: 509 pages of
-// 64 x 32 KiB take 342, 312, 311 us with 8, 64, 128 an SM, floor 315 at the
-// measured copy rate; a packing whose number of pages only the device knows
+// 64 x 32 KiB take 342, 312, 311 us with 8, 64, 128 an SM, and 314 would at the
+// rate of a plain copy of 2 GB; a packing whose number of pages only the device knows
 // 179, 167, 165, and 177 with 512).
 static unsigned int copy_grid(u64 units, int sms) {
     const u64 full = (u64)sms * 128;

@@ -49,13 +49,16 @@
 // 50 9, under top-p 12 (peaked) to 16 (flat); 64 x 131072 bf16 without
 // filters 16, under top-p 35; 256 x 262144 f32, a fifth of the rows greedy, most
 // others under top-k, top-p or both, 112 (268 MB: 2.4 TB/s, where reading alone
-// takes 40; DRAM 30 % busy). What bounds it is issue and latency, not reading: a
-// logit's weight is 15 f32 operations that round one by one, and some 30
-// instructions with its place in the histogram (3.6 logits a clock and SM);
-// around that are short steps between barriers, a cluster's 500 clocks or more
-// each. Instructions are issued in 50 % of the cycles under top-p (39 % for
-// the 256 rows, whose rows of unequal work also leave SMs idle at the end). Two
-// blocks of 16 warps an SM, 64 registers a thread: while one waits at a barrier
+// takes 40; DRAM 30 % busy). What bounds it is waiting more than issue, and
+// neither is HBM's rate. A logit's weight is 15 f32 operations that round one by
+// one, and some 30 instructions with its place in the histogram (3.6 logits a
+// clock and SM); with the later passes top-p takes 66 instructions a bf16 logit,
+// which the SMs would issue in 14 of the 35 us. The rest are barriers and short steps
+// between them, a cluster's 500 clocks or more each. Of the 256 rows' 112 us issue
+// is 30: three quarters of an f32 slice are not staged and come from L2 in every
+// pass, one load a lane ahead, and rows of unequal work leave SMs idle at the end.
+// (Instructions are issued in 50 and 39 % of the cycles in which an SM is at work.)
+// Two blocks of 16 warps an SM, 64 registers a thread: while one waits at a barrier
 // the other weighs.
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -1680,7 +1683,9 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleArgs a
 
 // Bytes of a row a block keeps in shared memory: two blocks an SM.
 constexpr unsigned int kMaxStage = 64 * 1024;
-constexpr unsigned int kResident = 304;  // blocks at a time: two on each of 152 SMs
+// Blocks at a time: two on each of a GB300's 152 SMs. (With fewer SMs at hand, as in a
+// partition, the rule below takes more rows for one wave than run in it; results are the same.)
+constexpr unsigned int kResident = 304;
 static_assert(sizeof(SampleShared) % 16 == 0 && offsetof(SampleShared, slots) % 16 == 0 && kLocal % 2 == 0,
               "16-byte accesses");
 static_assert(U32SCAN_MAX_VOCAB / 8 / kMaxCluster / kSWarps + 8 < 65536, "a warp's vectors in 16 bits");
