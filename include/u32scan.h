@@ -7,7 +7,8 @@
  * offsets -> gathered indices -> count) and a stable LSD radix-sort
  * permutation of U32 keys; and, for programs that decode with a language
  * model, token sampling and the operations of a paged cache, exact integer
- * arithmetic like the rest.
+ * arithmetic like the rest; and the logits' rules before the sampling, the
+ * writing of such a cache and attention over it, in floating point.
  *
  * Conventions for every entry point below:
  *   - Pointers named as device pointers must point to memory the current
@@ -83,13 +84,16 @@ typedef struct CUstream_st *u32scan_stream_t;
 #define U32SCAN_OP_SCAN_HOST 7 /* scan_exclusive_u32_host, scan_inclusive_u32_host */
 #define U32SCAN_OP_REDUCE 8    /* reduce_u32_op (the same size for every n) */
 #define U32SCAN_OP_PAGES 9     /* pages_fork, pages_free, pages_compact: n = pages + rows */
+#define U32SCAN_OP_ATTEND 10   /* pages_attend (the same size for every n) */
 
-/* Element types of logits (sample_tokens). */
+/* Element types (logits, queries, keys and values; E4M3: a cache's only). */
 #define U32SCAN_F32 0
 #define U32SCAN_F16 1
 #define U32SCAN_BF16 2
+#define U32SCAN_E4M3 3
 
-/* The largest vocabulary of sample_tokens (its weights' sums stay below 2^53). */
+/* The largest vocabulary of sample_tokens (its weights' sums stay below 2^53)
+ * and of adjust_logits. */
 #define U32SCAN_MAX_VOCAB (1u << 22)
 
 /* Bytes of device workspace an operation needs for n elements (a multiple
@@ -657,6 +661,53 @@ int sample_tokens(const void *logits, int type, size_t rows, size_t vocab, size_
                   const uint32_t *random, int32_t *tokens, float *probs, u32scan_stream_t stream);
 
 /*
+ * The rules of a request applied to its logits before a token is drawn (no
+ * counterpart on the pages). For every row, with x a logit as float and
+ * every f32 operation rounded alone:
+ *   repetition  a token that occurs in the row's history, with r finite and
+ *           above 0: x becomes x / r where x > 0, x * r elsewhere.
+ *   frequency, presence  a token that occurs c > 0 times in the history past
+ *           its first prompt_lens: x becomes (x - frequency * c) - presence.
+ *   bias    a token that the row's list names: x becomes x + bias; of a token
+ *           named more than once the last counts.
+ *   allowed a token whose bit is 0: x becomes -inf, whatever it was.
+ * in this order; then x is rounded to the logits' type. A logit that no rule
+ * reaches is copied bit for bit.
+ *   logits, type, rows, vocab, row_stride  as sample_tokens.
+ *   out     device, rows of `vocab` elements of `type`, out_stride elements
+ *           apart: the adjusted logits. May be `logits` itself with the same
+ *           stride (in place); otherwise the two must not overlap.
+ *   rules   host struct, read during the call. Absent (NULL) arrays change
+ *           nothing: a row without its own value has no penalty, an absent
+ *           history_lens stands for history_width, an absent prompt_lens for 0.
+ */
+typedef struct {
+    const int32_t *history; /* device, rows of history_width tokens, history_stride apart; numbers outside
+                               [0, vocab) (say -1) are skipped */
+    size_t history_width, history_stride;
+    const int32_t *history_lens; /* device, int32_t[rows]: tokens held, limited to [0, history_width] */
+    const int32_t *prompt_lens;  /* device, int32_t[rows]: how many of them are the prompt, likewise limited */
+    const float *repetition, *presence, *frequency; /* device, float[rows] each; a value that is not finite
+                                                       counts as none */
+    const int32_t *bias_tokens; /* device, int32_t[rows][biases]; numbers outside [0, vocab) are skipped */
+    const float *bias;          /* device, float[rows][biases] */
+    size_t biases;
+    const uint32_t *allowed; /* device, rows of ceil(vocab / 32) words, allowed_stride apart: token 32 w + j is
+                                allowed when bit j of word w is set */
+    size_t allowed_stride;
+} u32scan_logit_rules;
+
+/*
+ * No workspace. Errors: EINVAL (as sample_tokens; out_stride below vocab with
+ * more than one row; overlapping logits and out; a null rules; history or
+ * allowed rows that overlap partly do no harm, they are only read; widths at
+ * or above 2^31, a null array with a width above 0, misaligned pointers),
+ * ECUDA.
+ */
+int adjust_logits(const void *logits, int type, size_t rows, size_t vocab, size_t row_stride, void *out,
+                  size_t out_stride, const u32scan_logit_rules *rules, u32scan_stream_t stream);
+
+/*
  * A paged cache (no counterpart on the pages: their prefix sums, compaction
  * and runs layout, applied to a cache's pages). `pages` pages of
  * `page_bytes` bytes lie `page_stride` bytes apart in every one of
@@ -751,6 +802,123 @@ int pages_free(int32_t *table, size_t table_stride, size_t rows, size_t width, i
 int pages_compact(const u32scan_page_pool *pool, int32_t *table, size_t table_stride, size_t rows, size_t width,
                   const int32_t *lens, int32_t *refs, size_t pages, size_t page_tokens, int32_t *live,
                   int32_t *remap, void *ws, size_t ws_bytes, u32scan_stream_t stream);
+
+/*
+ * One layer's keys and values in a paged cache (a view of a pool's pages;
+ * read on the host during the call). Element d of head h of the token in
+ * slot t of page p lies at keys + p * page_stride + t * token_stride +
+ * h * head_stride + d elements, and likewise in values. With type E4M3 (8 bits,
+ * 4 of exponent, 3 of fraction, no infinity) a value is its code times the
+ * scale of its block: `blocks` blocks of page_tokens / blocks tokens a page,
+ * the scale of block b and head h at key_scales + p * scale_stride +
+ * b * heads + h. Scales, keys and values may lie in one page of a pool, so
+ * that its operations move them together.
+ */
+typedef struct {
+    void *keys, *values; /* device, aligned to their element */
+    int type;            /* U32SCAN_F32, _F16, _BF16 or _E4M3 */
+    size_t pages, page_tokens, heads, dim;
+    size_t page_stride, token_stride, head_stride; /* elements */
+    float *key_scales, *value_scales;              /* device; NULL without E4M3 */
+    size_t blocks, scale_stride;                   /* floats between two pages' scales */
+} u32scan_kv_cache;
+
+/*
+ * Which tokens belong to which row, for the two calls below: row s has the
+ * tokens starts[s] .. starts[s + 1] - 1 (device, int32_t[rows + 1], not
+ * falling, from 0), or, with starts NULL, token s alone (tokens = rows). They are the
+ * row's last: with n of them, token i of the row is at position
+ * lens[s] - n + i, its keys and values in page table[s][position /
+ * page_tokens], slot position mod page_tokens (table and lens as pages_fork
+ * left them after growing the row by n). Starts outside [0, tokens] count as
+ * the nearer end.
+ */
+
+/* The tokens that pages_append writes. Strides in elements; the elements of
+ * a head are adjacent. */
+typedef struct {
+    size_t tokens;
+    int type; /* of all four arrays: U32SCAN_F32, _F16 or _BF16 */
+    const void *keys;
+    size_t key_token_stride, key_head_stride;
+    const void *values;
+    size_t value_token_stride, value_head_stride;
+    const void *queries; /* NULL: no queries */
+    size_t q_heads, query_token_stride, query_head_stride;
+    void *queries_out; /* may be `queries` with the same strides, else they must not overlap */
+    size_t out_token_stride, out_head_stride;
+    const float *cos, *sin; /* device, float[positions][pairs]; NULL: no rotation */
+    size_t positions, pairs;
+    int interleaved;
+} u32scan_new_tokens;
+
+/*
+ * Appends keys and values to a paged cache, rotating the keys (and queries,
+ * if given) by their position on the way.
+ *   rotation  with c, s the angle's cosine and sine for the token's position
+ *           and pair i, the pair (a, b) becomes (a c - b s, b c + a s), every
+ *           f32 operation rounded alone; a, b are elements i and pairs + i of
+ *           a head, or 2 i and 2 i + 1 when interleaved; elements from 2 pairs
+ *           on, and values, stay.
+ *   storing  into a cache of 16 or 32 bits: rounded once to its type (the
+ *           cache's type is then the tokens'). Into an E4M3 cache: with m the
+ *           largest finite magnitude of a block's new values of one head, the
+ *           block's scale becomes the larger of the least 2^e with e >= -100
+ *           and m <= 448 * 2^e, and, if the block holds older tokens (of this
+ *           row, at positions before the new ones), its scale so far; one that is not finite and above 0 counts
+ *           as 0. If that raised it, the older tokens' codes become the codes
+ *           nearest to code * (old scale / new scale). A new value's code is
+ *           the nearest to x * (1 / scale) (each operation rounded alone; ties
+ *           to even; magnitudes past 448 become 448; NaN stays NaN).
+ *   queries_out  the rotated queries [tokens][q_heads][dim], rounded to the
+ *           type.
+ * Not written are tokens of a row s with status[s] < 0 (as pages_fork
+ * reports rows it did not serve; NULL: all are served), tokens at positions
+ * below 0 or past the row's `width` pages, those whose page number is
+ * outside [0, pages), and, with a rotation, those at positions from
+ * `positions` on; the rotated queries of tokens at positions outside
+ * [0, positions) are NaN. Tokens behind the last row's are left alone, in
+ * queries_out too.
+ * No two rows may write to one page (pages_fork sees to it), nor a row twice.
+ * No workspace. Errors: EINVAL (null pointers with sizes above 0, misaligned
+ * pointers, sizes at or above 2^31, strides at or above 2^40, rows and tokens
+ * that differ without starts, 2 pairs above dim, dim above 1024, blocks that do not
+ * divide page_tokens, an unknown type or a cache of another one), ECUDA.
+ */
+int pages_append(const u32scan_kv_cache *cache, const int32_t *table, size_t table_stride, size_t rows, size_t width,
+                 const int32_t *lens, const int32_t *starts, const int32_t *status,
+                 const u32scan_new_tokens *new_tokens, u32scan_stream_t stream);
+
+/*
+ * Attention over a paged E4M3 cache: for every token and query head, with
+ * q its query, k_j and v_j the keys and values (codes times scales) of the
+ * row's tokens at positions j up to the token's own,
+ *   out = sum_j softmax_j(scale * q . k_j) v_j.
+ * Query head h reads key head h / (q_heads / heads). Tokens that the table
+ * does not place (past `width` pages, a page number outside [0, pages)) are
+ * left out; a query that sees none gets zeros. Scales must be finite and not below 0.
+ * Codes that are NaN make NaN of what sees them.
+ * Products of queries (scaled by a power of two to f16, for bf16 exact but for
+ * elements below 2^-22 of a head's largest) and codes are exact and summed in
+ * f32, as are the softmax's sums; its weights are rounded to f16 (2^-11
+ * relative) before they meet the values; the result is rounded once to the type.
+ *   queries  device, [tokens][q_heads][dim] of `type` (F16 or BF16), strides in
+ *            elements; q_heads a multiple of the cache's heads.
+ *   out      device, [tokens][q_heads][dim] of `type`; must not overlap queries.
+ *            Tokens behind the last row's are left alone.
+ *   cache    type E4M3; dim a multiple of 16 up to 256; keys, values and the
+ *            strides in bytes multiples of 16; queries too.
+ *   ws, ws_bytes  u32scan_workspace_bytes(U32SCAN_OP_ATTEND, tokens) bytes.
+ * The result does not depend on the other calls that run; every sum is taken
+ * in an order fixed by the sizes, lens and starts.
+ * Errors: EINVAL (as pages_append; another cache type; the alignments above),
+ * EWORKSPACE, ECUDA.
+ */
+int pages_attend(const u32scan_kv_cache *cache, const int32_t *table, size_t table_stride, size_t rows, size_t width,
+                 const int32_t *lens, const int32_t *starts, size_t tokens, const void *queries, int type,
+                 size_t q_heads, size_t query_token_stride, size_t query_head_stride, void *out,
+                 size_t out_token_stride, size_t out_head_stride, float scale, void *ws, size_t ws_bytes,
+                 u32scan_stream_t stream);
 
 #ifdef __cplusplus
 }

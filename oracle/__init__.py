@@ -61,6 +61,20 @@ def _configure(lib):
     lib.oracle_pages_free.restype = i32
     lib.oracle_pages_compact.argtypes = [*table, u8p, _u64, _u64, _i32p]
     lib.oracle_pages_compact.restype = i32
+    f32p, f64p = ctypes.POINTER(f32), ctypes.POINTER(ctypes.c_double)
+    lib.oracle_adjust_row.argtypes = [f32p, _u64, _i32p, ctypes.c_int64, ctypes.c_int64, f32, f32, f32, _i32p, f32p,
+                                      _u64, _u32p, f32p, u8p]
+    lib.oracle_adjust_row.restype = None
+    lib.oracle_code_value.argtypes = [ctypes.c_uint8]
+    lib.oracle_code_value.restype = f32
+    lib.oracle_value_code.argtypes = [f32]
+    lib.oracle_value_code.restype = ctypes.c_uint8
+    lib.oracle_rotate_head.argtypes = [f32p, _u64, f32p, f32p, _u64, ctypes.c_int, f32p]
+    lib.oracle_rotate_head.restype = None
+    lib.oracle_append_block.argtypes = [f32p, _u64, _u64, _u64, u8p, _u64, f32]
+    lib.oracle_append_block.restype = f32
+    lib.oracle_attend_query.argtypes = [f64p, f64p, f64p, u8p, _u64, _u64, ctypes.c_double, f64p]
+    lib.oracle_attend_query.restype = None
     lib.oracle_scan_exclusive_u32.argtypes = [_u32p, _u64]
     lib.oracle_scan_exclusive_u32.restype = ctypes.c_uint32
     lib.oracle_scan_inclusive_u32.argtypes = [_u32p, _u64]
@@ -334,3 +348,160 @@ def pages_compact(table, lens, refs, page_tokens, pool=None):
     live = _load().oracle_pages_compact(_p(t, _i32p), t.shape[0], t.shape[1], _p(l, _i32p), _p(r, _i32p), r.size,
                                         page_tokens, ptr, planes, page_bytes, _p(remap, _i32p))
     return t, r, int(live), remap, p
+
+
+def _f32(a) -> np.ndarray:
+    return np.ascontiguousarray(np.asarray(a, dtype=np.float32))
+
+
+def _fp(a):
+    return a.ctypes.data_as(ctypes.POINTER(ctypes.c_float))
+
+
+def _up(a):
+    return a.ctypes.data_as(ctypes.POINTER(ctypes.c_uint8))
+
+
+def adjust_logits(logits, history=None, history_lens=None, prompt_lens=None, repetition=None, presence=None,
+                  frequency=None, bias_tokens=None, bias=None, allowed=None):
+    """(adjusted, touched): float32 logits [rows, vocab] under a request's
+    rules, before they are rounded to their type, and which of them a rule
+    reached."""
+    x = _f32(logits)
+    rows, vocab = x.shape
+    h = np.zeros((rows, 0), np.int32) if history is None else _i32(history)
+    held = np.full(rows, h.shape[1]) if history_lens is None else np.clip(history_lens, 0, h.shape[1])
+    prompt = np.zeros(rows, np.int64) if prompt_lens is None else np.clip(prompt_lens, 0, held)
+    none = np.full(rows, np.nan, np.float32)
+    r, p, f = (none if v is None else _f32(v) for v in (repetition, presence, frequency))
+    names = np.zeros((rows, 0), np.int32) if bias_tokens is None else _i32(bias_tokens)
+    adds = np.zeros((rows, 0), np.float32) if bias is None else _f32(bias)
+    out, touched = np.empty_like(x), np.empty(x.shape, np.uint8)
+    for b in range(rows):
+        mask = None if allowed is None else _u32(allowed[b])
+        hb, nb, ab = np.ascontiguousarray(h[b]), np.ascontiguousarray(names[b]), np.ascontiguousarray(adds[b])
+        _load().oracle_adjust_row(_fp(x[b]), vocab, _p(hb, _i32p), int(held[b]), int(prompt[b]), float(r[b]),
+                                  float(p[b]), float(f[b]), _p(nb, _i32p), _fp(ab), nb.size,
+                                  None if mask is None else _p(mask, _u32p), _fp(out[b]), _up(touched[b]))
+    return out, touched.astype(bool)
+
+
+def code_values(codes):
+    """float32 values of uint8 codes (8 bits: sign, 4 of exponent, 3 of fraction)."""
+    table = np.array([_load().oracle_code_value(c) for c in range(256)], np.float32)
+    return table[np.asarray(codes, np.uint8)]
+
+
+def value_codes(x):
+    """The nearest codes (uint8) of float32 values."""
+    flat = _f32(x).ravel()
+    return np.array([_load().oracle_value_code(float(v)) for v in flat], np.uint8).reshape(np.shape(x))
+
+
+def _row_tokens(lens, starts, tokens, s):
+    """(begin, n, first position) of row s's tokens."""
+    if starts is None:
+        return s, 1, int(lens[s]) - 1
+    b, e = (min(max(int(v), 0), tokens) for v in starts[s : s + 2])
+    n = max(e - b, 0)
+    return b, n, int(lens[s]) - n
+
+
+def rotate_heads(x, cos_row, sin_row, interleaved=False):
+    """One token's heads [heads, dim] (float32) rotated."""
+    x, c, s = _f32(x), _f32(cos_row), _f32(sin_row)
+    out = np.empty_like(x)
+    for h in range(x.shape[0]):
+        _load().oracle_rotate_head(_fp(x[h]), x.shape[1], _fp(c), _fp(s), c.size, int(interleaved), _fp(out[h]))
+    return out
+
+
+def pages_append(keys, values, table, lens, new_keys, new_values, starts=None, status=None, cos=None, sin=None,
+                 interleaved=False, key_scales=None, value_scales=None, queries=None, queries_out=None):
+    """(keys, values, key_scales, value_scales, queries_out) after the append.
+    keys, values: [pages, page_tokens, heads, dim], float32 (the caller
+    rounds them to the cache's type) or, with scales [pages, blocks, heads],
+    uint8 codes; queries_out: what it held before."""
+    keys, values, table, lens = keys.copy(), values.copy(), _i32(table), _i32(lens)
+    ks, vs = (None if a is None else _f32(a).copy() for a in (key_scales, value_scales))
+    pages, page_tokens, heads, dim = keys.shape
+    size = page_tokens // ks.shape[1] if ks is not None else page_tokens
+    tokens = new_keys.shape[0]
+    q = None if queries is None else _f32(queries_out).copy()
+    turn = cos is not None and np.shape(cos)[1] > 0
+    for s in range(lens.size):
+        begin, n, first = _row_tokens(lens, starts, tokens, s)
+        held, turned = [], {}
+        for i in range(n):
+            at = first + i
+            reached = not turn or 0 <= at < len(cos)
+            if q is not None:
+                row = _f32(queries[begin + i])
+                q[begin + i] = (rotate_heads(row, cos[at], sin[at], interleaved) if turn else row) if reached else np.nan
+            if at < 0 or not reached or (status is not None and status[s] < 0) or at // page_tokens >= table.shape[1]:
+                continue
+            if not 0 <= table[s, at // page_tokens] < pages:
+                continue
+            k = _f32(new_keys[begin + i])
+            turned[at] = (rotate_heads(k, cos[at], sin[at], interleaved) if turn else k, _f32(new_values[begin + i]))
+            held.append(at)
+        if ks is None:
+            for at in held:
+                p, t = table[s, at // page_tokens], at % page_tokens
+                keys[p, t], values[p, t] = turned[at]
+            continue
+        for at in held:
+            if at % size and at - 1 in turned:
+                continue  # not the first new one of its block
+            p, t = int(table[s, at // page_tokens]), at % page_tokens
+            last = at
+            while last + 1 in turned and (last + 1) % size:
+                last += 1
+            before, block = t % size, t // size
+            for which, codes, scales in ((0, keys, ks), (1, values, vs)):
+                for h in range(heads):
+                    x = _f32([turned[j][which][h] for j in range(at, last + 1)])
+                    part = np.ascontiguousarray(codes[p, t - before : t - before + size, h])
+                    scales[p, block, h] = _load().oracle_append_block(_fp(x), len(x), dim, before, _up(part), dim,
+                                                                      float(scales[p, block, h]))
+                    codes[p, t - before : t - before + size, h] = part
+    return keys, values, ks, vs, q
+
+
+def pages_attend(queries, keys, values, key_scales, value_scales, table, lens, starts=None, scale=None):
+    """Attention in 64 bits over codes [pages, page_tokens, heads, dim] and
+    scales [pages, blocks, heads]; NaN for tokens behind the last row's."""
+    table, lens = _i32(table), _i32(lens)
+    pages, page_tokens, heads, dim = keys.shape
+    size = page_tokens // key_scales.shape[1]
+    q = np.asarray(queries, np.float64)
+    tokens, q_heads, _ = q.shape
+    group = q_heads // heads
+    out = np.full(q.shape, np.nan)
+    f64p = ctypes.POINTER(ctypes.c_double)
+    for s in range(lens.size):
+        begin, n, first = _row_tokens(lens, starts, tokens, s)
+        top = max(first + n, 0)
+        at = np.arange(top)
+        nth = at // page_tokens
+        page = np.where(nth < table.shape[1], table[s, np.minimum(nth, max(table.shape[1] - 1, 0))]
+                        if table.shape[1] else -1, -1)
+        seen = ((page >= 0) & (page < pages)).astype(np.uint8)
+        page, slot = np.where(seen > 0, page, 0), at % page_tokens
+        if pages == 0:
+            page, seen = page[:0], seen[:0]
+            slot = slot[:0]
+        for h in range(heads):
+            kv = []
+            for codes, scales in ((keys, key_scales), (values, value_scales)):
+                x = code_values(codes[page, slot, h]).astype(np.float64)
+                kv.append(np.ascontiguousarray(x * scales[page, slot // size, h].astype(np.float64)[:, None]))
+            for i in range(n):
+                m = min(max(first + i + 1, 0), len(seen))
+                for j in range(h * group, (h + 1) * group):
+                    x, o = np.ascontiguousarray(q[begin + i, j]), np.empty(dim)
+                    _load().oracle_attend_query(x.ctypes.data_as(f64p), kv[0].ctypes.data_as(f64p),
+                                                kv[1].ctypes.data_as(f64p), _up(seen), m, dim,
+                                                dim**-0.5 if scale is None else scale, o.ctypes.data_as(f64p))
+                    out[begin + i, j] = o
+    return out

@@ -657,3 +657,153 @@ int32_t oracle_pages_compact(int32_t *table, uint64_t rows, uint64_t width, cons
         }
     return (int32_t)live;
 }
+
+/*
+ * A request's rules on one row of logits (as float; the caller rounds to the
+ * logits' type). touched[i] tells whether a rule reached token i.
+ */
+static int oracle_finite(float x) { return x - x == 0.0f; }
+
+void oracle_adjust_row(const float *logits, uint64_t vocab, const int32_t *history, int64_t held, int64_t prompt,
+                       float repetition, float presence, float frequency, const int32_t *bias_tokens,
+                       const float *bias, uint64_t biases, const uint32_t *allowed, float *out, uint8_t *touched)
+{
+    uint32_t *all = calloc(vocab ? vocab : 1, sizeof *all), *later = calloc(vocab ? vocab : 1, sizeof *later);
+    for (int64_t h = 0; h < held; ++h)
+        if (history[h] >= 0 && (uint64_t)history[h] < vocab) {
+            ++all[history[h]];
+            if (h >= prompt) ++later[history[h]];
+        }
+    for (uint64_t i = 0; i < vocab; ++i) {
+        float x = logits[i];
+        const uint32_t seen = all[i] != 0, made = later[i];
+        touched[i] = (uint8_t)seen;
+        if (seen && oracle_finite(repetition) && repetition > 0.0f) x = x > 0.0f ? x / repetition : x * repetition;
+        if (made) {
+            const float less = (oracle_finite(frequency) ? frequency : 0.0f) * (float)made;
+            const float y = x - less;
+            x = y - (oracle_finite(presence) ? presence : 0.0f);
+        }
+        for (uint64_t b = biases; b-- > 0;)
+            if (bias_tokens[b] >= 0 && (uint64_t)bias_tokens[b] == i) {
+                x = x + bias[b];
+                touched[i] = 1;
+                break;
+            }
+        if (allowed && !(allowed[i / 32] >> (i % 32) & 1u)) {
+            x = -INFINITY;
+            touched[i] = 1;
+        }
+        out[i] = x;
+    }
+    free(all);
+    free(later);
+}
+
+/* The value of an 8-bit code: sign, 4 bits of exponent (bias 7), 3 of fraction; 0x7f and 0xff are NaN. */
+float oracle_code_value(uint8_t code)
+{
+    const int e = code >> 3 & 15, f = code & 7;
+    if ((code & 0x7f) == 0x7f) return NAN;
+    const double m = e ? ldexp(8 + f, e - 10) : ldexp(f, -9);
+    return (float)(code & 0x80 ? -m : m);
+}
+
+/* The code nearest to x, ties to the even code; 448 is the largest magnitude. */
+uint8_t oracle_value_code(float x)
+{
+    const uint8_t sign = signbit(x) ? 0x80 : 0;
+    if (x != x) return 0x7f;
+    const double m = fabs((double)x);
+    if (m > 448.0) return (uint8_t)(sign | 0x7e);
+    int best = 0;
+    for (int c = 1; c < 0x7f; ++c) {
+        const double a = fabs(oracle_code_value((uint8_t)c) - m), b = fabs(oracle_code_value((uint8_t)best) - m);
+        if (a < b || (a == b && c % 2 == 0)) best = c;
+    }
+    return (uint8_t)(sign | best);
+}
+
+/* Element d of a head (float) rotated for a position. */
+static float oracle_rotated(const float *x, uint64_t d, const float *cos_row, const float *sin_row, uint64_t pairs,
+                            int interleaved)
+{
+    if (d >= 2 * pairs) return x[d];
+    const uint64_t pair = interleaved ? d / 2 : d % pairs;
+    const uint64_t ia = interleaved ? 2 * pair : pair, ib = interleaved ? 2 * pair + 1 : pairs + pair;
+    const float a = x[ia], b = x[ib], c = cos_row[pair], s = sin_row[pair];
+    if (d == ia) {
+        const float u = a * c, v = b * s;
+        return u - v;
+    }
+    const float u = b * c, v = a * s;
+    return u + v;
+}
+
+void oracle_rotate_head(const float *x, uint64_t dim, const float *cos_row, const float *sin_row, uint64_t pairs,
+                        int interleaved, float *out)
+{
+    for (uint64_t d = 0; d < dim; ++d) out[d] = oracle_rotated(x, d, cos_row, sin_row, pairs, interleaved);
+}
+
+/*
+ * n new heads (rotated, [n][dim] adjacent) into slots before .. before + n - 1
+ * of one block of an 8-bit cache: codes is the block's first slot, its slots
+ * `stride` bytes apart. Returns the block's scale.
+ */
+float oracle_append_block(const float *x, uint64_t n, uint64_t dim, uint64_t before, uint8_t *codes, uint64_t stride,
+                          float old)
+{
+    float m = 0.0f;
+    for (uint64_t i = 0; i < n * dim; ++i)
+        if (oracle_finite(x[i]) && fabsf(x[i]) > m) m = fabsf(x[i]);
+    int e = -100;
+    while ((double)m > ldexp(448.0, e)) ++e;
+    float scale = ldexpf(1.0f, e);
+    if (before) {
+        if (!(old > 0.0f && oracle_finite(old))) old = 0.0f;
+        if (old >= scale) {
+            scale = old;
+        } else {
+            const float ratio = old / scale;
+            for (uint64_t t = 0; t < before; ++t)
+                for (uint64_t d = 0; d < dim; ++d) {
+                    const float v = oracle_code_value(codes[t * stride + d]) * ratio;
+                    codes[t * stride + d] = oracle_value_code(v);
+                }
+        }
+    }
+    const float inv = 1.0f / scale;
+    for (uint64_t i = 0; i < n; ++i)
+        for (uint64_t d = 0; d < dim; ++d) {
+            const float v = x[i * dim + d] * inv;
+            codes[(before + i) * stride + d] = oracle_value_code(v);
+        }
+    return scale;
+}
+
+/*
+ * One query over n keys and values ([n][dim] doubles; seen[j] = 0 leaves j
+ * out), in 64 bits: the softmax's definition, zeros where nothing is seen.
+ */
+void oracle_attend_query(const double *q, const double *k, const double *v, const uint8_t *seen, uint64_t n,
+                         uint64_t dim, double scale, double *out)
+{
+    double *s = malloc((n ? n : 1) * sizeof *s), m = -INFINITY, l = 0.0;
+    for (uint64_t j = 0; j < n; ++j) {
+        double dot = 0.0;
+        for (uint64_t d = 0; d < dim; ++d) dot += q[d] * k[j * dim + d];
+        s[j] = dot * scale;
+        if (seen[j] && s[j] > m) m = s[j];
+    }
+    for (uint64_t d = 0; d < dim; ++d) out[d] = 0.0;
+    for (uint64_t j = 0; j < n; ++j) {
+        if (!seen[j]) continue;
+        const double w = exp(s[j] - m);
+        l += w;
+        for (uint64_t d = 0; d < dim; ++d) out[d] += w * v[j * dim + d];
+    }
+    if (l != 0.0)
+        for (uint64_t d = 0; d < dim; ++d) out[d] /= l;
+    free(s);
+}

@@ -37,6 +37,10 @@ _API = {
     "pages_fork",
     "pages_free",
     "pages_compact",
+    "adjust_logits",
+    "KVCache",
+    "pages_append",
+    "pages_attend",
     "check",
 }
 

@@ -28,14 +28,15 @@ OP_SCAN64 = 6
 OP_SCAN_HOST = 7
 OP_REDUCE = 8
 OP_PAGES = 9
+OP_ATTEND = 10
 
-F32, F16, BF16 = 0, 1, 2
+F32, F16, BF16, E4M3 = 0, 1, 2, 3
 MAX_VOCAB = 1 << 22
 
 _vp = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _int = ctypes.c_int
-
+_float = ctypes.c_float
 
 
 class PagePoolStruct(ctypes.Structure):
@@ -44,7 +45,37 @@ class PagePoolStruct(ctypes.Structure):
     _fields_ = [("planes", _vp), ("n_planes", _sz), ("pages", _sz), ("page_bytes", _sz), ("page_stride", _sz)]
 
 
+class LogitRulesStruct(ctypes.Structure):
+    """u32scan_logit_rules."""
+
+    _fields_ = [("history", _vp), ("history_width", _sz), ("history_stride", _sz), ("history_lens", _vp),
+                ("prompt_lens", _vp), ("repetition", _vp), ("presence", _vp), ("frequency", _vp),
+                ("bias_tokens", _vp), ("bias", _vp), ("biases", _sz), ("allowed", _vp), ("allowed_stride", _sz)]
+
+
+class KVCacheStruct(ctypes.Structure):
+    """u32scan_kv_cache."""
+
+    _fields_ = [("keys", _vp), ("values", _vp), ("type", _int), ("pages", _sz), ("page_tokens", _sz), ("heads", _sz),
+                ("dim", _sz), ("page_stride", _sz), ("token_stride", _sz), ("head_stride", _sz), ("key_scales", _vp),
+                ("value_scales", _vp), ("blocks", _sz), ("scale_stride", _sz)]
+
+
+class NewTokensStruct(ctypes.Structure):
+    """u32scan_new_tokens."""
+
+    _fields_ = [("tokens", _sz), ("type", _int), ("keys", _vp), ("key_token_stride", _sz), ("key_head_stride", _sz),
+                ("values", _vp), ("value_token_stride", _sz), ("value_head_stride", _sz), ("queries", _vp),
+                ("q_heads", _sz), ("query_token_stride", _sz), ("query_head_stride", _sz), ("queries_out", _vp),
+                ("out_token_stride", _sz), ("out_head_stride", _sz), ("cos", _vp), ("sin", _vp), ("positions", _sz),
+                ("pairs", _sz), ("interleaved", _int)]
+
+
 _pool = ctypes.POINTER(PagePoolStruct)
+_rules = ctypes.POINTER(LogitRulesStruct)
+_kv = ctypes.POINTER(KVCacheStruct)
+_new = ctypes.POINTER(NewTokensStruct)
+_rows = [_vp, _sz, _sz, _sz, _vp, _vp]  # table, stride, rows, width, lens, starts
 _table = [_vp, _sz, _sz, _sz, _vp, _vp, _sz, _sz]  # table, stride, rows, width, lens, refs, pages, page_tokens
 
 # name -> (restype, argtypes)
@@ -85,6 +116,9 @@ SIGNATURES = {
     "pages_fork": (_int, [*_table, _vp, _vp, _pool, _vp, _vp, _vp, _sz, _vp]),
     "pages_free": (_int, [*_table, _vp, _vp, _vp, _sz, _vp]),
     "pages_compact": (_int, [_pool, *_table, _vp, _vp, _vp, _sz, _vp]),
+    "adjust_logits": (_int, [_vp, _int, _sz, _sz, _sz, _vp, _sz, _rules, _vp]),
+    "pages_append": (_int, [_kv, *_rows, _vp, _new, _vp]),
+    "pages_attend": (_int, [_kv, *_rows, _sz, _vp, _int, _sz, _sz, _sz, _vp, _sz, _sz, _float, _vp, _sz, _vp]),
     "u32scan_test_scan_skip_publish": (_int, [_vp, _sz, _vp, _vp, _sz, ctypes.c_uint, ctypes.c_ulonglong, _vp]),
     "u32scan_test_segscan_skip_publish": (_int, [_vp, _vp, _sz, _vp, _sz, _vp, _vp, _sz, ctypes.c_uint,
                                                   ctypes.c_ulonglong, _vp]),

@@ -8,8 +8,8 @@ kernels; nothing here touches tensor data.
 U32 arrays are accepted as torch.int32 or torch.uint32 tensors (the bits are
 the same; wrapping u32 addition and two's-complement int32 addition agree).
 
-The library launches on the current device. sample_tokens and the pages_*
-calls refuse tensors, a stream or a workspace of another one.
+The library launches on the current device. sample_tokens, adjust_logits and
+the pages_* calls refuse tensors, a stream or a workspace of another one.
 """
 
 from __future__ import annotations
@@ -52,6 +52,10 @@ __all__ = [
     "pages_fork",
     "pages_free",
     "pages_compact",
+    "adjust_logits",
+    "KVCache",
+    "pages_append",
+    "pages_attend",
     "check",
 ]
 
@@ -612,8 +616,8 @@ def runs_owner_u32(ends: torch.Tensor, owner: torch.Tensor | None = None, capaci
     return owner
 
 
-def _new(n: int, dtype, device: torch.device, stream) -> torch.Tensor:
-    """An output for a call on `stream`, in memory of that stream: what the
+def _new(n, dtype, device: torch.device, stream) -> torch.Tensor:
+    """An output (of n elements or shape n) for a call on `stream`, in memory of that stream: what the
     current one gave back may still be in use there. The caller goes on with
     it on the current stream, so that one is noted too."""
     if stream is None or stream.cuda_stream == _stream_handle(None):
@@ -863,6 +867,320 @@ def pages_compact(pool: PagePool | None, table: torch.Tensor, lens: torch.Tensor
         None if pool is None else _pool_struct(pool, dev), *args, live_ptr,
         _arg(remap, "remap", torch.int32, pages, dev), ws.ptr, ws.nbytes, sh), "pages_compact")
     return live, remap
+
+
+def _matrix(t, name: str, dtype, rows: int, dev: int) -> tuple[int, int, int]:
+    """Pointer, width and row stride of a tensor [rows, width] whose rows'
+    elements are adjacent; (None, 0, 0) for None."""
+    if t is None:
+        return None, 0, 0
+    if not _tensor(t, name).is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    if t.dtype not in dtype:
+        raise TypeError(f"{name} must have dtype in {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must have two dimensions, the first of {rows}")
+    stride, step = t.stride()
+    if step != 1 and t.shape[1] > 1:
+        raise ValueError(f"the elements of a row of {name} must be adjacent")
+    return t.data_ptr(), t.shape[1], stride
+
+
+def adjust_logits(logits: torch.Tensor, *, history: torch.Tensor | None = None,
+                  history_lens: torch.Tensor | None = None, prompt_lens: torch.Tensor | None = None,
+                  repetition: torch.Tensor | None = None, presence: torch.Tensor | None = None,
+                  frequency: torch.Tensor | None = None, bias_tokens: torch.Tensor | None = None,
+                  bias: torch.Tensor | None = None, allowed: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """A request's rules applied to every row of logits [rows, vocab]
+    (float32, float16 or bfloat16; rows may be strided) before sample_tokens.
+
+    history [rows, width] (int32) holds each row's tokens, history_lens of them
+    (None: width), the first prompt_lens (None: 0) its prompt; tokens outside
+    the vocabulary are skipped. A token that occurs in it is divided by
+    repetition where its logit is above 0 and multiplied by it elsewhere; one
+    that occurs c times past the prompt loses frequency * c, then presence
+    (float32, one value a row). bias_tokens, bias [rows, n] (int32, float32) add
+    to the tokens they name (of a token named twice the last counts). A token whose bit in
+    allowed [rows, ceil(vocab / 32)] (int32 or uint32; token 32 w + j is bit j of
+    word w) is 0 becomes -inf.
+
+    Returns out, a new tensor unless one is given; out=logits works in place.
+    Exact: f32 operations in this order, each rounded alone, then rounded to
+    the type."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor (this library has no CPU path)")
+    kind = _LOGIT_TYPES.get(logits.dtype)
+    if kind is None:
+        raise TypeError(f"logits must have dtype in {tuple(_LOGIT_TYPES)}, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError("logits must have two dimensions, [rows, vocab]")
+    rows, vocab = logits.shape
+    row_stride, step = logits.stride()
+    if step != 1 and vocab > 1 and rows > 0:
+        raise ValueError("the elements of a row of logits must be adjacent")
+    dev = logits.get_device()
+    sh = _launch_stream(stream, dev)
+    if out is None:
+        out = _new((rows, vocab), logits.dtype, logits.device, stream)
+        out_ptr, out_stride = out.data_ptr(), vocab
+    else:
+        out_ptr, width, out_stride = _matrix(out, "out", (logits.dtype,), rows, dev)
+        if width != vocab:
+            raise ValueError("out must have the shape of logits")
+    f32, i32 = torch.float32, torch.int32
+    bias_ptr, biases, _ = _matrix(bias, "bias", (f32,), rows, dev)
+    named = _arg(bias_tokens, "bias_tokens", i32, rows * biases, dev) if bias is not None else None
+    if bias is None and bias_tokens is not None:
+        raise ValueError("bias_tokens needs bias")
+    if bias is not None and (not bias.is_contiguous() or bias_tokens.shape != bias.shape):
+        raise ValueError("bias_tokens and bias must be contiguous and agree in shape")
+    history_ptr, held, history_stride = _matrix(history, "history", (i32,), rows, dev)
+    mask_ptr, words, mask_stride = _matrix(allowed, "allowed", _U32_DTYPES, rows, dev)
+    if allowed is not None and words != (vocab + 31) // 32:
+        raise ValueError("allowed must have ceil(vocab / 32) words a row")
+    rules = _native.LogitRulesStruct(
+        history_ptr, held, history_stride, _optional(history_lens, "history_lens", i32, rows, dev),
+        _optional(prompt_lens, "prompt_lens", i32, rows, dev), _optional(repetition, "repetition", f32, rows, dev),
+        _optional(presence, "presence", f32, rows, dev), _optional(frequency, "frequency", f32, rows, dev), named,
+        bias_ptr, biases, mask_ptr, mask_stride)
+    _native.check(_native.lib().adjust_logits(logits.data_ptr(), kind, rows, vocab, row_stride, out_ptr, out_stride,
+                                              rules, sh), "adjust_logits")
+    return out
+
+
+_CACHE_TYPES = {**_LOGIT_TYPES, torch.float8_e4m3fn: _native.E4M3}
+
+
+class KVCache:
+    """One layer's keys and values in a paged cache, for pages_append and
+    pages_attend.
+
+    keys, values: CUDA tensors [pages, page_tokens, heads, dim] of one shape,
+    dtype (float32, float16, bfloat16 or float8_e4m3fn) and strides, with a
+    head's elements adjacent; views of a PagePool's planes, say. With
+    float8_e4m3fn, key_scales and value_scales (float32 [pages, blocks, heads],
+    a page's scales adjacent, one stride for both) hold a scale for every
+    block of page_tokens / blocks tokens and head: a value is its code times
+    its scale. To let the pages_* calls move scales with their codes, make
+    both views of one page of bytes. Keeps the tensors alive; make it once a
+    layer.
+    """
+
+    def __init__(self, keys: torch.Tensor, values: torch.Tensor, key_scales: torch.Tensor | None = None,
+                 value_scales: torch.Tensor | None = None):
+        for name, t in (("keys", keys), ("values", values)):
+            if not _tensor(t, name).is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+            if t.dtype not in _CACHE_TYPES:
+                raise TypeError(f"{name} must have dtype in {tuple(_CACHE_TYPES)}, got {t.dtype}")
+            if t.dim() != 4:
+                raise ValueError(f"{name} must have four dimensions, [pages, page_tokens, heads, dim]")
+        self.device = keys.device
+        if (keys.shape != values.shape or keys.stride() != values.stride() or keys.dtype != values.dtype
+                or keys.device != values.device):
+            raise ValueError("keys and values must agree in shape, strides, dtype and device")
+        if keys.stride(3) != 1 and keys.shape[3] > 1:
+            raise ValueError("the elements of a head must be adjacent")
+        pages, page_tokens, heads, dim = keys.shape
+        # sizes of which there is one need no stride, and torch keeps any there
+        strides = [s if n > 1 else 0 for s, n in zip(keys.stride()[:3], keys.shape[:3])]
+        spans = sorted((s, n) for s, n in zip(strides, keys.shape[:3]) if n > 1)
+        reach = dim
+        for s, n in spans:
+            if s < reach:
+                raise ValueError("a cache's elements must not overlap")
+            reach = s * (n - 1) + reach
+        coded = keys.dtype is torch.float8_e4m3fn
+        if coded != (key_scales is not None) or coded != (value_scales is not None):
+            raise ValueError("key_scales and value_scales belong to a cache of float8_e4m3fn")
+        blocks = scale_stride = 0
+        if coded:
+            for name, t in (("key_scales", key_scales), ("value_scales", value_scales)):
+                if not _tensor(t, name).is_cuda or t.device != self.device:
+                    raise ValueError(f"{name} must be on the keys' device")
+                if t.dtype is not torch.float32:
+                    raise TypeError(f"{name} must have dtype torch.float32, got {t.dtype}")
+                if t.dim() != 3 or t.shape[0] != pages or t.shape[2] != heads:
+                    raise ValueError(f"{name} must have the shape [pages, blocks, heads]")
+                if pages > 0 and not t[0].is_contiguous():
+                    raise ValueError(f"a page's {name} must be adjacent")
+            blocks = key_scales.shape[1]
+            if value_scales.shape != key_scales.shape or (pages > 1 and value_scales.stride(0) != key_scales.stride(0)):
+                raise ValueError("key_scales and value_scales must agree in shape and strides")
+            if blocks == 0 or page_tokens % blocks:
+                raise ValueError("a page's tokens must fall into equal blocks")
+            scale_stride = key_scales.stride(0) if pages > 1 else 0
+            if pages > 1 and scale_stride < blocks * heads:
+                raise ValueError("a cache's scales must not overlap")
+        self.keys, self.values, self.key_scales, self.value_scales = keys, values, key_scales, value_scales
+        self.dtype, self.heads, self.dim = keys.dtype, heads, dim
+        self.struct = _native.KVCacheStruct(
+            keys.data_ptr(), values.data_ptr(), _CACHE_TYPES[keys.dtype], pages, page_tokens, heads, dim, *strides,
+            key_scales.data_ptr() if coded else None, value_scales.data_ptr() if coded else None, blocks, scale_stride)
+
+
+def _cache_rows(cache, table, lens, starts, tokens: int):
+    """The checked leading arguments of the calls on a KVCache, and their
+    device."""
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+    dev = cache.device.index
+    ptr, width, stride = _matrix(_tensor(table, "table"), "table", (torch.int32,), table.shape[0] if table.dim() else 0,
+                                 dev)
+    rows = table.shape[0]
+    if rows <= 1:
+        stride = width
+    elif stride < width:
+        raise ValueError("the rows of table must not overlap")
+    lens_ptr = _arg(lens, "lens", torch.int32, rows, dev)
+    if lens.numel() != rows:
+        raise ValueError("lens must hold one length for every row of table")
+    if starts is not None:
+        starts_ptr = _arg(starts, "starts", torch.int32, rows + 1, dev)
+    elif tokens != rows:
+        raise ValueError("without starts there must be one token for every row of table")
+    else:
+        starts_ptr = None
+    return cache.struct, ptr, stride, rows, width, lens_ptr, starts_ptr
+
+
+def _heads_arg(t, name: str, dtype, tokens: int, heads: int | None, dim: int, dev: int):
+    """Pointer and strides of a tensor [tokens, heads, dim] whose heads'
+    elements are adjacent."""
+    if not _tensor(t, name).is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must have the shape [{tokens}, {'heads' if heads is None else heads}, {dim}]")
+    token_stride, head_stride, step = t.stride()
+    if step != 1 and dim > 1 and t.numel():
+        raise ValueError(f"the elements of a head of {name} must be adjacent")
+    return t.data_ptr(), token_stride if tokens > 1 else 0, head_stride if shape[1] > 1 else 0
+
+
+def _distinct(t, name: str) -> None:
+    """Refuses an output whose elements share memory (heads and tokens in
+    either order)."""
+    (tokens, heads, dim), (ts, hs, _) = t.shape, t.stride()
+    small, n = (hs, heads) if heads > 1 and (tokens <= 1 or hs <= ts) else (ts, tokens)
+    big = ts if (small, n) == (hs, heads) else hs
+    reach = dim if n <= 1 else (n - 1) * small + dim
+    both = tokens > 1 and heads > 1
+    if t.numel() and ((n > 1 and small < dim) or (both and big < reach)):
+        raise ValueError(f"the heads of {name} must not overlap")
+
+
+def pages_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_keys: torch.Tensor,
+                 new_values: torch.Tensor, *, starts: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                 cos: torch.Tensor | None = None, sin: torch.Tensor | None = None, interleaved: bool = False,
+                 queries: torch.Tensor | None = None, queries_out: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor | None:
+    """Writes new keys and values [tokens, heads, dim] (float32, float16 or
+    bfloat16) into the pages that pages_fork gave their rows, keys rotated by
+    their position on the way, and returns the rotated queries.
+
+    Row s has the tokens starts[s] .. starts[s + 1] - 1 (int32 [rows + 1];
+    None: one token a row), the last of its lens[s]. cos, sin (float32
+    [positions, pairs]) hold each position's angles; element i of a head pairs
+    with pairs + i, or 2 i with 2 i + 1 when interleaved, and elements from 2
+    pairs on stay. A cache of float8_e4m3fn gets a power of two for every
+    block's scale, the least under which the block's largest magnitude fits;
+    when new tokens raise the scale of a block that holds older ones, those are
+    rounded to it. Other caches have the tokens' dtype.
+
+    Rows with status[s] < 0 (pages_fork's answer) are left as they were, and so
+    are tokens whose position has no page or no angles; tokens behind the
+    last row's are ignored. queries [tokens, q_heads, dim], rotated likewise,
+    go to queries_out (a new tensor by default; queries itself works in place)."""
+    tokens = new_keys.shape[0] if _tensor(new_keys, "new_keys").dim() else 0
+    args = _cache_rows(cache, table, lens, starts, tokens)
+    dev, heads, dim = cache.device.index, cache.heads, cache.dim
+    sh = _launch_stream(stream, dev)
+    dtype = new_keys.dtype
+    kind = _LOGIT_TYPES.get(dtype)
+    if kind is None:
+        raise TypeError(f"new_keys must have dtype in {tuple(_LOGIT_TYPES)}, got {dtype}")
+    if cache.dtype is not torch.float8_e4m3fn and cache.dtype is not dtype:
+        raise TypeError(f"new_keys must have the cache's dtype {cache.dtype}, got {dtype}")
+    k = _heads_arg(new_keys, "new_keys", dtype, tokens, heads, dim, dev)
+    v = _heads_arg(new_values, "new_values", dtype, tokens, heads, dim, dev)
+    f32 = torch.float32
+    cos_ptr, pairs, _ = _matrix(cos, "cos", (f32,), cos.shape[0] if isinstance(cos, torch.Tensor) and cos.dim() else 0,
+                                dev)
+    positions = 0
+    sin_ptr = None
+    if cos is not None:
+        positions = cos.shape[0]
+        sin_ptr = _arg(sin, "sin", f32, positions * pairs, dev)
+        if not cos.is_contiguous() or sin.shape != cos.shape:
+            raise ValueError("cos and sin must be contiguous and agree in shape")
+        if 2 * pairs > dim:
+            raise ValueError("cos and sin have more pairs than a head")
+    elif sin is not None:
+        raise ValueError("sin needs cos")
+    q, q_heads, o = (None, 0, 0), 0, (None, 0, 0)
+    if queries is not None:
+        q = _heads_arg(queries, "queries", dtype, tokens, None, dim, dev)
+        q_heads = queries.shape[1]
+        if queries_out is None:
+            queries_out = _new((tokens, q_heads, dim), dtype, cache.device, stream)
+        o = _heads_arg(queries_out, "queries_out", dtype, tokens, q_heads, dim, dev)
+        _distinct(queries_out, "queries_out")
+    elif queries_out is not None:
+        raise ValueError("queries_out needs queries")
+    new = _native.NewTokensStruct(tokens, kind, *k, *v, q[0], q_heads, q[1], q[2], *o, cos_ptr, sin_ptr, positions,
+                                  pairs, bool(interleaved))
+    _native.check(_native.lib().pages_append(*args, _optional(status, "status", torch.int32, args[3], dev), new, sh),
+                  "pages_append")
+    return queries_out
+
+
+def pages_attend(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, queries: torch.Tensor, *,
+                 starts: torch.Tensor | None = None, scale: float | None = None, out: torch.Tensor | None = None,
+                 stream=None, workspace: Workspace | None = None) -> torch.Tensor:
+    """Attention of queries [tokens, q_heads, dim] (float16 or bfloat16) over
+    their rows' tokens in a cache of float8_e4m3fn: every token sees those at
+    positions up to its own, query head h reads key head h // (q_heads //
+    heads). Rows, starts and positions as pages_append; scale multiplies the
+    products (None: dim ** -0.5). dim is a multiple of 16 up to 256; a cache's
+    addresses and strides are multiples of 16 bytes, and so are the queries'.
+    A query that sees no token gets zeros. Returns out (a new tensor by
+    default; tokens behind the last row's are left alone in it)."""
+    shape = _tensor(queries, "queries").shape
+    tokens = shape[0] if len(shape) else 0
+    args = _cache_rows(cache, table, lens, starts, tokens)
+    dev, dim = cache.device.index, cache.dim
+    sh = _launch_stream(stream, dev)
+    if cache.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"the cache must have dtype torch.float8_e4m3fn, got {cache.dtype}")
+    dtype = queries.dtype
+    if dtype is not torch.float16 and dtype is not torch.bfloat16:
+        raise TypeError(f"queries must have dtype torch.float16 or torch.bfloat16, got {dtype}")
+    q = _heads_arg(queries, "queries", dtype, tokens, None, dim, dev)
+    q_heads = shape[1]
+    if cache.heads == 0 or q_heads == 0 or q_heads % cache.heads:
+        raise ValueError("queries must have a multiple of the cache's heads")
+    if out is None:
+        out = _new((tokens, q_heads, dim), dtype, cache.device, stream)
+    o = _heads_arg(out, "out", dtype, tokens, q_heads, dim, dev)
+    _distinct(out, "out")
+    if workspace is None:
+        workspace = Workspace.get(_native.OP_ATTEND, tokens, cache.device, sh)
+    elif workspace.buf.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}")
+    _native.check(_native.lib().pages_attend(
+        *args, tokens, q[0], _LOGIT_TYPES[dtype], q_heads, q[1], q[2], *o, dim**-0.5 if scale is None else scale,
+        workspace.ptr, workspace.nbytes, sh), "pages_attend")
+    return out
 
 
 def check(stream=None, workspace: Workspace | None = None, device=None) -> int:

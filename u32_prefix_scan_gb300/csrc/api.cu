@@ -50,6 +50,8 @@ extern "C" size_t u32scan_workspace_bytes(int op, size_t n) {
         return reduce_workspace_bytes();
     case U32SCAN_OP_PAGES:
         return pages_workspace_bytes(n);
+    case U32SCAN_OP_ATTEND:
+        return attend_workspace_bytes();
     default:
         return 0;
     }
