@@ -32,10 +32,10 @@
 // and packing those 7 us: bound by latency, the launches that wait for one
 // another and in each a chain of loads (row, entry, count).
 #include <cstdint>
-#include <mutex>
 #include <cuda_runtime.h>
 
 #include "internal.cuh"
+#include "launch.cuh"
 
 namespace u32scan {
 
@@ -626,38 +626,7 @@ compact_act_kernel(CompactArgs a, PagesWs w, Pool pool, unsigned int row_blocks,
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-static std::mutex g_pages_mu;
-static int g_pages_sms[64];
-
-static int sm_count(int *sms) {
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return U32SCAN_ECUDA;
-    std::lock_guard<std::mutex> lock(g_pages_mu);
-    if (g_pages_sms[dev] == 0 &&
-        cudaDeviceGetAttribute(&g_pages_sms[dev], cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return U32SCAN_ECUDA;
-    *sms = g_pages_sms[dev];
-    return U32SCAN_OK;
-}
-
 static int launched() { return cudaGetLastError() == cudaSuccess ? U32SCAN_OK : U32SCAN_ECUDA; }
-
-// A launch that may be set up while the one before it in the stream (of the
-// same call) still runs, and waits for its end before it reads anything
-// (forking 16 rows 8.2 and 7.7 us, of 2048 rows 16.8 and 16.0).
-template <typename... P, typename... A>
-static void launch_next(void (*kernel)(P...), unsigned int grid, int threads, cudaStream_t s, A... args) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3((unsigned int)threads);
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kernel, P(args)...);  // launched() sees its error
-}
 
 static bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
 
