@@ -131,6 +131,20 @@ def test_long_and_many(u, rows, length):
     c.check(call(u, c.gpu()))
 
 
+@pytest.mark.parametrize("length,heads,drafts,group,dim", [(60000, 1, 5, 7, 64), (50000, 2, 1, 8, 128), (30000, 4, 3, 5, 128)])
+def test_one_long_row_in_many_parts(u, length, heads, drafts, group, dim):
+    """A row's tiles of queries cut into more parts than are joined at a time."""
+    c = Case(length, [length], [drafts], heads=heads, group=group, dim=dim, page_tokens=16)
+    c.check(call(u, c.gpu()))
+
+
+@pytest.mark.parametrize("rows", [255, 256, 257, 700])
+def test_rows_more_than_threads(u, rows):
+    lens = np.arange(rows) * 37 % 90
+    c = Case(rows, lens, heads=4, group=1, dim=64, page_tokens=8)
+    c.check(call(u, c.gpu()))
+
+
 @pytest.mark.parametrize("counts", [[1, 1, 1], [5, 1, 3], [0, 7, 0], [16, 33, 2], [70, 9, 80]])
 @pytest.mark.parametrize("group,dim", [(1, 64), (4, 128), (7, 64), (8, 256), (2, 96)])
 def test_drafts(u, counts, group, dim):

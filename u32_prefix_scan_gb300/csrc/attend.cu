@@ -20,10 +20,10 @@
 // w is rounded to f16 (2^-11 relative; products and sums are f32): the
 // codes it meets have 4 bits, and the result's type 8 or 11.
 //
-// The work of all rows is one line of units (64 tokens of one row, key head
-// and tile of queries), cut into equal pieces for the blocks, however ragged
-// the rows are. A tile whose units fall to several blocks is joined from
-// their partial sums, in order, by a second launch.
+// The work of all rows is one line of units (a tile of 16 tokens for each of a
+// block's four warps, of heads beside each other), cut into equal pieces for the blocks, however ragged
+// the rows are. Where a tile of queries falls to several blocks, the one that
+// comes last joins their partial sums, in order.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -35,18 +35,22 @@
 
 namespace u32scan {
 
-constexpr int kQThreads = 128;
-constexpr int kQWarps = kQThreads / 32;
+#ifndef WL
+#define WL 4
+#endif
+#ifndef BL
+#define BL 2
+#endif
 constexpr int kTile = 16;                 // tokens of a warp at a time
-constexpr int kUnit = kTile * kQWarps;    // tokens of a unit
 constexpr int kMaxDim = 256;
-constexpr unsigned int kMaxBlocks = 640;  // bounds the workspace
+constexpr unsigned int kMaxBlocks = 304;  // bounds the workspace
+constexpr unsigned int kLevels = 4;       // of piece sizes, each with a piece for every block
 constexpr uint32_t kTileCost = 2;         // what a tile of queries takes beside its units, in units
 constexpr uint64_t kLeastUnits = kTileCost + 2;  // of a block's piece
-constexpr int kMaxElements = 2048;        // queries x dimensions of a tile of queries
-constexpr int kMaxTileRows = 32;
+constexpr int kMaxElements = 4096;        // heads x queries x dimensions of a tile of queries
+constexpr int kMaxPairs = 64;             // its heads x queries
 constexpr float kNoMax = -1e30f;
-constexpr float kMaxWeight = 256.0f, kMaxP = 4294967296.0f;
+constexpr float kMaxWeight = 256.0f, kMaxAbove = 32.0f;
 
 struct AttendArgs {
     RowsView v;
@@ -58,19 +62,13 @@ struct AttendArgs {
     const void *queries;
     void *out;
     uint64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    uint32_t pair_heads;  // log2 of the key heads that a block's warps have beside each other: 0, 1 or 2
     float scale;  // times log2(e)
-    bool boxes;   // 16 tokens from a multiple of 16 on lie in one page
+    bool wide_blocks;  // and in one block
     WsHeader *hdr;
-    float *partial;      // [2 blocks][elements of a tile]
-    float2 *partial_ml;  // [2 blocks][rows of a tile]: reference and sum
-    struct Boundary *boundary;
-};
-
-// Where a block's piece begins, for the launch that joins.
-struct Boundary {
-    uint32_t row, head, tile, unit;  // unit: of the tile's, the first in this piece; 0: nothing to join here
-    uint64_t units, per;
-    uint64_t pad[2];
+    float4 *partial;     // [2 pieces][heads][sums of a tile of queries, as the lanes hold them]
+    float2 *partial_ml;  // [2 pieces][heads][queries of a tile]: reference and sum
+    unsigned long long *arrived, clear_words;  // the workspace's tile words
 };
 
 template <typename T>
@@ -157,14 +155,19 @@ struct RowUnits {
     uint32_t units, tiles;
 };
 
-__device__ __forceinline__ RowUnits row_units(const AttendArgs &a, uint64_t s, uint32_t tile_rows) {
+// A unit is a tile of 16 tokens for each warp: the warps take 1, 2 or 4 heads, and of each as many tiles beside each
+// other as there are warps left.
+__device__ __forceinline__ uint32_t unit_of(const AttendArgs &a, int warps) { return (uint32_t)(kTile * warps) >> a.pair_heads; }
+
+__device__ __forceinline__ RowUnits row_units(const AttendArgs &a, uint64_t s, uint32_t tile_rows, int warps) {
     RowUnits r;
     tokens_of(a.v, s, &r.begin, &r.n);
     const int32_t len = a.v.lens[s];
     r.len = len;
     const uint64_t placed = a.v.pages == 0 ? 0 : a.v.width * a.v.page_tokens.d;
     r.limit = (uint32_t)(len <= 0 ? 0 : (uint64_t)len < placed ? (uint64_t)len : placed);
-    r.units = r.n == 0 ? 0u : r.limit <= kUnit ? 1u : (r.limit + kUnit - 1) / kUnit;
+    const uint32_t unit_tokens = unit_of(a, warps);
+    r.units = r.n == 0 ? 0u : r.limit <= unit_tokens ? 1u : (r.limit - 1) / unit_tokens + 1;
     r.tiles = (uint32_t)((r.n * a.group.d + tile_rows - 1) / tile_rows);
     return r;
 }
@@ -175,18 +178,22 @@ __device__ __forceinline__ RowUnits row_units(const AttendArgs &a, uint64_t s, u
 template <int DP, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
+    static constexpr bool kSmall = DP * NT <= 128;  // 128 registers a thread do, else 255
+    static constexpr int kWarps = kSmall ? 8 : WL, kThreads = 32 * kWarps;
+    static constexpr uint32_t kMostPaired = kSmall ? 2 : 1;  // log2 of the heads beside each other
+    static constexpr int kVectors = NT * (DP / 16) * 32;     // a tile's sums, four at a time
     static constexpr int kPitch = DP >= 128 ? 128 : 64;
     static constexpr int kHalves = DP / kPitch;
     static constexpr int kHalfBytes = kTile * kPitch;
     static constexpr int kKeyChunks = DP / 64;                    // of 16 bytes, for each of a lane's two keys
     static constexpr int kValueBytes = DP >= 128 ? 16 : 8;        // for each of a lane's four values and each half
-    static constexpr int kBlocks = DP * NT <= 128 ? 4 : 3;        // an SM
+    static constexpr int kBlocks = kSmall ? 2 : BL;               // an SM
     static constexpr int kStageBytes = DP * 2 * kTile;            // of a warp
-    static constexpr int kStages = (228 * 1024 / kBlocks - 4096) / (kQWarps * (kStageBytes + 128));
-    static constexpr int kRing = kStages * kQWarps * kStageBytes;
-    static constexpr int kShared = kRing + kStages * kQWarps * (128 + 8) + 1024;  // scales, barriers, alignment
-    static_assert(kQWarps * (kRows * DP + 2 * kRows) * 4 <= kRing, "the warps' sums take the ring's place");
-    static_assert(kRows * DP <= kMaxElements && kRows <= kMaxTileRows, "the workspace's slots");
+    static constexpr int kStages = (228 * 1024 / kBlocks - 4096) / (kWarps * (kStageBytes + 128));
+    static constexpr int kRing = kStages * kWarps * kStageBytes;
+    static constexpr int kShared = kRing + kStages * kWarps * (128 + 8) + 1024;  // scales, barriers, alignment
+    static_assert(kWarps * (kRows * DP + 2 * kRows) * 4 <= kRing, "the warps' sums take the ring's place");
+    static_assert((kRows * DP << kMostPaired) <= kMaxElements && (kRows << kMostPaired) <= kMaxPairs, "the workspace's slots");
     static_assert(kBlocks * (kShared + 1024 + 256) <= 228 * 1024, "blocks of an SM");
 
     // Where 16-byte chunk c of row r lies in a half.
@@ -200,83 +207,215 @@ struct Shape {
     }
 };
 
-// The piece [*from, *to) of block `block`, and the row and unit in it where it begins.
-struct Piece {
-    uint64_t from, to, per;
-    uint64_t row, unit;
+// The line of all rows' units and its pieces. Blocks do not read equally fast (equal pieces of one call took from 42 to
+// 103 us), so every block starts with a piece of half its share and draws the others, of a quarter, an eighth and an
+// eighth, as it gets done; a short line has one piece a block.
+template <int WARPS>
+struct Line {
+    static constexpr int kThreads = 32 * WARPS;
+    uint64_t total, begin[kLevels], size[kLevels];
+    uint32_t pieces;        // that are not empty
+    uint64_t share, until;  // of row threadIdx.x: its units, and those up to its end
+
+    __device__ static uint64_t share_of(const AttendArgs &a, uint64_t s, uint32_t tile_rows) {
+        if (s >= a.v.rows) return 0;
+        const RowUnits r = row_units(a, s, tile_rows, WARPS);
+        return r.units ? ((uint64_t)r.units + kTileCost) * r.tiles * (a.heads >> a.pair_heads) : 0;
+    }
+
+    // The sum of x up to this thread's, and (into *all) over the block.
+    __device__ static uint64_t scan(uint64_t x, uint64_t *sums, uint64_t *all) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        __syncthreads();  // the sums were read
+        if (lane == 31) sums[warp] = x;
+        __syncthreads();
+        *all = 0;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) x += sums[w];
+            *all += sums[w];
+        }
+        return x;
+    }
+
+    __device__ void measure(const AttendArgs &a, uint32_t tile_rows, uint64_t *sums) {
+        share = share_of(a, threadIdx.x, tile_rows);
+        uint64_t mine = share;
+        for (uint64_t s = threadIdx.x + kThreads; s < a.v.rows; s += kThreads) mine += share_of(a, s, tile_rows);
+        until = scan(mine, sums, &total);  // (a row's, where there is one for each thread)
+        const uint64_t blocks = gridDim.x;
+        const bool one = total <= blocks * (kLeastUnits << kLevels);
+#pragma unroll
+        for (uint32_t i = 0; i < kLevels; ++i) {
+            const uint32_t part = one ? 0 : i + 1 < kLevels ? i + 1 : i;  // 2^-part of a block's share
+            size[i] = (total + (blocks << part) - 1) / (blocks << part);
+            if (size[i] < kLeastUnits) size[i] = kLeastUnits;
+            begin[i] = i == 0 ? 0 : begin[i - 1] + blocks * size[i - 1];
+        }
+        pieces = total ? piece_at(total - 1) + 1 : 0;
+    }
+
+    __device__ uint64_t begin_of(uint32_t piece) const {
+        const uint32_t i = piece / gridDim.x;
+        if (i >= kLevels) return total;
+        uint64_t at = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kLevels; ++k)
+            if (k == i) at = begin[k] + (uint64_t)(piece - k * gridDim.x) * size[k];
+        return at < total ? at : total;
+    }
+
+    __device__ uint32_t piece_at(uint64_t at) const {
+        uint32_t i = 0;
+        uint64_t from = 0, by = size[0];
+#pragma unroll
+        for (uint32_t k = 1; k < kLevels; ++k)
+            if (at >= begin[k]) i = k, from = begin[k], by = size[k];
+        return i * gridDim.x + (uint32_t)((at - from) / by);
+    }
+
+    // The row that holds place `at` of the line, and which of its units that is.
+    __device__ void locate(const AttendArgs &a, uint32_t tile_rows, uint64_t at, uint64_t *sums, uint64_t *found) const {
+        if (a.v.rows <= kThreads) {
+            if (at < until && at >= until - share) found[0] = threadIdx.x, found[1] = at - (until - share);
+        } else {
+            uint64_t before = 0, all;
+            for (uint64_t base = 0; base < a.v.rows && before <= at; base += kThreads, before += all) {
+                const uint64_t x = share_of(a, base + threadIdx.x, tile_rows), end = before + scan(x, sums, &all);
+                if (at < end && at >= end - x) found[0] = base + threadIdx.x, found[1] = at - (end - x);
+            }
+        }
+        __syncthreads();
+    }
 };
 
-__device__ Piece piece_of(const AttendArgs &a, uint32_t tile_rows, uint64_t block, uint64_t blocks) {
-    __shared__ uint64_t sums[kQWarps], found[2];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint64_t rows = a.v.rows;
-    auto share = [&](uint64_t s) -> uint64_t {
-        if (s >= rows) return 0;
-        const RowUnits r = row_units(a, s, tile_rows);
-        return r.units ? ((uint64_t)r.units + kTileCost) * r.tiles * a.heads : 0;
-    };
-    auto warp_sum = [&](uint64_t x) {
-        for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        return x;
-    };
-    uint64_t mine = 0;
-    for (uint64_t s = threadIdx.x; s < rows; s += kQThreads) mine += share(s);
-    mine = warp_sum(mine);
-    if (lane == 0) sums[warp] = mine;
-    __syncthreads();
-    uint64_t total = 0;
-    for (int w = 0; w < kQWarps; ++w) total += sums[w];
-    Piece p;
-    p.per = (total + blocks - 1) / blocks;
-    if (p.per < kLeastUnits) p.per = kLeastUnits;
-    p.from = block * p.per;
-    p.to = p.from + p.per < total ? p.from + p.per : total;
-    p.row = p.unit = 0;
-    if (p.from >= total) return p;
-    uint64_t before = 0;
-    for (uint64_t base = 0; base < rows; base += kQThreads) {
-        const uint64_t x = share(base + threadIdx.x);
-        uint64_t incl = x;
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-        }
-        __syncthreads();  // sums and found were read
-        if (lane == 31) sums[warp] = incl;
-        if (threadIdx.x == 0) found[0] = ~0ull;
-        __syncthreads();
-        uint64_t all = 0;
-        incl += before;
-        for (int w = 0; w < kQWarps; ++w) {
-            if (w < warp) incl += sums[w];
-            all += sums[w];
-        }
-        if (p.from < incl && p.from >= incl - x) {
-            found[0] = base + threadIdx.x;
-            found[1] = p.from - (incl - x);
-        }
-        before += all;
-        __syncthreads();
-        if (found[0] != ~0ull) break;
-    }
-    p.row = found[0];
-    p.unit = found[1];
-    return p;
+// Counts a block in at a word of the workspace: tags grow from launch to launch (and the words are cleared before they
+// start again), so the larger of the word and this launch's tag is a count of this launch. (Of 63 blocks at a time
+// each takes its turn once; by compare-and-swap, where one of all that try succeeds, they took 50 us.)
+__device__ __forceinline__ uint32_t count_arrival(unsigned long long *word, unsigned long long tag) {
+    atomicMax(word, tag);
+    return (uint32_t)atomicAdd(word, 1ull) + 1u;
 }
 
 // Row r of a tile of queries: its token of the row and query head of the key head.
-__device__ __forceinline__ bool query_of(const AttendArgs &a, const RowUnits &row, uint32_t tile, uint32_t tile_rows,
+__device__ __forceinline__ bool query_of(const AttendArgs &a, int64_t n, uint32_t tile, uint32_t tile_rows,
                                          uint32_t r, uint32_t *token, uint32_t *j) {
-    const uint64_t f = (uint64_t)tile * tile_rows + r;
-    if (f >= (uint64_t)row.n * a.group.d) return false;
-    // (a tile of n * group rows may pass 2^31; the divisor's bound is that)
-    *token = f < (1ull << 31) ? divide((uint32_t)f, a.group) : (uint32_t)(f / a.group.d);
-    *j = (uint32_t)(f - (uint64_t)*token * a.group.d);
+    const uint32_t f = tile * tile_rows + r;  // (tokens times the group stay below 2^31)
+    if (f >= (uint64_t)n * a.group.d) return false;
+    *token = divide(f, a.group);
+    *j = f - *token * a.group.d;
     return true;
 }
 
+// Writes vector v of head h's sums of a tile of queries: x[2 k + j] is dimension d + k of query 2 t + j.
 template <typename T, int DP, int NT>
-__global__ void __launch_bounds__(kQThreads, Shape<DP, NT>::kBlocks)
+__device__ __forceinline__ void write_out(const AttendArgs &a, const RowUnits &row, uint32_t head, uint32_t tile, uint32_t v,
+                                          const float4 &x, const float (&sum)[2]) {
+    using S = Shape<DP, NT>;
+    const uint32_t lane = v % 32, i = v / 32 % (DP / 16), nt = v / 32 / (DP / 16), g = lane >> 2, t = lane & 3;
+    constexpr uint32_t kPer = S::kValueBytes / 2;  // vectors of a half
+    const uint32_t d = S::kPitch * (i / kPer) + S::kValueBytes * (DP >= 128 ? g >> 1 | (g & 1) << 2 : g) + 2 * (i % kPer);
+    if (d >= a.dim) return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        uint32_t token, q;
+        if (!query_of(a, row.n, tile, S::kRows, nt * 8 + 2 * t + j, &token, &q)) continue;
+        T *to = static_cast<T *>(a.out) + (uint64_t)(row.begin + token) * a.out_token_stride +
+                ((uint64_t)head * a.group.d + q) * a.out_head_stride + d;
+        const float y[2] = {j ? x.y : x.x, j ? x.w : x.z};
+        to[0] = QType<T>::put(sum[j] == 0.0f ? 0.0f : y[0] / sum[j]);
+        to[1] = QType<T>::put(sum[j] == 0.0f ? 0.0f : y[1] / sum[j]);
+    }
+}
+
+// Joins the parts of a tile of queries that pieces first .. first + parts - 1 left, in order: each part's reference and
+// sum into shared memory, their maxima, sums and weights, then the parts, weighted, four vectors a thread at a time.
+template <typename T, int DP, int NT>
+__device__ void join_parts(const AttendArgs &a, uint8_t *shared, uint64_t first, uint32_t parts, const RowUnits &row,
+                           uint32_t group, uint32_t tile) {
+    using S = Shape<DP, NT>;
+    const uint32_t pairs = S::kRows << a.pair_heads;  // of a head and a query
+    float2 *const total = reinterpret_cast<float2 *>(shared), *const each = total + kMaxPairs;
+    const uint32_t room = (S::kRing / sizeof(float2) - kMaxPairs) / pairs;  // parts at a time
+    auto from = [&](uint32_t part) { return (2 * (first + part) + (part == 0 ? 1 : 0)) << a.pair_heads; };
+    auto fetch = [&](uint32_t p0, uint32_t n) {
+        __syncthreads();
+#pragma unroll 4
+        for (uint32_t e = threadIdx.x; e < n * pairs; e += S::kThreads)
+            each[e] = __ldcg(a.partial_ml + from(p0 + e / pairs) * S::kRows + e % pairs);
+        __syncthreads();
+    };
+    auto weigh = [&](uint32_t n) {
+        for (uint32_t i = threadIdx.x; i < pairs; i += S::kThreads) {
+            const float top = total[i].x;
+#pragma unroll 4
+            for (uint32_t k = 0; k < n; ++k) each[k * pairs + i].x = exp2_approx(each[k * pairs + i].x - top);
+        }
+        __syncthreads();
+    };
+    for (uint32_t p0 = 0; p0 < parts; p0 += room) {
+        const uint32_t n = parts - p0 < room ? parts - p0 : room;
+        fetch(p0, n);
+        for (uint32_t i = threadIdx.x; i < pairs; i += S::kThreads) {
+            const float2 was = p0 ? total[i] : make_float2(kNoMax, 0.0f);
+            float top = was.x;
+#pragma unroll 4
+            for (uint32_t k = 0; k < n; ++k) top = fmaxf(top, each[k * pairs + i].x);
+            float sum = was.y * exp2_approx(was.x - top);
+#pragma unroll 4
+            for (uint32_t k = 0; k < n; ++k) sum += each[k * pairs + i].y * exp2_approx(each[k * pairs + i].x - top);
+            total[i] = make_float2(top, sum);
+        }
+    }
+    if (parts <= room) weigh(parts);
+    constexpr int kAtOnce = 4;
+    const uint32_t vectors = S::kVectors << a.pair_heads;
+    for (uint32_t e0 = 0; e0 < vectors; e0 += kAtOnce * S::kThreads) {
+        float4 x[kAtOnce] = {};
+        uint32_t pair[kAtOnce];
+#pragma unroll
+        for (int v = 0; v < kAtOnce; ++v) {
+            const uint32_t e = e0 + v * S::kThreads + threadIdx.x, in = e % S::kVectors;
+            pair[v] = e / S::kVectors * S::kRows + in / (DP / 16 * 32) * 8 + 2 * (e & 3);
+        }
+        for (uint32_t p0 = 0; p0 < parts; p0 += room) {
+            const uint32_t n = parts - p0 < room ? parts - p0 : room;
+            if (parts > room) {
+                fetch(p0, n);
+                weigh(n);
+            }
+#pragma unroll 4
+            for (uint32_t k = 0; k < n; ++k) {
+                const float4 *part = a.partial + from(p0 + k) * S::kVectors;
+#pragma unroll
+                for (int v = 0; v < kAtOnce; ++v) {
+                    const uint32_t e = e0 + v * S::kThreads + threadIdx.x;
+                    if (e >= vectors) continue;
+                    const float4 y = __ldcg(part + e);
+                    const float b0 = each[k * pairs + pair[v]].x, b1 = each[k * pairs + pair[v] + 1].x;
+                    x[v].x += y.x * b0;
+                    x[v].y += y.y * b1;
+                    x[v].z += y.z * b0;
+                    x[v].w += y.w * b1;
+                }
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < kAtOnce; ++v) {
+            const uint32_t e = e0 + v * S::kThreads + threadIdx.x;
+            if (e >= vectors) continue;
+            const float sum[2] = {total[pair[v]].y, total[pair[v] + 1].y};
+            write_out<T, DP, NT>(a, row, (group << a.pair_heads) + e / S::kVectors, tile, e % S::kVectors, x[v], sum);
+        }
+    }
+}
+
+// BOX: 16 tokens from a multiple of 16 on lie in one page.
+template <typename T, int DP, int NT, bool BOX>
+__global__ void __launch_bounds__(Shape<DP, NT>::kThreads, Shape<DP, NT>::kBlocks)
 attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
               const __grid_constant__ CUtensorMap value_map) {
     using S = Shape<DP, NT>;
@@ -286,31 +425,47 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t g = lane >> 2, t = lane & 3;
     // stage i of this warp: codes at codes_at + i * kNextStage, scales (16 of keys, 16 of values) and barrier behind the ring
-    constexpr uint32_t kNextStage = kQWarps * S::kStageBytes, kValuesAt = DP * kTile;
+    constexpr uint32_t kNextStage = S::kWarps * S::kStageBytes, kValuesAt = DP * kTile;
     const uint32_t codes_at = ring_at + warp * S::kStageBytes;
     const uint32_t scales_at = ring_at + S::kRing + warp * S::kStages * 128 + lane * 4;
-    const uint32_t bars_at = ring_at + S::kRing + S::kStages * kQWarps * 128 + warp * S::kStages * 8;
-    if (a.boxes && lane < S::kStages) mbar_init(bars_at + lane * 8, 1);
+    const uint32_t bars_at = ring_at + S::kRing + S::kStages * S::kWarps * 128 + warp * S::kStages * 8;
+    if (BOX && lane < S::kStages) mbar_init(bars_at + lane * 8, 1);
     fence_mbar_init();
-    const Piece piece = piece_of(a, S::kRows, blockIdx.x, gridDim.x);  // (block barriers within)
-    if (piece.from >= piece.to) {
-        if (threadIdx.x == 0) a.boundary[blockIdx.x].unit = 0u;
-        return;
+    __shared__ uint64_t sums64[S::kWarps], found[2];
+    __shared__ uint32_t next_piece, last_here;
+    uint32_t epoch = 0;
+    if (threadIdx.x == 0) epoch = next_piece = ld_relaxed_u32(&a.hdr->epoch);
+    Line<S::kWarps> line;
+    line.measure(a, S::kRows, sums64);  // (block barriers within)
+    epoch = next_piece;
+    __syncthreads();
+    // Every block draws once for its first piece (by its own number) and once for each that it drew; who draws the
+    // last number re-arms the header.
+    const uint32_t draws = gridDim.x + (line.pieces > gridDim.x ? line.pieces - gridDim.x : 0);
+    const uint32_t unit_tokens = unit_of(a, S::kWarps), warp_head = warp & ((1u << a.pair_heads) - 1), warp_tile = warp >> a.pair_heads;
+    // what the lane reads of a stage: its first key and two values
+    uint32_t key_at = S::chunk(S::token(g), t), value_at[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t r = S::token(2 * t + k);
+        value_at[k] = kValuesAt + (DP >= 128 ? S::chunk(r, g >> 1 | (g & 1) << 2) : S::chunk(r, g >> 1) + 8 * (g & 1));
     }
-    uint64_t row_at = piece.row;
-    RowUnits row = row_units(a, row_at, S::kRows);
-    uint64_t left = piece.to - piece.from;
-    const uint64_t width = (uint64_t)row.units + kTileCost;  // of a tile of queries on the line
-    uint32_t skip = (uint32_t)(piece.unit % width);          // what of it lies before this piece
-    uint32_t tile = (uint32_t)(piece.unit / width % row.tiles);
-    uint32_t head = (uint32_t)(piece.unit / width / row.tiles);
-    if (threadIdx.x == 0)
-        a.boundary[blockIdx.x] = Boundary{(uint32_t)row_at, head, tile, skip > kTileCost ? skip - kTileCost : 0u,
-                                          row.units, piece.per, {0, 0}};
-
+    asm volatile("" : "+r"(key_at), "+r"(value_at[0]), "+r"(value_at[1]));  // kept, not computed in every turn
     uint32_t stage = 0, parity = 0;  // of the tile that is consumed next
     uint32_t in_flight = 0;
     bool gave_up = false;
+    uint32_t piece = blockIdx.x;
+    while (true) {
+    const uint32_t drawn = threadIdx.x == 0 ? atom_add_acq_rel(&a.hdr->counter, 1u) : 0u;  // for later
+    if (piece < line.pieces) {
+    uint64_t at_line = line.begin_of(piece), left = line.begin_of(piece + 1) - at_line;
+    line.locate(a, S::kRows, at_line, sums64, found);
+    uint64_t row_at = found[0];
+    RowUnits row = row_units(a, row_at, S::kRows, S::kWarps);
+    const uint32_t width = row.units + kTileCost;        // of a tile of queries on the line
+    uint32_t skip = (uint32_t)(found[1] % width);        // what of it lies before this piece
+    uint32_t tile = (uint32_t)(found[1] / width % row.tiles);
+    uint32_t group = (uint32_t)(found[1] / width / row.tiles);  // of heads
     while (true) {
         // units [unit, unit + n_units) of the tile
         const uint64_t here = (uint64_t)row.units + kTileCost - skip;
@@ -318,6 +473,7 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
         const uint32_t unit = skip > kTileCost ? skip - kTileCost : 0u;
         const uint32_t n_units = skip + taken > kTileCost ? skip + taken - kTileCost - unit : 0u;
         if (n_units > 0) {
+            const uint32_t head = (group << a.pair_heads) + warp_head;
             // queries: lane (g, t) holds elements 64 c + 16 t .. + 15 of row g of each eight
             uint32_t q[NT][S::kKeyChunks * 8];
             float factor[NT][2];  // of the queries 2 t, 2 t + 1: what makes a product a score
@@ -325,13 +481,13 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
             int64_t first_last, last_last;
             {
                 const int64_t before = row.len - row.n;
-                const uint64_t f0 = (uint64_t)tile * S::kRows, f1 = f0 + S::kRows - 1, all = (uint64_t)row.n * a.group.d;
-                first_last = before + (int64_t)(f0 / a.group.d);
-                last_last = before + (int64_t)((f1 < all ? f1 : all - 1) / a.group.d);
+                const uint32_t f0 = tile * S::kRows, f1 = f0 + S::kRows - 1, all = (uint32_t)row.n * a.group.d;
+                first_last = before + (int64_t)divide(f0, a.group);
+                last_last = before + (int64_t)divide(f1 < all ? f1 : all - 1, a.group);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     uint32_t token = 0, j = 0;
-                    const bool real = query_of(a, row, tile, S::kRows, nt * 8 + g, &token, &j);
+                    const bool real = query_of(a, row.n, tile, S::kRows, nt * 8 + g, &token, &j);
                     const T *x = static_cast<const T *>(a.queries) + (uint64_t)(row.begin + token) * a.q_token_stride +
                                  ((uint64_t)head * a.group.d + j) * a.q_head_stride;
                     uint4 raw[S::kKeyChunks][2];
@@ -376,6 +532,7 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
             }
             const uint32_t limit = last_last + 1 < (int64_t)row.limit ? (uint32_t)(last_last + 1 > 0 ? last_last + 1 : 0)
                                                                       : row.limit;
+            const int32_t whole_until = (int32_t)(first_last - (kTile - 1) < -1 ? -1 : first_last - (kTile - 1));
             const int32_t *table = a.v.table + row_at * a.v.table_stride;
 
             float o[DP / 16][NT][4], m[NT][2], l[NT][2], c_ref[NT][2];
@@ -389,42 +546,64 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                 for (int k = 0; k < 2; ++k) m[nt][k] = kNoMax, l[nt][k] = 0.0f, c_ref[nt][k] = 1.0f;
             }
 
-            // the warp's tiles: 16 tokens from (unit + i) * 64 + warp * 16 on
-            const uint64_t start = (uint64_t)unit * kUnit + warp * kTile;
-            const uint32_t most = start < limit ? (uint32_t)((limit - start + kUnit - 1) / kUnit) : 0u;
+            // the warp's tiles: 16 tokens from (unit + i) * unit_tokens + warp_tile * 16 on
+            const uint64_t start = (uint64_t)unit * unit_tokens + warp_tile * kTile;
+            const uint32_t most = start < limit ? (uint32_t)(limit - start - 1) / unit_tokens + 1 : 0u;
             const uint32_t n_tiles = n_units < most ? n_units : most;
-            // the page of token `lane mod 16` of tile i
-            auto page_at = [&](uint32_t i) -> int32_t {
-                const uint64_t at = start + (lane & 15) + (uint64_t)i * kUnit;
-                return i < n_tiles && at < limit ? __ldg(table + divide((uint32_t)at, a.v.page_tokens)) : -1;
+            // Starts the copies of tile i into a stage. BOX: lane j knows the pages of tile 32 n + j; else lane j (and
+            // 16 + j) those of token j of the next tile.
+            int32_t page = -1;
+            uint32_t slot = 0;
+            uint64_t scale_from = 0;
+            uint32_t absent = 0;  // bit i: the tile in stage i has no page
+            auto look_up = [&](uint32_t i) {
+                const uint64_t at = start + (BOX ? 0 : lane & 15) + (uint64_t)(BOX ? i + lane : i) * unit_tokens;
+                const uint32_t nth = divide((uint32_t)at, a.v.page_tokens);
+                const int32_t p = (BOX ? i + lane : i) < n_tiles && at < limit ? __ldg(table + nth) : -1;
+                slot = (uint32_t)at - nth * a.v.page_tokens.d;
+                page = p >= 0 && (uint64_t)p < a.v.pages ? p : -1;
+                if (BOX) scale_from = (uint64_t)(uint32_t)page * a.scale_stride +
+                                      (a.wide_blocks ? (uint64_t)divide(slot, a.block_tokens) * a.heads : 0) + head;
             };
-            auto issue = [&](uint32_t i, int32_t page, uint32_t to_stage) {
+            auto issue = [&](uint32_t i, uint32_t to_stage) {
                 const uint32_t to = codes_at + to_stage * kNextStage;
-                const uint32_t at = (uint32_t)start + (lane & 15) + i * kUnit;
-                const bool held = page >= 0 && (uint64_t)page < a.v.pages;
-                const uint32_t slot = at - divide(at, a.v.page_tokens) * a.v.page_tokens.d;
-                in_flight += gave_up ? 0 : 1;
-                if (a.boxes && lane == 0 && !gave_up) {
-                    const uint32_t bar = bars_at + to_stage * 8;
-                    mbar_arrive_expect_tx(bar, S::kStageBytes);
+                if (BOX) {
+                    if (i % 32 == 0) look_up(i);
+                    const int32_t its_page = __shfl_sync(0xffffffffu, page, i % 32);
+                    const uint32_t its_slot = __shfl_sync(0xffffffffu, slot, i % 32);
+                    uint64_t from = __shfl_sync(0xffffffffu, scale_from, i % 32);
+                    absent = its_page < 0 ? absent | 1u << to_stage : absent & ~(1u << to_stage);
+                    if (lane == 0 && !gave_up) {
+                        const uint32_t bar = bars_at + to_stage * 8;
+                        if (its_page < 0) {
+                            mbar_arrive(bar);
+                        } else {
+                            mbar_arrive_expect_tx(bar, S::kStageBytes);
 #pragma unroll
-                    for (int h = 0; h < S::kHalves; ++h) {
-                        copy_box(to + h * S::kHalfBytes, &key_map, bar, S::kPitch * h, (int)head, (int)slot, page);
-                        copy_box(to + kValuesAt + h * S::kHalfBytes, &value_map, bar, S::kPitch * h, (int)head, (int)slot, page);
+                            for (int h = 0; h < S::kHalves; ++h) {
+                                copy_box(to + h * S::kHalfBytes, &key_map, bar, S::kPitch * h, (int)head, (int)its_slot, its_page);
+                                copy_box(to + kValuesAt + h * S::kHalfBytes, &value_map, bar, S::kPitch * h, (int)head, (int)its_slot,
+                                         its_page);
+                            }
+                        }
                     }
-                }
-                if (held) {
-                    const uint64_t block = (uint64_t)page * a.scale_stride +
-                                           (uint64_t)divide(slot, a.block_tokens) * a.heads + head;
-                    copy_async<4>(scales_at + to_stage * 128, (lane < 16 ? a.key_scales : a.value_scales) + block, true);
+                    in_flight += gave_up ? 0 : 1;
+                    if (its_page >= 0) {
+                        if (!a.wide_blocks) from += (uint64_t)divide(its_slot + (lane & 15), a.block_tokens) * a.heads;
+                        copy_async<4>(scales_at + to_stage * 128, (lane < 16 ? a.key_scales : a.value_scales) + from, true);
+                    }
                 } else {
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales_at + to_stage * 128), "f"(lane < 16 ? -1.0f : 0.0f)
-                                 : "memory");
-                }
-                if (!a.boxes) {
-                    const uint64_t off = held ? (uint64_t)page * a.page_stride + (uint64_t)slot * a.token_stride +
-                                                    (uint64_t)head * a.head_stride
-                                              : ~0ull;
+                    uint64_t off = ~0ull;
+                    if (page >= 0) {
+                        off = (uint64_t)page * a.page_stride + (uint64_t)slot * a.token_stride + (uint64_t)head * a.head_stride;
+                        const uint64_t block = (uint64_t)page * a.scale_stride +
+                                               (uint64_t)divide(slot, a.block_tokens) * a.heads + head;
+                        copy_async<4>(scales_at + to_stage * 128, (lane < 16 ? a.key_scales : a.value_scales) + block, true);
+                    } else {
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(scales_at + to_stage * 128), "f"(lane < 16 ? -1.0f : 0.0f)
+                                     : "memory");
+                    }
+                    look_up(i + 1);
                     constexpr uint32_t kChunks = S::kPitch / 16, kRowsAtOnce = 32 / kChunks;
                     const uint32_t c = lane % kChunks;
 #pragma unroll
@@ -442,48 +621,45 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                 }
             };
 
-            int32_t page = page_at(0);
+            if (!BOX) look_up(0);
             uint32_t ahead = stage;  // the stage that is filled next
 #pragma unroll
             for (int i = 0; i < S::kStages - 1; ++i) {
-                const int32_t now = page;
-                page = page_at(i + 1);
                 if ((uint32_t)i < n_tiles) {
-                    issue(i, now, ahead);
+                    issue(i, ahead);
                     ahead = ahead + 1 == S::kStages ? 0 : ahead + 1;
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             }
             for (uint32_t i = 0; i < n_tiles; ++i) {
                 __syncwarp();  // every lane has read the stage that is filled now
-                {
-                    const int32_t now = page;
-                    page = page_at(i + S::kStages);
-                    if (i + S::kStages - 1 < n_tiles) {
-                        issue(i + S::kStages - 1, now, ahead);
-                        ahead = ahead + 1 == S::kStages ? 0 : ahead + 1;
-                    }
-                    asm volatile("cp.async.commit_group;" ::: "memory");
+                if (i + S::kStages - 1 < n_tiles) {
+                    issue(i + S::kStages - 1, ahead);
+                    ahead = ahead + 1 == S::kStages ? 0 : ahead + 1;
                 }
+                asm volatile("cp.async.commit_group;" ::: "memory");
                 wait_copies<S::kStages - 1>();
-                if (a.boxes) {
+                if (BOX) {
                     // (having given up, a warp starts no more copies, and waits for those in flight alone)
                     if (in_flight > 0) {
                         --in_flight;
-                        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bars_at + stage * 8, parity, kDefaultLimitNs))) {
+                        const uint32_t bar = bars_at + stage * 8;
+                        if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)) &&
+                            !__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, kDefaultLimitNs))) {
                             if (lane == 0) report_timeout(a.hdr, blockIdx.x);
                             gave_up = true;
                         }
                     }
                 } else {
-                    in_flight = 0;
                     __syncwarp();
                 }
                 const uint8_t *at = ring + warp * S::kStageBytes + stage * kNextStage;
                 float own;
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(own) : "r"(scales_at + stage * 128) : "memory");
+                const bool none = BOX && (absent >> stage & 1u);
                 if (++stage == S::kStages) stage = 0, parity ^= 1;
-                const uint32_t base = (uint32_t)start + i * kUnit;
+                if (none) continue;
+                const uint32_t base = (uint32_t)start + i * unit_tokens;
 
                 float s[NT][4];
 #pragma unroll
@@ -492,8 +668,7 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                     for (int k = 0; k < 4; ++k) s[nt][k] = 0.0f;
 #pragma unroll
                 for (int c = 0; c < S::kKeyChunks; ++c) {
-                    const uint8_t *from = at + (DP >= 128 ? c / 2 * S::kHalfBytes : 0) +
-                                          S::chunk(S::token(g), DP >= 128 ? t + 4 * (c & 1) : t);
+                    const uint8_t *from = at + (DP >= 128 ? c / 2 * S::kHalfBytes : 0) + (key_at ^ (c & 1) << 6);
                     const uint4 x = *reinterpret_cast<const uint4 *>(from);
                     const uint4 y = *reinterpret_cast<const uint4 *>(from + 8 * S::kPitch);
                     const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
@@ -512,26 +687,32 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                     ks[k] = __shfl_sync(0xffffffffu, own, S::token(g) + 8 * k);
                     vs[k] = __shfl_sync(0xffffffffu, own, 16 + S::token(g) + 8 * k);
                 }
-                const bool partly = (int64_t)base + kTile - 1 > first_last;  // some query does not see some token
-                float p[NT][4], w[NT][4], top_w = 0.0f, top_p = 0.0f;
+                const bool partly = (int32_t)base > whole_until;  // some query does not see some token
+                float p[NT][4], w[NT][4], top_w = 0.0f, top_x = 0.0f;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float &x = s[nt][2 * k + j];
-                            x = ks[k] < 0.0f ? -INFINITY : x * (ks[k] * factor[nt][j]);
+                            float x = fmaf(s[nt][2 * k + j], ks[k] * factor[nt][j], -m[nt][j]);
+                            if (!BOX && ks[k] < 0.0f) x = -INFINITY;
                             if (partly && (int32_t)(base + S::token(g) + 8 * k) > last[nt][j]) x = -INFINITY;
-                            p[nt][2 * k + j] = exp2_approx(x - m[nt][j]);
+                            p[nt][2 * k + j] = exp2_approx(x);
                             w[nt][2 * k + j] = p[nt][2 * k + j] * (vs[k] * c_ref[nt][j]);
                             top_w = fmaxf(top_w, w[nt][2 * k + j]);
-                            top_p = fmaxf(top_p, p[nt][2 * k + j]);
+                            top_x = fmaxf(top_x, x);
                         }
-                if (__any_sync(0xffffffffu, top_w > kMaxWeight || top_p > kMaxP)) {
+                if (__any_sync(0xffffffffu, top_w > kMaxWeight || top_x > kMaxAbove)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float by[2];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const bool hidden = (!BOX && ks[k >> 1] < 0.0f) ||
+                                                (partly && (int32_t)(base + S::token(g) + 8 * (k >> 1)) > last[nt][k & 1]);
+                            s[nt][k] = hidden ? -INFINITY : s[nt][k] * (ks[k >> 1] * factor[nt][k & 1]);
+                        }
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             float top = fmaxf(s[nt][j], s[nt][2 + j]);
@@ -584,8 +765,10 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
-                                sees[nt][k] = transposed(pack_half(s[nt][2 * k] == -INFINITY ? 0.0f : 1.0f,
-                                                                   s[nt][2 * k + 1] == -INFINITY ? 0.0f : 1.0f));
+                                {
+                                const int32_t its = (int32_t)(base + S::token(g) + 8 * k);
+                                sees[nt][k] = transposed(pack_half(its > last[nt][0] ? 0.0f : 1.0f, its > last[nt][1] ? 0.0f : 1.0f));
+                            }
                     }
                 }
                 // values: lane (g, t) has tokens 2 t, 2 t + 1, 2 t + 8, 2 t + 9 of the order, and of each half's
@@ -596,9 +779,7 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                     uint32_t v[4][kWords];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t r = S::token(2 * t + (k & 1));
-                        const uint8_t *from = at + kValuesAt + h * S::kHalfBytes + 8 * (k >> 1) * S::kPitch +
-                                              (DP >= 128 ? S::chunk(r, g >> 1 | (g & 1) << 2) : S::chunk(r, g >> 1) + 8 * (g & 1));
+                        const uint8_t *from = at + h * S::kHalfBytes + 8 * (k >> 1) * S::kPitch + value_at[k & 1];
                         if (S::kValueBytes == 16) {
                             const uint4 x = *reinterpret_cast<const uint4 *>(from);
                             v[k][0] = x.x, v[k][1] = x.y, v[k][kWords - 2] = x.z, v[k][kWords - 1] = x.w;
@@ -644,126 +825,116 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                 }
             }
 
-            // Joins the warps' sums. Element 2 k + j of o[(h * kWords + x) * 2 + i] is dimension 4 x + 2 i + k of the lane's
-            // chunk, query 2 t + j.
+            // Joins the warps' sums, as the lanes hold them.
             wait_copies<0>();
             __syncthreads();
-            float *const sums = reinterpret_cast<float *>(ring);
-            float2 *const refs = reinterpret_cast<float2 *>(sums + kQWarps * S::kRows * DP);
+            float4 *const sums = reinterpret_cast<float4 *>(ring);
+            float2 *const refs = reinterpret_cast<float2 *>(sums + S::kWarps * S::kVectors);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float out_of[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     float x = l[nt][j];
                     for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-                    const uint32_t r = nt * 8 + 2 * t + j;
-                    if (g == 0) refs[warp * S::kRows + r] = make_float2(m[nt][j], x);
-                    const float out_of = 1.0f / c_ref[nt][j];
-#pragma unroll
-                    for (int i = 0; i < DP / 16; ++i) {
-                        constexpr int kPer = S::kValueBytes / 2;  // of o, for a half
-                        const uint32_t chunk = DP >= 128 ? g >> 1 | (g & 1) << 2 : g;
-                        const uint32_t d = S::kPitch * (i / kPer) + S::kValueBytes * chunk + 2 * (i % kPer);
-                        float2 *to = reinterpret_cast<float2 *>(sums + (warp * S::kRows + r) * DP + d);
-                        *to = make_float2(o[i][nt][j] * out_of, o[i][nt][2 + j] * out_of);
-                    }
+                    if (g == 0) refs[warp * S::kRows + nt * 8 + 2 * t + j] = make_float2(m[nt][j], x);
+                    out_of[j] = 1.0f / c_ref[nt][j];
                 }
+#pragma unroll
+                for (int i = 0; i < DP / 16; ++i)
+                    sums[warp * S::kVectors + (nt * (DP / 16) + i) * 32 + lane] =
+                        make_float4(o[i][nt][0] * out_of[0], o[i][nt][1] * out_of[1], o[i][nt][2] * out_of[0],
+                                    o[i][nt][3] * out_of[1]);
+            }
             __syncthreads();
             const bool whole = unit == 0 && n_units == row.units;
-            const uint64_t place = 2ull * blockIdx.x + (unit == 0 ? 1 : 0);
-            for (int e = threadIdx.x; e < S::kRows * (DP / 2); e += kQThreads) {
-                const uint32_t r = e / (DP / 2), d = e % (DP / 2) * 2;
-                float top = kNoMax;
-#pragma unroll
-                for (int w = 0; w < kQWarps; ++w) top = fmaxf(top, refs[w * S::kRows + r].x);
-                float x = 0.0f, y = 0.0f, sum = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kQWarps; ++w) {
-                    const float2 ml = refs[w * S::kRows + r];
-                    const float by = exp2_approx(ml.x - top);
-                    const float2 v = *reinterpret_cast<const float2 *>(sums + (w * S::kRows + r) * DP + d);
-                    x += v.x * by;
-                    y += v.y * by;
-                    sum += ml.y * by;
+            const uint64_t place = (2ull * piece + (unit == 0 ? 1 : 0)) << a.pair_heads;
+            const uint32_t heads = 1u << a.pair_heads;
+            for (uint32_t e = threadIdx.x; e < (uint32_t)S::kVectors << a.pair_heads; e += S::kThreads) {
+                const uint32_t h = e / S::kVectors, v = e % S::kVectors, r = v / (DP / 16 * 32) * 8 + 2 * (v & 3);
+                float top[2] = {kNoMax, kNoMax}, sum[2] = {0.0f, 0.0f};
+                for (uint32_t w = h; w < S::kWarps; w += heads) {
+                    top[0] = fmaxf(top[0], refs[w * S::kRows + r].x);
+                    top[1] = fmaxf(top[1], refs[w * S::kRows + r + 1].x);
+                }
+                float4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (uint32_t w = h; w < S::kWarps; w += heads) {
+                    const float2 m0 = refs[w * S::kRows + r], m1 = refs[w * S::kRows + r + 1];
+                    const float b0 = exp2_approx(m0.x - top[0]), b1 = exp2_approx(m1.x - top[1]);
+                    const float4 y = sums[w * S::kVectors + v];
+                    x.x += y.x * b0;
+                    x.y += y.y * b1;
+                    x.z += y.z * b0;
+                    x.w += y.w * b1;
+                    sum[0] += m0.y * b0;
+                    sum[1] += m1.y * b1;
                 }
                 if (whole) {
-                    uint32_t token, j;
-                    if (d < a.dim && query_of(a, row, tile, S::kRows, r, &token, &j)) {
-                        T *to = static_cast<T *>(a.out) + (uint64_t)(row.begin + token) * a.out_token_stride +
-                                ((uint64_t)head * a.group.d + j) * a.out_head_stride + d;
-                        to[0] = QType<T>::put(sum == 0.0f ? 0.0f : x / sum);
-                        to[1] = QType<T>::put(sum == 0.0f ? 0.0f : y / sum);
-                    }
+                    write_out<T, DP, NT>(a, row, (group << a.pair_heads) + h, tile, v, x, sum);
                 } else {
-                    *reinterpret_cast<float2 *>(a.partial + place * (S::kRows * DP) + r * DP + d) = make_float2(x, y);
-                    if (d == 0) a.partial_ml[place * S::kRows + r] = make_float2(top, sum);
+                    a.partial[(place + h) * S::kVectors + v] = x;
+                    if (v % (DP / 16 * 32) < 4) {  // a lane for every two queries
+                        a.partial_ml[(place + h) * S::kRows + r] = make_float2(top[0], sum[0]);
+                        a.partial_ml[(place + h) * S::kRows + r + 1] = make_float2(top[1], sum[1]);
+                    }
+                }
+            }
+            if (!whole) {
+                // Pieces first .. have this tile of queries; the block that comes last joins their sums, in order.
+                const uint64_t units_at = at_line - skip + kTileCost;
+                const uint32_t first = line.piece_at(units_at), parts = line.piece_at(units_at + row.units - 1) - first + 1;
+                __threadfence();
+                __syncthreads();
+                if (threadIdx.x == 0) last_here = count_arrival(a.arrived + first, tag_of(epoch)) == parts;
+                __syncthreads();
+                if (last_here) {
+                    __threadfence();
+                    join_parts<T, DP, NT>(a, ring, first, parts, row, group, tile);
                 }
             }
             fence_proxy_async_smem();  // the sums' place becomes the ring again
             __syncthreads();
         }
         left -= taken;
+        at_line += taken;
         if (left == 0) break;
         skip = 0;
         if (++tile == row.tiles) {
             tile = 0;
-            if (++head == a.heads) {
-                head = 0;
+            if (++group == a.heads >> a.pair_heads) {
+                group = 0;
                 do {
-                    if (++row_at >= a.v.rows) return;  // (lens that change meanwhile)
-                    row = row_units(a, row_at, S::kRows);
+                    if (++row_at >= a.v.rows) break;  // (lens that change meanwhile)
+                    row = row_units(a, row_at, S::kRows, S::kWarps);
                 } while (row.units == 0);
+                if (row_at >= a.v.rows) break;
             }
         }
     }
-}
-
-// Joins the partial sums of the tile in which block c's piece begins, where that is the first piece to begin within it:
-// block c - 1 ended with its first units, the blocks from c on began with the others.
-template <typename T, int DP, int NT>
-__global__ void __launch_bounds__(kQThreads) join_kernel(const AttendArgs a) {
-    using S = Shape<DP, NT>;
-    cudaGridDependencySynchronize();  // what the launch before wrote
-    const uint64_t block = blockIdx.x + 1;
-    const Boundary b = a.boundary[block];
-    if (b.unit == 0 || b.unit > b.per) return;
-    const uint64_t end = block * b.per - b.unit + b.units;
-    const uint64_t stop = (end + b.per - 1) / b.per;  // the first block that begins behind the tile
-    const RowUnits row = row_units(a, b.row, S::kRows);
-    for (int e = threadIdx.x; e < S::kRows * (DP / 4); e += kQThreads) {
-        const uint32_t r = e / (DP / 4), d = e % (DP / 4) * 4;
-        uint32_t token, j;
-        if (d >= a.dim || !query_of(a, row, b.tile, S::kRows, r, &token, &j)) continue;
-        float top = kNoMax, sum = 0.0f, x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (uint64_t k = block - 1; k < stop; ++k) {
-            const uint64_t slot = 2 * k + (k == block - 1 ? 1 : 0);
-            const float2 ml = a.partial_ml[slot * S::kRows + r];
-            const float4 v = *reinterpret_cast<const float4 *>(a.partial + slot * (S::kRows * DP) + r * DP + d);
-            const float now = fmaxf(top, ml.x);
-            const float old = exp2_approx(top - now), by = exp2_approx(ml.x - now);
-            top = now;
-            sum = sum * old + ml.y * by;
-            x[0] = x[0] * old + v.x * by;
-            x[1] = x[1] * old + v.y * by;
-            x[2] = x[2] * old + v.z * by;
-            x[3] = x[3] * old + v.w * by;
-        }
-        T *to = static_cast<T *>(a.out) + (uint64_t)(row.begin + token) * a.out_token_stride +
-                ((uint64_t)b.head * a.group.d + j) * a.out_head_stride + d;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) to[k] = QType<T>::put(sum == 0.0f ? 0.0f : x[k] / sum);
     }
+    if (threadIdx.x == 0) {
+        next_piece = gridDim.x + drawn;
+        if (drawn == draws - 1) {
+            st_relaxed_u32(&a.hdr->counter, 0u);
+            st_relaxed_u32(&a.hdr->epoch, epoch + 1u);
+        }
+    }
+    __syncthreads();
+    piece = next_piece;
+    if (piece >= line.pieces) break;
+    __syncthreads();  // (next_piece was read)
+    }
+    finish_period(a.hdr, epoch, a.arrived, a.clear_words);
 }
 
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-constexpr size_t kPartialBytes = 2ull * kMaxBlocks * kMaxElements * sizeof(float);
-constexpr size_t kPartialMlBytes = 2ull * kMaxBlocks * kMaxTileRows * sizeof(float2);
-constexpr size_t kBoundaryBytes = kMaxBlocks * sizeof(Boundary);
+constexpr size_t kPartialBytes = 2ull * kMaxBlocks * kLevels * kMaxElements * sizeof(float);
+constexpr size_t kPartialMlBytes = 2ull * kMaxBlocks * kLevels * kMaxPairs * sizeof(float2);
 
 size_t attend_workspace_bytes() {
-    return round_up(round_up(tile_word_reach(), 256) + kPartialBytes + kPartialMlBytes + kBoundaryBytes, 256);
+    return round_up(round_up(tile_word_reach(), 256) + kPartialBytes + kPartialMlBytes, 256);
 }
 
 // The cache's codes as a tensor of dimensions, heads, slots and pages.
@@ -795,28 +966,42 @@ static int attend_launch(AttendArgs a, cudaStream_t s) {
     int sms = 0;
     const int rc = sm_count(&sms);
     if (rc != U32SCAN_OK) return rc;
-    if (cudaFuncSetAttribute(attend_kernel<T, DP, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kShared) !=
-        cudaSuccess)
-        return U32SCAN_ECUDA;
-    unsigned int blocks = (unsigned int)sms * S::kBlocks;
+    uint64_t blocks = (uint64_t)sms * S::kBlocks;
     if (blocks > kMaxBlocks) blocks = kMaxBlocks;
-    CUtensorMap maps[2] = {};
-    if (a.boxes && (!box_map(&maps[0], a.keys, a, DP >= 128) || !box_map(&maps[1], a.values, a, DP >= 128)))
+    // Tiles of queries, and units if every row is as long as its table: at most these. Several heads beside each other read
+    // a page's memory together, but leave fewer and larger parts to join.
+    const uint64_t tiles = a.v.tokens * a.group.d / S::kRows + a.v.rows;
+    a.pair_heads = a.heads % 4 == 0 ? 2 : a.heads % 2 == 0 ? 1 : 0;
+    if (a.pair_heads > S::kMostPaired) a.pair_heads = S::kMostPaired;
+    while (a.pair_heads > 0 && tiles * (a.heads >> a.pair_heads) * 8 < blocks) --a.pair_heads;
+#ifdef PH
+    a.pair_heads = PH;
+#endif
+    const uint64_t placed = a.v.width * a.v.page_tokens.d, length = placed < (1ull << 31) ? placed : (1ull << 31);
+    const double units = (double)tiles * (a.heads >> a.pair_heads) *
+                         (double)(length / ((kTile * S::kWarps) >> a.pair_heads) + 1 + kTileCost);
+    if (units < (double)(blocks * kLeastUnits)) blocks = (uint64_t)units / kLeastUnits + 1;
+    const bool box = a.v.page_tokens.d % kTile == 0 && a.v.pages > 0;
+    const auto kernel = box ? attend_kernel<T, DP, NT, true> : attend_kernel<T, DP, NT, false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kShared) != cudaSuccess)
         return U32SCAN_ECUDA;
-    attend_kernel<T, DP, NT><<<blocks, kQThreads, S::kShared, s>>>(a, maps[0], maps[1]);
-    if (blocks > 1) launch_next(join_kernel<T, DP, NT>, blocks - 1, kQThreads, s, a);
+    CUtensorMap maps[2] = {};
+    if (box && (!box_map(&maps[0], a.keys, a, DP >= 128) || !box_map(&maps[1], a.values, a, DP >= 128)))
+        return U32SCAN_ECUDA;
+    kernel<<<(unsigned int)blocks, S::kThreads, S::kShared, s>>>(a, maps[0], maps[1]);
     return cudaGetLastError() == cudaSuccess ? U32SCAN_OK : U32SCAN_ECUDA;
 }
 
-// Eight queries at a time, more where a row has them: the codes are read and converted once for all of a tile.
+// Eight queries at a time, more where a row has them (a row of one token has `group` for each key head; of
+// ragged ones the mean is known here): the codes are read and converted once for all of a tile.
 template <typename T>
-static int attend_dispatch(const AttendArgs &a, uint64_t rows_of_queries, cudaStream_t s) {
+static int attend_dispatch(const AttendArgs &a, cudaStream_t s) {
+    const uint64_t queries = (a.v.tokens + a.v.rows - 1) / a.v.rows * a.group.d;
     if (a.dim <= 64) {
-        if (rows_of_queries <= 8) return attend_launch<T, 64, 1>(a, s);
-        if (rows_of_queries <= 16) return attend_launch<T, 64, 2>(a, s);
-        return attend_launch<T, 64, 4>(a, s);
+        if (queries <= 8) return attend_launch<T, 64, 1>(a, s);
+        return queries <= 16 ? attend_launch<T, 64, 2>(a, s) : attend_launch<T, 64, 4>(a, s);
     }
-    if (a.dim <= 128) return rows_of_queries <= 8 ? attend_launch<T, 128, 1>(a, s) : attend_launch<T, 128, 2>(a, s);
+    if (a.dim <= 128) return queries <= 8 ? attend_launch<T, 128, 1>(a, s) : attend_launch<T, 128, 2>(a, s);
     return attend_launch<T, 256, 1>(a, s);
 }
 
@@ -842,6 +1027,7 @@ extern "C" int pages_attend(const u32scan_kv_cache *cache, const int32_t *table,
         ((cache->page_stride | cache->token_stride | cache->head_stride) & 15) != 0 ||
         ((query_token_stride | query_head_stride) & 7) != 0)
         return U32SCAN_EINVAL;
+    if (tokens * (q_heads / cache->heads) >= (1ull << 31)) return U32SCAN_EINVAL;
     if (tokens == 0 || rows == 0) return U32SCAN_OK;
     if (queries == nullptr || out == nullptr) return U32SCAN_EINVAL;
     if (ws == nullptr || misaligned(ws, 256) || ws_bytes < attend_workspace_bytes()) return U32SCAN_EWORKSPACE;
@@ -867,15 +1053,14 @@ extern "C" int pages_attend(const u32scan_kv_cache *cache, const int32_t *table,
     a.out_token_stride = out_token_stride;
     a.out_head_stride = out_head_stride;
     a.scale = scale * 1.4426950408889634f;
-    a.boxes = cache->page_tokens % kTile == 0 && cache->pages > 0;
+    a.wide_blocks = cache->page_tokens / cache->blocks % kTile == 0;
     a.hdr = static_cast<WsHeader *>(ws);
     char *w = static_cast<char *>(ws) + round_up(tile_word_reach(), 256);  // past every operation's tile words
-    a.partial = reinterpret_cast<float *>(w);
+    a.partial = reinterpret_cast<float4 *>(w);
     a.partial_ml = reinterpret_cast<float2 *>(w + kPartialBytes);
-    a.boundary = reinterpret_cast<Boundary *>(w + kPartialBytes + kPartialMlBytes);
-    // rows of one token have `group` queries a key head; of ragged ones the mean is known here
-    const uint64_t mean = starts == nullptr ? 1 : (tokens + rows - 1) / rows;
+    a.arrived = reinterpret_cast<unsigned long long *>(static_cast<char *>(ws) + kHeaderBytes);
+    a.clear_words = tile_words_to_clear(ws_bytes);
     const cudaStream_t s = (cudaStream_t)stream;
-    if (type == U32SCAN_F16) return attend_dispatch<__half>(a, mean * a.group.d, s);
-    return attend_dispatch<__nv_bfloat16>(a, mean * a.group.d, s);
+    if (type == U32SCAN_F16) return attend_dispatch<__half>(a, s);
+    return attend_dispatch<__nv_bfloat16>(a, s);
 }
