@@ -35,18 +35,14 @@
 
 namespace u32scan {
 
-#ifndef WL
-#define WL 4
-#endif
-#ifndef BL
-#define BL 2
-#endif
 constexpr int kTile = 16;                 // tokens of a warp at a time
 constexpr int kMaxDim = 256;
 constexpr unsigned int kMaxBlocks = 304;  // bounds the workspace
-constexpr unsigned int kLevels = 4;       // of piece sizes, each with a piece for every block
-constexpr uint32_t kTileCost = 2;         // what a tile of queries takes beside its units, in units
-constexpr uint64_t kLeastUnits = kTileCost + 2;  // of a block's piece
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+// What a tile of queries takes beside its units, in units (64 ragged rows of up to 8192 tokens 117, 110, 112 us with 2,
+// 4, 6, drafts 49, 46, 45), and the least piece (one row of 4000 tokens 15.1 us with 4 units, 14.3 with 3).
+constexpr uint32_t kTileCost = 5;
+constexpr uint64_t kLeastUnits = 3;
 constexpr int kMaxElements = 4096;        // heads x queries x dimensions of a tile of queries
 constexpr int kMaxPairs = 64;             // its heads x queries
 constexpr float kNoMax = -1e30f;
@@ -66,8 +62,8 @@ struct AttendArgs {
     float scale;  // times log2(e)
     bool wide_blocks;  // and in one block
     WsHeader *hdr;
-    float4 *partial;     // [2 pieces][heads][sums of a tile of queries, as the lanes hold them]
-    float2 *partial_ml;  // [2 pieces][heads][queries of a tile]: reference and sum
+    float4 *partial;     // [2 blocks][heads][sums of a tile of queries, as the lanes hold them]
+    float2 *partial_ml;  // [2 blocks][heads][queries of a tile]: reference and sum
     unsigned long long *arrived, clear_words;  // the workspace's tile words
 };
 
@@ -157,16 +153,16 @@ struct RowUnits {
 
 // A unit is a tile of 16 tokens for each warp: the warps take 1, 2 or 4 heads, and of each as many tiles beside each
 // other as there are warps left.
-__device__ __forceinline__ uint32_t unit_of(const AttendArgs &a, int warps) { return (uint32_t)(kTile * warps) >> a.pair_heads; }
+__device__ __forceinline__ uint32_t unit_of(const AttendArgs &a) { return (uint32_t)(kTile * kWarps) >> a.pair_heads; }
 
-__device__ __forceinline__ RowUnits row_units(const AttendArgs &a, uint64_t s, uint32_t tile_rows, int warps) {
+__device__ __forceinline__ RowUnits row_units(const AttendArgs &a, uint64_t s, uint32_t tile_rows) {
     RowUnits r;
     tokens_of(a.v, s, &r.begin, &r.n);
     const int32_t len = a.v.lens[s];
     r.len = len;
     const uint64_t placed = a.v.pages == 0 ? 0 : a.v.width * a.v.page_tokens.d;
     r.limit = (uint32_t)(len <= 0 ? 0 : (uint64_t)len < placed ? (uint64_t)len : placed);
-    const uint32_t unit_tokens = unit_of(a, warps);
+    const uint32_t unit_tokens = unit_of(a);
     r.units = r.n == 0 ? 0u : r.limit <= unit_tokens ? 1u : (r.limit - 1) / unit_tokens + 1;
     r.tiles = (uint32_t)((r.n * a.group.d + tile_rows - 1) / tile_rows);
     return r;
@@ -179,7 +175,6 @@ template <int DP, int NT>
 struct Shape {
     static constexpr int kRows = 8 * NT;
     static constexpr bool kSmall = DP * NT <= 128;  // 128 registers a thread do, else 255
-    static constexpr int kWarps = kSmall ? 8 : WL, kThreads = 32 * kWarps;
     static constexpr uint32_t kMostPaired = kSmall ? 2 : 1;  // log2 of the heads beside each other
     static constexpr int kVectors = NT * (DP / 16) * 32;     // a tile's sums, four at a time
     static constexpr int kPitch = DP >= 128 ? 128 : 64;
@@ -187,7 +182,7 @@ struct Shape {
     static constexpr int kHalfBytes = kTile * kPitch;
     static constexpr int kKeyChunks = DP / 64;                    // of 16 bytes, for each of a lane's two keys
     static constexpr int kValueBytes = DP >= 128 ? 16 : 8;        // for each of a lane's four values and each half
-    static constexpr int kBlocks = kSmall ? 2 : BL;               // an SM
+    static constexpr int kBlocks = kSmall ? 2 : 1;                // an SM
     static constexpr int kStageBytes = DP * 2 * kTile;            // of a warp
     static constexpr int kStages = (228 * 1024 / kBlocks - 4096) / (kWarps * (kStageBytes + 128));
     static constexpr int kRing = kStages * kWarps * kStageBytes;
@@ -207,19 +202,14 @@ struct Shape {
     }
 };
 
-// The line of all rows' units and its pieces. Blocks do not read equally fast (equal pieces of one call took from 42 to
-// 103 us), so every block starts with a piece of half its share and draws the others, of a quarter, an eighth and an
-// eighth, as it gets done; a short line has one piece a block.
-template <int WARPS>
+// The line of all rows' units, and its equal pieces, one for each block.
 struct Line {
-    static constexpr int kThreads = 32 * WARPS;
-    uint64_t total, begin[kLevels], size[kLevels];
-    uint32_t pieces;        // that are not empty
+    uint64_t total, per;
     uint64_t share, until;  // of row threadIdx.x: its units, and those up to its end
 
     __device__ static uint64_t share_of(const AttendArgs &a, uint64_t s, uint32_t tile_rows) {
         if (s >= a.v.rows) return 0;
-        const RowUnits r = row_units(a, s, tile_rows, WARPS);
+        const RowUnits r = row_units(a, s, tile_rows);
         return r.units ? ((uint64_t)r.units + kTileCost) * r.tiles * (a.heads >> a.pair_heads) : 0;
     }
 
@@ -234,7 +224,7 @@ struct Line {
         if (lane == 31) sums[warp] = x;
         __syncthreads();
         *all = 0;
-        for (int w = 0; w < WARPS; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             if (w < warp) x += sums[w];
             *all += sums[w];
         }
@@ -246,35 +236,8 @@ struct Line {
         uint64_t mine = share;
         for (uint64_t s = threadIdx.x + kThreads; s < a.v.rows; s += kThreads) mine += share_of(a, s, tile_rows);
         until = scan(mine, sums, &total);  // (a row's, where there is one for each thread)
-        const uint64_t blocks = gridDim.x;
-        const bool one = total <= blocks * (kLeastUnits << kLevels);
-#pragma unroll
-        for (uint32_t i = 0; i < kLevels; ++i) {
-            const uint32_t part = one ? 0 : i + 1 < kLevels ? i + 1 : i;  // 2^-part of a block's share
-            size[i] = (total + (blocks << part) - 1) / (blocks << part);
-            if (size[i] < kLeastUnits) size[i] = kLeastUnits;
-            begin[i] = i == 0 ? 0 : begin[i - 1] + blocks * size[i - 1];
-        }
-        pieces = total ? piece_at(total - 1) + 1 : 0;
-    }
-
-    __device__ uint64_t begin_of(uint32_t piece) const {
-        const uint32_t i = piece / gridDim.x;
-        if (i >= kLevels) return total;
-        uint64_t at = 0;
-#pragma unroll
-        for (uint32_t k = 0; k < kLevels; ++k)
-            if (k == i) at = begin[k] + (uint64_t)(piece - k * gridDim.x) * size[k];
-        return at < total ? at : total;
-    }
-
-    __device__ uint32_t piece_at(uint64_t at) const {
-        uint32_t i = 0;
-        uint64_t from = 0, by = size[0];
-#pragma unroll
-        for (uint32_t k = 1; k < kLevels; ++k)
-            if (at >= begin[k]) i = k, from = begin[k], by = size[k];
-        return i * gridDim.x + (uint32_t)((at - from) / by);
+        per = (total + gridDim.x - 1) / gridDim.x;
+        if (per < kLeastUnits) per = kLeastUnits;
     }
 
     // The row that holds place `at` of the line, and which of its units that is.
@@ -331,8 +294,8 @@ __device__ __forceinline__ void write_out(const AttendArgs &a, const RowUnits &r
     }
 }
 
-// Joins the parts of a tile of queries that pieces first .. first + parts - 1 left, in order: each part's reference and
-// sum into shared memory, their maxima, sums and weights, then the parts, weighted, four vectors a thread at a time.
+// Joins the parts of a tile of queries that blocks first .. first + parts - 1 left, in order: each part's reference and
+// sum into shared memory, their maxima, sums and weights, then the parts, weighted, a vector of four a thread.
 template <typename T, int DP, int NT>
 __device__ void join_parts(const AttendArgs &a, uint8_t *shared, uint64_t first, uint32_t parts, const RowUnits &row,
                            uint32_t group, uint32_t tile) {
@@ -344,12 +307,12 @@ __device__ void join_parts(const AttendArgs &a, uint8_t *shared, uint64_t first,
     auto fetch = [&](uint32_t p0, uint32_t n) {
         __syncthreads();
 #pragma unroll 4
-        for (uint32_t e = threadIdx.x; e < n * pairs; e += S::kThreads)
+        for (uint32_t e = threadIdx.x; e < n * pairs; e += kThreads)
             each[e] = __ldcg(a.partial_ml + from(p0 + e / pairs) * S::kRows + e % pairs);
         __syncthreads();
     };
     auto weigh = [&](uint32_t n) {
-        for (uint32_t i = threadIdx.x; i < pairs; i += S::kThreads) {
+        for (uint32_t i = threadIdx.x; i < pairs; i += kThreads) {
             const float top = total[i].x;
 #pragma unroll 4
             for (uint32_t k = 0; k < n; ++k) each[k * pairs + i].x = exp2_approx(each[k * pairs + i].x - top);
@@ -359,7 +322,7 @@ __device__ void join_parts(const AttendArgs &a, uint8_t *shared, uint64_t first,
     for (uint32_t p0 = 0; p0 < parts; p0 += room) {
         const uint32_t n = parts - p0 < room ? parts - p0 : room;
         fetch(p0, n);
-        for (uint32_t i = threadIdx.x; i < pairs; i += S::kThreads) {
+        for (uint32_t i = threadIdx.x; i < pairs; i += kThreads) {
             const float2 was = p0 ? total[i] : make_float2(kNoMax, 0.0f);
             float top = was.x;
 #pragma unroll 4
@@ -371,51 +334,45 @@ __device__ void join_parts(const AttendArgs &a, uint8_t *shared, uint64_t first,
         }
     }
     if (parts <= room) weigh(parts);
-    constexpr int kAtOnce = 4;
-    const uint32_t vectors = S::kVectors << a.pair_heads;
-    for (uint32_t e0 = 0; e0 < vectors; e0 += kAtOnce * S::kThreads) {
-        float4 x[kAtOnce] = {};
-        uint32_t pair[kAtOnce];
-#pragma unroll
-        for (int v = 0; v < kAtOnce; ++v) {
-            const uint32_t e = e0 + v * S::kThreads + threadIdx.x, in = e % S::kVectors;
-            pair[v] = e / S::kVectors * S::kRows + in / (DP / 16 * 32) * 8 + 2 * (e & 3);
-        }
+    // 16 parts' loads under way at a time: with the cache's copies in the same memory a load takes some 1.4 us
+    constexpr uint32_t kAtOnce = 16;
+    const uint32_t vectors = S::kVectors << a.pair_heads;  // (a multiple of the threads or, of few, of a warp)
+    for (uint32_t e0 = 0; e0 < vectors; e0 += kThreads) {
+        const uint32_t e = e0 + threadIdx.x, in = e % S::kVectors;
+        const uint32_t pair = e / S::kVectors * S::kRows + in / (DP / 16 * 32) * 8 + 2 * (e & 3);
+        float4 x = {0.0f, 0.0f, 0.0f, 0.0f};
         for (uint32_t p0 = 0; p0 < parts; p0 += room) {
             const uint32_t n = parts - p0 < room ? parts - p0 : room;
             if (parts > room) {
                 fetch(p0, n);
                 weigh(n);
             }
-#pragma unroll 4
-            for (uint32_t k = 0; k < n; ++k) {
-                const float4 *part = a.partial + from(p0 + k) * S::kVectors;
+            if (e >= vectors) continue;
+            for (uint32_t k0 = 0; k0 < n; k0 += kAtOnce) {
+                float4 y[kAtOnce];
 #pragma unroll
-                for (int v = 0; v < kAtOnce; ++v) {
-                    const uint32_t e = e0 + v * S::kThreads + threadIdx.x;
-                    if (e >= vectors) continue;
-                    const float4 y = __ldcg(part + e);
-                    const float b0 = each[k * pairs + pair[v]].x, b1 = each[k * pairs + pair[v] + 1].x;
-                    x[v].x += y.x * b0;
-                    x[v].y += y.y * b1;
-                    x[v].z += y.z * b0;
-                    x[v].w += y.w * b1;
+                for (uint32_t k = 0; k < kAtOnce; ++k)
+                    y[k] = k0 + k < n ? __ldcg(a.partial + from(p0 + k0 + k) * S::kVectors + e) : float4{0, 0, 0, 0};
+#pragma unroll
+                for (uint32_t k = 0; k < kAtOnce; ++k) {
+                    if (k0 + k >= n) break;
+                    const float b0 = each[(k0 + k) * pairs + pair].x, b1 = each[(k0 + k) * pairs + pair + 1].x;
+                    x.x += y[k].x * b0;
+                    x.y += y[k].y * b1;
+                    x.z += y[k].z * b0;
+                    x.w += y[k].w * b1;
                 }
             }
         }
-#pragma unroll
-        for (int v = 0; v < kAtOnce; ++v) {
-            const uint32_t e = e0 + v * S::kThreads + threadIdx.x;
-            if (e >= vectors) continue;
-            const float sum[2] = {total[pair[v]].y, total[pair[v] + 1].y};
-            write_out<T, DP, NT>(a, row, (group << a.pair_heads) + e / S::kVectors, tile, e % S::kVectors, x[v], sum);
-        }
+        if (e >= vectors) continue;
+        const float sum[2] = {total[pair].y, total[pair + 1].y};
+        write_out<T, DP, NT>(a, row, (group << a.pair_heads) + e / S::kVectors, tile, in, x, sum);
     }
 }
 
 // BOX: 16 tokens from a multiple of 16 on lie in one page.
 template <typename T, int DP, int NT, bool BOX>
-__global__ void __launch_bounds__(Shape<DP, NT>::kThreads, Shape<DP, NT>::kBlocks)
+__global__ void __launch_bounds__(kThreads, Shape<DP, NT>::kBlocks)
 attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
               const __grid_constant__ CUtensorMap value_map) {
     using S = Shape<DP, NT>;
@@ -425,24 +382,22 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t g = lane >> 2, t = lane & 3;
     // stage i of this warp: codes at codes_at + i * kNextStage, scales (16 of keys, 16 of values) and barrier behind the ring
-    constexpr uint32_t kNextStage = S::kWarps * S::kStageBytes, kValuesAt = DP * kTile;
+    constexpr uint32_t kNextStage = kWarps * S::kStageBytes, kValuesAt = DP * kTile;
     const uint32_t codes_at = ring_at + warp * S::kStageBytes;
     const uint32_t scales_at = ring_at + S::kRing + warp * S::kStages * 128 + lane * 4;
-    const uint32_t bars_at = ring_at + S::kRing + S::kStages * S::kWarps * 128 + warp * S::kStages * 8;
+    const uint32_t bars_at = ring_at + S::kRing + S::kStages * kWarps * 128 + warp * S::kStages * 8;
     if (BOX && lane < S::kStages) mbar_init(bars_at + lane * 8, 1);
     fence_mbar_init();
-    __shared__ uint64_t sums64[S::kWarps], found[2];
-    __shared__ uint32_t next_piece, last_here;
-    uint32_t epoch = 0;
-    if (threadIdx.x == 0) epoch = next_piece = ld_relaxed_u32(&a.hdr->epoch);
-    Line<S::kWarps> line;
+    __shared__ uint64_t sums64[kWarps], found[2];
+    __shared__ uint32_t last_here;
+    uint32_t epoch, nth_block = 0;
+    if (threadIdx.x == 0) last_here = ld_relaxed_u32(&a.hdr->epoch);
+    Line line;
     line.measure(a, S::kRows, sums64);  // (block barriers within)
-    epoch = next_piece;
-    __syncthreads();
-    // Every block draws once for its first piece (by its own number) and once for each that it drew; who draws the
-    // last number re-arms the header.
-    const uint32_t draws = gridDim.x + (line.pieces > gridDim.x ? line.pieces - gridDim.x : 0);
-    const uint32_t unit_tokens = unit_of(a, S::kWarps), warp_head = warp & ((1u << a.pair_heads) - 1), warp_tile = warp >> a.pair_heads;
+    epoch = last_here;
+    // (every block has read the epoch when it counts itself; what the count was is looked at in the end)
+    if (threadIdx.x == 0) nth_block = atom_add_acq_rel(&a.hdr->counter, 1u);
+    const uint32_t unit_tokens = unit_of(a), warp_head = warp & ((1u << a.pair_heads) - 1), warp_tile = warp >> a.pair_heads;
     // what the lane reads of a stage: its first key and two values
     uint32_t key_at = S::chunk(S::token(g), t), value_at[2];
 #pragma unroll
@@ -454,19 +409,20 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
     uint32_t stage = 0, parity = 0;  // of the tile that is consumed next
     uint32_t in_flight = 0;
     bool gave_up = false;
-    uint32_t piece = blockIdx.x;
-    while (true) {
-    const uint32_t drawn = threadIdx.x == 0 ? atom_add_acq_rel(&a.hdr->counter, 1u) : 0u;  // for later
-    if (piece < line.pieces) {
-    uint64_t at_line = line.begin_of(piece), left = line.begin_of(piece + 1) - at_line;
-    line.locate(a, S::kRows, at_line, sums64, found);
-    uint64_t row_at = found[0];
-    RowUnits row = row_units(a, row_at, S::kRows, S::kWarps);
-    const uint32_t width = row.units + kTileCost;        // of a tile of queries on the line
-    uint32_t skip = (uint32_t)(found[1] % width);        // what of it lies before this piece
-    uint32_t tile = (uint32_t)(found[1] / width % row.tiles);
-    uint32_t group = (uint32_t)(found[1] / width / row.tiles);  // of heads
-    while (true) {
+    uint64_t at_line = blockIdx.x * line.per, left = at_line < line.total ? min(line.per, line.total - at_line) : 0;
+    uint64_t row_at = 0;
+    RowUnits row = {};
+    uint32_t skip = 0, tile = 0, group = 0;  // group: of heads; skip: what of the tile of queries lies before this piece
+    if (left > 0) {
+        line.locate(a, S::kRows, at_line, sums64, found);
+        row_at = found[0];
+        row = row_units(a, row_at, S::kRows);
+        const uint32_t width = row.units + kTileCost;  // of a tile of queries on the line
+        skip = (uint32_t)(found[1] % width);
+        tile = (uint32_t)(found[1] / width % row.tiles);
+        group = (uint32_t)(found[1] / width / row.tiles);
+    }
+    while (left > 0) {
         // units [unit, unit + n_units) of the tile
         const uint64_t here = (uint64_t)row.units + kTileCost - skip;
         const uint32_t taken = (uint32_t)(left < here ? left : here);
@@ -829,7 +785,7 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
             wait_copies<0>();
             __syncthreads();
             float4 *const sums = reinterpret_cast<float4 *>(ring);
-            float2 *const refs = reinterpret_cast<float2 *>(sums + S::kWarps * S::kVectors);
+            float2 *const refs = reinterpret_cast<float2 *>(sums + kWarps * S::kVectors);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float out_of[2];
@@ -848,17 +804,17 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
             }
             __syncthreads();
             const bool whole = unit == 0 && n_units == row.units;
-            const uint64_t place = (2ull * piece + (unit == 0 ? 1 : 0)) << a.pair_heads;
+            const uint64_t place = (2ull * blockIdx.x + (unit == 0 ? 1 : 0)) << a.pair_heads;
             const uint32_t heads = 1u << a.pair_heads;
-            for (uint32_t e = threadIdx.x; e < (uint32_t)S::kVectors << a.pair_heads; e += S::kThreads) {
+            for (uint32_t e = threadIdx.x; e < (uint32_t)S::kVectors << a.pair_heads; e += kThreads) {
                 const uint32_t h = e / S::kVectors, v = e % S::kVectors, r = v / (DP / 16 * 32) * 8 + 2 * (v & 3);
                 float top[2] = {kNoMax, kNoMax}, sum[2] = {0.0f, 0.0f};
-                for (uint32_t w = h; w < S::kWarps; w += heads) {
+                for (uint32_t w = h; w < kWarps; w += heads) {
                     top[0] = fmaxf(top[0], refs[w * S::kRows + r].x);
                     top[1] = fmaxf(top[1], refs[w * S::kRows + r + 1].x);
                 }
                 float4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (uint32_t w = h; w < S::kWarps; w += heads) {
+                for (uint32_t w = h; w < kWarps; w += heads) {
                     const float2 m0 = refs[w * S::kRows + r], m1 = refs[w * S::kRows + r + 1];
                     const float b0 = exp2_approx(m0.x - top[0]), b1 = exp2_approx(m1.x - top[1]);
                     const float4 y = sums[w * S::kVectors + v];
@@ -880,9 +836,10 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                 }
             }
             if (!whole) {
-                // Pieces first .. have this tile of queries; the block that comes last joins their sums, in order.
+                // Blocks first .. have this tile of queries; the block that comes last joins their sums, in order.
                 const uint64_t units_at = at_line - skip + kTileCost;
-                const uint32_t first = line.piece_at(units_at), parts = line.piece_at(units_at + row.units - 1) - first + 1;
+                const uint64_t first = units_at / line.per;
+                const uint32_t parts = (uint32_t)((units_at + row.units - 1) / line.per - first) + 1;
                 __threadfence();
                 __syncthreads();
                 if (threadIdx.x == 0) last_here = count_arrival(a.arrived + first, tag_of(epoch)) == parts;
@@ -905,24 +862,15 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                 group = 0;
                 do {
                     if (++row_at >= a.v.rows) break;  // (lens that change meanwhile)
-                    row = row_units(a, row_at, S::kRows, S::kWarps);
+                    row = row_units(a, row_at, S::kRows);
                 } while (row.units == 0);
                 if (row_at >= a.v.rows) break;
             }
         }
     }
-    }
-    if (threadIdx.x == 0) {
-        next_piece = gridDim.x + drawn;
-        if (drawn == draws - 1) {
-            st_relaxed_u32(&a.hdr->counter, 0u);
-            st_relaxed_u32(&a.hdr->epoch, epoch + 1u);
-        }
-    }
-    __syncthreads();
-    piece = next_piece;
-    if (piece >= line.pieces) break;
-    __syncthreads();  // (next_piece was read)
+    if (threadIdx.x == 0 && nth_block == gridDim.x - 1) {  // the last to count itself re-arms the header
+        st_relaxed_u32(&a.hdr->counter, 0u);
+        st_relaxed_u32(&a.hdr->epoch, epoch + 1u);
     }
     finish_period(a.hdr, epoch, a.arrived, a.clear_words);
 }
@@ -930,8 +878,8 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
 // ---------------------------------------------------------------------------
 // Host side
 // ---------------------------------------------------------------------------
-constexpr size_t kPartialBytes = 2ull * kMaxBlocks * kLevels * kMaxElements * sizeof(float);
-constexpr size_t kPartialMlBytes = 2ull * kMaxBlocks * kLevels * kMaxPairs * sizeof(float2);
+constexpr size_t kPartialBytes = 2ull * kMaxBlocks * kMaxElements * sizeof(float);
+constexpr size_t kPartialMlBytes = 2ull * kMaxBlocks * kMaxPairs * sizeof(float2);
 
 size_t attend_workspace_bytes() {
     return round_up(round_up(tile_word_reach(), 256) + kPartialBytes + kPartialMlBytes, 256);
@@ -974,12 +922,9 @@ static int attend_launch(AttendArgs a, cudaStream_t s) {
     a.pair_heads = a.heads % 4 == 0 ? 2 : a.heads % 2 == 0 ? 1 : 0;
     if (a.pair_heads > S::kMostPaired) a.pair_heads = S::kMostPaired;
     while (a.pair_heads > 0 && tiles * (a.heads >> a.pair_heads) * 8 < blocks) --a.pair_heads;
-#ifdef PH
-    a.pair_heads = PH;
-#endif
     const uint64_t placed = a.v.width * a.v.page_tokens.d, length = placed < (1ull << 31) ? placed : (1ull << 31);
     const double units = (double)tiles * (a.heads >> a.pair_heads) *
-                         (double)(length / ((kTile * S::kWarps) >> a.pair_heads) + 1 + kTileCost);
+                         (double)(length / ((kTile * kWarps) >> a.pair_heads) + 1 + kTileCost);
     if (units < (double)(blocks * kLeastUnits)) blocks = (uint64_t)units / kLeastUnits + 1;
     const bool box = a.v.page_tokens.d % kTile == 0 && a.v.pages > 0;
     const auto kernel = box ? attend_kernel<T, DP, NT, true> : attend_kernel<T, DP, NT, false>;
@@ -988,7 +933,7 @@ static int attend_launch(AttendArgs a, cudaStream_t s) {
     CUtensorMap maps[2] = {};
     if (box && (!box_map(&maps[0], a.keys, a, DP >= 128) || !box_map(&maps[1], a.values, a, DP >= 128)))
         return U32SCAN_ECUDA;
-    kernel<<<(unsigned int)blocks, S::kThreads, S::kShared, s>>>(a, maps[0], maps[1]);
+    kernel<<<(unsigned int)blocks, kThreads, S::kShared, s>>>(a, maps[0], maps[1]);
     return cudaGetLastError() == cudaSuccess ? U32SCAN_OK : U32SCAN_ECUDA;
 }
 
