@@ -700,8 +700,8 @@ typedef struct {
 /*
  * No workspace. Errors: EINVAL (as sample_tokens; out_stride below vocab with
  * more than one row; overlapping logits and out; a null rules; history or
- * allowed rows that overlap partly do no harm, they are only read; widths at
- * or above 2^31, a null array with a width above 0, misaligned pointers),
+ * allowed rows that overlap do no harm, they are only read; history_width at
+ * or above 2^30, biases at or above 2^31, a null array with a width above 0, misaligned pointers),
  * ECUDA.
  */
 int adjust_logits(const void *logits, int type, size_t rows, size_t vocab, size_t row_stride, void *out,

@@ -1,8 +1,13 @@
 // append.cu -- new keys and values written into the pages of a paged cache,
 // keys (and queries) rotated by their position on the way.
 //
-// A warp takes one head of one token at a time; for the 8-bit cache, the new
-// tokens of one block of a page.
+// A block takes one token. Heads are handled in units of two vectors: the two
+// halves of eight (f32: four) pairs, or two adjacent vectors; a thread keeps to one
+// unit of a head and goes over the heads, its angles in registers. For the
+// 8-bit cache a warp takes one head of one block of a page: the largest
+// magnitude of its new tokens first, the codes in a second pass (the tokens
+// come from L1 then). The tokens of a block share its heads between them.
+// Heads of other sizes, strides or addresses go element by element.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -105,98 +110,260 @@ __device__ __forceinline__ const T *head_of(const Heads &h, uint64_t token, uint
     return static_cast<const T *>(h.data) + token * h.token_stride + head * h.head_stride;
 }
 
-// One block of one head: the scale that its new values need beside the old ones, then the codes.
-template <typename T>
-__device__ void append_block(const AppendArgs &a, const Place &p, uint64_t token, uint64_t head, bool key, int lane) {
-    const Heads &src = key ? a.keys : a.values;
-    uint8_t *codes = static_cast<uint8_t *>(key ? a.cache_keys : a.cache_values) + p.page * a.page_stride +
-                     head * a.head_stride;
-    const uint32_t nth = divide(p.slot, a.block_tokens), size = a.block_tokens.d;
-    const uint32_t before = p.slot - nth * size;  // older tokens of the block
-    float *scale_at = (key ? a.key_scales : a.value_scales) + p.page * a.scale_stride +
-                      (uint64_t)nth * a.keys.heads + head;
-    const int64_t len = a.v.lens[p.row];
-    uint32_t n = size - before;
-    if ((int64_t)n > len - p.position) n = (uint32_t)(len - p.position);
-    if (a.cos && (int64_t)n > (int64_t)a.positions - p.position) n = (uint32_t)((int64_t)a.positions - p.position);
-    const bool turn = key && a.cos;
-    float m = 0.0f;
-    for (uint32_t i = 0; i < n; ++i) {
-        const T *x = head_of<T>(src, token + i, head);
-        for (uint32_t d = lane; d < a.dim; d += 32) {
-            const float y = fabsf(rotated(a, x, d, p.position + i, turn));
-            if (y < INFINITY) m = fmaxf(m, y);
-        }
+// A rotated pair.
+__device__ __forceinline__ void turn_pair(float &x, float &y, float c, float s) {
+    const float a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+    y = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+    x = a;
+}
+
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Vector {
+    T x[N];
+};
+
+// Unit u of a head, two vectors of N elements: where they begin, and the first pair if it is turned.
+struct Unit {
+    uint32_t at[2], pair;
+    bool turned;
+};
+
+template <int N>
+__device__ __forceinline__ Unit unit_of(const AppendArgs &a, uint32_t u, bool turn) {
+    Unit x;
+    x.turned = turn && u * N < a.pairs;
+    x.pair = x.turned ? u * N : 0;
+    x.at[0] = x.turned && !a.interleaved ? u * N : 2 * u * N;
+    x.at[1] = x.turned && !a.interleaved ? a.pairs + u * N : x.at[0] + N;
+    return x;
+}
+
+template <int N>
+__device__ __forceinline__ void angles_of(const AppendArgs &a, const Unit &u, int64_t position, float (&c)[N], float (&s)[N]) {
+    if (!u.turned) return;
+    const uint64_t from = (uint64_t)position * a.pairs + u.pair;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4 *>(a.cos + from + i));
+        const float4 y = __ldg(reinterpret_cast<const float4 *>(a.sin + from + i));
+        c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+        s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
     }
-    m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+
+// The unit's values, turned.
+template <typename T, int N>
+__device__ __forceinline__ void turned_unit(const AppendArgs &a, const Unit &u, const Vector<T, N> &x, const Vector<T, N> &y,
+                                            const float (&c)[N], const float (&s)[N], float (&v)[2][N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[0][i] = Num<T>::get(x.x[i]), v[1][i] = Num<T>::get(y.x[i]);
+    if (!u.turned) return;
+    if (!a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) turn_pair(v[0][i], v[1][i], c[i], s[i]);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < N; i += 2) turn_pair(v[h][i], v[h][i + 1], c[(h * N + i) / 2], s[(h * N + i) / 2]);
+    }
+}
+
+// Where a block of a page stands, and the part of it that is new.
+struct Part {
+    float *scale;
+    uint8_t *codes;     // of the first new slot
+    uint32_t n, before; // new tokens, older ones in front of them
+    int64_t position;   // of the first new one
+    uint64_t token;
+    bool key;
+};
+
+// The largest magnitudes' scale: the least power of two that holds them, or the old one if it does; the older codes are
+// told in it (by the warp, element by element: they are few and seldom).
+__device__ float part_scale(const AppendArgs &a, const Part &p, float m, int lane) {
     // least e with m <= 1.75 * 2^(8 + e)
     int e = (int)(__float_as_uint(m) >> 23) - 127 - 8 + ((__float_as_uint(m) & 0x7fffffu) > 0x600000u ? 1 : 0);
     if (e < -100) e = -100;
     float scale = __uint_as_float((uint32_t)(e + 127) << 23);
-    if (before) {
-        float old = *scale_at;
+    if (p.before) {
+        float old = *p.scale;
         if (!(old > 0.0f && old < INFINITY)) old = 0.0f;
-        if (old >= scale) {
-            scale = old;
-        } else {
-            const float ratio = __fdiv_rn(old, scale);
-            for (uint32_t t = 0; t < before; ++t)
-                for (uint32_t d = lane; d < a.dim; d += 32) {
-                    uint8_t *c = codes + (uint64_t)(p.slot - before + t) * a.token_stride + d;
-                    *c = value_code(__fmul_rn(code_value(*c), ratio));
-                }
-        }
+        if (old >= scale) return old;
+        const float ratio = __fdiv_rn(old, scale);
+        for (uint32_t t = 1; t <= p.before; ++t)
+            for (uint32_t d = lane; d < a.dim; d += 32) {
+                uint8_t *c = p.codes - (uint64_t)t * a.token_stride + d;
+                *c = value_code(__fmul_rn(code_value(*c), ratio));
+            }
     }
-    const float inv = __fdiv_rn(1.0f, scale);
-    for (uint32_t i = 0; i < n; ++i) {
-        const T *x = head_of<T>(src, token + i, head);
-        for (uint32_t d = lane; d < a.dim; d += 32)
-            codes[(uint64_t)(p.slot + i) * a.token_stride + d] =
-                value_code(__fmul_rn(rotated(a, x, d, p.position + i, turn), inv));
-    }
-    __syncwarp();
-    if (lane == 0) *scale_at = scale;
+    return scale;
 }
 
-template <typename T, bool CODED>
+template <typename T>
+__device__ __forceinline__ T *cache_at(const AppendArgs &a, bool key, uint64_t page, uint64_t slot, uint64_t head) {
+    return static_cast<T *>(key ? a.cache_keys : a.cache_values) + page * a.page_stride + slot * a.token_stride +
+           head * a.head_stride;
+}
+
+// The part's codes and scale. N: vectors of N elements, or 0: one element at a time.
+template <typename T, int N>
+__device__ void append_part(const AppendArgs &a, const Part &p, uint64_t head, int lane) {
+    const Heads &src = p.key ? a.keys : a.values;
+    const bool turn = p.key && a.cos;
+    float m = 0.0f, inv = 0.0f;
+    for (int pass = 0; pass < 2; ++pass) {
+        if constexpr (N > 0) {
+            const uint32_t units = a.dim / (2 * N), abreast = 32 / units;  // of a token; tokens beside each other
+            const uint32_t mine = lane / units;
+            const Unit u = unit_of<N>(a, lane % units, turn);
+            if (mine < abreast) {
+#pragma unroll 4
+                for (uint32_t i = mine; i < p.n; i += abreast) {
+                    const T *x = head_of<T>(src, p.token + i, head);
+                    float c[N], s[N], v[2][N];
+                    angles_of<N>(a, u, p.position + i, c, s);
+                    turned_unit<T, N>(a, u, *reinterpret_cast<const Vector<T, N> *>(x + u.at[0]),
+                                      *reinterpret_cast<const Vector<T, N> *>(x + u.at[1]), c, s, v);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (pass == 0) {
+#pragma unroll
+                            for (int k = 0; k < N; ++k)
+                                if (fabsf(v[h][k]) < INFINITY) m = fmaxf(m, fabsf(v[h][k]));
+                        } else {
+                            uint32_t w = 0;
+#pragma unroll
+                            for (int k = 0; k < N; k += 2)
+                                w |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v[h][k], inv), __fmul_rn(v[h][k + 1], inv)),
+                                                                        __NV_SATFINITE, __NV_E4M3)
+                                     << 8 * k;
+                            *reinterpret_cast<uint32_t *>(p.codes + (uint64_t)i * a.token_stride + u.at[h]) = w;
+                        }
+                    }
+                }
+            }
+        } else {
+            for (uint32_t i = 0; i < p.n; ++i) {
+                const T *x = head_of<T>(src, p.token + i, head);
+                for (uint32_t d = lane; d < a.dim; d += 32) {
+                    const float y = rotated(a, x, d, p.position + i, turn);
+                    if (pass == 0) {
+                        if (fabsf(y) < INFINITY) m = fmaxf(m, fabsf(y));
+                    } else {
+                        p.codes[(uint64_t)i * a.token_stride + d] = value_code(__fmul_rn(y, inv));
+                    }
+                }
+            }
+        }
+        if (pass == 0) {
+            m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+            const float scale = part_scale(a, p, m, lane);
+            inv = __fdiv_rn(1.0f, scale);
+            __syncwarp();  // every lane has read the old scale
+            if (lane == 0) *p.scale = scale;
+        }
+    }
+}
+
+// WIDE: vectors of 16 bytes (for codes: of four values), else elements.
+template <typename T, bool CODED, bool WIDE>
 __global__ void __launch_bounds__(kNThreads) append_kernel(const AppendArgs a) {
     const uint64_t token = blockIdx.x;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Place p = place_of(a, token);
     if (p.row < 0) return;
     const bool turn = a.cos != nullptr, reached = !turn || (p.position >= 0 && (uint64_t)p.position < a.positions);
-    for (uint64_t h = warp; h < a.queries.heads; h += kNWarps) {
-        const T *x = head_of<T>(a.queries, token, h);
-        T *y = const_cast<T *>(head_of<T>(a.out, token, h));
-        float r[32];
-        int k = 0;
-        for (uint32_t d = lane; d < a.dim; d += 32) r[k++] = reached ? rotated(a, x, d, p.position, turn) : NAN;
-        __syncwarp();  // in place: every element read before any is written
-        k = 0;
-        for (uint32_t d = lane; d < a.dim; d += 32) y[d] = Num<T>::put(r[k++]);
+    if (CODED && p.held) {
+        // the block's new tokens, of which this is number `rank`; they take its heads in turn
+        const uint32_t size = a.block_tokens.d, nth = divide(p.slot, a.block_tokens), within = p.slot - nth * size;
+        const int64_t back = p.position - p.first;  // new tokens of the row before this one
+        const uint32_t rank = back < (int64_t)within ? (uint32_t)back : within, before = within - rank;
+        const int64_t position = p.position - rank;
+        int64_t n = (int64_t)a.v.lens[p.row] - position;
+        if (n > (int64_t)(size - before)) n = size - before;
+        if (turn && n > (int64_t)a.positions - position) n = (int64_t)a.positions - position;
+        for (uint64_t task = rank + (uint64_t)n * warp; task < 2 * a.keys.heads; task += (uint64_t)n * kNWarps) {
+            const uint64_t head = task >> 1;
+            const bool key = !(task & 1);
+            const Part part{(key ? a.key_scales : a.value_scales) + p.page * a.scale_stride + (uint64_t)nth * a.keys.heads + head,
+                            cache_at<uint8_t>(a, key, p.page, p.slot - rank, head), (uint32_t)n, before, position, token - rank,
+                            key};
+            append_part<T, WIDE ? 4 : 0>(a, part, head, lane);
+        }
     }
-    if (!p.held) return;
-    if (CODED) {
-        const uint32_t within = p.slot - divide(p.slot, a.block_tokens) * a.block_tokens.d;
-        if (within != 0 && p.position != p.first) return;  // the block's first new token writes it
-        for (uint64_t h = warp; h < 2 * a.keys.heads; h += kNWarps)
-            append_block<T>(a, p, token, h >> 1, !(h & 1), lane);
+    if constexpr (WIDE) {
+        constexpr int N = 16 / sizeof(T);
+        const uint32_t units = a.dim / (2 * N), abreast = kNThreads / units, mine = threadIdx.x / units;
+        if (mine >= abreast) return;
+        const Unit u = unit_of<N>(a, threadIdx.x % units, turn), plain = unit_of<N>(a, threadIdx.x % units, false);
+        float c[N], s[N];
+        if (reached) angles_of<N>(a, u, p.position, c, s);
+        const uint64_t heads = a.queries.heads + (!CODED && p.held ? 2 * a.keys.heads : 0);
+#pragma unroll 4
+        for (uint64_t h = mine; h < heads; h += abreast) {
+            const bool query = h < a.queries.heads, key = h < a.queries.heads + a.keys.heads;
+            const uint64_t head = query ? h : key ? h - a.queries.heads : h - a.queries.heads - a.keys.heads;
+            const Unit &x = key ? u : plain;
+            const T *from = head_of<T>(query ? a.queries : key ? a.keys : a.values, token, head);
+            T *to = query ? const_cast<T *>(head_of<T>(a.out, token, head)) : cache_at<T>(a, key, p.page, p.slot, head);
+            Vector<T, N> v[2] = {*reinterpret_cast<const Vector<T, N> *>(from + x.at[0]),
+                                 *reinterpret_cast<const Vector<T, N> *>(from + x.at[1])};
+            if (x.turned || !reached) {
+                float y[2][N];
+                turned_unit<T, N>(a, x, v[0], v[1], c, s, y);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    v[0].x[i] = Num<T>::put(reached ? y[0][i] : NAN);
+                    v[1].x[i] = Num<T>::put(reached ? y[1][i] : NAN);
+                }
+            }
+            *reinterpret_cast<Vector<T, N> *>(to + x.at[0]) = v[0];
+            *reinterpret_cast<Vector<T, N> *>(to + x.at[1]) = v[1];
+        }
     } else {
-        for (uint64_t h = warp; h < 2 * a.keys.heads; h += kNWarps) {
+        for (uint64_t h = warp; h < a.queries.heads; h += kNWarps) {
+            const T *x = head_of<T>(a.queries, token, h);
+            T *y = const_cast<T *>(head_of<T>(a.out, token, h));
+            float r[32];
+            int k = 0;
+            for (uint32_t d = lane; d < a.dim; d += 32) r[k++] = reached ? rotated(a, x, d, p.position, turn) : NAN;
+            __syncwarp();  // in place: every element read before any is written
+            k = 0;
+            for (uint32_t d = lane; d < a.dim; d += 32) y[d] = Num<T>::put(r[k++]);
+        }
+        const uint64_t heads = CODED || !p.held ? 0 : 2 * a.keys.heads;
+        for (uint64_t h = warp; h < heads; h += kNWarps) {
             const bool key = !(h & 1);
             const T *x = head_of<T>(key ? a.keys : a.values, token, h >> 1);
-            T *y = static_cast<T *>(key ? a.cache_keys : a.cache_values) + p.page * a.page_stride +
-                   (uint64_t)p.slot * a.token_stride + (h >> 1) * a.head_stride;
+            T *y = cache_at<T>(a, key, p.page, p.slot, h >> 1);
             for (uint32_t d = lane; d < a.dim; d += 32) y[d] = Num<T>::put(rotated(a, x, d, p.position, key && turn));
         }
     }
 }
 
+// Whether every address that a vector kernel forms is a multiple of its vector's size (16 bytes; codes: 4).
+static bool wide(const AppendArgs &a, size_t elem, bool coded) {
+    const uint64_t n = 16 / elem;
+    if (a.dim % (2 * n) != 0 || a.dim > 256 || (a.cos && (a.pairs % n != 0 || misaligned(a.cos, 16) || misaligned(a.sin, 16))))
+        return false;
+    for (const Heads *h : {&a.keys, &a.values, &a.queries, &a.out})
+        if (h->heads > 0 && (misaligned(h->data, 16) || (h->token_stride | h->head_stride) % n != 0)) return false;
+    const uint64_t m = coded ? 4 : n;
+    return !misaligned(a.cache_keys, coded ? 4 : 16) && !misaligned(a.cache_values, coded ? 4 : 16) &&
+           (a.page_stride | a.token_stride | a.head_stride) % m == 0;
+}
+
 template <typename T>
 static void append_launch(const AppendArgs &a, bool coded, cudaStream_t s) {
     const unsigned int grid = (unsigned int)a.v.tokens;
-    if (coded) append_kernel<T, true><<<grid, kNThreads, 0, s>>>(a);
-    else append_kernel<T, false><<<grid, kNThreads, 0, s>>>(a);
+    if (wide(a, sizeof(T), coded)) {
+        if (coded) append_kernel<T, true, true><<<grid, kNThreads, 0, s>>>(a);
+        else append_kernel<T, false, true><<<grid, kNThreads, 0, s>>>(a);
+    } else {
+        if (coded) append_kernel<T, true, false><<<grid, kNThreads, 0, s>>>(a);
+        else append_kernel<T, false, false><<<grid, kNThreads, 0, s>>>(a);
+    }
 }
 
 }  // namespace u32scan
