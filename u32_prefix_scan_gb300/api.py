@@ -638,15 +638,23 @@ def _tensor(t, name: str) -> torch.Tensor:
     return t
 
 
+def _misplaced(t, name: str, dev: int) -> ValueError:
+    if not t.is_cuda:
+        return ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    return ValueError(f"{name} must be on cuda:{dev}")
+
+
 def _arg(t, name: str, dtype, numel: int, dev: int) -> int:
     """The device pointer of a contiguous tensor of at least numel elements
     on CUDA device `dev`."""
-    if not _tensor(t, name).is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise _misplaced(t, name, dev)
     if t.dtype is not dtype:
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
+        raise _misplaced(t, name, dev)
     if t.numel() < numel:
         raise ValueError(f"{name} must hold at least {numel} elements")
     if not t.is_contiguous():
@@ -869,23 +877,26 @@ def pages_compact(pool: PagePool | None, table: torch.Tensor, lens: torch.Tensor
     return live, remap
 
 
-def _matrix(t, name: str, dtype, rows: int, dev: int) -> tuple[int, int, int]:
+def _matrix(t, name: str, dtypes, rows: int, dev: int) -> tuple[int, int, int]:
     """Pointer, width and row stride of a tensor [rows, width] whose rows'
     elements are adjacent; (None, 0, 0) for None."""
     if t is None:
         return None, 0, 0
-    if not _tensor(t, name).is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
-    if t.dtype not in dtype:
-        raise TypeError(f"{name} must have dtype in {dtype}, got {t.dtype}")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        if not t.is_cuda:
+            raise _misplaced(t, name, dev)
+        raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
     if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
-    if t.dim() != 2 or t.shape[0] != rows:
+        raise _misplaced(t, name, dev)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows:
         raise ValueError(f"{name} must have two dimensions, the first of {rows}")
     stride, step = t.stride()
-    if step != 1 and t.shape[1] > 1:
+    if step != 1 and shape[1] > 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent")
-    return t.data_ptr(), t.shape[1], stride
+    return t.data_ptr(), shape[1], stride
 
 
 def adjust_logits(logits: torch.Tensor, *, history: torch.Tensor | None = None,
@@ -1052,12 +1063,14 @@ def _cache_rows(cache, table, lens, starts, tokens: int):
 def _heads_arg(t, name: str, dtype, tokens: int, heads: int | None, dim: int, dev: int):
     """Pointer and strides of a tensor [tokens, heads, dim] whose heads'
     elements are adjacent."""
-    if not _tensor(t, name).is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (this library has no CPU path)")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
+        if not t.is_cuda:
+            raise _misplaced(t, name, dev)
         raise TypeError(f"{name} must have dtype {dtype}, got {t.dtype}")
     if t.get_device() != dev:
-        raise ValueError(f"{name} must be on cuda:{dev}")
+        raise _misplaced(t, name, dev)
     shape = t.shape
     if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or (heads is not None and shape[1] != heads):
         raise ValueError(f"{name} must have the shape [{tokens}, {'heads' if heads is None else heads}, {dim}]")
@@ -1070,13 +1083,15 @@ def _heads_arg(t, name: str, dtype, tokens: int, heads: int | None, dim: int, de
 def _distinct(t, name: str) -> None:
     """Refuses an output whose elements share memory (heads and tokens in
     either order)."""
-    (tokens, heads, dim), (ts, hs, _) = t.shape, t.stride()
-    small, n = (hs, heads) if heads > 1 and (tokens <= 1 or hs <= ts) else (ts, tokens)
-    big = ts if (small, n) == (hs, heads) else hs
-    reach = dim if n <= 1 else (n - 1) * small + dim
-    both = tokens > 1 and heads > 1
-    if t.numel() and ((n > 1 and small < dim) or (both and big < reach)):
-        raise ValueError(f"the heads of {name} must not overlap")
+    if t.is_contiguous():
+        return
+    (tokens, heads, dim), (token_stride, head_stride, _) = t.shape, t.stride()
+    reach = dim
+    for stride, n in sorted(((token_stride, tokens), (head_stride, heads))):
+        if n > 1 and stride < reach and t.numel():
+            raise ValueError(f"the heads of {name} must not overlap")
+        if n > 1:
+            reach += stride * (n - 1)
 
 
 def pages_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_keys: torch.Tensor,

@@ -18,8 +18,7 @@
 
 namespace u32scan {
 
-constexpr int kNThreads = 256;
-constexpr int kNWarps = kNThreads / 32;
+constexpr int kNThreads = 256;  // at most
 
 struct Heads {
     const void *data;
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(kNThreads) append_kernel(const AppendArgs a) {
         int64_t n = (int64_t)a.v.lens[p.row] - position;
         if (n > (int64_t)(size - before)) n = size - before;
         if (turn && n > (int64_t)a.positions - position) n = (int64_t)a.positions - position;
-        for (uint64_t task = rank + (uint64_t)n * warp; task < 2 * a.keys.heads; task += (uint64_t)n * kNWarps) {
+        for (uint64_t task = rank + (uint64_t)n * warp; task < 2 * a.keys.heads; task += (uint64_t)n * (blockDim.x / 32)) {
             const uint64_t head = task >> 1;
             const bool key = !(task & 1);
             const Part part{(key ? a.key_scales : a.value_scales) + p.page * a.scale_stride + (uint64_t)nth * a.keys.heads + head,
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(kNThreads) append_kernel(const AppendArgs a) {
     }
     if constexpr (WIDE) {
         constexpr int N = 16 / sizeof(T);
-        const uint32_t units = a.dim / (2 * N), abreast = kNThreads / units, mine = threadIdx.x / units;
+        const uint32_t units = a.dim / (2 * N), abreast = blockDim.x / units, mine = threadIdx.x / units;
         if (mine >= abreast) return;
         const Unit u = unit_of<N>(a, threadIdx.x % units, turn), plain = unit_of<N>(a, threadIdx.x % units, false);
         float c[N], s[N];
@@ -322,7 +321,7 @@ __global__ void __launch_bounds__(kNThreads) append_kernel(const AppendArgs a) {
             *reinterpret_cast<Vector<T, N> *>(to + x.at[1]) = v[1];
         }
     } else {
-        for (uint64_t h = warp; h < a.queries.heads; h += kNWarps) {
+        for (uint64_t h = warp; h < a.queries.heads; h += blockDim.x / 32) {
             const T *x = head_of<T>(a.queries, token, h);
             T *y = const_cast<T *>(head_of<T>(a.out, token, h));
             float r[32];
@@ -332,8 +331,7 @@ __global__ void __launch_bounds__(kNThreads) append_kernel(const AppendArgs a) {
             k = 0;
             for (uint32_t d = lane; d < a.dim; d += 32) y[d] = Num<T>::put(r[k++]);
         }
-        const uint64_t heads = CODED || !p.held ? 0 : 2 * a.keys.heads;
-        for (uint64_t h = warp; h < heads; h += kNWarps) {
+        for (uint64_t h = warp; !CODED && p.held && h < 2 * a.keys.heads; h += blockDim.x / 32) {
             const bool key = !(h & 1);
             const T *x = head_of<T>(key ? a.keys : a.values, token, h >> 1);
             T *y = cache_at<T>(a, key, p.page, p.slot, h >> 1);
@@ -357,13 +355,20 @@ static bool wide(const AppendArgs &a, size_t elem, bool coded) {
 template <typename T>
 static void append_launch(const AppendArgs &a, bool coded, cudaStream_t s) {
     const unsigned int grid = (unsigned int)a.v.tokens;
-    if (wide(a, sizeof(T), coded)) {
-        if (coded) append_kernel<T, true, true><<<grid, kNThreads, 0, s>>>(a);
-        else append_kernel<T, false, true><<<grid, kNThreads, 0, s>>>(a);
-    } else {
+    if (!wide(a, sizeof(T), coded)) {
         if (coded) append_kernel<T, true, false><<<grid, kNThreads, 0, s>>>(a);
         else append_kernel<T, false, false><<<grid, kNThreads, 0, s>>>(a);
+        return;
     }
+    // Of many tokens (more blocks of 64 threads than run at a time) a thread takes several units, whose loads overlap; of few
+    // as many threads as a token has units, or warps as it has heads of its block. 64, 128, 256 threads: 8192 tokens of
+    // 64 + 16 heads of 128 bf16 60, 60, 70 us, 16384 tokens of 16 + 32 heads of 64 into 8 bits 85, 90, 135; 64 tokens of
+    // 32 + 16 heads into 8 bits 11.5, 7.3, 5.2.
+    const uint64_t units = a.queries.heads * (a.dim * sizeof(T) / 32) + (coded ? 0 : 2 * a.keys.heads * (a.dim * sizeof(T) / 32));
+    const uint64_t work = coded && units < 64 * a.keys.heads ? 64 * a.keys.heads : units;
+    const int threads = a.v.tokens >= 2432 || work <= 64 ? 64 : work <= 128 ? 128 : kNThreads;
+    if (coded) append_kernel<T, true, true><<<grid, threads, 0, s>>>(a);
+    else append_kernel<T, false, true><<<grid, threads, 0, s>>>(a);
 }
 
 }  // namespace u32scan

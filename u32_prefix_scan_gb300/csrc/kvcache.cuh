@@ -52,21 +52,25 @@ __device__ __forceinline__ void tokens_of(const RowsView &v, uint64_t s, int64_t
 }
 
 // The row of a token of the call, or -1 behind the last row's tokens: the
-// last row that begins at or before it.
+// last row that begins at or before it. A whole warp looks, 32 rows at a time
+// (one after the other, in halves, the loads are what a small append waits for).
 __device__ __forceinline__ int64_t row_of(const RowsView &v, uint64_t token, int64_t *begin, int64_t *n) {
-    int64_t lo = (int64_t)token;
+    uint64_t lo = token;
     if (v.starts) {
-        int64_t hi = (int64_t)v.rows;
-        lo = -1;
-        while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) / 2;
-            if ((int64_t)v.starts[mid] <= (int64_t)token) lo = mid;
-            else hi = mid;
-        }
-        if (lo < 0) return -1;
+        uint64_t left = v.rows;  // the row is one of lo .. lo + left - 1, or none
+        lo = 0;
+        do {
+            const uint64_t step = (left + 31) / 32, at = (threadIdx.x & 31) * step;
+            const bool before = at < left && (int64_t)v.starts[lo + at] <= (int64_t)token;
+            const int found = __popc(__ballot_sync(0xffffffffu, before));
+            if (found == 0) return -1;
+            const uint64_t skip = (found - 1) * step;
+            lo += skip;
+            left = left - skip < step ? left - skip : step;
+        } while (left > 1);
     }
-    tokens_of(v, (uint64_t)lo, begin, n);
-    return (int64_t)token < *begin + *n ? lo : -1;
+    tokens_of(v, lo, begin, n);
+    return (int64_t)token < *begin + *n ? (int64_t)lo : -1;
 }
 
 static inline bool misaligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
