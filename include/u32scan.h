@@ -881,7 +881,8 @@ typedef struct {
  * queries_out too.
  * No two rows may write to one page (pages_fork sees to it), nor a row twice.
  * No workspace. Errors: EINVAL (null pointers with sizes above 0, misaligned
- * pointers, sizes at or above 2^31, strides at or above 2^40, rows and tokens
+ * pointers, sizes at or above 2^31, strides at or above 2^40 or 0 where there
+ * is more than one, rows and tokens
  * that differ without starts, 2 pairs above dim, dim above 1024, blocks that do not
  * divide page_tokens, an unknown type or a cache of another one), ECUDA.
  */
@@ -911,8 +912,9 @@ int pages_append(const u32scan_kv_cache *cache, const int32_t *table, size_t tab
  *   ws, ws_bytes  u32scan_workspace_bytes(U32SCAN_OP_ATTEND, tokens) bytes.
  * The result does not depend on the other calls that run; every sum is taken
  * in an order fixed by the sizes, lens and starts.
- * Errors: EINVAL (as pages_append; another cache type; the alignments above),
- * EWORKSPACE, ECUDA.
+ * Errors: EINVAL (as pages_append; another cache type; the alignments above;
+ * tokens times query heads of a key head at or above 2^31), EWORKSPACE, ECUDA; a
+ * copy that does not land within its time as the scan's.
  */
 int pages_attend(const u32scan_kv_cache *cache, const int32_t *table, size_t table_stride, size_t rows, size_t width,
                  const int32_t *lens, const int32_t *starts, size_t tokens, const void *queries, int type,

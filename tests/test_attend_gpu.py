@@ -370,3 +370,51 @@ def test_none_of_it(u):
     assert not u.pages_attend(empty, d["table"], d["lens"], d["queries"]).any()
     no_width = u.pages_attend(cache, d["table"][:, :0], d["lens"], d["queries"])
     assert not no_width.any()
+
+
+def test_a_workspace_shared_with_other_operations(u):
+    """Scans, sorts and page operations leave their words and buffers where the
+    call keeps its counts and partial sums, and the other way round."""
+    from u32_prefix_scan_gb300 import _native, inputs
+
+    c = Case(19, [900, 30, 400, 77], heads=4, group=4, dim=128)
+    d = c.gpu()
+    want = call(u, d)
+    n = (1 << 20) + 77
+    sizes = [(1, n), (4, n), (9, 500), (10, 1)]
+    ws = u.Workspace(max(_native.lib().u32scan_workspace_bytes(*s) for s in sizes), torch.device("cuda"))
+    values = inputs.splitmix_u32(7, 0, n)
+    scanned, total = oracle.scan_exclusive(values)
+    refs = torch.zeros(400, dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        a = torch.from_numpy(values.view(np.int32).copy()).cuda()
+        u.scan_exclusive_u32(a, workspace=ws)
+        assert torch.equal(call(u, d, workspace=ws), want)
+        perm = u.radix_sort_perm_u32(torch.from_numpy(values.view(np.int32).copy()).cuda(), workspace=ws)
+        assert torch.equal(call(u, d, workspace=ws), want)
+        lens, table = torch.zeros(5, dtype=torch.int32, device="cuda"), torch.full((5, 4), -1, dtype=torch.int32, device="cuda")
+        status, _ = u.pages_fork(table, lens, refs * 0, 16, grow=lens + 20, workspace=ws)
+        assert torch.equal(call(u, d, workspace=ws), want)
+        assert np.array_equal(a.cpu().numpy().view(np.uint32), scanned) and status.tolist() == [2] * 5
+        assert np.array_equal(perm.cpu().numpy(), oracle.sort_perm(values))
+    assert u.check(workspace=ws) == _native.OK
+
+
+def test_the_end_of_a_tag_period(u):
+    """The launch that ends a period of tags clears the counts, so that the
+    same tags start from none."""
+    c = Case(20, [5000, 3000], heads=2, group=4, dim=128)
+    d = c.gpu()
+    want = call(u, d)
+    ws = u.Workspace(u._native.lib().u32scan_workspace_bytes(10, 1), torch.device("cuda"))
+
+    def set_epoch(e):
+        ws.buf[4:8].copy_(torch.tensor([e], dtype=torch.int64).to(torch.int32).view(torch.uint8))
+
+    period = 1 << 29
+    for start in (period - 2, 2 * period - 2, 3 * period - 2):
+        set_epoch(start)
+        for _ in range(4):  # two before the period's end, two behind
+            assert torch.equal(call(u, d, workspace=ws), want)
+        head = ws.buf[:8].view(torch.int32).tolist()
+        assert head[0] == 0 and head[1] & 0xFFFFFFFF == start + 4

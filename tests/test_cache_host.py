@@ -149,6 +149,8 @@ def test_shapes_types_and_layouts_that_are_refused(gpu):
     for call in (
             lambda: u.KVCache(a.keys, on(a.values[:, :, :1]), *a.scales),
             lambda: u.KVCache(on(a.keys[0]), on(a.values[0]), *a.scales),
+            lambda: u.KVCache(on(a.keys[:, :0]), on(a.values[:, :0]), *a.scales),
+            lambda: u.KVCache(on(a.keys[:, :, :, :0]), on(a.values[:, :, :, :0]), *a.scales),
             lambda: u.KVCache(a.keys, a.values), lambda: u.KVCache(a.keys, a.values, a.scales[0]),
             lambda: u.KVCache(a.keys, a.values, new(6, 3, 2, dtype=F32), new(6, 3, 2, dtype=F32)),
             lambda: u.KVCache(a.keys, a.values, new(6, 0, 2, dtype=F32), new(6, 0, 2, dtype=F32)),

@@ -226,7 +226,7 @@ BAD_CACHE = [dict(type=4), dict(type=-1), dict(pages=1 << 31), dict(page_tokens=
              dict(heads=0), dict(heads=1 << 16), dict(dim=0), dict(dim=1025), dict(page_stride=1 << 40),
              dict(token_stride=1 << 40), dict(head_stride=1 << 40), dict(keys=None), dict(values=None),
              dict(key_scales=None), dict(value_scales=None), dict(blocks=0), dict(blocks=3), dict(key_scales=FAKE + 2),
-             dict(scale_stride=1 << 40)]
+             dict(scale_stride=1 << 40), dict(page_stride=0), dict(token_stride=0), dict(head_stride=0)]
 
 
 def test_append_rejects_bad_arguments_on_host(lib):
@@ -267,7 +267,7 @@ def test_attend_rejects_bad_arguments_on_host(lib):
         assert call(cache=cache) == _native.EINVAL, cache
     for kw in (dict(type=0), dict(type=3), dict(tokens=1 << 31), dict(queries=None), dict(out=None),
                dict(queries=FAKE + 8), dict(qs=260), dict(qh=68), dict(out=FAKE + 1), dict(q_heads=0), dict(q_heads=5),
-               dict(q_heads=1 << 16), dict(qs=1 << 40), dict(oh=1 << 40)):
+               dict(q_heads=1 << 16), dict(qs=1 << 40), dict(oh=1 << 40), dict(tokens=1 << 30, q_heads=8)):
         assert call(**kw) == _native.EINVAL, kw
     for kw in (dict(ws=None), dict(ws=FAKE + 128), dict(ws_bytes=need - 256)):
         assert call(**kw) == _native.EWORKSPACE, kw

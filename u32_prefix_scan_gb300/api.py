@@ -998,6 +998,8 @@ class KVCache:
         if keys.stride(3) != 1 and keys.shape[3] > 1:
             raise ValueError("the elements of a head must be adjacent")
         pages, page_tokens, heads, dim = keys.shape
+        if 0 in (page_tokens, heads, dim):
+            raise ValueError("a cache needs tokens, heads and dimensions")
         # sizes of which there is one need no stride, and torch keeps any there
         strides = [s if n > 1 else 0 for s, n in zip(keys.stride()[:3], keys.shape[:3])]
         spans = sorted((s, n) for s, n in zip(strides, keys.shape[:3]) if n > 1)

@@ -82,6 +82,9 @@ static inline bool cache_ok(const u32scan_kv_cache *c) {
     if (c->pages >= (1ull << 31) || c->page_tokens == 0 || c->page_tokens >= (1ull << 31)) return false;
     if (c->heads == 0 || c->heads >= (1ull << 16) || c->dim == 0 || c->dim > 1024) return false;
     if (c->page_stride >= (1ull << 40) || c->token_stride >= (1ull << 40) || c->head_stride >= (1ull << 40)) return false;
+    if ((c->pages > 1 && c->page_stride == 0) || (c->page_tokens > 1 && c->token_stride == 0) ||
+        (c->heads > 1 && c->head_stride == 0))
+        return false;
     if (c->pages > 0 && (c->keys == nullptr || c->values == nullptr)) return false;
     if (misaligned(c->keys, element_bytes(c->type)) || misaligned(c->values, element_bytes(c->type))) return false;
     if (c->type == U32SCAN_E4M3) {
