@@ -29,7 +29,7 @@
 // Measured on one GB300, launches back to back: 64 ragged rows of up to 8192
 // tokens of 8 heads of 128, groups of eight, 111 us (540 MB, 4.9 TB/s), 16384
 // tokens each 374 us (5.8 TB/s), two rows of 200000 tokens 164 us, 33 rows of
-// drafts (up to five tokens, groups of seven, heads of 64, pages of 20) 43 us, one
+// drafts (up to five tokens, groups of seven, heads of 64, pages of 20) 32 us, one
 // row of 4000 tokens 14 us. Bound by the reading of the cache, unevenly: some
 // groups of SMs read 18 % slower than the rest and end last; the same grid with
 // its copies alone takes 100 of the 111 us. A block's fixed part (queries, page
@@ -949,16 +949,16 @@ static int attend_launch(AttendArgs a, cudaStream_t s) {
     return cudaGetLastError() == cudaSuccess ? U32SCAN_OK : U32SCAN_ECUDA;
 }
 
-// Eight queries at a time, more where a row has them (a row of one token has `group` for each key head; of
-// ragged ones the mean is known here): the codes are read and converted once for all of a tile.
+// Eight queries at a time, or sixteen where the mean row has nearly that many for each key head: the codes are then read and
+// converted once for both, in twice the registers. 64 rows of up to 8192 tokens, 8 heads of 128, with 8 and 16 at a time:
+// groups of 16 173 and 151 us, of 8 with one or two tokens (12 queries in the mean) 110 and 144, with one to five
+// (24) 227 and 218; 33 short rows of drafts, heads of 64 (21), 28 and 32, 200 longer ones 165 and 151. (32 at a
+// time, heads of 64: 42 and 218.)
 template <typename T>
 static int attend_dispatch(const AttendArgs &a, cudaStream_t s) {
-    const uint64_t queries = (a.v.tokens + a.v.rows - 1) / a.v.rows * a.group.d;
-    if (a.dim <= 64) {
-        if (queries <= 8) return attend_launch<T, 64, 1>(a, s);
-        return queries <= 16 ? attend_launch<T, 64, 2>(a, s) : attend_launch<T, 64, 4>(a, s);
-    }
-    if (a.dim <= 128) return queries <= 8 ? attend_launch<T, 128, 1>(a, s) : attend_launch<T, 128, 2>(a, s);
+    const bool many = a.v.tokens * a.group.d >= 14 * a.v.rows;
+    if (a.dim <= 64) return many ? attend_launch<T, 64, 2>(a, s) : attend_launch<T, 64, 1>(a, s);
+    if (a.dim <= 128) return many ? attend_launch<T, 128, 2>(a, s) : attend_launch<T, 128, 1>(a, s);
     return attend_launch<T, 256, 1>(a, s);
 }
 
