@@ -305,3 +305,20 @@ def test_another_stream_and_a_graph(u):
         graph.replay()
         torch.cuda.synchronize()
         fresh.check(d)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(u, cache):
+    """Pages half a gigabyte apart."""
+    c = Case(51, [30, 41], [13, 41], cache=cache, heads=2, dim=32, page_tokens=8, blocks=2)
+    d = c.gpu()
+    room = torch.empty(c.pages << 29, dtype=torch.uint8, device="cuda").view(c.pages, 1 << 29)
+    assert room.numel() > 1 << 32
+    for at, k in ((0, "keys"), (1 << 28, "values")):
+        t = d[k]
+        size = 8 * 2 * 32 * t.element_size()
+        view = room[:, at : at + size].view(t.dtype).view(c.pages, 8, 2, 32)
+        view.view(torch.uint8).copy_(t.view(torch.uint8))
+        d[k] = view
+    call(u, d)
+    c.check({**d, "keys": d["keys"].contiguous(), "values": d["values"].contiguous()})

@@ -418,3 +418,36 @@ def test_the_end_of_a_tag_period(u):
             assert torch.equal(call(u, d, workspace=ws), want)
         head = ws.buf[:8].view(torch.int32).tolist()
         assert head[0] == 0 and head[1] & 0xFFFFFFFF == start + 4
+
+
+@pytest.mark.parametrize("page_tokens", [16, 20])
+def test_offsets_past_32_bits(u, page_tokens):
+    """Pages half a gigabyte apart."""
+    c = Case(23, [page_tokens * 4 + 3, 50], [2, 1], heads=2, group=3, dim=64, page_tokens=page_tokens)
+    d = c.gpu()
+    room = torch.empty(c.pages << 29, dtype=torch.uint8, device="cuda").view(c.pages, 1 << 29)
+    assert room.numel() > 1 << 32
+    size = page_tokens * 2 * 64
+    for at, k in ((0, "keys"), (1 << 28, "values")):
+        view = room[:, at : at + size].view(torch.float8_e4m3fn).view(c.pages, page_tokens, 2, 64)
+        view.view(torch.uint8).copy_(d[k].view(torch.uint8))
+        d[k] = view
+    c.check(call(u, d))
+
+
+def test_two_streams_at_once(u):
+    """Each stream has a workspace of its own; neither call sees the other's."""
+    cases = [Case(24, [3000, 20, 700], heads=4, group=4, dim=128), Case(25, [1500] * 9, [3] * 9, heads=2, group=2, dim=64)]
+    ds = [c.gpu() for c in cases]
+    want = [call(u, d) for d in ds]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for i, (d, s) in enumerate(zip(ds, streams)):
+            cache = u.KVCache(d["keys"], d["values"], d["key_scales"], d["value_scales"])
+            outs[i].append(u.pages_attend(cache, d["table"], d["lens"], d["queries"], starts=d["starts"], stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])

