@@ -201,9 +201,15 @@ def test_what_the_library_gets(gpu):
     assert (s.type, s.pages, s.page_tokens, s.heads, s.dim) == (_native.E4M3, 6, 16, 2, 32)
     assert (s.page_stride, s.token_stride, s.head_stride, s.blocks, s.scale_stride) == (1024, 64, 32, 4, 8)
     u.pages_append(a.cache, a.table, a.lens, a.k, a.v, cos=a.angles, sin=a.angles, interleaved=True)
-    n = gpu.lib.calls[-1][1][8]
+    n = _native.NewTokensStruct.from_buffer_copy(gpu.lib.calls[-1][1][8])
     assert (n.tokens, n.type, n.key_token_stride, n.key_head_stride, n.positions, n.pairs) == (4, _native.BF16, 64, 32, 50, 16)
     assert n.queries is None and n.interleaved == 1
     u.adjust_logits(a.logits, allowed=on(a.matrix[:1].expand(4, -1)))
-    r = gpu.lib.calls[-1][1][7]
+    r = _native.LogitRulesStruct.from_buffer_copy(gpu.lib.calls[-1][1][7])
     assert r.history is None and r.allowed_stride == 0 and r.allowed == a.matrix.data_ptr()
+
+
+def test_packed_arguments_are_the_structures():
+    for kind, pack in ((_native.LogitRulesStruct, _native.pack_logit_rules), (_native.NewTokensStruct, _native.pack_new_tokens)):
+        values = [i + 1 for i in range(len(kind._fields_))]
+        assert pack(*values) == bytes(kind(*values))

@@ -188,7 +188,7 @@ def rules(**kw):
 
 def test_adjust_rejects_bad_arguments_on_host(lib):
     def call(logits=FAKE, type=0, rows=4, vocab=100, stride=100, out=FAKE + (1 << 20), out_stride=100, **kw):
-        return lib.adjust_logits(logits, type, rows, vocab, stride, out, out_stride, rules(**kw), None)
+        return lib.adjust_logits(logits, type, rows, vocab, stride, out, out_stride, ctypes.byref(rules(**kw)), None)
 
     for kw in (dict(type=3), dict(type=-1), dict(logits=None), dict(out=None), dict(logits=FAKE + 2), dict(out=FAKE + 1),
                dict(type=1, logits=FAKE + 1), dict(rows=1 << 28), dict(vocab=(1 << 22) + 1, out_stride=1 << 23),
@@ -232,7 +232,7 @@ BAD_CACHE = [dict(type=4), dict(type=-1), dict(pages=1 << 31), dict(page_tokens=
 def test_append_rejects_bad_arguments_on_host(lib):
     def call(cache=None, new=None, table=FAKE, stride=4, rows=3, width=4, lens=FAKE, starts=FAKE, status=None):
         return lib.pages_append(kv(**(cache or {})), table, stride, rows, width, lens, starts, status,
-                                new_tokens(**(new or {})), None)
+                                ctypes.byref(new_tokens(**(new or {}))), None)
 
     for kw in BAD_ROWS + [dict(status=FAKE + 1)]:
         assert call(**kw) == _native.EINVAL, kw
@@ -244,7 +244,7 @@ def test_append_rejects_bad_arguments_on_host(lib):
                 dict(positions=1 << 31), dict(key_head_stride=1 << 40), dict(out_token_stride=1 << 40),
                 dict(q_heads=1 << 16)):
         assert call(new=new) == _native.EINVAL, new
-    assert lib.pages_append(None, FAKE, 4, 3, 4, FAKE, FAKE, None, new_tokens(), None) == _native.EINVAL
+    assert lib.pages_append(None, FAKE, 4, 3, 4, FAKE, FAKE, None, ctypes.byref(new_tokens()), None) == _native.EINVAL
     assert lib.pages_append(kv(), FAKE, 4, 3, 4, FAKE, FAKE, None, None, None) == _native.EINVAL
     assert call(new=dict(tokens=0)) == _native.OK
     assert call(rows=0, lens=None, table=None) == _native.OK

@@ -879,9 +879,9 @@ def pages_compact(pool: PagePool | None, table: torch.Tensor, lens: torch.Tensor
 
 def _matrix(t, name: str, dtypes, rows: int, dev: int) -> tuple[int, int, int]:
     """Pointer, width and row stride of a tensor [rows, width] whose rows'
-    elements are adjacent; (None, 0, 0) for None."""
+    elements are adjacent; zeros for None."""
     if t is None:
-        return None, 0, 0
+        return 0, 0, 0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
@@ -945,7 +945,7 @@ def adjust_logits(logits: torch.Tensor, *, history: torch.Tensor | None = None,
             raise ValueError("out must have the shape of logits")
     f32, i32 = torch.float32, torch.int32
     bias_ptr, biases, _ = _matrix(bias, "bias", (f32,), rows, dev)
-    named = _arg(bias_tokens, "bias_tokens", i32, rows * biases, dev) if bias is not None else None
+    named = _arg(bias_tokens, "bias_tokens", i32, rows * biases, dev) if bias is not None else 0
     if bias is None and bias_tokens is not None:
         raise ValueError("bias_tokens needs bias")
     if bias is not None and (not bias.is_contiguous() or bias_tokens.shape != bias.shape):
@@ -954,10 +954,10 @@ def adjust_logits(logits: torch.Tensor, *, history: torch.Tensor | None = None,
     mask_ptr, words, mask_stride = _matrix(allowed, "allowed", _U32_DTYPES, rows, dev)
     if allowed is not None and words != (vocab + 31) // 32:
         raise ValueError("allowed must have ceil(vocab / 32) words a row")
-    rules = _native.LogitRulesStruct(
-        history_ptr, held, history_stride, _optional(history_lens, "history_lens", i32, rows, dev),
-        _optional(prompt_lens, "prompt_lens", i32, rows, dev), _optional(repetition, "repetition", f32, rows, dev),
-        _optional(presence, "presence", f32, rows, dev), _optional(frequency, "frequency", f32, rows, dev), named,
+    rules = _native.pack_logit_rules(
+        history_ptr, held, history_stride, _optional(history_lens, "history_lens", i32, rows, dev) or 0,
+        _optional(prompt_lens, "prompt_lens", i32, rows, dev) or 0, _optional(repetition, "repetition", f32, rows, dev) or 0,
+        _optional(presence, "presence", f32, rows, dev) or 0, _optional(frequency, "frequency", f32, rows, dev) or 0, named,
         bias_ptr, biases, mask_ptr, mask_stride)
     _native.check(_native.lib().adjust_logits(logits.data_ptr(), kind, rows, vocab, row_stride, out_ptr, out_stride,
                                               rules, sh), "adjust_logits")
@@ -1134,7 +1134,7 @@ def pages_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_ke
     cos_ptr, pairs, _ = _matrix(cos, "cos", (f32,), cos.shape[0] if isinstance(cos, torch.Tensor) and cos.dim() else 0,
                                 dev)
     positions = 0
-    sin_ptr = None
+    sin_ptr = 0
     if cos is not None:
         positions = cos.shape[0]
         sin_ptr = _arg(sin, "sin", f32, positions * pairs, dev)
@@ -1144,7 +1144,7 @@ def pages_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_ke
             raise ValueError("cos and sin have more pairs than a head")
     elif sin is not None:
         raise ValueError("sin needs cos")
-    q, q_heads, o = (None, 0, 0), 0, (None, 0, 0)
+    q, q_heads, o = (0, 0, 0), 0, (0, 0, 0)
     if queries is not None:
         q = _heads_arg(queries, "queries", dtype, tokens, None, dim, dev)
         q_heads = queries.shape[1]
@@ -1154,7 +1154,7 @@ def pages_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_ke
         _distinct(queries_out, "queries_out")
     elif queries_out is not None:
         raise ValueError("queries_out needs queries")
-    new = _native.NewTokensStruct(tokens, kind, *k, *v, q[0], q_heads, q[1], q[2], *o, cos_ptr, sin_ptr, positions,
+    new = _native.pack_new_tokens(tokens, kind, *k, *v, q[0], q_heads, q[1], q[2], *o, cos_ptr, sin_ptr, positions,
                                   pairs, bool(interleaved))
     _native.check(_native.lib().pages_append(*args, _optional(status, "status", torch.int32, args[3], dev), new, sh),
                   "pages_append")
