@@ -897,8 +897,9 @@ int pages_append(const u32scan_kv_cache *cache, const int32_t *table, size_t tab
  *   out = sum_j softmax_j(scale * q . k_j) v_j.
  * Query head h reads key head h / (q_heads / heads). Tokens that the table
  * does not place (past `width` pages, a page number outside [0, pages)) are
- * left out; a query that sees none gets zeros. Scales must be finite and not below 0.
- * Codes that are NaN make NaN of what sees them.
+ * left out; a query that sees none gets zeros. The scales of a block that holds a token that
+ * is seen must be finite and not below 0; other blocks' scales, like the codes of tokens that
+ * are not seen, may hold anything. Codes that are NaN make NaN of what sees them.
  * Products of queries (scaled by a power of two to f16, for bf16 exact but for
  * elements below 2^-22 of a head's largest) and codes are exact and summed in
  * f32, as are the softmax's sums; its weights are rounded to f16 (2^-11

@@ -451,3 +451,54 @@ def test_two_streams_at_once(u):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+@pytest.mark.parametrize("page_tokens,blocks", [(16, 2), (16, 16), (48, 2), (32, 4), (20, 2)])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), 3e38])
+@pytest.mark.parametrize("dim,group", [(64, 2), (128, 8), (256, 4)])
+def test_scales_of_unwritten_blocks(u, page_tokens, blocks, poison, dim, group):
+    """A row's last page may hold blocks that no token was written to: their scales are anybody's."""
+    c = Case(26, [5, 20, 50, 33], [1, 3, 9, 1], dim=dim, group=group, page_tokens=page_tokens, blocks=blocks)
+    d = c.gpu()
+    clean = call(u, d)
+    c.check(clean)
+    size, poisoned = page_tokens // blocks, 0
+    for s, length in enumerate(c.lens):
+        page, nth = c.table[s, (length - 1) // page_tokens], (length - 1) % page_tokens // size
+        for k in ("key_scales", "value_scales"):
+            d[k][page, nth + 1 :] = poison
+            poisoned += blocks - 1 - nth
+    assert poisoned > 0
+    assert torch.equal(call(u, d), clean)
+
+
+@pytest.mark.parametrize("which", ["key_scales", "value_scales"])
+def test_scales_of_drafts_not_seen_yet(u, which):
+    """A block that holds a row's last draft alone: only that draft meets its scale."""
+    c = Case(27, [41, 25], [6, 2], page_tokens=16, blocks=2)
+    d = c.gpu()
+    clean = call(u, d)
+    for s, length in enumerate(c.lens):
+        d[which][c.table[s, (length - 1) // 16], (length - 1) % 16 // 8] = float("nan")
+    got = call(u, d)
+    last = c.starts[1:] - 1
+    rest = np.setdiff1d(np.arange(c.tokens), last)
+    assert torch.equal(got[rest], clean[rest])
+    assert got[last].isnan().all()
+
+
+def test_a_small_weight_meets_a_large_scale(u):
+    """A warp's first tile has values of 0 at the least scale; in its next one the weights are 0 in
+    f32 and the scale is large: their product is nothing."""
+    rows = 320  # so that a block has whole rows
+    c = Case(28, [144] * rows, heads=1, group=1, dim=64)
+    c.table[:] = c.table[0]
+    c.keys[...] = 0
+    c.keys[c.table[0, 0], 0] = 0x38  # token 0's score is 3 * 8 * 64, the others' 0: e^-1536
+    c.key_scales[...] = 1.0
+    c.queries[...] = 8.0
+    c.values[c.table[0, 0]] = 0
+    c.value_scales[...] = 1.0
+    c.value_scales[c.table[0, 0]] = 2.0**-100
+    c.value_scales[c.table[0, 8]] = 2.0**30  # tokens 128 to 143: the same warp's next tile
+    assert not call(u, c.gpu(), scale=3.0).any()

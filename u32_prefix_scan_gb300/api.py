@@ -1170,8 +1170,10 @@ def pages_attend(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, querie
     heads). Rows, starts and positions as pages_append; scale multiplies the
     products (None: dim ** -0.5). dim is a multiple of 16 up to 256; a cache's
     addresses and strides are multiples of 16 bytes, and so are the queries'.
-    A query that sees no token gets zeros. Returns out (a new tensor by
-    default; tokens behind the last row's are left alone in it)."""
+    The scales of blocks that hold a seen token must be finite and not below 0
+    (as pages_append writes them); other blocks may hold anything. A query that
+    sees no token gets zeros. Returns out (a new tensor by default; tokens
+    behind the last row's are left alone in it)."""
     shape = _tensor(queries, "queries").shape
     tokens = shape[0] if len(shape) else 0
     args = _cache_rows(cache, table, lens, starts, tokens)

@@ -664,9 +664,12 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                         for (int j = 0; j < 2; ++j) {
                             float x = fmaf(s[nt][2 * k + j], ks[k] * factor[nt][j], -m[nt][j]);
                             if (!BOX && ks[k] < 0.0f) x = -INFINITY;
-                            if (partly && (int32_t)(base + S::token(g) + 8 * k) > last[nt][j]) x = -INFINITY;
+                            const bool hidden = partly && (int32_t)(base + S::token(g) + 8 * k) > last[nt][j];
+                            if (hidden) x = -INFINITY;
                             p[nt][2 * k + j] = exp2_approx(x);
-                            w[nt][2 * k + j] = p[nt][2 * k + j] * (vs[k] * c_ref[nt][j]);
+                            // (of a hidden token the scale may be anybody's; and p first: its product with a seen token's
+                            // scale is finite, or past kMaxWeight, where scale times reference may be infinite beside p = 0)
+                            w[nt][2 * k + j] = hidden ? 0.0f : p[nt][2 * k + j] * vs[k] * c_ref[nt][j];
                             top_w = fmaxf(top_w, w[nt][2 * k + j]);
                             top_x = fmaxf(top_x, x);
                         }
@@ -674,11 +677,12 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float by[2];
+                        bool hidden[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const bool hidden = (!BOX && ks[k >> 1] < 0.0f) ||
-                                                (partly && (int32_t)(base + S::token(g) + 8 * (k >> 1)) > last[nt][k & 1]);
-                            s[nt][k] = hidden ? -INFINITY : s[nt][k] * (ks[k >> 1] * factor[nt][k & 1]);
+                            hidden[k] = (!BOX && ks[k >> 1] < 0.0f) ||
+                                        (partly && (int32_t)(base + S::token(g) + 8 * (k >> 1)) > last[nt][k & 1]);
+                            s[nt][k] = hidden[k] ? -INFINITY : s[nt][k] * (ks[k >> 1] * factor[nt][k & 1]);
                         }
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
@@ -690,7 +694,7 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 p[nt][2 * k + j] = exp2_approx(s[nt][2 * k + j] - top);
-                                heavy = fmaxf(heavy, p[nt][2 * k + j] * vs[k]);
+                                heavy = fmaxf(heavy, hidden[2 * k + j] ? 0.0f : p[nt][2 * k + j] * vs[k]);
                             }
                             for (int d = 4; d < 32; d <<= 1) heavy = fmaxf(heavy, __shfl_xor_sync(0xffffffffu, heavy, d));
                             const float fit = heavy > 0.0f ? fminf(1.0f / heavy, 0x1p100f) : 0x1p100f;
@@ -700,7 +704,8 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                             m[nt][j] = top;
                             c_ref[nt][j] = c_new;
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) w[nt][2 * k + j] = p[nt][2 * k + j] * (vs[k] * c_new);
+                            for (int k = 0; k < 2; ++k)
+                                w[nt][2 * k + j] = hidden[2 * k + j] ? 0.0f : p[nt][2 * k + j] * vs[k] * c_new;
                         }
 #pragma unroll
                         for (int i2 = 0; i2 < DP / 16; ++i2)
