@@ -902,8 +902,10 @@ int pages_append(const u32scan_kv_cache *cache, const int32_t *table, size_t tab
  * are not seen, may hold anything. Codes that are NaN make NaN of what sees them.
  * Products of queries (scaled by a power of two to f16, for bf16 exact but for
  * elements below 2^-22 of a head's largest) and codes are exact and summed in
- * f32, as are the softmax's sums; its weights are rounded to f16 (2^-11
- * relative) before they meet the values; the result is rounded once to the type.
+ * f32, as are the softmax's sums. Before they meet the values its weights w_j are
+ * rounded to f16: with s_j the scale of v_j's block and H the largest w_j s_j of the
+ * query, w_j s_j is off by 2^-11 of itself or by 2^-32 H, whichever is more. The
+ * result is rounded once to the type.
  *   queries  device, [tokens][q_heads][dim] of `type` (F16 or BF16), strides in
  *            elements; q_heads a multiple of the cache's heads.
  *   out      device, [tokens][q_heads][dim] of `type`; must not overlap queries.

@@ -502,3 +502,68 @@ def test_a_small_weight_meets_a_large_scale(u):
     c.value_scales[c.table[0, 0]] = 2.0**-100
     c.value_scales[c.table[0, 8]] = 2.0**30  # tokens 128 to 143: the same warp's next tile
     assert not call(u, c.gpu(), scale=3.0).any()
+
+
+def own_bound(c, got):
+    """The largest quotient of a result's error, against attention in 64 bits, and its bound. With w_j
+    the tokens' softmax weights, v_j their codes, s_j the scales of their values' blocks and H the largest
+    w_j s_j of the query: a weight is rounded to f16, to 2^-11 of itself or, below f16's normal
+    range, half of f16's least step, 2^-25, where H has become 2^7 at least: 2^-32 H. A score is off by
+    its f32 sum of dim products and the roundings after it, (dim + 8) 2^-23 of its sum of magnitudes (a step a sum,
+    whichever way they are rounded), which acts on both sides of the quotient. 2^-18 for the sums of products, and half a step (f16: 2^-25 at least)
+    of the result's own."""
+    worst, got = 0.0, got.double().cpu().numpy()
+    page_tokens, heads = c.keys.shape[1:3]
+    size = page_tokens // c.key_scales.shape[1]
+    tokens, q_heads, dim = c.queries.shape
+    group = q_heads // heads
+    half = float(torch.finfo(TYPES[c.dtype]).eps) / 2
+    codes = oracle.code_values(np.arange(256)).astype(np.float64)
+    starts = np.arange(len(c.lens) + 1) if c.starts is None else c.starts
+    scale = c.dim**-0.5 if c.scale is None else c.scale
+    for row, length in enumerate(c.lens):
+        at = np.arange(min(int(length), c.table.shape[1] * page_tokens))
+        page = c.table[row, at // page_tokens]
+        placed = (page >= 0) & (page < c.pages)
+        at, page = at[placed], page[placed]
+        slot = at % page_tokens
+        for h in range(heads):
+            ks, vs = (t[page, slot // size, h].astype(np.float64) for t in (c.key_scales, c.value_scales))
+            k, v = codes[c.keys[page, slot, h]] * ks[:, None], codes[c.values[page, slot, h]]
+            size_of_v = np.abs(v)
+            for token in range(starts[row], starts[row + 1]):
+                n = int((at <= length - starts[row + 1] + token).sum())
+                q = c.queries[token, h * group : (h + 1) * group].double().numpy()
+                its = got[token, h * group : (h + 1) * group]
+                if n == 0:
+                    assert not its.any()
+                    continue
+                s = q @ k[:n].T * scale
+                score = (dim + 8) * 2.0**-23 * (np.abs(q) @ np.abs(k[:n]).T).max() * abs(scale)
+                w = np.exp(s - s.max(1, keepdims=True))
+                w = w / w.sum(1, keepdims=True) * vs[:n]
+                want = w @ v[:n]
+                tol = (w @ size_of_v[:n]) * (2.0**-11 + 2.0**-18 + 2 * score) + half * np.abs(want)
+                tol += 2.0**-32 * w.max(1)[:, None] * size_of_v[:n].sum(0) + 2.0**-25
+                off = np.abs(its - want)
+                assert np.isfinite(off).all()
+                worst = max(worst, float((off / tol).max()))
+    return worst
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("gap", [12, 18, 24, 26])
+@pytest.mark.parametrize("length", [128, 5000])
+def test_many_small_weights_beside_sinks(u, length, gap, dtype):
+    """One token of every 16 takes all the weight, and its value is 0: what comes out is the others'."""
+    c = Case(29, [length], heads=1, group=2, dim=64, dtype=dtype)
+    c.keys[...] = 0
+    c.keys[:, 0] = 0x38  # 1
+    c.key_scales[...] = 1.0
+    c.queries[...] = 1.0
+    c.scale = gap * float(np.log(2)) / 64  # the others' weight: 2^-gap
+    c.values[...] = np.random.default_rng(gap).integers(0x70, 0x7F, c.values.shape)  # 128 to 448
+    c.values[:, 0] = 0
+    c.value_scales[...] = 2.0 ** min(gap - 9, 7)  # (the results lie in f16's normal range)
+    worst = own_bound(c, call(u, c.gpu(), scale=c.scale))
+    assert worst <= 1, worst

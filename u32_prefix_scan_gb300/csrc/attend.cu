@@ -15,10 +15,14 @@
 // The softmax in one pass: per query a reference m for the sum l of
 // p = 2^(s - m), and a second one, c, for what the values are weighted by,
 // w = p * (scale of the value's block) * c, so that f16 holds the weights of
-// blocks whose scales lie far apart. Both stay until a weight exceeds 2^8
-// (p: 2^32); only then the warp takes new maxima and rescales its sums.
-// w is rounded to f16 (2^-11 relative; products and sums are f32): the
-// codes it meets have 4 bits, and the result's type 8 or 11.
+// blocks whose scales lie far apart. The heaviest w of the tile that sets c
+// is 2^7; both stay until one exceeds 2^15 (p: 2^32), and only then the warp
+// takes new maxima and rescales its sums. w is rounded to f16 (products and
+// sums are f32): to 2^-11 of itself, or below f16's normal range by 2^-25, so by
+// 2^-32 of the query's heaviest (p in l is not rounded, so what is lost here is
+// lost from the result). The codes it meets have 4 bits, and the result's type 8
+// or 11. (With a heaviest of 1 and a limit of 2^8, which take the same time, tokens
+// below 2^-25 of it were lost, by the thousand beside one that takes all.)
 //
 // The work of all rows is one line of units (a tile of 16 tokens for each of a
 // block's eight warps: of up to four heads beside each other, so that a page's
@@ -57,7 +61,7 @@ constexpr uint64_t kLeastUnits = 3;
 constexpr int kMaxElements = 4096;        // heads x queries x dimensions of a tile of queries
 constexpr int kMaxPairs = 64;             // its heads x queries
 constexpr float kNoMax = -1e30f;
-constexpr float kMaxWeight = 256.0f, kMaxAbove = 32.0f;
+constexpr float kHeaviest = 0x1p7f, kMaxWeight = 0x1p15f, kMaxAbove = 32.0f;
 
 struct AttendArgs {
     RowsView v;
@@ -697,7 +701,7 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                                 heavy = fmaxf(heavy, hidden[2 * k + j] ? 0.0f : p[nt][2 * k + j] * vs[k]);
                             }
                             for (int d = 4; d < 32; d <<= 1) heavy = fmaxf(heavy, __shfl_xor_sync(0xffffffffu, heavy, d));
-                            const float fit = heavy > 0.0f ? fminf(1.0f / heavy, 0x1p100f) : 0x1p100f;
+                            const float fit = heavy > 0.0f ? fminf(kHeaviest / heavy, 0x1p100f) : 0x1p100f;
                             const float c_new = fminf(c_ref[nt][j] * more, fit);
                             by[j] = less > 0.0f ? c_new / c_ref[nt][j] * less : 0.0f;
                             l[nt][j] *= less;
