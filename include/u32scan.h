@@ -897,7 +897,8 @@ int pages_append(const u32scan_kv_cache *cache, const int32_t *table, size_t tab
  *   out = sum_j softmax_j(scale * q . k_j) v_j.
  * Query head h reads key head h / (q_heads / heads). Tokens that the table
  * does not place (past `width` pages, a page number outside [0, pages)) are
- * left out; a query that sees none gets zeros. The scales of a block that holds a token that
+ * left out; a query that sees none gets zeros (and so does one all of whose scores are
+ * -infinity in f32). The scales of a block that holds a token that
  * is seen must be finite and not below 0; other blocks' scales, like the codes of tokens that
  * are not seen, may hold anything. Codes that are NaN make NaN of what sees them.
  * Products of queries (scaled by a power of two to f16, for bf16 exact but for

@@ -567,3 +567,17 @@ def test_many_small_weights_beside_sinks(u, length, gap, dtype):
     c.value_scales[...] = 2.0 ** min(gap - 9, 7)  # (the results lie in f16's normal range)
     worst = own_bound(c, call(u, c.gpu(), scale=c.scale))
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("low", [20, 99, 110, 127])
+def test_scores_far_below_zero(u, low):
+    """Equal scores weigh the same, however low they are; a row's only token weighs 1."""
+    c = Case(30, [40, 700, 1], heads=2, group=2, dim=64)
+    c.keys[...] = 0x38
+    c.key_scales[...] = 1.0
+    c.queries[...] = -(2.0 ** (low - 6))  # scores of -2^low
+    got = call(u, c.gpu(), scale=1.0)
+    c.queries[...] = 0.0
+    c.scale = 1.0
+    worst = own_bound(c, got)
+    assert worst <= 1, worst

@@ -60,7 +60,7 @@ constexpr uint32_t kTileCost = 5;
 constexpr uint64_t kLeastUnits = 3;
 constexpr int kMaxElements = 4096;        // heads x queries x dimensions of a tile of queries
 constexpr int kMaxPairs = 64;             // its heads x queries
-constexpr float kNoMax = -1e30f;
+constexpr float kNoMax = -0x1.fffffep127f;  // the least f32: every finite score takes its place
 constexpr float kHeaviest = 0x1p7f, kMaxWeight = 0x1p15f, kMaxAbove = 32.0f;
 
 struct AttendArgs {
@@ -666,7 +666,8 @@ attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap key_map,
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float x = fmaf(s[nt][2 * k + j], ks[k] * factor[nt][j], -m[nt][j]);
+                            // (the product rounded alone, as where m is taken: equal scores are equal, however large)
+                            float x = __fsub_rn(__fmul_rn(s[nt][2 * k + j], ks[k] * factor[nt][j]), m[nt][j]);
                             if (!BOX && ks[k] < 0.0f) x = -INFINITY;
                             const bool hidden = partly && (int32_t)(base + S::token(g) + 8 * k) > last[nt][j];
                             if (hidden) x = -INFINITY;
