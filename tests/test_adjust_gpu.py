@@ -198,3 +198,25 @@ def test_another_stream_a_graph_and_then_sampling(u):
         check(out, logits, rules)
         want, _ = oracle.sample_tokens(out.float().cpu().numpy(), words.cpu().numpy().view(np.uint32))
         assert np.array_equal(tokens.cpu().numpy(), want) and tokens[rows // 2] == -1
+
+
+# from 304 blocks of four vectors a thread on: 8192 f32 logits a block, 16384 of 16 bits
+@pytest.mark.parametrize("rows,vocab,dtype", [(40, 65537, "f32"), (80, 65543, "bf16"), (77, 65536, "f16"), (304, 8201, "f32")])
+@pytest.mark.parametrize("off", [0, 3, 8])
+def test_large_batches(u, rows, vocab, dtype, off):
+    """Rows at any place within a vector, in place too; more names in one slice than a block keeps, and the same ones
+    again; a history longer than a slice."""
+    logits = logits_for(rows, vocab, off, dtype)
+    rules = rules_for(rows, vocab, off + 1, width=9000 if rows < 50 else 700, biases=700)
+    rules["bias_tokens"][1] = 5000 + np.arange(700) % 601
+    rules["bias_tokens"][2] = np.random.default_rng(off).permutation(8000)[:700]
+    g = on_gpu(rules)
+    wide = torch.full((rows, vocab + off + 5), 9.0, dtype=TYPES[dtype], device="cuda")
+    view = wide[:, off : off + vocab]
+    view.copy_(logits)
+    out = torch.full_like(wide, 7.0)
+    check(u.adjust_logits(view, out=out[:, off : off + vocab], **g), logits, rules)
+    assert torch.all(out[:, :off] == 7) and torch.all(out[:, off + vocab :] == 7)
+    u.adjust_logits(view, out=view, **g)
+    assert np.array_equal(bits(wide[:, off : off + vocab]), bits(out[:, off : off + vocab]))
+    assert torch.all(wide[:, :off] == 9) and torch.all(wide[:, off + vocab :] == 9)

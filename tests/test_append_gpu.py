@@ -322,3 +322,30 @@ def test_offsets_past_32_bits(u, cache):
         d[k] = view
     call(u, d)
     c.check({**d, "keys": d["keys"].contiguous(), "values": d["values"].contiguous()})
+
+
+@pytest.mark.parametrize("dtype,cache", CACHES)
+@pytest.mark.parametrize("dim,heads,q_heads,page_tokens,blocks", [(64, 2, 6, 16, 1), (128, 1, 2, 48, 2)])
+def test_many_tokens(u, dtype, cache, dim, heads, q_heads, page_tokens, blocks):
+    """More tokens than blocks of 64 threads run at a time."""
+    c = Case(dim, [900, 1500, 17, 3, 400], [700, 1500, 1, 0, 300], dim=dim, dtype=dtype, cache=cache, heads=heads, q_heads=q_heads,
+             page_tokens=page_tokens, blocks=blocks, tail=5)
+    assert c.tokens > 2432
+    d = c.gpu()
+    call(u, d)
+    c.check(d)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,most", [(32, 3), (33, 2), (100, 5), (1025, 2), (1500, 3)])
+def test_many_rows_of_any_number_of_tokens(u, cache, rows, most):
+    """Rows found among more than 32 and more than 32 * 32, empty ones beside each other among them."""
+    rng = np.random.default_rng(rows)
+    counts = rng.integers(0, most + 1, rows)
+    counts[rows // 3 : rows // 3 + 40] = 0
+    counts[[0, -1]] = [0, 1]
+    lens = counts + rng.integers(0, 20, rows)
+    c = Case(rows, lens, counts, dim=16, heads=1, q_heads=2, page_tokens=8, blocks=2, cache=cache, tail=2)
+    d = c.gpu()
+    call(u, d)
+    c.check(d)

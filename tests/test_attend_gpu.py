@@ -581,3 +581,46 @@ def test_scores_far_below_zero(u, low):
     c.scale = 1.0
     worst = own_bound(c, got)
     assert worst <= 1, worst
+
+
+def segments(c):
+    """Values that tell their places: token j of a row has one element that is not 0, the one of its share of the row."""
+    page_tokens, heads, dim = c.keys.shape[1:]
+    rng = np.random.default_rng(len(c.lens))
+    c.values[...] = 0
+    for row, length in enumerate(c.lens):
+        at = np.arange(int(length))
+        page, d = c.table[row, at // page_tokens], at * dim // max(int(length), 1)
+        ok = page >= 0
+        for h in range(heads):
+            c.values[page[ok], at[ok] % page_tokens, h, d[ok]] = rng.integers(0x60, 0x7F, int(ok.sum()))
+    return c
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("length,heads,drafts,group,dim", [(60000, 1, 5, 7, 64), (50000, 2, 1, 8, 128), (30000, 4, 3, 5, 128),
+                                                          (20000, 2, 2, 3, 256), (40000, 1, 1, 16, 80)])
+def test_every_token_of_a_long_row_counts(u, length, heads, drafts, group, dim, dtype):
+    """A part that is lost, or joined with a wrong weight, is missed in its tokens' own elements."""
+    c = segments(Case(length, [length], [drafts], heads=heads, group=group, dim=dim, dtype=dtype))
+    worst = own_bound(c, call(u, c.gpu()))
+    assert worst <= 1, worst
+
+
+# heads beside each other in a block: 4 for 8 x 8 and 4 x 3, 2 for six heads, two heads, 256 dimensions and groups of 16
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,length,heads,group,dim,page_tokens,blocks", [
+    (64, 2500, 8, 8, 128, 16, 1), (40, 2000, 4, 3, 64, 32, 2), (40, 1500, 6, 2, 128, 64, 4), (80, 1800, 2, 4, 64, 16, 2),
+    (48, 700, 8, 1, 256, 16, 1), (60, 1200, 4, 16, 128, 32, 2), (64, 900, 8, 8, 96, 48, 2), (50, 1100, 8, 2, 48, 16, 16),
+    (300, 300, 4, 4, 128, 16, 1)])
+@pytest.mark.parametrize("drafts", [0, 3])
+def test_batches_of_heads_beside_each_other(u, rows, length, heads, group, dim, page_tokens, blocks, dtype, drafts):
+    lens = np.linspace(3, length, rows).astype(int)[np.random.default_rng(rows).permutation(rows)]
+    lens[::17] = 0
+    counts = None if drafts == 0 else 1 + np.arange(rows) % drafts
+    c = segments(Case(rows, lens, counts, heads=heads, group=group, dim=dim, page_tokens=page_tokens, blocks=blocks,
+                      dtype=dtype))
+    for row in range(1, rows, 9):  # pages that are not there
+        c.table[row, int(lens[row]) // page_tokens // 2] = -1 if row % 2 else c.pages
+    worst = own_bound(c, call(u, c.gpu()))
+    assert worst <= 1, worst
