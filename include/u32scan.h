@@ -909,7 +909,8 @@ int pages_append(const u32scan_kv_cache *cache, const int32_t *table, size_t tab
  * result is rounded once to the type.
  *   queries  device, [tokens][q_heads][dim] of `type` (F16 or BF16), strides in
  *            elements; q_heads a multiple of the cache's heads.
- *   out      device, [tokens][q_heads][dim] of `type`; must not overlap queries.
+ *   out      device, [tokens][q_heads][dim] of `type`; must share no memory with
+ *            queries (their tokens or heads may lie between each other's).
  *            Tokens behind the last row's are left alone.
  *   cache    type E4M3; dim a multiple of 16 up to 256; keys, values and the
  *            strides in bytes multiples of 16; queries too.
@@ -917,6 +918,7 @@ int pages_append(const u32scan_kv_cache *cache, const int32_t *table, size_t tab
  * The result does not depend on the other calls that run; every sum is taken
  * in an order fixed by the sizes, lens and starts.
  * Errors: EINVAL (as pages_append; another cache type; the alignments above;
+ * an out that shares memory with queries;
  * tokens times query heads of a key head at or above 2^31), EWORKSPACE, ECUDA; a
  * copy that does not land within its time as the scan's.
  */

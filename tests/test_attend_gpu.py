@@ -624,3 +624,22 @@ def test_batches_of_heads_beside_each_other(u, rows, length, heads, group, dim, 
         c.table[row, int(lens[row]) // page_tokens // 2] = -1 if row % 2 else c.pages
     worst = own_bound(c, call(u, c.gpu()))
     assert worst <= 1, worst
+
+
+def test_outputs_beside_queries_and_over_them(u):
+    """Queries and outputs in one tensor, every token's beside each other; outputs over queries are refused."""
+    from u32_prefix_scan_gb300 import _native
+
+    c = Case(31, [70, 45], [3, 2], heads=2, dim=64)
+    d = c.gpu()
+    want = call(u, d)
+    both = torch.zeros(c.tokens, 2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    both[:, 0] = d["queries"]
+    before = both[:, 0].clone()
+    assert torch.equal(call(u, {**d, "queries": both[:, 0]}, out=both[:, 1]), want)
+    assert torch.equal(both[:, 0], before)
+    for out in (d["queries"], both.flatten(1, 2)[:, 1:5], both.flatten(1, 2)[:, :4]):
+        queries = d["queries"] if out is d["queries"] else both[:, 0]
+        with pytest.raises(_native.U32ScanError):
+            call(u, {**d, "queries": queries}, out=out)
+    assert torch.equal(both[:, 0], before) and torch.equal(both[:, 1], want)

@@ -273,3 +273,57 @@ def test_attend_rejects_bad_arguments_on_host(lib):
         assert call(**kw) == _native.EWORKSPACE, kw
     assert call(tokens=0) == _native.OK
     assert call(rows=0, lens=None, table=None) == _native.OK
+
+
+def shared(a, b):
+    """Whether two arrays (first element, counts, strides, run) have an element in common."""
+    places = []
+    for at, counts, strides, run in (a, b):
+        i = np.arange(at, at + run)
+        for n, s in zip(counts, strides):
+            i = (i[None] + np.arange(n)[:, None] * s).ravel()
+        places.append(np.unique(i))
+    return np.intersect1d(*places).size > 0
+
+
+def attend_refuses(lib, tokens, q_heads, q, out):
+    """Whether pages_attend refuses queries and out ((first element, token stride, head stride) of bf16, heads of 16
+    elements), by what it says where both are sound but the workspace is missing."""
+    cache = kv(dim=16, heads=1, head_stride=0, token_stride=16, page_stride=256)
+    status = lib.pages_attend(cache, FAKE, 4, tokens, 4, FAKE, None, tokens, FAKE + 2 * q[0], _native.BF16, q_heads, *q[1:],
+                              FAKE + 2 * out[0], *out[1:], 1.0, None, 0, None)
+    assert status in (_native.EINVAL, _native.EWORKSPACE)
+    return status == _native.EINVAL
+
+
+def test_attend_refuses_an_output_that_shares_memory_with_the_queries(lib):
+    for q, out, refused in (
+            ((0, 64, 16), (0, 64, 16), True), ((0, 64, 16), (8, 64, 16), True), ((0, 64, 16), (64, 64, 16), True),
+            ((0, 64, 16), (64 * 5, 64, 16), False), ((64 * 5, 64, 16), (0, 64, 16), False),
+            ((64 * 5, 64, 16), (1, 64, 16), True), ((64 * 5 + 8, 64, 16), (1, 64, 16), False),
+            ((0, 192, 16), (64, 192, 16), False), ((0, 192, 16), (128, 192, 16), False),  # parts of one row
+            ((0, 192, 16), (56, 192, 16), True), ((0, 192, 48), (16, 192, 48), False), ((0, 192, 48), (9, 192, 48), True),
+            ((0, 16, 80), (0, 64, 16), True), ((0, 0, 0), (0, 64, 16), True), ((0, 0, 0), (16, 64, 16), False)):
+        assert attend_refuses(lib, 5, 4, q, out) == refused, (q, out)
+
+
+@pytest.mark.parametrize("seed", range(3))
+def test_shared_memory_is_found_exactly(lib, seed):
+    rng, found = np.random.default_rng(seed), 0
+    for _ in range(400):
+        tokens, heads = (int(x) for x in rng.integers(1, 7, 2))
+        q, out = ((int(rng.integers(0, 30)) * 8, int(rng.integers(0, 30)) * 8, int(rng.integers(0, 30)) * 8) for _ in range(2))
+        if rng.random() < 0.5:
+            out = (out[0], *q[1:])
+        want = shared(*((x[0], (tokens, heads), x[1:], 16) for x in (q, out)))
+        assert attend_refuses(lib, tokens, heads, q, out) == want, (tokens, heads, q, out)
+        found += want
+    assert 40 < found < 360
+
+
+def test_shared_memory_of_the_largest_sizes(lib):
+    """Strides and counts whose products pass 64 bits."""
+    far = 1 << 39
+    assert not attend_refuses(lib, (1 << 31) // 8 - 1, 8, (0, far, 16), (128, far, 16))
+    assert attend_refuses(lib, (1 << 31) // 8 - 1, 8, (0, far, 16), (120, far, 16))
+    assert attend_refuses(lib, (1 << 31) // 8 - 1, 8, (far * 1000, far, 16), (0, far, 16))

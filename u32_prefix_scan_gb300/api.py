@@ -1172,8 +1172,9 @@ def pages_attend(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, querie
     addresses and strides are multiples of 16 bytes, and so are the queries'.
     The scales of blocks that hold a seen token must be finite and not below 0
     (as pages_append writes them); other blocks may hold anything. A query that
-    sees no token gets zeros. Returns out (a new tensor by default; tokens
-    behind the last row's are left alone in it)."""
+    sees no token gets zeros. Returns out (a new tensor by default, else one
+    that shares no memory with queries; tokens behind the last row's are left
+    alone in it)."""
     shape = _tensor(queries, "queries").shape
     tokens = shape[0] if len(shape) else 0
     args = _cache_rows(cache, table, lens, starts, tokens)

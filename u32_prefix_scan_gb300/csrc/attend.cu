@@ -997,6 +997,10 @@ extern "C" int pages_attend(const u32scan_kv_cache *cache, const int32_t *table,
     if (tokens * (q_heads / cache->heads) >= (1ull << 31)) return U32SCAN_EINVAL;
     if (tokens == 0 || rows == 0) return U32SCAN_OK;
     if (queries == nullptr || out == nullptr) return U32SCAN_EINVAL;
+    const size_t run = 2 * cache->dim;
+    if (share_memory(Strided{queries, run, {tokens, q_heads, 1}, {2 * query_token_stride, 2 * query_head_stride, 0}},
+                     Strided{out, run, {tokens, q_heads, 1}, {2 * out_token_stride, 2 * out_head_stride, 0}}))
+        return U32SCAN_EINVAL;
     if (ws == nullptr || misaligned(ws, 256) || ws_bytes < attend_workspace_bytes()) return U32SCAN_EWORKSPACE;
     AttendArgs a{};
     a.v = RowsView{table, lens, starts, table_stride, rows, width, tokens, cache->pages,
