@@ -845,7 +845,8 @@ typedef struct {
     size_t value_token_stride, value_head_stride;
     const void *queries; /* NULL: no queries */
     size_t q_heads, query_token_stride, query_head_stride;
-    void *queries_out; /* may be `queries` with the same strides, else they must not overlap */
+    void *queries_out; /* may be `queries` with the same strides; shares no memory with queries, keys or values
+                          otherwise */
     size_t out_token_stride, out_head_stride;
     const float *cos, *sin; /* device, float[positions][pairs]; NULL: no rotation */
     size_t positions, pairs;
@@ -883,7 +884,7 @@ typedef struct {
  * No workspace. Errors: EINVAL (null pointers with sizes above 0, misaligned
  * pointers, sizes at or above 2^31, strides at or above 2^40 or 0 where there
  * is more than one, rows and tokens
- * that differ without starts, 2 pairs above dim, dim above 1024, blocks that do not
+ * that differ without starts, queries_out over another array, 2 pairs above dim, dim above 1024, blocks that do not
  * divide page_tokens, an unknown type or a cache of another one), ECUDA.
  */
 int pages_append(const u32scan_kv_cache *cache, const int32_t *table, size_t table_stride, size_t rows, size_t width,

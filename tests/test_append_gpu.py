@@ -349,3 +349,29 @@ def test_many_rows_of_any_number_of_tokens(u, cache, rows, most):
     d = c.gpu()
     call(u, d)
     c.check(d)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_rotated_queries_beside_the_inputs_and_over_them(u, cache):
+    """Queries, keys and values cut out of one projection, queries rotated in place in it or into a
+    part of it of their own; over keys, values or other queries they are refused."""
+    from u32_prefix_scan_gb300 import _native
+
+    c = Case(61, [30, 17, 9], [13, 17, 1], cache=cache, heads=3, dim=32, q_heads=5, page_tokens=8, blocks=2)
+    for place in ("in place", "beside"):
+        d = c.gpu()
+        fused = torch.zeros(c.tokens, 16, 32, dtype=torch.bfloat16, device="cuda")
+        for k, at, n in (("queries", 0, 5), ("new_keys", 5, 3), ("new_values", 8, 3)):
+            fused[:, at : at + n] = d[k]
+            d[k] = fused[:, at : at + n]
+        if place == "in place":
+            d["queries_out"] = d["queries"]
+        else:
+            d["queries_out"] = fused[:, 11:].fill_(7.0)
+        before = fused.clone()
+        for out in (fused[:, 1:6], fused[:, 5:10], fused[:, 6:11], fused[:, 4:9]):
+            with pytest.raises(_native.U32ScanError):
+                call(u, d, queries_out=out)
+        assert torch.equal(fused, before)
+        call(u, d)
+        c.check(d)

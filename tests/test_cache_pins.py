@@ -327,3 +327,16 @@ def test_shared_memory_of_the_largest_sizes(lib):
     assert not attend_refuses(lib, (1 << 31) // 8 - 1, 8, (0, far, 16), (128, far, 16))
     assert attend_refuses(lib, (1 << 31) // 8 - 1, 8, (0, far, 16), (120, far, 16))
     assert attend_refuses(lib, (1 << 31) // 8 - 1, 8, (far * 1000, far, 16), (0, far, 16))
+
+
+@pytest.mark.parametrize("type", [_native.F32, _native.BF16])
+def test_append_refuses_rotated_queries_over_its_inputs(lib, type):
+    """8 tokens of 4 heads of 64 elements, queries_out over a part of another array or over queries laid out otherwise."""
+    size, far = 4 if type == _native.F32 else 2, 1 << 24
+    apart = dict(type=type, keys=FAKE + far, values=FAKE + 2 * far, queries=FAKE + 3 * far, queries_out=FAKE + 4 * far)
+    for name, at in (("keys", FAKE + far), ("values", FAKE + 2 * far), ("queries", FAKE + 3 * far)):
+        for kw in (dict(queries_out=at + 64 * size), dict(queries_out=at - 63 * size),
+                   dict(queries_out=at, out_token_stride=320), dict(queries_out=at, out_head_stride=512, out_token_stride=64),
+                   dict(queries_out=at + (128 * 7 + 64) * size)):
+            new = new_tokens(**{**apart, **kw})
+            assert lib.pages_append(kv(type=type), FAKE, 4, 3, 4, FAKE, FAKE, None, ctypes.byref(new), None) == _native.EINVAL, (name, kw)

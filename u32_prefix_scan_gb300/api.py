@@ -1117,7 +1117,8 @@ def pages_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_ke
     Rows with status[s] < 0 (pages_fork's answer) are left as they were, and so
     are tokens whose position has no page or no angles; tokens behind the
     last row's are ignored. queries [tokens, q_heads, dim], rotated likewise,
-    go to queries_out (a new tensor by default; queries itself works in place)."""
+    go to queries_out (a new tensor by default; queries itself works in place,
+    other memory of queries, new_keys or new_values does not)."""
     tokens = new_keys.shape[0] if _tensor(new_keys, "new_keys").dim() else 0
     args = _cache_rows(cache, table, lens, starts, tokens)
     dev, heads, dim = cache.device.index, cache.heads, cache.dim

@@ -22,6 +22,7 @@
 #include <cuda_runtime.h>
 
 #include "kvcache.cuh"
+#include "launch.cuh"
 
 namespace u32scan {
 
@@ -348,6 +349,18 @@ __global__ void __launch_bounds__(kNThreads, 5) append_kernel(const AppendArgs a
     }
 }
 
+// Whether the rotated queries would lie over what other blocks still read. (Queries themselves, place by place, may.)
+static bool queries_over_inputs(const AppendArgs &a, size_t elem) {
+    auto view = [&](const Heads &h) {
+        return Strided{h.data, a.dim * elem, {a.v.tokens, h.heads, 1}, {h.token_stride * elem, h.head_stride * elem, 0}};
+    };
+    const Heads &q = a.queries, &o = a.out;
+    const bool in_place = q.data == o.data && (a.v.tokens == 1 || q.token_stride == o.token_stride) &&
+                          (q.heads == 1 || q.head_stride == o.head_stride);
+    return q.heads > 0 && ((!in_place && share_memory(view(o), view(q))) || share_memory(view(o), view(a.keys)) ||
+                           share_memory(view(o), view(a.values)));
+}
+
 // Whether every address that a vector kernel forms is a multiple of its vector's size (16 bytes; codes: 4).
 static bool wide(const AppendArgs &a, size_t elem, bool coded) {
     const uint64_t n = 16 / elem;
@@ -432,6 +445,7 @@ extern "C" int pages_append(const u32scan_kv_cache *cache, const int32_t *table,
         a.scale_stride = cache->scale_stride;
         a.block_tokens = divisor((uint32_t)(cache->page_tokens / cache->blocks));
     }
+    if (queries_over_inputs(a, elem)) return U32SCAN_EINVAL;
     const cudaStream_t s = (cudaStream_t)stream;
     if (t.type == U32SCAN_F32) append_launch<float>(a, coded, s);
     else if (t.type == U32SCAN_F16) append_launch<__half>(a, coded, s);
