@@ -880,7 +880,9 @@ typedef struct {
  * `positions` on; the rotated queries of tokens at positions outside
  * [0, positions) are NaN. Tokens behind the last row's are left alone, in
  * queries_out too.
- * No two rows may write to one page (pages_fork sees to it), nor a row twice.
+ * No two rows may write to one page (pages_fork sees to it), nor a row twice. The cache's
+ * keys, values and scales share no memory with each other, nor with the new tokens where they
+ * are written.
  * No workspace. Errors: EINVAL (null pointers with sizes above 0, misaligned
  * pointers, sizes at or above 2^31, strides at or above 2^40 or 0 where there
  * is more than one, rows and tokens

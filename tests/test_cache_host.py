@@ -213,3 +213,40 @@ def test_packed_arguments_are_the_structures():
     for kind, pack in ((_native.LogitRulesStruct, _native.pack_logit_rules), (_native.NewTokensStruct, _native.pack_new_tokens)):
         values = [i + 1 for i in range(len(kind._fields_))]
         assert pack(*values) == bytes(kind(*values))
+
+
+def test_a_cache_that_shares_memory_is_only_read(gpu):
+    """Keys that are the values, or a part of them; scales likewise. Views of one page beside each other are not."""
+    a = Args(gpu)
+    room = on(torch.zeros(6, 3, 16, 2, 32, dtype=E4M3))
+    page = on(torch.zeros(6, 4, 16, 2, 40, dtype=E4M3))
+    scales = gpu.new(6, 9, 2, dtype=F32)
+
+    def views(t, i, j):
+        return on(t[:, i]), on(t[:, j])
+
+    shared = [(a.keys, a.keys, *a.scales), (on(room[:, 0]), on(room[:, 0]), *a.scales),
+              (on(room.flatten(1, 2)[:, :16]), on(room.flatten(1, 2)[:, 15:31]), *a.scales),
+              (on(room.flatten(1, 2)[:, 5:21]), on(room.flatten(1, 2)[:, :16]), *a.scales),
+              (on(page[:, 0, :, :, :32]), on(page[:, 0, :, :, 8:]), *a.scales),
+              (a.keys, a.values, a.scales[0], a.scales[0]),
+              (a.keys, a.values, on(scales[:, :4]), on(scales[:, 3:7])),
+              (a.keys, a.values, on(scales[:, 5:]), on(scales[:, 4:8]))]
+    apart = [(a.keys, a.values, *a.scales), (*views(room, 0, 1), *a.scales), (*views(room, 2, 0), *a.scales),
+             (*views(page, 3, 1), *a.scales), (a.keys, a.values, on(scales[:, :4]), on(scales[:, 4:8])),
+             (on(room[:1, 0]), on(room[1:2, 0]), on(a.scales[0][:1]), on(a.scales[0][1:2])),
+             (on(page[..., :8]).flatten(1, 2)[:, :16], on(page[..., 8:16]).flatten(1, 2)[:, :16], *a.scales)]
+    none = [on(torch.zeros(0, 16, 2, 32, dtype=E4M3)) for _ in range(2)]
+    apart.append((*none, *[on(torch.zeros(0, 4, 2)) for _ in range(2)]))
+    rows = (a.table, a.lens)
+    for parts in shared:
+        cache = u.KVCache(*map(on, parts))
+        with pytest.raises(ValueError, match="share memory"):
+            u.pages_append(cache, *rows, a.k, a.v)
+        u.pages_attend(cache, *rows, on(a.q))
+    reads = len(gpu.lib.calls)
+    for parts in apart:
+        cache = u.KVCache(*map(on, parts))
+        k = gpu.new(4, 2, cache.dim, dtype=BF16)
+        u.pages_append(cache, *rows, k, k)
+    assert reads == len(shared) and len(gpu.lib.calls) == reads + len(apart)

@@ -967,6 +967,17 @@ def adjust_logits(logits: torch.Tensor, *, history: torch.Tensor | None = None,
 _CACHE_TYPES = {**_LOGIT_TYPES, torch.float8_e4m3fn: _native.E4M3}
 
 
+def _meet(apart: int, axes, run: int) -> bool:
+    """Whether two arrays of the same nested strides, `apart` elements from
+    each other, share one: axes (stride, size), the widest first, over runs of
+    adjacent elements."""
+    if not axes:
+        return abs(apart) < run
+    (stride, n), rest = axes[0], axes[1:]
+    nearest = apart // stride  # (what the rest adds is less than a stride, up or down)
+    return any(abs(k) < n and _meet(apart - k * stride, rest, run) for k in (nearest, nearest + 1))
+
+
 class KVCache:
     """One layer's keys and values in a paged cache, for pages_append and
     pages_attend.
@@ -979,7 +990,8 @@ class KVCache:
     block of page_tokens / blocks tokens and head: a value is its code times
     its scale. To let the pages_* calls move scales with their codes, make
     both views of one page of bytes. Keeps the tensors alive; make it once a
-    layer.
+    layer. One whose keys and values (or their scales) share memory can be
+    read, but not appended to.
     """
 
     def __init__(self, keys: torch.Tensor, values: torch.Tensor, key_scales: torch.Tensor | None = None,
@@ -1008,6 +1020,8 @@ class KVCache:
             if s < reach:
                 raise ValueError("a cache's elements must not overlap")
             reach = s * (n - 1) + reach
+        apart = values.data_ptr() - keys.data_ptr()
+        self.shared = pages > 0 and _meet(apart // keys.element_size(), spans[::-1], dim)
         coded = keys.dtype is torch.float8_e4m3fn
         if coded != (key_scales is not None) or coded != (value_scales is not None):
             raise ValueError("key_scales and value_scales belong to a cache of float8_e4m3fn")
@@ -1030,6 +1044,8 @@ class KVCache:
             scale_stride = key_scales.stride(0) if pages > 1 else 0
             if pages > 1 and scale_stride < blocks * heads:
                 raise ValueError("a cache's scales must not overlap")
+            apart = value_scales.data_ptr() - key_scales.data_ptr()
+            self.shared |= pages > 0 and _meet(apart // 4, [(scale_stride, pages)] if pages > 1 else [], blocks * heads)
         self.keys, self.values, self.key_scales, self.value_scales = keys, values, key_scales, value_scales
         self.dtype, self.heads, self.dim = keys.dtype, heads, dim
         self.struct = _native.KVCacheStruct(
@@ -1121,6 +1137,8 @@ def pages_append(cache: KVCache, table: torch.Tensor, lens: torch.Tensor, new_ke
     other memory of queries, new_keys or new_values does not)."""
     tokens = new_keys.shape[0] if _tensor(new_keys, "new_keys").dim() else 0
     args = _cache_rows(cache, table, lens, starts, tokens)
+    if cache.shared:
+        raise ValueError("the cache's keys and values share memory: it can only be read")
     dev, heads, dim = cache.device.index, cache.heads, cache.dim
     sh = _launch_stream(stream, dev)
     dtype = new_keys.dtype
