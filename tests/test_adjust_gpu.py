@@ -220,3 +220,18 @@ def test_large_batches(u, rows, vocab, dtype, off):
     u.adjust_logits(view, out=view, **g)
     assert np.array_equal(bits(wide[:, off : off + vocab]), bits(out[:, off : off + vocab]))
     assert torch.all(wide[:, :off] == 9) and torch.all(wide[:, off + vocab :] == 9)
+
+
+@pytest.mark.parametrize("vocab", [1000, 1003, 70001])
+def test_results_between_the_logits(u, vocab):
+    """Rows of logits and of results in one tensor, every row's beside each other; over each other they are refused."""
+    logits, rules = logits_for(6, vocab, 5, "bf16"), rules_for(6, vocab, 6)
+    both = torch.full((6, 2, vocab + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    both[:, 0, :vocab] = logits
+    g = on_gpu(rules)
+    check(u.adjust_logits(both[:, 0, :vocab], out=both[:, 1, :vocab], **g), logits, rules)
+    assert np.array_equal(bits(both[:, 0, :vocab]), bits(logits)) and torch.all(both[:, :, vocab:] == 7)
+    flat = both.flatten(1)
+    for at in (1, vocab - 1):
+        with pytest.raises(u_error()):
+            u.adjust_logits(flat[:, :vocab], out=flat[:, at : at + vocab], **g)

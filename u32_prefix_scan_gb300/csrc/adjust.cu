@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include "internal.cuh"
+#include "launch.cuh"
 
 namespace u32scan {
 
@@ -290,9 +291,10 @@ extern "C" int adjust_logits(const void *logits, int type, size_t rows, size_t v
     if (logits == nullptr || out == nullptr) return U32SCAN_EINVAL;
     if (r.history_width > 0 && r.history == nullptr) return U32SCAN_EINVAL;
     if (r.biases > 0 && (r.bias_tokens == nullptr || r.bias == nullptr)) return U32SCAN_EINVAL;
-    const u64 in_span = ((rows - 1) * row_stride + vocab) * elem, out_span = ((rows - 1) * out_stride + vocab) * elem;
     const bool in_place = from == to && (rows == 1 || row_stride == out_stride);
-    if (!in_place && from < to + out_span && to < from + in_span) return U32SCAN_EINVAL;
+    if (!in_place && share_memory(Strided{logits, vocab * elem, {rows, 1, 1}, {row_stride * elem, 0, 0}},
+                                  Strided{out, vocab * elem, {rows, 1, 1}, {out_stride * elem, 0, 0}}))
+        return U32SCAN_EINVAL;
     AdjustArgs a{logits, out, rows, vocab, rows > 1 ? row_stride : 0, rows > 1 ? out_stride : 0, r, 0};
     if (a.r.history_width == 0) a.r.history = nullptr;
     const cudaStream_t s = (cudaStream_t)stream;
