@@ -13,8 +13,12 @@
 // 128 (bf16 into bf16, 340 MB) 57 us, 5.9 TB/s, bound by the memory; 16384 tokens
 // of 16 + 32 heads of 64 into 8 bits (170 MB) 80 us, bound by latency and
 // instructions: the chain from a token's row over its page to the scale, and two
-// passes over the values; 64 rows' next tokens 5 us, one row's 2.7, a launch and
-// that chain.
+// passes over the values; 64 rows' next tokens into 8 bits 5 us, one row's into
+// bf16 2.8, a launch and that chain. The 5 us are of scales that hold: where a
+// new token raises its block's, a warp tells the older codes anew a byte a lane
+// at a time, and the launch lasts as long as the slowest: with 2, 20, 100 % of
+// the (64 x 16, blocks of 16 tokens of 128) scales growing 15, 22, 27 us, in blocks of
+// 64 tokens of 256 96, 172, 190 us (5.8 with none).
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -273,8 +277,9 @@ __device__ void append_part(const AppendArgs &a, const Part &p, uint64_t head, i
     }
 }
 
-// WIDE: vectors of 16 bytes (for codes: of four values), else elements. (At 48 registers a thread, five blocks of 256 an SM:
-// 8192 tokens of 64 + 16 heads of 128 bf16 57 us; at 64, four, 60; at 40, six, 87.)
+// WIDE: vectors of 16 bytes (for codes: of four values), else elements. (At 48 registers a thread, five blocks of 256 an SM,
+// with 24 to 48 bytes a thread spilled: 8192 tokens of 64 + 16 heads of 128 bf16 57 us, 16384 into 8 bits 80, 64 rows' next 5.2,
+// one row's 2.7; at 64, four, 60, 80, 5.0, 2.7; at 40, six, 87, 79, 5.6, 3.2.)
 template <typename T, bool CODED, bool WIDE>
 __global__ void __launch_bounds__(kNThreads, 5) append_kernel(const AppendArgs a) {
     const uint64_t token = blockIdx.x;
@@ -382,9 +387,9 @@ static void append_launch(const AppendArgs &a, bool coded, cudaStream_t s) {
         return;
     }
     // Of many tokens (more blocks of 64 threads than run at a time) a thread takes several units, whose loads overlap; of few
-    // as many threads as a token has units, or warps as it has heads of its block. 64, 128, 256 threads (at 64 registers):
-    // 8192 tokens of 64 + 16 heads of 128 bf16 60, 60, 70 us, 16384 tokens of 16 + 32 heads of 64 into 8 bits 85, 90, 135; 64 tokens of
-    // 32 + 16 heads into 8 bits 11.5, 7.3, 5.2.
+    // as many threads as a token has units, or warps as it has heads of its block. 64, 128, 256 threads: 8192 tokens of 64 +
+    // 16 heads of 128 bf16 57, 57, 64 us, 16384 tokens of 16 + 32 heads of 64 into 8 bits 80, 81, 112; 64 tokens of 32 + 16 heads into
+    // 8 bits 10.9, 6.8, 5.2, one of them into bf16 4.2, 3.0, 2.7.
     const uint64_t units = a.queries.heads * (a.dim * sizeof(T) / 32) + (coded ? 0 : 2 * a.keys.heads * (a.dim * sizeof(T) / 32));
     const uint64_t work = coded && units < 64 * a.keys.heads ? 64 * a.keys.heads : units;
     const int threads = a.v.tokens >= 2432 || work <= 64 ? 64 : work <= 128 ? 128 : kNThreads;

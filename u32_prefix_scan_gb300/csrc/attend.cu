@@ -30,15 +30,18 @@
 // however ragged the rows are. Where a tile of queries falls to several blocks,
 // the one that comes last joins their partial sums, in order.
 //
-// Measured on one GB300, launches back to back: 64 ragged rows of up to 8192
-// tokens of 8 heads of 128, groups of eight, 111 us (540 MB, 4.9 TB/s), 16384
-// tokens each 374 us (5.8 TB/s), two rows of 200000 tokens 164 us, 33 rows of
-// drafts (up to five tokens, groups of seven, heads of 64, pages of 20) 32 us, one
-// row of 4000 tokens 14 us. Bound by the reading of the cache, unevenly: some
-// groups of SMs read 18 % slower than the rest and end last; the same grid with
-// its copies alone takes 100 of the 111 us. A block's fixed part (queries, page
-// numbers, the first copies, the join) is some 10 us of latency, which is what
-// one row takes.
+// Measured on GB300s, launches back to back: 64 ragged rows of up to 8192
+// tokens of 8 heads of 128, groups of eight, 108 to 111 us (540 MB, 4.9 TB/s);
+// heads of 64, 80, 96 71, 103, 95 us, 4 heads of 256 101 us, groups of sixteen
+// 152 us (4 heads of 256: 163, read twice). 16384 tokens each 374 us (5.8 TB/s),
+// two rows of 200000 tokens 153 to 167 us, 33 rows of drafts (up to five tokens,
+// groups of seven, heads of 64, pages of 20) 32 us, one row of 4000 tokens 14 us.
+// Bound by the reading of the cache, unevenly: some groups of SMs read 18 %
+// slower than the rest and end last; the same grid with its copies alone takes
+// 100 of the 111 us. A block's fixed part (queries, page numbers, the first
+// copies, the join) is some 10 us of latency, which is what one row takes. Many
+// queries a row are not what it is for: each 16 of a key head read the cache
+// again, and 5 rows of 8192 tokens with 256 new ones in the mean take 2.8 ms.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -54,8 +57,9 @@ constexpr int kTile = 16;                 // tokens of a warp at a time
 constexpr int kMaxDim = 256;
 constexpr unsigned int kMaxBlocks = 304;  // two on each of a GB300's 152 SMs; bounds the workspace
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-// What a tile of queries takes beside its units, in units (64 ragged rows of up to 8192 tokens 117, 110, 112 us with 2,
-// 4, 6, drafts 49, 46, 45), and the least piece (one row of 4000 tokens 15.1 us with 4 units, 14.3 with 3).
+// What a tile of queries takes beside its units, in units (with 2, 4, 5, 6, 8: 64 ragged rows of up to 8192 tokens 114,
+// 107, 108, 107, 106 us, drafts 33.4, 32.3, 31.9, 31.8, 32.9, two rows of 200000 156, 155, 154, 152, 154), and the least
+// piece (with 2, 3, 4 units: one row of 4000 tokens 13.7, 14.5, 15.0 us, drafts 31.9; parts to join are the more of, the less).
 constexpr uint32_t kTileCost = 5;
 constexpr uint64_t kLeastUnits = 3;
 constexpr int kMaxElements = 4096;        // heads x queries x dimensions of a tile of queries
@@ -75,7 +79,7 @@ struct AttendArgs {
     uint64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
     uint32_t pair_heads;  // log2 of the key heads that a block's warps have beside each other: 0, 1 or 2
     float scale;  // times log2(e)
-    bool wide_blocks;  // and in one block
+    bool wide_blocks;  // a scale's block is a multiple of 16 tokens: 16 in one page have one scale
     WsHeader *hdr;
     float4 *partial;     // [2 blocks][heads][sums of a tile of queries, as the lanes hold them]
     float2 *partial_ml;  // [2 blocks][heads][queries of a tile]: reference and sum
@@ -938,8 +942,11 @@ static int attend_launch(AttendArgs a, cudaStream_t s) {
     uint64_t blocks = (uint64_t)sms * S::kBlocks;
     if (blocks > kMaxBlocks) blocks = kMaxBlocks;
     // Tiles of queries, and units if every row is as long as its table: at most these. Several heads beside each other read
-    // a page's memory together, but leave fewer and larger parts, which one block each joins: 64 rows of 8192 tokens 127,
-    // 116, 124 us with 1, 2, 4 heads and 608 blocks of four warps, two rows of 200000 182, 179, 211.
+    // a page's memory together, but leave fewer and larger parts, which one block each joins. With 1, 2, 4 heads, us: 256
+    // rows of up to 2048 tokens 124, 109, 106, of 500 61, 50, 48, 200 of 1500 of 16 heads 149, 128, 121, heads of 64: 77, 71, 71
+    // and, of 16 heads, 105, 75, 73; but 64 rows of 8192 100 to 110, 100 to 102, 108 to 111 and 32 of them 62, 63, 72; two
+    // rows of 200000 154 each. (As many as there are: long rows of 128 dimensions would go 8 to 13 % faster with two,
+    // short ones 2 to 9 % slower.)
     const uint64_t tiles = a.v.tokens * a.group.d / S::kRows + a.v.rows;
     a.pair_heads = a.heads % 4 == 0 ? 2 : a.heads % 2 == 0 ? 1 : 0;
     if (a.pair_heads > S::kMostPaired) a.pair_heads = S::kMostPaired;
@@ -961,9 +968,9 @@ static int attend_launch(AttendArgs a, cudaStream_t s) {
 
 // Eight queries at a time, or sixteen where the mean row has nearly that many for each key head: the codes are then read and
 // converted once for both, in twice the registers. 64 rows of up to 8192 tokens, 8 heads of 128, with 8 and 16 at a time:
-// groups of 16 173 and 151 us, of 8 with one or two tokens (12 queries in the mean) 110 and 144, with one to five
-// (24) 227 and 218; 33 short rows of drafts, heads of 64 (21), 28 and 32, 200 longer ones 165 and 151. (32 at a
-// time, heads of 64: 42 and 218.)
+// groups of 16 173 and 152 us, of 8 with one or two tokens (12 queries in the mean) 111 and 145, with one to five
+// (24) 225 and 219, these with heads of 64 155 and 133; 33 short rows of drafts, heads of 64 (21), 28 and 32, 200 of them
+// 96 and 92. (32 at a time, 33 rows: 42.)
 template <typename T>
 static int attend_dispatch(const AttendArgs &a, cudaStream_t s) {
     const bool many = a.v.tokens * a.group.d >= 14 * a.v.rows;
